@@ -11,6 +11,10 @@ in the library's CUDA kernels.  PyTorch only provides device memory and
 streams.  There is no CPU fallback: if ``libgs.so`` is missing or no CUDA
 device is present, the calls raise.
 
+Next to the path stand the token operators of a network that predicts Gaussians
+and is trained through it: ``gs_qk_norm_rope``, ``gs_attention_fwd``,
+``gs_dropout_add`` and their gradients.
+
 ``Rasterizer`` is a convenience that allocates the outputs and workspaces of
 one view and runs the five calls in order.
 """
@@ -30,6 +34,9 @@ __all__ = [
     "gs_loss_l1_ssim", "gs_loss_workspace_bytes", "LossSettings",
     "gs_bin_sort_workspace_bytes", "gs_raster_workspace_bytes", "gs_bin_sort_noalloc",
     "gs_raster_stats", "gs_default_settings", "gs_status_string", "gs_num_tiles",
+    "gs_qk_norm_rope", "gs_qk_norm_rope_bwd", "gs_qk_norm_rope_workspace_bytes",
+    "gs_attention_fwd", "gs_attention_bwd", "gs_attention_workspace_bytes",
+    "gs_dropout_add", "gs_dropout_add_bwd",
     "Camera", "Settings", "Rasterizer", "library",
     "GSError", "TILE", "GRAD2D", "SPLAT_FLOATS",
 ]
@@ -102,6 +109,24 @@ class LossSettings(C.Structure):
         return cls(0.2, 0.01 ** 2, 0.03 ** 2, 1.5)
 
 
+class Heads(C.Structure):
+    """gs_heads: a [tokens, heads, head_dim] array read by strides (in elements)."""
+    _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class HeadNorm(C.Structure):
+    """gs_head_norm: element type, rotated values, pairing, eps, rows of the angle table."""
+    _fields_ = [("type", C.c_int32), ("rot", C.c_int32), ("interleaved", C.c_int32),
+                ("eps", C.c_float), ("table_rows", C.c_int64)]
+
+
+class AttentionShape(C.Structure):
+    """gs_attention_shape: tokens, sequences, heads, mask and scale of an attention call."""
+    _fields_ = [("tokens_q", C.c_int64), ("tokens_k", C.c_int64), ("batch", C.c_int32),
+                ("heads_q", C.c_int32), ("heads_k", C.c_int32), ("head_dim", C.c_int32),
+                ("causal", C.c_int32), ("scale", C.c_float)]
+
+
 _lib = None
 _lib_lock = threading.Lock()
 _P = C.c_void_p
@@ -163,6 +188,25 @@ def _declare(lib: C.CDLL) -> None:
     lib.gs_loss_l1_ssim.restype = st
     lib.gs_loss_l1_ssim.argtypes = [C.c_int32, C.c_int32, _P, _P, C.POINTER(LossSettings), _P, _P,
                                     _P, C.c_size_t, _P]
+    H, N, A = C.POINTER(Heads), C.POINTER(HeadNorm), C.POINTER(AttentionShape)
+    i32 = C.c_int32
+    lib.gs_qk_norm_rope.restype = st
+    lib.gs_qk_norm_rope.argtypes = [_I64, i32, i32, i32, N, H, H, _P, _P, _P, _P, H, H, _P]
+    lib.gs_qk_norm_rope_workspace_bytes.restype = C.c_size_t
+    lib.gs_qk_norm_rope_workspace_bytes.argtypes = [_I64, i32, i32, i32]
+    lib.gs_qk_norm_rope_bwd.restype = st
+    lib.gs_qk_norm_rope_bwd.argtypes = ([_I64, i32, i32, i32, N, H, H] + [_P] * 4 + [H] * 4 +
+                                        [_P, _P, _P, C.c_size_t, _P])
+    lib.gs_attention_workspace_bytes.restype = C.c_size_t
+    lib.gs_attention_workspace_bytes.argtypes = [A]
+    lib.gs_attention_fwd.restype = st
+    lib.gs_attention_fwd.argtypes = [A, H, H, H, _P, _P, H, _P, _P, C.c_size_t, _P]
+    lib.gs_attention_bwd.restype = st
+    lib.gs_attention_bwd.argtypes = [A, H, H, H, _P, _P, H, _P, H, H, H, H, _P, C.c_size_t, _P]
+    lib.gs_dropout_add.restype = st
+    lib.gs_dropout_add.argtypes = [_I64, i32, _P, _P, _P, _P, C.c_float, _P]
+    lib.gs_dropout_add_bwd.restype = st
+    lib.gs_dropout_add_bwd.argtypes = [_I64, i32, _P, _P, _P, C.c_float, _P]
     lib.gs_bin_sort_noalloc.restype = st
     lib.gs_bin_sort_noalloc.argtypes = [C.POINTER(Camera), _I64, _P, _P, _P, _P, _I64, _P, _P, _P,
                                         _P, _P]
@@ -451,6 +495,185 @@ def gs_loss_l1_ssim(width, height, image, target, dL_dimage, loss_out, workspace
         C.byref(ls), _ptr(dL_dimage, "dL_dimage", f, P), _ptr(loss_out, "loss_out", f, 3),
         _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
     _check("gs_loss_l1_ssim", st)
+
+
+# ---------------------------------------------------------------------------
+# token operators
+# ---------------------------------------------------------------------------
+def _heads(t, name, tokens=None, heads=None, dim=None, dtype=None) -> Heads:
+    """A CUDA tensor [tokens, heads, head_dim], contiguous in its last dimension, as gs_heads."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected [tokens, heads, head_dim], got {tuple(t.shape)}")
+    want = (t.shape[0] if tokens is None else tokens, t.shape[1] if heads is None else heads,
+            t.shape[2] if dim is None else dim)
+    if tuple(t.shape) != want:
+        raise ValueError(f"{name}: expected shape {want}, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.numel() > 0 and t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return Heads(t.data_ptr() if t.numel() > 0 else None, t.stride(0), t.stride(1))
+
+
+def _element_type(t, name) -> int:
+    import torch
+
+    types = {torch.float32: 0, torch.bfloat16: 1}
+    if not isinstance(t, torch.Tensor) or t.dtype not in types:
+        raise ValueError(f"{name}: expected a float32 or bfloat16 tensor")
+    return types[t.dtype]
+
+
+def _norm_args(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved):
+    import torch
+
+    qh = _heads(q, "q")
+    T, hq, D = q.shape
+    kh = _heads(k, "k", tokens=T, dim=D, dtype=q.dtype)
+    rows, rot = (0, 0)
+    if cos_sin is not None:
+        if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
+            raise ValueError("cos_sin: expected a [rows, rot] tensor")
+        rows, rot = cos_sin.shape
+    norm = HeadNorm(_element_type(q, "q"), rot, int(bool(interleaved)), float(eps), rows)
+    f = torch.float32
+    return (T, hq, k.shape[1], D), norm, qh, kh, (
+        _ptr(q_weight, "q_weight", f, D, optional=True),
+        _ptr(k_weight, "k_weight", f, D, optional=True),
+        _ptr(cos_sin, "cos_sin", f, rows * rot, optional=True),
+        _ptr(positions, "positions", torch.int32, T, optional=True))
+
+
+def gs_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out, eps=1e-6,
+                    interleaved=False, stream=None):
+    """RMS norm of every head of q and k and the position rotation, in one pass (see gs.h).
+    q, k, q_out, k_out: [tokens, heads, head_dim] float32 or bfloat16, any strides with a
+    contiguous last dimension; cos_sin [rows, rot] float32 (None: no rotation); weights and
+    positions may be None."""
+    (T, hq, hk, D), norm, qh, kh, ptrs = _norm_args(q, k, q_weight, k_weight, cos_sin, positions,
+                                                    eps, interleaved)
+    st = library().gs_qk_norm_rope(
+        T, hq, hk, D, C.byref(norm), C.byref(qh), C.byref(kh), *ptrs,
+        C.byref(_heads(q_out, "q_out", T, hq, D, q.dtype)),
+        C.byref(_heads(k_out, "k_out", T, hk, D, q.dtype)), _stream(stream))
+    _check("gs_qk_norm_rope", st)
+
+
+def gs_qk_norm_rope_workspace_bytes(tokens, heads_q, heads_k, head_dim) -> int:
+    return int(library().gs_qk_norm_rope_workspace_bytes(int(tokens), int(heads_q), int(heads_k),
+                                                         int(head_dim)))
+
+
+def gs_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk_out, dq, dk,
+                        dq_weight, dk_weight, workspace, eps=1e-6, interleaved=False, stream=None):
+    """Gradient of gs_qk_norm_rope (see gs.h); dq_weight and dk_weight (float32 [head_dim]) may
+    be None."""
+    import torch
+
+    (T, hq, hk, D), norm, qh, kh, ptrs = _norm_args(q, k, q_weight, k_weight, cos_sin, positions,
+                                                    eps, interleaved)
+    f = torch.float32
+    st = library().gs_qk_norm_rope_bwd(
+        T, hq, hk, D, C.byref(norm), C.byref(qh), C.byref(kh), *ptrs,
+        C.byref(_heads(dq_out, "dq_out", T, hq, D, q.dtype)),
+        C.byref(_heads(dk_out, "dk_out", T, hk, D, q.dtype)),
+        C.byref(_heads(dq, "dq", T, hq, D, q.dtype)), C.byref(_heads(dk, "dk", T, hk, D, q.dtype)),
+        _ptr(dq_weight, "dq_weight", f, D, optional=True),
+        _ptr(dk_weight, "dk_weight", f, D, optional=True),
+        _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+    _check("gs_qk_norm_rope_bwd", st)
+
+
+def gs_attention_workspace_bytes(tokens_q, tokens_k, batch, heads_q, heads_k, head_dim) -> int:
+    shape = AttentionShape(int(tokens_q), int(tokens_k), int(batch), int(heads_q), int(heads_k),
+                           int(head_dim), 0, 1.0)
+    return int(library().gs_attention_workspace_bytes(C.byref(shape)))
+
+
+def _attention_args(q, k, v, cu_q, cu_k, causal, scale):
+    import torch
+
+    bf = torch.bfloat16
+    qh = _heads(q, "q", dtype=bf)
+    Tq, hq, D = q.shape
+    kh = _heads(k, "k", dim=D, dtype=bf)
+    Tk, hk = k.shape[:2]
+    vh = _heads(v, "v", Tk, hk, D, bf)
+    if (cu_q is None) != (cu_k is None):
+        raise ValueError("cu_q and cu_k: give both or neither")
+    batch = 1
+    if cu_q is not None:
+        batch = cu_q.numel() - 1
+        if batch < 1 or cu_k.numel() != batch + 1:
+            raise ValueError("cu_q and cu_k: expected batch + 1 offsets each")
+    shape = AttentionShape(Tq, Tk, batch, hq, hk, D, int(bool(causal)),
+                           float(D ** -0.5 if scale is None else scale))
+    cu = (_ptr(cu_q, "cu_q", torch.int32, optional=True),
+          _ptr(cu_k, "cu_k", torch.int32, optional=True))
+    return shape, (C.byref(qh), C.byref(kh), C.byref(vh)), cu
+
+
+def gs_attention_fwd(q, k, v, out, lse, workspace, cu_q=None, cu_k=None, causal=False, scale=None,
+                     stream=None):
+    """Softmax attention over a ragged batch (see gs.h).  q, out [tokens_q, heads_q, head_dim],
+    k, v [tokens_k, heads_k, head_dim] bfloat16, any strides with a contiguous last dimension;
+    lse [heads_q, tokens_q] float32; cu_q, cu_k [batch + 1] int32 offsets (None: one sequence);
+    scale defaults to head_dim ** -0.5."""
+    import torch
+
+    shape, heads, cu = _attention_args(q, k, v, cu_q, cu_k, causal, scale)
+    n = shape.tokens_q * shape.heads_q
+    st = library().gs_attention_fwd(
+        C.byref(shape), *heads, *cu,
+        C.byref(_heads(out, "out", *q.shape, torch.bfloat16)), _ptr(lse, "lse", torch.float32, n),
+        _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+    _check("gs_attention_fwd", st)
+
+
+def gs_attention_bwd(q, k, v, out, lse, dout, dq, dk, dv, workspace, cu_q=None, cu_k=None,
+                     causal=False, scale=None, stream=None):
+    """Gradient of gs_attention_fwd from its out and lse (see gs.h)."""
+    import torch
+
+    shape, heads, cu = _attention_args(q, k, v, cu_q, cu_k, causal, scale)
+    bf = torch.bfloat16
+    n = shape.tokens_q * shape.heads_q
+    st = library().gs_attention_bwd(
+        C.byref(shape), *heads, *cu, C.byref(_heads(out, "out", *q.shape, bf)),
+        _ptr(lse, "lse", torch.float32, n), C.byref(_heads(dout, "dout", *q.shape, bf)),
+        C.byref(_heads(dq, "dq", *q.shape, bf)), C.byref(_heads(dk, "dk", *k.shape, bf)),
+        C.byref(_heads(dv, "dv", *k.shape, bf)), _ptr(workspace, "workspace", torch.uint8),
+        workspace.numel(), _stream(stream))
+    _check("gs_attention_bwd", st)
+
+
+def gs_dropout_add(x, residual, out, rng, p, stream=None):
+    """out = residual + dropout(x) (see gs.h); residual may be None, out may be x or residual;
+    rng: CUDA int64[2], seed and offset."""
+    import torch
+
+    n = x.numel()
+    st = library().gs_dropout_add(
+        n, _element_type(x, "x"), _ptr(x, "x"), _ptr(residual, "residual", x.dtype, n, optional=True),
+        _ptr(out, "out", x.dtype, n), _ptr(rng, "rng", torch.int64, 2), float(p), _stream(stream))
+    _check("gs_dropout_add", st)
+
+
+def gs_dropout_add_bwd(dout, dx, rng, p, stream=None):
+    """Gradient of gs_dropout_add by x, with the same rng (the residual's is dout itself)."""
+    import torch
+
+    n = dout.numel()
+    st = library().gs_dropout_add_bwd(
+        n, _element_type(dout, "dout"), _ptr(dout, "dout"), _ptr(dx, "dx", dout.dtype, n),
+        _ptr(rng, "rng", torch.int64, 2), float(p), _stream(stream))
+    _check("gs_dropout_add_bwd", st)
 
 
 def gs_raster_stats(workspace, stream=None) -> dict:

@@ -16,8 +16,9 @@
  *
  * Around them: gs_loss_l1_ssim (the L1 + SSIM loss between the forward and
  * the backward), gs_project_bwd_adam (the chain rule fused with one Adam
- * step), bfloat16-SH variants of the projection and its chain rule, and
- * gs_bin_sort_noalloc.
+ * step), bfloat16-SH variants of the projection and its chain rule,
+ * gs_bin_sort_noalloc, and the token operators of a network that predicts the
+ * Gaussians (gs_qk_norm_rope, gs_attention_fwd, gs_dropout_add, their gradients).
  *
  * Sources (page title, section / equation):
  *   [RY]  Ryu & Yoo, "Mitigating SM-Level Load Imbalance in 3D Gaussian
@@ -412,6 +413,156 @@ gs_status gs_bin_sort_noalloc(const gs_camera* cam, int64_t n, const float* spla
                               int32_t* sorted_ids, int64_t capacity, int32_t* tile_ranges,
                               int32_t* lpt_order, int64_t* counts_device, int64_t* n_pairs_host,
                               void* stream);
+
+/*
+ * Token operators: the hot operators of a network that predicts Gaussians and is
+ * trained through this rasterizer (tokens of an image, one per 16 x 16 tile for
+ * instance; gs_project_bwd hands back the gradients of what it predicts).  The
+ * pages have no counterpart.  Their order in a block:
+ *
+ *   gs_qk_norm_rope   RMS norm of each query and key head, position rotation
+ *   gs_attention_fwd  softmax attention
+ *   gs_dropout_add    residual + dropout
+ *
+ * and back: gs_dropout_add_bwd, gs_attention_bwd, gs_qk_norm_rope_bwd.  Every call
+ * is deterministic: the same inputs give the same bits.
+ *
+ * gs_heads: a [tokens][heads][head_dim] array read by strides, so that queries, keys
+ * and values may lie in one packed projection or in another order of dimensions.
+ * The head_dim values of a row are contiguous; strides are in elements, multiples of
+ * 16 bytes, rows do not overlap, and the larger stride is a multiple of the smaller.
+ * Strides of dimensions of one element are not read.
+ */
+#define GS_TYPE_F32 0
+#define GS_TYPE_BF16 1
+
+typedef struct {
+    void* data; /* device, 16-byte aligned */
+    int64_t token_stride, head_stride;
+} gs_heads;
+
+/*
+ * gs_qk_norm_rope -- per token and head, for queries and keys alike,
+ *   n = w x (mean(x^2) + eps)^(-1/2)
+ * (w: head_dim weights shared by the heads; NULL = 1), then the first `rot` values of
+ * n are turned: the pair (a, b) of index i becomes (a c - b s, b c + a s) with c, s
+ * the token's cosine and sine.  Pair i is (n[i], n[i + rot/2]), or, interleaved,
+ * (n[2i], n[2i+1]); the other values stay as they are.
+ *
+ *   tokens >= 0; heads_q, heads_k in 1..1024; head_dim a multiple of 8, 8..256
+ *   norm       element type of q, k and the outputs; rot even, 0..head_dim; eps > 0
+ *   cos_sin    [table_rows][rot] fp32: rot/2 cosines, then rot/2 sines (not read when
+ *              rot = 0)
+ *   positions  [tokens] int32, the token's row of cos_sin; a negative position leaves
+ *              the token unturned (tokens without a place); one beyond the table gives
+ *              NaN in its turned values.  NULL: token t takes row t
+ *              (table_rows >= tokens)
+ *   q_out, k_out   may be q and k themselves (same data, same strides)
+ *
+ * gs_qk_norm_rope_bwd -- with g the outputs' gradient turned back,
+ *   dx = r (w g - x r^2 mean(w g x)),  dw = sum over tokens and heads of g x r,
+ * r = (mean(x^2) + eps)^(-1/2) recomputed from x.
+ *   q, k              the forward's inputs
+ *   dq_out, dk_out    gradients of the forward's outputs
+ *   dq, dk            out; may be dq_out and dk_out, or q and k, themselves
+ *   dq_weight, dk_weight   out, fp32 [head_dim] (NULL = not wanted)
+ *   workspace         >= gs_qk_norm_rope_workspace_bytes(...)
+ */
+typedef struct {
+    int32_t type; /* GS_TYPE_F32 or GS_TYPE_BF16 */
+    int32_t rot;
+    int32_t interleaved;
+    float eps;
+    int64_t table_rows;
+} gs_head_norm;
+
+gs_status gs_qk_norm_rope(int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t head_dim,
+                          const gs_head_norm* norm, const gs_heads* q, const gs_heads* k,
+                          const float* q_weight, const float* k_weight, const float* cos_sin,
+                          const int32_t* positions, const gs_heads* q_out, const gs_heads* k_out,
+                          void* stream);
+
+size_t gs_qk_norm_rope_workspace_bytes(int64_t tokens, int32_t heads_q, int32_t heads_k,
+                                       int32_t head_dim);
+
+gs_status gs_qk_norm_rope_bwd(int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t head_dim,
+                              const gs_head_norm* norm, const gs_heads* q, const gs_heads* k,
+                              const float* q_weight, const float* k_weight, const float* cos_sin,
+                              const int32_t* positions, const gs_heads* dq_out,
+                              const gs_heads* dk_out, const gs_heads* dq, const gs_heads* dk,
+                              float* dq_weight, float* dk_weight, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * gs_attention_fwd -- for every sequence of a ragged batch and every head h, over the
+ * sequence's keys j (key head h / (heads_q / heads_k)):
+ *   s_ij = scale q_i . k_j,  out_i = sum_j softmax_j(s_i) v_j,
+ *   lse_i = ln sum_j exp(s_ij)
+ * With causal, query i of n sees key j of m iff j <= i + m - n (the last query sees
+ * the last key).  A query that sees no key gives out 0 and lse -infinity.  What lies
+ * outside a sequence never reaches its results, NaN and infinities included; inside
+ * one, keys and values hidden from some of its queries must be finite.
+ *
+ *   shape      heads_q a multiple of heads_k; head_dim a multiple of 8, 8..128
+ *   q, out [tokens_q][heads_q][head_dim], k, v [tokens_k][heads_k][head_dim]: bfloat16
+ *   cu_q, cu_k [batch + 1] int32 offsets of the sequences' tokens, ascending from 0 to
+ *              tokens_q and tokens_k; lengths may be 0.  Both NULL: one sequence
+ *              (batch = 1).  Offsets beyond the arrays are cut to them; tokens that no
+ *              sequence holds are left unwritten
+ *   lse        out [heads_q][tokens_q] fp32
+ *   workspace  >= gs_attention_workspace_bytes(shape); holds nothing between calls
+ *
+ * Scores, probabilities' sums and the accumulated outputs are fp32; the probabilities
+ * are rounded to bfloat16 (unnormalised, relative to the row's maximum) for the second
+ * product.
+ *
+ * gs_attention_bwd -- the gradient, from the forward's out and lse:
+ *   P = exp(s - lse), delta_i = out_i . dout_i, dV = P^T dout,
+ *   dS = P (dout V^T - delta), dQ = scale dS K, dK = scale dS^T Q,
+ * keys' gradients summed over the query heads that share them.  Queries that see no
+ * key, and keys that no query sees, get zeros.  dq, dk and dv overlap no input.
+ */
+typedef struct {
+    int64_t tokens_q, tokens_k;
+    int32_t batch, heads_q, heads_k, head_dim;
+    int32_t causal; /* 0 or 1 */
+    float scale;
+} gs_attention_shape;
+
+size_t gs_attention_workspace_bytes(const gs_attention_shape* shape);
+
+gs_status gs_attention_fwd(const gs_attention_shape* shape, const gs_heads* q, const gs_heads* k,
+                           const gs_heads* v, const int32_t* cu_q, const int32_t* cu_k,
+                           const gs_heads* out, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+gs_status gs_attention_bwd(const gs_attention_shape* shape, const gs_heads* q, const gs_heads* k,
+                           const gs_heads* v, const int32_t* cu_q, const int32_t* cu_k,
+                           const gs_heads* out, const float* lse, const gs_heads* dout,
+                           const gs_heads* dq, const gs_heads* dk, const gs_heads* dv,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gs_dropout_add -- out = residual + x / (1 - p') where an element is kept, residual
+ * elsewhere (residual NULL = 0).  gs_dropout_add_bwd -- dx = dout / (1 - p') where it
+ * is kept, 0 elsewhere, from the same rng (the residual's gradient is dout itself).
+ * The mask is made from rng and never stored: element e takes the 16-bit number e mod 8
+ * of Philox4x32-10 (Salmon et al. 2011) with key rng[0] and counter (e / 8, rng[1]),
+ * and is dropped iff it is below round(65536 p); p' = round(65536 p) / 65536.  A
+ * dropped element counts as 0 whatever it holds.
+ *
+ *   n      elements, contiguous; type GS_TYPE_F32 or GS_TYPE_BF16 of all arrays
+ *   rng    DEVICE int64[2]: seed and offset (take another offset for every call that is
+ *          to have its own mask; being on the device, it can change between replays of
+ *          a captured graph)
+ *   p      0 <= p < 1 - 2^-17
+ *   out    may be x or residual; dx may be dout
+ */
+gs_status gs_dropout_add(int64_t n, int32_t type, const void* x, const void* residual, void* out,
+                         const int64_t* rng, float p, void* stream);
+
+gs_status gs_dropout_add_bwd(int64_t n, int32_t type, const void* dout, void* dx,
+                             const int64_t* rng, float p, void* stream);
 
 #ifdef __cplusplus
 }
