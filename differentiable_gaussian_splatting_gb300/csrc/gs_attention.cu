@@ -10,30 +10,27 @@
 #include <cmath>
 #include <cstdint>
 
+#include "gs_attention.cuh"
 #include "gs_device.cuh"
 #include "gs_internal.h"
 #include "gs_tokens.h"
 
 namespace gs {
+
 namespace {
+
+__device__ unsigned int g_gave_up;
 
 constexpr int kAtThreads = 128;
 constexpr int kPer = 4;  // values of a head per lane: head_dim <= 128
-
-struct View {
-    __nv_bfloat16* p;
-    int64_t ts, hs;
-    __device__ const __nv_bfloat16* row(int64_t t, int h) const { return p + t * ts + h * hs; }
-    __device__ __nv_bfloat16* row(int64_t t, int h) { return p + t * ts + h * hs; }
-};
 
 struct AtParams {
     int64_t tq, tk;
     int batch, hq, hk, dim, causal;
     float scale;
-    View q, k, v, o, dout, dq, dk, dv;
-    const float* lse_in;
-    float *lse, *delta;
+    HeadView q, k, v, o, dout, dq, dk, dv;
+    const float* lse;
+    float* delta;
     const int32_t *cu_q, *cu_k;
 };
 
@@ -84,34 +81,6 @@ __device__ float warp_dot(const float (&a)[kPer], const float (&b)[kPer]) {
     return s;
 }
 
-__global__ void __launch_bounds__(kAtThreads) attention_fwd_simple(AtParams p) {
-    grid_dep_sync();
-    const int64_t w = ((int64_t)blockIdx.x * kAtThreads + threadIdx.x) >> 5;
-    if (w >= p.tq * p.hq) return;
-    const int64_t t = w / p.hq;
-    const int h = (int)(w % p.hq), kh = h / (p.hq / p.hk);
-    const int b = sequence_of(p.cu_q, p.batch, t);
-    if (b < 0) return;
-    const Span s = span_of(p, b);
-    int64_t end = s.k1;
-    if (p.causal) end = min64(s.k1, t - s.q0 + 1 + (s.k1 - s.k0) - (s.q1 - s.q0) + s.k0);
-    float q[kPer], k[kPer], v[kPer], acc[kPer] = {};
-    load_row(q, p.q.row(t, h), p.dim);
-    float m = -INFINITY, l = 0.f;
-    for (int64_t j = s.k0; j < end; ++j) {
-        load_row(k, p.k.row(j, kh), p.dim);
-        load_row(v, p.v.row(j, kh), p.dim);
-        const float x = warp_dot(q, k) * p.scale;
-        const float m2 = fmaxf(m, x), f = __expf(m - m2), e = __expf(x - m2);
-        l = l * f + e;
-        m = m2;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) acc[i] = acc[i] * f + e * v[i];
-    }
-    store_row(p.o.row(t, h), acc, p.dim, l > 0.f ? 1.f / l : 0.f);
-    if ((threadIdx.x & 31) == 0) p.lse[h * p.tq + t] = l > 0.f ? m + logf(l) : -INFINITY;
-}
-
 __global__ void __launch_bounds__(kAtThreads) attention_bwd_dq_simple(AtParams p) {
     grid_dep_sync();
     const int64_t w = ((int64_t)blockIdx.x * kAtThreads + threadIdx.x) >> 5;
@@ -127,7 +96,7 @@ __global__ void __launch_bounds__(kAtThreads) attention_bwd_dq_simple(AtParams p
     load_row(q, p.q.row(t, h), p.dim);
     load_row(o, p.o.row(t, h), p.dim);
     load_row(d, p.dout.row(t, h), p.dim);
-    const float delta = warp_dot(o, d), lse = p.lse_in[h * p.tq + t];
+    const float delta = warp_dot(o, d), lse = p.lse[h * p.tq + t];
     if ((threadIdx.x & 31) == 0) p.delta[h * p.tq + t] = delta;
     for (int64_t j = s.k0; j < end; ++j) {
         load_row(k, p.k.row(j, kh), p.dim);
@@ -158,7 +127,7 @@ __global__ void __launch_bounds__(kAtThreads) attention_bwd_dkv_simple(AtParams 
         for (int64_t t = first; t < s.q1; ++t) {
             load_row(q, p.q.row(t, h), p.dim);
             load_row(d, p.dout.row(t, h), p.dim);
-            const float e = __expf(warp_dot(q, k) * p.scale - p.lse_in[h * p.tq + t]);
+            const float e = __expf(warp_dot(q, k) * p.scale - p.lse[h * p.tq + t]);
             const float ds = e * (warp_dot(d, v) - p.delta[h * p.tq + t]);
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
@@ -170,7 +139,7 @@ __global__ void __launch_bounds__(kAtThreads) attention_bwd_dkv_simple(AtParams 
     store_row(p.dv.row(j, kh), dv, p.dim, 1.f);
 }
 
-View view(const gs_heads& h) {
+HeadView view(const gs_heads& h) {
     return {static_cast<__nv_bfloat16*>(h.data), h.token_stride, h.head_stride};
 }
 
@@ -204,15 +173,42 @@ size_t attention_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, 
     return ((size_t)tokens_q * heads_q * sizeof(float) + 255) / 256 * 256 + 256;
 }
 
-cudaError_t launch_attention_fwd(const gs_attention_shape& s, const gs_heads& q, const gs_heads& k,
-                                 const gs_heads& v, const gs_heads& out, float* lse,
-                                 const int32_t* cu_q, const int32_t* cu_k, void* ws,
-                                 cudaStream_t st) {
-    (void)ws;
-    AtParams p = params(s, q, k, v, out, cu_q, cu_k);
-    p.lse = lse;
-    if (s.tokens_q == 0) return cudaSuccess;
-    return launch(attention_fwd_simple, warps(p.tq * p.hq), dim3(kAtThreads), 0, st, p);
+cudaError_t gave_up_word(unsigned int** word) {
+    void* p = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&p, g_gave_up);
+    *word = static_cast<unsigned int*>(p);
+    return e;
+}
+
+cudaError_t head_map(CUtensorMap* map, const void* data, int64_t ts, int64_t hs, int64_t tokens,
+                     int heads, int dim, bool* swapped) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    // the driver's function, looked up once (a function's address does not change)
+    static const Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                             cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<Encode>(f);
+    }();
+    if (!encode) return cudaErrorNotSupported;
+    *swapped = ts < hs;
+    const cuuint64_t size[3] = {(cuuint64_t)dim, (cuuint64_t)(*swapped ? tokens : heads),
+                                (cuuint64_t)(*swapped ? heads : tokens)};
+    const cuuint64_t stride[2] = {(cuuint64_t)(*swapped ? ts : hs) * 2,
+                                  (cuuint64_t)(*swapped ? hs : ts) * 2};
+    const cuuint32_t box[3] = {kBlockCols, *swapped ? kTileRows : 1u, *swapped ? 1u : kTileRows};
+    const cuuint32_t step[3] = {1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(data),
+                              size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 cudaError_t launch_attention_bwd(const gs_attention_shape& s, const gs_heads& q, const gs_heads& k,
@@ -221,7 +217,7 @@ cudaError_t launch_attention_bwd(const gs_attention_shape& s, const gs_heads& q,
                                  const gs_heads& dv, const int32_t* cu_q, const int32_t* cu_k,
                                  void* ws, cudaStream_t st) {
     AtParams p = params(s, q, k, v, out, cu_q, cu_k);
-    p.lse_in = lse;
+    p.lse = lse;
     p.delta = static_cast<float*>(ws);
     p.dout = view(dout);
     p.dq = view(dq);
