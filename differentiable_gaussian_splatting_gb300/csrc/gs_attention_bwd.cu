@@ -1,0 +1,725 @@
+// gs_attention_bwd.cu -- the gradient of softmax attention on the tensor cores, with the
+// probabilities recomputed from the forward's row sums.
+//
+//   P = exp(scale Q K^T - lse),  dV = P^T dO,  dS = P (dO V^T - delta),
+//   dQ = scale dS K,  dK = scale dS^T Q,  delta_i = O_i . dO_i
+//
+// Three kernels.  The first makes delta.  The second gives a block 128 keys and walks the
+// queries of every head that shares them: dK and dV stay in tensor memory, so the sum over
+// a group's heads and over queries needs no atomics.  The third gives a block 128 queries
+// and walks the keys, with dQ in tensor memory.  S and dO V^T are formed in both: seven
+// products instead of five.  The other way, dQ added to memory from the second kernel,
+// moves 64 KB of fp32 additions per 128 x 128 tile, about as many bytes per clock as L2
+// takes, and its result would depend on their order.
+//
+// The transposes come out of the operand descriptors: a tile of rows in shared memory
+// serves both as an operand contracted along its columns and as one contracted along its
+// rows.  P^T and dS^T (second kernel) and dS (third) go back to tensor memory in bfloat16
+// over the scores they came from, as first operands.  P, dP - delta and the sums are fp32;
+// P and dS are rounded to bfloat16 once, for the products.
+//
+// Rows of a tile that lie beyond the sequence and are contracted over are zeroed in shared
+// memory, and P and dS are set to zero there by selection, so that what lies behind a
+// sequence (NaN included) does not reach it.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "gs_attention.cuh"
+#include "gs_internal.h"
+#include "gs_tokens.h"
+
+namespace gs {
+namespace {
+
+constexpr int kMathWarps = 8;
+constexpr int kBwdThreads = (kMathWarps + 2) * 32;
+constexpr int kDeltaThreads = 256;
+
+struct BwdParams {
+    int64_t tq, tk;
+    int batch, group, dim;
+    bool causal, negative, swap_q, swap_k, swap_v, swap_d;
+    float scale, log2_scale;  // scale, and |scale| log2(e)
+    HeadView o, dout, dq, dk, dv;
+    const float* lse;
+    float2* rows;  // [heads][tokens]: (lse log2(e), delta)
+    unsigned int* gave_up;
+    const int32_t *cu_q, *cu_k;
+};
+
+// ---------------------------------------------------------------------------
+// (lse log2(e), delta) of every query row
+// ---------------------------------------------------------------------------
+// 16 lanes a row; lse is +infinity for a row that saw no key, so that P comes out 0
+__global__ void __launch_bounds__(kDeltaThreads) attention_delta_kernel(const BwdParams p, int heads) {
+    grid_dep_sync();
+    const int64_t at = ((int64_t)blockIdx.x * kDeltaThreads + threadIdx.x) >> 4;
+    const int lane = threadIdx.x & 15;
+    const int64_t t = at / heads;
+    const int h = (int)(at - t * heads);
+    float s = 0.f;
+    if (t < p.tq && lane * 8 < p.dim) {
+        const uint4 a = *reinterpret_cast<const uint4*>(p.o.row(t, h) + lane * 8);
+        const uint4 b = *reinterpret_cast<const uint4*>(p.dout.row(t, h) + lane * 8);
+        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            s = fmaf(__uint_as_float(x[k] << 16), __uint_as_float(y[k] << 16), s);
+            s = fmaf(__uint_as_float(x[k] & 0xffff0000u), __uint_as_float(y[k] & 0xffff0000u), s);
+        }
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (t < p.tq && lane == 0) {
+        const float l = p.lse[h * p.tq + t];
+        p.rows[h * p.tq + t] =
+            make_float2(l == -INFINITY ? INFINITY : l * 1.4426950408889634f, s);
+    }
+}
+
+// D[128 x N] (+)= A B, A in tensor memory in two halves of 64 contracted rows, 64 columns
+// apart: each half was written by the warps that read the scores it covers
+__device__ __forceinline__ void product_halves(uint32_t d, uint32_t a, uint32_t b, uint32_t word,
+                                               bool add) {
+    const uint64_t base = operand_base(kBlockBytes);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        mma_ts(d, a + (k >> 2) * 64 + (k & 3) * 8, operand(base, b + k * 2048), word,
+               add || k > 0);
+}
+
+// 64 values of a row of tensor memory, in bfloat16, over the first 32 of the 64 columns
+__device__ __forceinline__ void store_half(uint32_t at, const float* v) {
+    uint32_t w[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) w[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+    tmem_st32(at, w);
+}
+
+// kDim columns of a row of tensor memory, times f, to memory in bfloat16
+template <int kDim>
+__device__ __forceinline__ void store_row(uint32_t at, __nv_bfloat16* out, int dim, float f,
+                                          bool valid, bool zero) {
+#pragma unroll
+    for (int c = 0; c < kDim; c += 32) {
+        uint32_t o[32];
+        if (!zero) {
+            tmem_ld32(o, at + c);
+            tmem_wait_ld();
+        }
+        if (!valid) continue;
+#pragma unroll
+        for (int k = 0; k < 32; k += 8) {
+            if (c + k < dim) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = zero ? 0u
+                                : pack_bf16(__uint_as_float(o[k + 2 * e]) * f,
+                                            __uint_as_float(o[k + 2 * e + 1]) * f);
+                *reinterpret_cast<uint4*>(out + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dK and dV
+// ---------------------------------------------------------------------------
+template <int DP>
+struct DkvShape {
+    static constexpr int kBlocks = DP / kBlockCols;
+    static constexpr uint32_t kTileBytes = kBlocks * kBlockBytes;
+    static constexpr int kSlots = DP == 128 ? 2 : 4;
+    static constexpr uint32_t kSmem = (2 + 2 * kSlots) * kTileBytes + 1024;
+};
+
+template <int DP>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    attention_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
+                         const __grid_constant__ CUtensorMap map_k,
+                         const __grid_constant__ CUtensorMap map_v,
+                         const __grid_constant__ CUtensorMap map_d, const BwdParams p) {
+    using Sh = DkvShape<DP>;
+    extern __shared__ char smem_raw[];
+    __shared__ uint64_t bar_k, bar_v, bar_s, bar_dp, bar_p, bar_ds, bar_done, bar_raw, bar_drain;
+    __shared__ uint64_t full_q[Sh::kSlots], empty_q[Sh::kSlots], full_d[Sh::kSlots],
+        empty_d[Sh::kSlots];
+    __shared__ __align__(16) float2 rows[Sh::kSlots][kTileRows];
+    __shared__ uint32_t tmem_at;
+    __shared__ volatile int dead;
+    __shared__ int sh_b, sh_tile, sh_found;
+
+    grid_dep_sync();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0) {
+        int b = 0, tile = 0;
+        const bool found = find_tile(p.cu_k, p.batch, p.tk, kTileRows, blockIdx.x, &b, &tile);
+        if (lane == 0) sh_b = b, sh_tile = tile, sh_found = found, dead = 0;
+    }
+    __syncthreads();
+    if (!sh_found) return;
+    Sequence sq;
+    cut(p.cu_q, sh_b, p.tq, &sq.q0, &sq.n);
+    cut(p.cu_k, sh_b, p.tk, &sq.k0, &sq.m);
+    const int key0 = sh_tile * kTileRows;
+    const int khead = blockIdx.y;
+    // the query tiles that see one of these keys, for each head of the group
+    const int q_tiles = (sq.n + kTileRows - 1) / kTileRows;
+    const int q_first =
+        p.causal ? min(q_tiles, max(0, key0 + sq.n - sq.m) / kTileRows) : 0;
+    const int per_head = q_tiles - q_first, items = per_head * p.group;
+
+    const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t at_k = smem, at_v = smem + Sh::kTileBytes;
+    const uint32_t at_q = smem + 2 * Sh::kTileBytes, at_d = at_q + Sh::kSlots * Sh::kTileBytes;
+    if (warp == kMathWarps) {
+        tmem_alloc(smem_u32(&tmem_at), 512);
+    } else if (threadIdx.x == 0) {
+        for (uint64_t* b : {&bar_k, &bar_v, &bar_s, &bar_dp, &bar_done, &bar_raw, &bar_drain})
+            mbar_init(smem_u32(b), 1);
+        mbar_init(smem_u32(&bar_p), kMathWarps);
+        mbar_init(smem_u32(&bar_ds), kMathWarps);
+        for (int i = 0; i < Sh::kSlots; ++i) {
+            mbar_init(smem_u32(&full_q[i]), 2);  // the tile, and its rows' lse and delta
+            mbar_init(smem_u32(&empty_q[i]), 1);
+            mbar_init(smem_u32(&full_d[i]), 1);
+            mbar_init(smem_u32(&empty_d[i]), 1);
+        }
+        fence_barrier_init();
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = tmem_at;
+    const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
+
+    if (items > 0 && warp == kMathWarps + 1) {
+        // ---- the producer ----
+        if (elect_one()) {
+            mbar_expect(smem_u32(&bar_k), Sh::kTileBytes);
+            load_tile<Sh::kBlocks>(at_k, &map_k, smem_u32(&bar_k), khead, sq.k0 + key0, p.swap_k);
+            mbar_expect(smem_u32(&bar_v), Sh::kTileBytes);
+            load_tile<Sh::kBlocks>(at_v, &map_v, smem_u32(&bar_v), khead, sq.k0 + key0, p.swap_v);
+        }
+        __syncwarp();
+        int i = 0, mends = 0;
+        bool ok = true;
+        // one tile of queries (which = 0) or of output gradients (1) into slot `slot`
+        const auto bring = [&](bool of_d, uint32_t dst, uint32_t full, int head, int i0) {
+            const int valid = sq.n - i0;
+            const bool mend = valid < kTileRows && sq.q0 + sq.n < p.tq;
+            const uint32_t bar = mend ? smem_u32(&bar_raw) : full;
+            if (elect_one()) {
+                mbar_expect(bar, Sh::kTileBytes);
+                load_tile<Sh::kBlocks>(dst, of_d ? &map_d : &map_q, bar, head, sq.q0 + i0,
+                                       of_d ? p.swap_d : p.swap_q);
+            }
+            __syncwarp();
+            if (mend) {
+                const int parity = mends++ & 1;
+                if (!mbar_wait(bar, parity, &dead)) {
+                    mbar_drain(bar, parity);
+                    return false;
+                }
+                zero_rows<Sh::kBlocks>(smem_raw + (dst - smem_u32(smem_raw)), valid);
+                fence_async_shared();
+                __syncwarp();
+                if (elect_one()) mbar_arrive(full);
+                __syncwarp();
+            }
+            return true;
+        };
+        int head = khead * p.group, tile = q_first;
+        for (; i < items && ok; ++i) {
+            const int slot = i % Sh::kSlots, use = i / Sh::kSlots, i0 = tile * kTileRows;
+            if (use > 0) ok = mbar_wait(smem_u32(&empty_q[slot]), (use - 1) & 1, &dead);
+            if (!ok) break;
+            const uint32_t full = smem_u32(&full_q[slot]);
+            ok = bring(false, at_q + slot * Sh::kTileBytes, full, head, i0);
+            if (!ok) break;
+            const float2* src = p.rows + (int64_t)head * p.tq + sq.q0 + i0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = k * 32 + lane;
+                rows[slot][r] = i0 + r < sq.n ? src[r] : make_float2(INFINITY, 0.f);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full);
+            if (use > 0) ok = mbar_wait(smem_u32(&empty_d[slot]), (use - 1) & 1, &dead);
+            if (!ok) break;
+            ok = bring(true, at_d + slot * Sh::kTileBytes, smem_u32(&full_d[slot]), head, i0);
+            if (++tile == q_tiles) tile = q_first, ++head;
+        }
+        if (!ok) {  // gave up: no copy outlives the block
+            mbar_drain(smem_u32(&bar_k), 0);
+            mbar_drain(smem_u32(&bar_v), 0);
+            for (int u = max(0, i + 1 - Sh::kSlots); u <= i; ++u) {
+                mbar_drain(smem_u32(&full_q[u % Sh::kSlots]), (u / Sh::kSlots) & 1);
+                mbar_drain(smem_u32(&full_d[u % Sh::kSlots]), (u / Sh::kSlots) & 1);
+            }
+        }
+    } else if (items > 0 && warp == kMathWarps) {
+        // ---- the products ----
+        if (elect_one()) {
+            constexpr uint32_t word_o = mma_word(128, DP, false, true);
+            constexpr uint32_t word_dp = mma_word(128, 128, false, false);
+            const uint32_t word_s = word_dp | (p.negative ? kNegateA : 0u);
+            bool ok = mbar_wait(smem_u32(&bar_k), 0, &dead);
+            const auto slot_of = [&](int i) { return i % Sh::kSlots; };
+            const auto parity_of = [&](int i) { return (i / Sh::kSlots) & 1; };
+            const auto scores = [&](int i) {
+                ok = ok && mbar_wait(smem_u32(&full_q[slot_of(i)]), parity_of(i), &dead);
+                if (!ok) return;
+                tmem_fence_after();
+                product_columns<DP>(t_s, at_k, kBlockBytes, at_q + slot_of(i) * Sh::kTileBytes,
+                                    kBlockBytes, word_s, false);
+                mma_commit(smem_u32(&bar_s));
+            };
+            const auto dprobs = [&](int i) {
+                ok = ok && mbar_wait(smem_u32(&full_d[slot_of(i)]), parity_of(i), &dead);
+                if (!ok) return;
+                tmem_fence_after();
+                product_columns<DP>(t_dp, at_v, kBlockBytes, at_d + slot_of(i) * Sh::kTileBytes,
+                                    kBlockBytes, word_dp, false);
+                mma_commit(smem_u32(&bar_dp));
+            };
+            scores(0);
+            ok = ok && mbar_wait(smem_u32(&bar_v), 0, &dead);
+            dprobs(0);
+            for (int i = 0; i < items && ok; ++i) {
+                // while the other warps form dS(i): dV, and the next scores
+                ok = mbar_wait(smem_u32(&bar_p), i & 1, &dead);
+                if (!ok) break;
+                tmem_fence_after();
+                product_halves(t_dv, t_s, at_d + slot_of(i) * Sh::kTileBytes, word_o, i > 0);
+                mma_commit(smem_u32(&empty_d[slot_of(i)]));
+                if (i + 1 < items) scores(i + 1);
+                // while they form P(i + 1): dK, and the next dO V^T
+                ok = ok && mbar_wait(smem_u32(&bar_ds), i & 1, &dead);
+                if (!ok) break;
+                tmem_fence_after();
+                product_halves(t_dk, t_dp, at_q + slot_of(i) * Sh::kTileBytes, word_o, i > 0);
+                mma_commit(smem_u32(&empty_q[slot_of(i)]));
+                if (i + 1 < items) dprobs(i + 1);
+            }
+            if (ok) mma_commit(smem_u32(&bar_done));
+            if (!ok) {  // leave no product in flight
+                mma_commit(smem_u32(&bar_drain));
+                mbar_drain(smem_u32(&bar_drain), 0);
+            }
+        }
+    } else if (warp < kMathWarps) {
+        // ---- P and dS: one key a thread, half of the tile's queries ----
+        const int half = warp >> 2, r = (warp & 3) * 32 + lane, key = key0 + r;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const uint32_t s_at = t_s + lanes + half * 64, dp_at = t_dp + lanes + half * 64;
+        const float sl = p.log2_scale;
+        // the first query that sees this thread's key; the last of the tile's keys' first
+        const int sees = p.causal ? max(0, key + sq.n - sq.m) : 0;
+        const int all_see = p.causal ? max(0, key0 + kTileRows - 1 + sq.n - sq.m) : 0;
+        bool ok = true;
+        int tile = q_first;
+        for (int i = 0; i < items && ok; ++i) {
+            const int slot = i % Sh::kSlots, i0 = tile * kTileRows;
+            if (++tile == q_tiles) tile = q_first;
+            const bool masked = i0 < all_see || i0 + kTileRows > sq.n;
+            const int lo = sees - i0 - half * 64, hi = sq.n - i0 - half * 64;
+            ok = mbar_wait(smem_u32(&full_q[slot]), (i / Sh::kSlots) & 1, &dead) &&
+                 mbar_wait(smem_u32(&bar_s), i & 1, &dead);
+            if (!ok) break;
+            tmem_fence_after();
+            float pr[64];
+            tmem_ld32(reinterpret_cast<uint32_t*>(pr), s_at);
+            tmem_ld32(reinterpret_cast<uint32_t*>(pr) + 32, s_at + 32);
+            tmem_wait_ld();
+            const float4* rw = reinterpret_cast<const float4*>(rows[slot] + half * 64);
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+                const float4 v = rw[c >> 1];
+                pr[c] = ex2_approx(fmaf(pr[c], sl, -v.x));
+                pr[c + 1] = ex2_approx(fmaf(pr[c + 1], sl, -v.z));
+            }
+            if (masked) {
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                    if (c < lo || c >= hi) pr[c] = 0.f;
+            }
+            store_half(s_at, pr);
+            tmem_wait_st();
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar_p));
+            ok = mbar_wait(smem_u32(&bar_dp), i & 1, &dead);
+            if (!ok) break;
+            tmem_fence_after();
+            float dp[64];
+            tmem_ld32(reinterpret_cast<uint32_t*>(dp), dp_at);
+            tmem_ld32(reinterpret_cast<uint32_t*>(dp) + 32, dp_at + 32);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+                const float4 v = rw[c >> 1];
+                dp[c] = pr[c] * (dp[c] - v.y);
+                dp[c + 1] = pr[c + 1] * (dp[c + 1] - v.w);
+            }
+            if (masked) {
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                    if (c < lo || c >= hi) dp[c] = 0.f;
+            }
+            store_half(dp_at, dp);
+            tmem_wait_st();
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar_ds));
+        }
+        if (ok && items > 0) ok = mbar_wait(smem_u32(&bar_done), 0, &dead);
+        if (ok) {
+            tmem_fence_after();
+            const bool valid = key < sq.m, zero = items == 0;
+            const HeadView& g = half ? p.dk : p.dv;
+            store_row<DP>((half ? t_dk : t_dv) + lanes, valid ? g.row(sq.k0 + key, khead) : nullptr,
+                          p.dim, half ? p.scale : 1.f, valid, zero);
+        }
+    }
+    tmem_fence_before();
+    __syncthreads();
+    if (dead && threadIdx.x == 0) *p.gave_up = 1;
+    if (warp == kMathWarps) {
+        __syncwarp();
+        tmem_fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dQ
+// ---------------------------------------------------------------------------
+template <int DP>
+struct DqShape {
+    static constexpr int kBlocks = DP / kBlockCols;
+    static constexpr uint32_t kTileBytes = kBlocks * kBlockBytes;
+    static constexpr int kSlotsK = DP == 128 ? 3 : 4, kSlotsV = DP == 128 ? 2 : 4;
+    static constexpr uint32_t kSmem = (2 + kSlotsK + kSlotsV) * kTileBytes + 1024;
+};
+
+template <int DP>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    attention_dq_kernel(const __grid_constant__ CUtensorMap map_q,
+                        const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_v,
+                        const __grid_constant__ CUtensorMap map_d, const BwdParams p) {
+    using Sh = DqShape<DP>;
+    extern __shared__ char smem_raw[];
+    __shared__ uint64_t bar_q, bar_d, bar_s[2], bar_dp, bar_ds, bar_done, bar_raw, bar_drain;
+    __shared__ uint64_t full_k[Sh::kSlotsK], empty_k[Sh::kSlotsK], full_v[Sh::kSlotsV],
+        empty_v[Sh::kSlotsV];
+    __shared__ uint32_t tmem_at;
+    __shared__ volatile int dead;
+    __shared__ int sh_b, sh_tile, sh_found;
+
+    grid_dep_sync();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0) {
+        int b = 0, tile = 0;
+        const bool found = find_tile(p.cu_q, p.batch, p.tq, kTileRows, blockIdx.x, &b, &tile);
+        if (lane == 0) sh_b = b, sh_tile = tile, sh_found = found, dead = 0;
+    }
+    __syncthreads();
+    if (!sh_found) return;
+    Sequence sq;
+    cut(p.cu_q, sh_b, p.tq, &sq.q0, &sq.n);
+    cut(p.cu_k, sh_b, p.tk, &sq.k0, &sq.m);
+    const int row0 = sh_tile * kTileRows;
+    const int head = blockIdx.y, khead = head / p.group;
+    const int last = min(sq.n, row0 + kTileRows) - 1;
+    const int tiles = (seen_keys(last, sq.n, sq.m, p.causal) + kTileRows - 1) / kTileRows;
+
+    const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t at_q = smem, at_d = smem + Sh::kTileBytes;
+    const uint32_t at_k = smem + 2 * Sh::kTileBytes, at_v = at_k + Sh::kSlotsK * Sh::kTileBytes;
+    if (warp == kMathWarps) {
+        tmem_alloc(smem_u32(&tmem_at), 512);
+    } else if (threadIdx.x == 0) {
+        for (uint64_t* b : {&bar_q, &bar_d, &bar_s[0], &bar_s[1], &bar_dp, &bar_done, &bar_raw,
+                            &bar_drain})
+            mbar_init(smem_u32(b), 1);
+        mbar_init(smem_u32(&bar_ds), kMathWarps);
+        for (int i = 0; i < Sh::kSlotsK; ++i) {
+            mbar_init(smem_u32(&full_k[i]), 1);
+            mbar_init(smem_u32(&empty_k[i]), 1);
+        }
+        for (int i = 0; i < Sh::kSlotsV; ++i) {
+            mbar_init(smem_u32(&full_v[i]), 1);
+            mbar_init(smem_u32(&empty_v[i]), 1);
+        }
+        fence_barrier_init();
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = tmem_at;
+    const uint32_t t_dp = tmem + 256, t_dq = tmem + 384;
+
+    if (tiles > 0 && warp == kMathWarps + 1) {
+        // ---- the producer ----
+        if (elect_one()) {
+            mbar_expect(smem_u32(&bar_q), Sh::kTileBytes);
+            load_tile<Sh::kBlocks>(at_q, &map_q, smem_u32(&bar_q), head, sq.q0 + row0, p.swap_q);
+            mbar_expect(smem_u32(&bar_d), Sh::kTileBytes);
+            load_tile<Sh::kBlocks>(at_d, &map_d, smem_u32(&bar_d), head, sq.q0 + row0, p.swap_d);
+        }
+        __syncwarp();
+        int j = 0;
+        bool ok = true;
+        for (; j < tiles && ok; ++j) {
+            const int sk = j % Sh::kSlotsK, uk = j / Sh::kSlotsK;
+            const int sv = j % Sh::kSlotsV, uv = j / Sh::kSlotsV;
+            const int64_t token = sq.k0 + (int64_t)j * kTileRows;
+            if (uk > 0) ok = mbar_wait(smem_u32(&empty_k[sk]), (uk - 1) & 1, &dead);
+            if (!ok) break;
+            const int valid = sq.m - j * kTileRows;
+            const bool mend = valid < kTileRows && sq.k0 + sq.m < p.tk;
+            const uint32_t full = smem_u32(&full_k[sk]), dst = at_k + sk * Sh::kTileBytes;
+            const uint32_t bar = mend ? smem_u32(&bar_raw) : full;
+            if (elect_one()) {
+                mbar_expect(bar, Sh::kTileBytes);
+                load_tile<Sh::kBlocks>(dst, &map_k, bar, khead, token, p.swap_k);
+            }
+            __syncwarp();
+            if (mend) {  // once, at the last tile
+                ok = mbar_wait(bar, 0, &dead);
+                if (!ok) {
+                    mbar_drain(bar, 0);
+                    break;
+                }
+                zero_rows<Sh::kBlocks>(smem_raw + (dst - smem_u32(smem_raw)), valid);
+                fence_async_shared();
+                __syncwarp();
+                if (elect_one()) mbar_arrive(full);
+                __syncwarp();
+            }
+            if (uv > 0) ok = mbar_wait(smem_u32(&empty_v[sv]), (uv - 1) & 1, &dead);
+            if (!ok) break;
+            if (elect_one()) {
+                mbar_expect(smem_u32(&full_v[sv]), Sh::kTileBytes);
+                load_tile<Sh::kBlocks>(at_v + sv * Sh::kTileBytes, &map_v, smem_u32(&full_v[sv]),
+                                       khead, token, p.swap_v);
+            }
+            __syncwarp();
+        }
+        if (!ok) {  // gave up: no copy outlives the block
+            mbar_drain(smem_u32(&bar_q), 0);
+            mbar_drain(smem_u32(&bar_d), 0);
+            for (int u = max(0, j + 1 - Sh::kSlotsK); u <= j; ++u)
+                mbar_drain(smem_u32(&full_k[u % Sh::kSlotsK]), (u / Sh::kSlotsK) & 1);
+            for (int u = max(0, j - Sh::kSlotsV); u < j; ++u)
+                mbar_drain(smem_u32(&full_v[u % Sh::kSlotsV]), (u / Sh::kSlotsV) & 1);
+        }
+    } else if (tiles > 0 && warp == kMathWarps) {
+        // ---- the products ----
+        if (elect_one()) {
+            constexpr uint32_t word_o = mma_word(128, DP, false, true);
+            constexpr uint32_t word_dp = mma_word(128, 128, false, false);
+            const uint32_t word_s = word_dp | (p.negative ? kNegateA : 0u);
+            bool ok = mbar_wait(smem_u32(&bar_q), 0, &dead);
+            const auto scores = [&](int j) {
+                const int sk = j % Sh::kSlotsK;
+                ok = ok && mbar_wait(smem_u32(&full_k[sk]), (j / Sh::kSlotsK) & 1, &dead);
+                if (!ok) return;
+                tmem_fence_after();
+                product_columns<DP>(tmem + (j & 1) * 128, at_q, kBlockBytes,
+                                    at_k + sk * Sh::kTileBytes, kBlockBytes, word_s, false);
+                mma_commit(smem_u32(&bar_s[j & 1]));
+            };
+            const auto dprobs = [&](int j) {
+                const int sv = j % Sh::kSlotsV;
+                ok = ok && mbar_wait(smem_u32(&full_v[sv]), (j / Sh::kSlotsV) & 1, &dead);
+                if (!ok) return;
+                tmem_fence_after();
+                product_columns<DP>(t_dp, at_d, kBlockBytes, at_v + sv * Sh::kTileBytes,
+                                    kBlockBytes, word_dp, false);
+                mma_commit(smem_u32(&bar_dp));
+                mma_commit(smem_u32(&empty_v[sv]));
+            };
+            scores(0);
+            ok = ok && mbar_wait(smem_u32(&bar_d), 0, &dead);
+            dprobs(0);
+            if (tiles > 1) scores(1);
+            for (int j = 0; j < tiles && ok; ++j) {
+                ok = mbar_wait(smem_u32(&bar_ds), j & 1, &dead);
+                if (!ok) break;
+                // dS(j) lies over S(j), and dP(j) is read: the next dO V^T first, which the
+                // other warps wait for
+                tmem_fence_after();
+                if (j + 1 < tiles) dprobs(j + 1);
+                if (!ok) break;
+                const int sk = j % Sh::kSlotsK;
+                product_halves(t_dq, tmem + (j & 1) * 128, at_k + sk * Sh::kTileBytes, word_o,
+                               j > 0);
+                mma_commit(smem_u32(&empty_k[sk]));
+                if (j + 2 < tiles) scores(j + 2);
+            }
+            if (ok) mma_commit(smem_u32(&bar_done));
+            if (!ok) {  // leave no product in flight
+                mma_commit(smem_u32(&bar_drain));
+                mbar_drain(smem_u32(&bar_drain), 0);
+            }
+        }
+    } else if (warp < kMathWarps) {
+        // ---- dS: one query a thread, half of the tile's keys ----
+        const int half = warp >> 2, r = (warp & 3) * 32 + lane, i = row0 + r;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const uint32_t dp_at = t_dp + lanes + half * 64;
+        const float sl = p.log2_scale;
+        const int limit = seen_keys(i, sq.n, sq.m, p.causal);
+        const int first_limit = seen_keys(row0 + (warp & 3) * 32, sq.n, sq.m, p.causal);
+        float2 row = make_float2(INFINITY, 0.f);
+        if (i < sq.n) row = p.rows[(int64_t)head * p.tq + sq.q0 + i];
+        bool ok = true;
+        for (int j = 0; j < tiles && ok; ++j) {
+            const uint32_t s_at = tmem + (j & 1) * 128 + lanes + half * 64;
+            ok = mbar_wait(smem_u32(&bar_s[j & 1]), (j >> 1) & 1, &dead);
+            if (!ok) break;
+            tmem_fence_after();
+            float pr[64];
+            tmem_ld32(reinterpret_cast<uint32_t*>(pr), s_at);
+            tmem_ld32(reinterpret_cast<uint32_t*>(pr) + 32, s_at + 32);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 64; ++c) pr[c] = ex2_approx(fmaf(pr[c], sl, -row.x));
+            ok = mbar_wait(smem_u32(&bar_dp), j & 1, &dead);
+            if (!ok) break;
+            tmem_fence_after();
+            float dp[64];
+            tmem_ld32(reinterpret_cast<uint32_t*>(dp), dp_at);
+            tmem_ld32(reinterpret_cast<uint32_t*>(dp) + 32, dp_at + 32);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 64; ++c) dp[c] = pr[c] * (dp[c] - row.y);
+            if ((j + 1) * kTileRows > first_limit) {
+                const int left = limit - j * kTileRows - half * 64;
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                    if (c >= left) dp[c] = 0.f;
+            }
+            store_half(s_at, dp);
+            tmem_wait_st();
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar_ds));
+        }
+        if (ok && tiles > 0) ok = mbar_wait(smem_u32(&bar_done), 0, &dead);
+        if (ok) {
+            tmem_fence_after();
+            const bool valid = i < sq.n, zero = tiles == 0;
+            // each half of the warps writes half of the columns
+            const int c0 = half * (DP / 2);
+            store_row<DP / 2>(t_dq + lanes + c0,
+                              valid ? p.dq.row(sq.q0 + i, head) + c0 : nullptr, p.dim - c0, p.scale,
+                              valid, zero);
+        }
+    }
+    tmem_fence_before();
+    __syncthreads();
+    if (dead && threadIdx.x == 0) *p.gave_up = 1;
+    if (warp == kMathWarps) {
+        __syncwarp();
+        tmem_fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+struct BwdMaps {
+    CUtensorMap q, k, v, d;
+};
+
+template <int DP>
+cudaError_t launch_dim(const BwdMaps& m, const BwdParams& p, int heads_q, int heads_k,
+                       cudaStream_t st) {
+    const auto tiles = [&](int64_t tokens) {
+        return (unsigned)(p.cu_q ? tokens / kTileRows + p.batch
+                                 : (tokens + kTileRows - 1) / kTileRows);
+    };
+    cudaError_t e = cudaSuccess;
+    if (p.tk > 0) {
+        e = cudaFuncSetAttribute(attention_dkv_kernel<DP>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)DkvShape<DP>::kSmem);
+        if (e == cudaSuccess)
+            e = launch(attention_dkv_kernel<DP>, dim3(tiles(p.tk), (unsigned)heads_k),
+                       dim3(kBwdThreads), DkvShape<DP>::kSmem, st, m.q, m.k, m.v, m.d, p);
+    }
+    if (e == cudaSuccess && p.tq > 0) {
+        e = cudaFuncSetAttribute(attention_dq_kernel<DP>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)DqShape<DP>::kSmem);
+        if (e == cudaSuccess)
+            e = launch(attention_dq_kernel<DP>, dim3(tiles(p.tq), (unsigned)heads_q),
+                       dim3(kBwdThreads), DqShape<DP>::kSmem, st, m.q, m.k, m.v, m.d, p);
+    }
+    return e;
+}
+
+HeadView view(const gs_heads& h) {
+    return {static_cast<__nv_bfloat16*>(h.data), h.token_stride, h.head_stride};
+}
+
+}  // namespace
+
+cudaError_t launch_attention_bwd(const gs_attention_shape& s, const gs_heads& q, const gs_heads& k,
+                                 const gs_heads& v, const gs_heads& out, const float* lse,
+                                 const gs_heads& dout, const gs_heads& dq, const gs_heads& dk,
+                                 const gs_heads& dv, const int32_t* cu_q, const int32_t* cu_k,
+                                 void* ws, cudaStream_t st) {
+    BwdParams p{};
+    p.tq = s.tokens_q;
+    p.tk = s.tokens_k;
+    p.batch = s.batch;
+    p.group = s.heads_q / s.heads_k;
+    p.dim = s.head_dim;
+    p.causal = s.causal != 0;
+    p.negative = s.scale < 0.f;
+    p.scale = s.scale;
+    p.log2_scale = fabsf(s.scale) * 1.4426950408889634f;
+    p.o = view(out);
+    p.dout = view(dout);
+    p.dq = view(dq);
+    p.dk = view(dk);
+    p.dv = view(dv);
+    p.lse = lse;
+    p.rows = static_cast<float2*>(ws);
+    p.cu_q = cu_q;
+    p.cu_k = cu_k;
+    cudaError_t e = gave_up_word(&p.gave_up);
+    if (e != cudaSuccess) return e;
+    BwdMaps m;
+    const auto map = [&](CUtensorMap* out_map, const gs_heads& h, int64_t tokens, int heads,
+                         bool* swapped) {
+        if (e == cudaSuccess && tokens > 0)
+            e = head_map(out_map, h.data, h.token_stride, h.head_stride, tokens, heads, s.head_dim,
+                         swapped);
+    };
+    map(&m.q, q, s.tokens_q, s.heads_q, &p.swap_q);
+    map(&m.d, dout, s.tokens_q, s.heads_q, &p.swap_d);
+    map(&m.k, k, s.tokens_k, s.heads_k, &p.swap_k);
+    map(&m.v, v, s.tokens_k, s.heads_k, &p.swap_v);
+    if (s.tokens_q == 0) m.q = m.d = m.k;  // nothing is loaded by them
+    if (s.tokens_k == 0) m.k = m.v = m.q;
+    if (e != cudaSuccess) return e;
+    if (p.tq > 0) {
+        const int64_t threads = p.tq * s.heads_q * 16;
+        e = launch(attention_delta_kernel,
+                   dim3((unsigned)((threads + kDeltaThreads - 1) / kDeltaThreads)),
+                   dim3(kDeltaThreads), 0, st, p, s.heads_q);
+        if (e != cudaSuccess) return e;
+    }
+    return s.head_dim <= 64 ? launch_dim<64>(m, p, s.heads_q, s.heads_k, st)
+                            : launch_dim<128>(m, p, s.heads_q, s.heads_k, st);
+}
+
+}  // namespace gs
