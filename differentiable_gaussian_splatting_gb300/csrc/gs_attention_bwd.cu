@@ -80,17 +80,6 @@ __global__ void __launch_bounds__(kDeltaThreads) attention_delta_kernel(const Bw
     }
 }
 
-// D[128 x N] (+)= A B, A in tensor memory in two halves of 64 contracted rows, 64 columns
-// apart: each half was written by the warps that read the scores it covers
-__device__ __forceinline__ void product_halves(uint32_t d, uint32_t a, uint32_t b, uint32_t word,
-                                               bool add) {
-    const uint64_t base = operand_base(kBlockBytes);
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        mma_ts(d, a + (k >> 2) * 64 + (k & 3) * 8, operand(base, b + k * 2048), word,
-               add || k > 0);
-}
-
 // 64 values of a row of tensor memory, in bfloat16, over the first 32 of the 64 columns
 __device__ __forceinline__ void store_half(uint32_t at, const float* v) {
     uint32_t w[32];
@@ -275,16 +264,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 ok = ok && mbar_wait(smem_u32(&full_q[slot_of(i)]), parity_of(i), &dead);
                 if (!ok) return;
                 tmem_fence_after();
-                product_columns<DP>(t_s, at_k, kBlockBytes, at_q + slot_of(i) * Sh::kTileBytes,
-                                    kBlockBytes, word_s, false);
+                product_columns<DP>(t_s, operand_columns(at_k),
+                                    operand_columns(at_q + slot_of(i) * Sh::kTileBytes), word_s,
+                                    false);
                 mma_commit(smem_u32(&bar_s));
             };
             const auto dprobs = [&](int i) {
                 ok = ok && mbar_wait(smem_u32(&full_d[slot_of(i)]), parity_of(i), &dead);
                 if (!ok) return;
                 tmem_fence_after();
-                product_columns<DP>(t_dp, at_v, kBlockBytes, at_d + slot_of(i) * Sh::kTileBytes,
-                                    kBlockBytes, word_dp, false);
+                product_columns<DP>(t_dp, operand_columns(at_v),
+                                    operand_columns(at_d + slot_of(i) * Sh::kTileBytes), word_dp,
+                                    false);
                 mma_commit(smem_u32(&bar_dp));
             };
             scores(0);
@@ -295,14 +286,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 ok = mbar_wait(smem_u32(&bar_p), i & 1, &dead);
                 if (!ok) break;
                 tmem_fence_after();
-                product_halves(t_dv, t_s, at_d + slot_of(i) * Sh::kTileBytes, word_o, i > 0);
+                product_rows(t_dv, t_s, 64, operand_rows(at_d + slot_of(i) * Sh::kTileBytes), word_o,
+                             i > 0);
                 mma_commit(smem_u32(&empty_d[slot_of(i)]));
                 if (i + 1 < items) scores(i + 1);
                 // while they form P(i + 1): dK, and the next dO V^T
                 ok = ok && mbar_wait(smem_u32(&bar_ds), i & 1, &dead);
                 if (!ok) break;
                 tmem_fence_after();
-                product_halves(t_dk, t_dp, at_q + slot_of(i) * Sh::kTileBytes, word_o, i > 0);
+                product_rows(t_dk, t_dp, 64, operand_rows(at_q + slot_of(i) * Sh::kTileBytes), word_o,
+                             i > 0);
                 mma_commit(smem_u32(&empty_q[slot_of(i)]));
                 if (i + 1 < items) dprobs(i + 1);
             }
@@ -532,8 +525,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 ok = ok && mbar_wait(smem_u32(&full_k[sk]), (j / Sh::kSlotsK) & 1, &dead);
                 if (!ok) return;
                 tmem_fence_after();
-                product_columns<DP>(tmem + (j & 1) * 128, at_q, kBlockBytes,
-                                    at_k + sk * Sh::kTileBytes, kBlockBytes, word_s, false);
+                product_columns<DP>(tmem + (j & 1) * 128, operand_columns(at_q),
+                                    operand_columns(at_k + sk * Sh::kTileBytes), word_s, false);
                 mma_commit(smem_u32(&bar_s[j & 1]));
             };
             const auto dprobs = [&](int j) {
@@ -541,8 +534,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 ok = ok && mbar_wait(smem_u32(&full_v[sv]), (j / Sh::kSlotsV) & 1, &dead);
                 if (!ok) return;
                 tmem_fence_after();
-                product_columns<DP>(t_dp, at_d, kBlockBytes, at_v + sv * Sh::kTileBytes,
-                                    kBlockBytes, word_dp, false);
+                product_columns<DP>(t_dp, operand_columns(at_d),
+                                    operand_columns(at_v + sv * Sh::kTileBytes), word_dp, false);
                 mma_commit(smem_u32(&bar_dp));
                 mma_commit(smem_u32(&empty_v[sv]));
             };
@@ -559,8 +552,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (j + 1 < tiles) dprobs(j + 1);
                 if (!ok) break;
                 const int sk = j % Sh::kSlotsK;
-                product_halves(t_dq, tmem + (j & 1) * 128, at_k + sk * Sh::kTileBytes, word_o,
-                               j > 0);
+                product_rows(t_dq, tmem + (j & 1) * 128, 64,
+                             operand_rows(at_k + sk * Sh::kTileBytes), word_o, j > 0);
                 mma_commit(smem_u32(&empty_k[sk]));
                 if (j + 2 < tiles) scores(j + 2);
             }

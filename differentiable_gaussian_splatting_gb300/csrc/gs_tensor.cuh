@@ -178,31 +178,35 @@ __host__ __device__ constexpr uint32_t mma_word(int M, int N, bool rows_a, bool 
 }
 constexpr uint32_t kNegateA = 1u << 13;
 
-// Descriptor of a swizzled operand, without its address.  Contracted along the columns:
-// atoms of eight rows follow each other (1,024 bytes).  Along the rows: atoms of eight
-// contracted rows follow each other, and blocks of 64 columns lie `block` bytes apart.
-__device__ __forceinline__ uint64_t operand_base(uint32_t block) {
-    return ((uint64_t)(block >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
-           (2ull << 61);
+// Descriptors of swizzled operands: their low words, address and the distance of their
+// blocks of 64 columns (128 rows each; not read where the product is contracted along the
+// columns).  The high word is the same for all: atoms of eight rows follow each other
+// (1,024 bytes), 128-byte swizzle.  In 32 bits the address steps are single additions; with
+// 64-bit descriptors the issuing thread held up the forward by 2 %.
+constexpr uint32_t kOperandHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t operand_columns(uint32_t addr) {
+    return ((addr & 0x3ffff) >> 4) | (1u << 16);
 }
-__device__ __forceinline__ uint64_t operand(uint64_t base, uint32_t addr) {
-    return base | ((uint64_t)(addr & 0x3ffff) >> 4);
+__device__ __forceinline__ uint32_t operand_rows(uint32_t addr) {
+    return ((addr & 0x3ffff) >> 4) | ((128u * 128u >> 4) << 16);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t word,
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t word,
                                        bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(word), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(word), "r"((uint32_t)add), "r"(kOperandHigh)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t word,
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t word,
                                        bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(word), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(word), "r"((uint32_t)add), "r"(kOperandHigh)
         : "memory");
 }
 // the barrier gets one arrival when all products issued so far by this thread are done
@@ -213,34 +217,35 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 }
 
 // D[128 x N] (+)= A B^T over kDim columns, both operands contracted along their columns:
-// A 128 rows, B N rows, blocks of 64 columns `block_a`, `block_b` bytes apart.
+// A 128 rows, B N rows, blocks of 64 columns of 128 rows each.  The steps along the columns
+// add to the descriptors' address.
 template <int kDim>
-__device__ __forceinline__ void product_columns(uint32_t d, uint32_t a, uint32_t block_a,
-                                                uint32_t b, uint32_t block_b, uint32_t word,
+__device__ __forceinline__ void product_columns(uint32_t d, uint32_t a, uint32_t b, uint32_t word,
                                                 bool add) {
-    const uint64_t base = operand_base(16);
 #pragma unroll
     for (int k = 0; k < kDim / 16; ++k) {
-        const uint32_t in = (k & 3) * 32;
-        mma_ss(d, operand(base, a + (k >> 2) * block_a + in),
-               operand(base, b + (k >> 2) * block_b + in), word, add || k > 0);
+        const uint32_t in = (k >> 2) * (128 * 128 / 16) + (k & 3) * 2;
+        mma_ss(d, a + in, b + in, word, add || k > 0);
     }
 }
 
-// D[128 x N] (+)= A B with A [128 x kRows] in tensor memory (two bfloat16 a column) and B
-// contracted along its kRows rows, its blocks of 64 columns `block_b` bytes apart.
-template <int kRows>
-__device__ __forceinline__ void product_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t block_b,
+// D[128 x N] (+)= A B with A [128 x 128] in tensor memory (two bfloat16 a column) and B
+// contracted along its 128 rows.  A's halves of 64 contracted rows lie `half` columns apart.
+__device__ __forceinline__ void product_rows(uint32_t d, uint32_t a, uint32_t half, uint32_t b,
                                              uint32_t word, bool add) {
-    const uint64_t base = operand_base(block_b);
 #pragma unroll
-    for (int k = 0; k < kRows / 16; ++k)
-        mma_ts(d, a + k * 8, operand(base, b + k * 2048), word, add || k > 0);
+    for (int k = 0; k < 8; ++k)
+        mma_ts(d, a + (k >> 2) * half + (k & 3) * 8, b + k * 128, word, add || k > 0);
 }
 
 // ---------------------------------------------------------------------------
 // arithmetic
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
