@@ -43,51 +43,139 @@ __device__ __forceinline__ void cut(const int32_t* cu, int b, int64_t tokens, in
     *n = (int)(e - a);
 }
 
-// By one whole warp: the sequence and the tile of `rows` rows in it that are number
-// `target` of the batch's tiles, counted from the last tile of the last sequence (under
-// the causal mask the tiles at a sequence's end have the most work and go first).  False
-// beyond the last tile.
-__device__ __forceinline__ bool find_tile(const int32_t* cu, int batch, int64_t tokens, int rows,
-                                          int target, int* b_out, int* tile_out) {
-    if (!cu) {
-        const int tiles = (int)((tokens + rows - 1) / rows);
-        *b_out = 0;
-        *tile_out = tiles - 1 - target;
-        return target < tiles;
+// how many keys query i of a sequence sees
+__device__ __forceinline__ int seen_keys(int i, int n, int m, bool causal) {
+    return causal ? min(m, max(0, i + 1 + m - n)) : m;
+}
+
+// A block's place: `rows` queries (or keys) of one sequence and a head.
+struct Place {
+    int b, tile, head;
+};
+
+struct Batch {
+    const int32_t *cu_q, *cu_k;
+    int64_t tq, tk;
+    int batch;
+    bool causal;
+};
+
+// How many of a sequence's tiles cost at least c (c >= 1), cost being the 128-row tiles of
+// the other side that a tile meets.  Tiles of queries cost more towards the sequence's end
+// under the causal mask, tiles of keys towards its start.
+template <bool kKeys>
+__device__ __forceinline__ int tiles_from(int n, int m, int rows, bool causal, int c) {
+    const int of = kKeys ? m : n, other = kKeys ? n : m;
+    const int tiles = (of + rows - 1) / rows;
+    const int most = (other + kTileRows - 1) / kTileRows;
+    if (c > most) return 0;
+    if (!causal) return tiles;
+    if (kKeys) {
+        // the tile at `key` meets most - max(0, key + n - m) / 128 tiles of queries
+        const int64_t y = (int64_t)(most - c + 1) * kTileRows + m - n;
+        return y <= 0 ? 0 : (int)min64(tiles, (y + rows - 1) / rows);
+    }
+    // the tile up to query e (exclusive) meets ceil((e + m - n) / 128) tiles of keys
+    const int64_t x = (int64_t)(c - 1) * kTileRows + n - m;
+    if (n <= x) return 0;
+    return tiles - (int)max64(0, x / rows);
+}
+
+// By one whole warp: block `id` of the batch's tiles and heads, costliest first where costs
+// differ, so that the last blocks to start are short.  False beyond the last one.  Batches
+// of more than 32 sequences go sequence by sequence instead, from the last.
+template <bool kKeys>
+__device__ __forceinline__ bool find_place(const Batch& v, int rows, int heads, int id, Place* at) {
+    if (v.batch == 1) {
+        int64_t unused;
+        int of;
+        cut(kKeys ? v.cu_k : v.cu_q, 0, kKeys ? v.tk : v.tq, &unused, &of);
+        const int tiles = (of + rows - 1) / rows;
+        at->b = 0;
+        if (v.causal) {
+            at->head = id % heads;
+            const int rank = id / heads;
+            at->tile = kKeys ? rank : tiles - 1 - rank;
+            return rank < tiles;
+        }
+        // head by head: its keys and values stay in L2 (16,320 tokens x 16 heads x 128 took
+        // 8 % longer with the heads in turn)
+        at->head = tiles > 0 ? id / tiles : heads;
+        at->tile = id - at->head * tiles;
+        return at->head < heads;
     }
     const int lane = threadIdx.x & 31;
+    const unsigned all = 0xffffffffu;
+    int rank = id / heads;
+    at->head = id - rank * heads;
+    if (v.batch <= 32) {
+        int64_t unused;
+        int n = 0, m = 0;
+        if (lane < v.batch) {
+            cut(v.cu_q, lane, v.tq, &unused, &n);
+            cut(v.cu_k, lane, v.tk, &unused, &m);
+        }
+        const int tiles = ((kKeys ? m : n) + rows - 1) / rows;
+        if (rank >= (int)__reduce_add_sync(all, tiles)) return false;
+        // the largest cost that more than `rank` tiles reach (every tile reaches 0)
+        int lo = 0, hi = (int)__reduce_max_sync(all, ((kKeys ? n : m) + kTileRows - 1) / kTileRows);
+        while (lo < hi) {
+            const int c = (lo + hi + 1) >> 1;
+            const int from = tiles_from<kKeys>(n, m, rows, v.causal, c);
+            if ((int)__reduce_add_sync(all, from) > rank)
+                lo = c;
+            else
+                hi = c - 1;
+        }
+        const int reach = lo == 0 ? tiles : tiles_from<kKeys>(n, m, rows, v.causal, lo);
+        const int above = tiles_from<kKeys>(n, m, rows, v.causal, lo + 1);
+        rank -= (int)__reduce_add_sync(all, above);
+        int sum = reach - above;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(all, sum, o);
+            if (lane >= o) sum += u;
+        }
+        const int l = __ffs(__ballot_sync(all, sum > rank)) - 1;
+        const int within = rank - (sum - (reach - above));
+        const int tile = kKeys ? above + within : tiles - reach + within;
+        at->b = l;
+        at->tile = __shfl_sync(all, tile, l);
+        return true;
+    }
     int before = 0;
-    for (int base = 0; base < batch; base += 32) {
-        const int b = batch - 1 - base - lane;
+    for (int base = 0; base < v.batch; base += 32) {
+        const int b = v.batch - 1 - base - lane;
         int tiles = 0;
         if (b >= 0) {
-            int64_t at;
+            int64_t unused;
             int n;
-            cut(cu, b, tokens, &at, &n);
+            cut(kKeys ? v.cu_k : v.cu_q, b, kKeys ? v.tk : v.tq, &unused, &n);
             tiles = (n + rows - 1) / rows;
         }
         int sum = tiles;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += v;
+            const int u = __shfl_up_sync(all, sum, o);
+            if (lane >= o) sum += u;
         }
-        const uint32_t hit = __ballot_sync(0xffffffffu, before + sum > target);
+        const unsigned hit = __ballot_sync(all, before + sum > rank);
         if (hit) {
             const int l = __ffs(hit) - 1;
-            const int upto = __shfl_sync(0xffffffffu, sum, l);
-            *b_out = batch - 1 - base - l;
-            *tile_out = before + upto - 1 - target;
+            const int upto = before + __shfl_sync(all, sum, l);
+            const int own = __shfl_sync(all, tiles, l);
+            at->b = v.batch - 1 - base - l;
+            at->tile = kKeys ? rank - (upto - own) : upto - 1 - rank;
             return true;
         }
-        before += __shfl_sync(0xffffffffu, sum, 31);
+        before += __shfl_sync(all, sum, 31);
     }
     return false;
 }
 
-// how many keys query i of a sequence sees
-__device__ __forceinline__ int seen_keys(int i, int n, int m, bool causal) {
-    return causal ? min(m, max(0, i + 1 + m - n)) : m;
+// an upper bound of the tiles of a batch
+inline int64_t tiles_at_most(int64_t tokens, int rows, int batch) {
+    return batch > 1 ? tokens / rows + batch : (tokens + rows - 1) / rows;
 }
 
 // By one whole warp: zeros in rows first..127 of a tile (blocks of 64 columns).
@@ -110,10 +198,6 @@ cudaError_t gave_up_word(unsigned int** word);
 // by ascending stride; *swapped says that tokens come before heads.
 cudaError_t head_map(CUtensorMap* map, const void* data, int64_t ts, int64_t hs, int64_t tokens,
                      int heads, int dim, bool* swapped);
-
-struct MapSwaps {
-    bool q, k, v, o;
-};
 
 __device__ __forceinline__ void load_block(uint32_t dst, const CUtensorMap* map, uint32_t bar,
                                            int x, int head, int64_t token, bool swapped) {

@@ -39,29 +39,28 @@ constexpr int kBwdThreads = (kMathWarps + 2) * 32;
 constexpr int kDeltaThreads = 256;
 
 struct BwdParams {
-    int64_t tq, tk;
-    int batch, group, dim;
-    bool causal, negative, swap_q, swap_k, swap_v, swap_d;
+    Batch batch;
+    int heads_q, heads_k, group, dim;
+    bool negative, swap_q, swap_k, swap_v, swap_d;
     float scale, log2_scale;  // scale, and |scale| log2(e)
     HeadView o, dout, dq, dk, dv;
     const float* lse;
     float2* rows;  // [heads][tokens]: (lse log2(e), delta)
     unsigned int* gave_up;
-    const int32_t *cu_q, *cu_k;
 };
 
 // ---------------------------------------------------------------------------
 // (lse log2(e), delta) of every query row
 // ---------------------------------------------------------------------------
 // 16 lanes a row; lse is +infinity for a row that saw no key, so that P comes out 0
-__global__ void __launch_bounds__(kDeltaThreads) attention_delta_kernel(const BwdParams p, int heads) {
+__global__ void __launch_bounds__(kDeltaThreads) attention_delta_kernel(const BwdParams p) {
     grid_dep_sync();
     const int64_t at = ((int64_t)blockIdx.x * kDeltaThreads + threadIdx.x) >> 4;
     const int lane = threadIdx.x & 15;
-    const int64_t t = at / heads;
-    const int h = (int)(at - t * heads);
+    const int64_t t = at / p.heads_q;
+    const int h = (int)(at - t * p.heads_q);
     float s = 0.f;
-    if (t < p.tq && lane * 8 < p.dim) {
+    if (t < p.batch.tq && lane * 8 < p.dim) {
         const uint4 a = *reinterpret_cast<const uint4*>(p.o.row(t, h) + lane * 8);
         const uint4 b = *reinterpret_cast<const uint4*>(p.dout.row(t, h) + lane * 8);
         const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
@@ -73,9 +72,9 @@ __global__ void __launch_bounds__(kDeltaThreads) attention_delta_kernel(const Bw
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (t < p.tq && lane == 0) {
-        const float l = p.lse[h * p.tq + t];
-        p.rows[h * p.tq + t] =
+    if (t < p.batch.tq && lane == 0) {
+        const float l = p.lse[h * p.batch.tq + t];
+        p.rows[h * p.batch.tq + t] =
             make_float2(l == -INFINITY ? INFINITY : l * 1.4426950408889634f, s);
     }
 }
@@ -140,26 +139,28 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     __shared__ __align__(16) float2 rows[Sh::kSlots][kTileRows];
     __shared__ uint32_t tmem_at;
     __shared__ volatile int dead;
-    __shared__ int sh_b, sh_tile, sh_found;
+    __shared__ Place place;
+    __shared__ int found;
 
     grid_dep_sync();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
-        int b = 0, tile = 0;
-        const bool found = find_tile(p.cu_k, p.batch, p.tk, kTileRows, blockIdx.x, &b, &tile);
-        if (lane == 0) sh_b = b, sh_tile = tile, sh_found = found, dead = 0;
+        Place at{};
+        const bool ok = find_place<true>(p.batch, kTileRows, p.heads_k, blockIdx.x, &at);
+        if (lane == 0) place = at, found = ok, dead = 0;
     }
     __syncthreads();
-    if (!sh_found) return;
+    if (!found) return;
+    const bool causal = p.batch.causal;
     Sequence sq;
-    cut(p.cu_q, sh_b, p.tq, &sq.q0, &sq.n);
-    cut(p.cu_k, sh_b, p.tk, &sq.k0, &sq.m);
-    const int key0 = sh_tile * kTileRows;
-    const int khead = blockIdx.y;
+    cut(p.batch.cu_q, place.b, p.batch.tq, &sq.q0, &sq.n);
+    cut(p.batch.cu_k, place.b, p.batch.tk, &sq.k0, &sq.m);
+    const int key0 = place.tile * kTileRows;
+    const int khead = place.head;
     // the query tiles that see one of these keys, for each head of the group
     const int q_tiles = (sq.n + kTileRows - 1) / kTileRows;
     const int q_first =
-        p.causal ? min(q_tiles, max(0, key0 + sq.n - sq.m) / kTileRows) : 0;
+        causal ? min(q_tiles, max(0, key0 + sq.n - sq.m) / kTileRows) : 0;
     const int per_head = q_tiles - q_first, items = per_head * p.group;
 
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // one tile of queries (which = 0) or of output gradients (1) into slot `slot`
         const auto bring = [&](bool of_d, uint32_t dst, uint32_t full, int head, int i0) {
             const int valid = sq.n - i0;
-            const bool mend = valid < kTileRows && sq.q0 + sq.n < p.tq;
+            const bool mend = valid < kTileRows && sq.q0 + sq.n < p.batch.tq;
             const uint32_t bar = mend ? smem_u32(&bar_raw) : full;
             if (elect_one()) {
                 mbar_expect(bar, Sh::kTileBytes);
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const uint32_t full = smem_u32(&full_q[slot]);
             ok = bring(false, at_q + slot * Sh::kTileBytes, full, head, i0);
             if (!ok) break;
-            const float2* src = p.rows + (int64_t)head * p.tq + sq.q0 + i0;
+            const float2* src = p.rows + (int64_t)head * p.batch.tq + sq.q0 + i0;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int r = k * 32 + lane;
@@ -312,8 +313,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const uint32_t s_at = t_s + lanes + half * 64, dp_at = t_dp + lanes + half * 64;
         const float sl = p.log2_scale;
         // the first query that sees this thread's key; the last of the tile's keys' first
-        const int sees = p.causal ? max(0, key + sq.n - sq.m) : 0;
-        const int all_see = p.causal ? max(0, key0 + kTileRows - 1 + sq.n - sq.m) : 0;
+        const int sees = causal ? max(0, key + sq.n - sq.m) : 0;
+        const int all_see = causal ? max(0, key0 + kTileRows - 1 + sq.n - sq.m) : 0;
         bool ok = true;
         int tile = q_first;
         for (int i = 0; i < items && ok; ++i) {
@@ -413,24 +414,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         empty_v[Sh::kSlotsV];
     __shared__ uint32_t tmem_at;
     __shared__ volatile int dead;
-    __shared__ int sh_b, sh_tile, sh_found;
+    __shared__ Place place;
+    __shared__ int found;
 
     grid_dep_sync();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
-        int b = 0, tile = 0;
-        const bool found = find_tile(p.cu_q, p.batch, p.tq, kTileRows, blockIdx.x, &b, &tile);
-        if (lane == 0) sh_b = b, sh_tile = tile, sh_found = found, dead = 0;
+        Place at{};
+        const bool ok = find_place<false>(p.batch, kTileRows, p.heads_q, blockIdx.x, &at);
+        if (lane == 0) place = at, found = ok, dead = 0;
     }
     __syncthreads();
-    if (!sh_found) return;
+    if (!found) return;
+    const bool causal = p.batch.causal;
     Sequence sq;
-    cut(p.cu_q, sh_b, p.tq, &sq.q0, &sq.n);
-    cut(p.cu_k, sh_b, p.tk, &sq.k0, &sq.m);
-    const int row0 = sh_tile * kTileRows;
-    const int head = blockIdx.y, khead = head / p.group;
+    cut(p.batch.cu_q, place.b, p.batch.tq, &sq.q0, &sq.n);
+    cut(p.batch.cu_k, place.b, p.batch.tk, &sq.k0, &sq.m);
+    const int row0 = place.tile * kTileRows;
+    const int head = place.head, khead = head / p.group;
     const int last = min(sq.n, row0 + kTileRows) - 1;
-    const int tiles = (seen_keys(last, sq.n, sq.m, p.causal) + kTileRows - 1) / kTileRows;
+    const int tiles = (seen_keys(last, sq.n, sq.m, causal) + kTileRows - 1) / kTileRows;
 
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t at_q = smem, at_d = smem + Sh::kTileBytes;
@@ -476,7 +479,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (uk > 0) ok = mbar_wait(smem_u32(&empty_k[sk]), (uk - 1) & 1, &dead);
             if (!ok) break;
             const int valid = sq.m - j * kTileRows;
-            const bool mend = valid < kTileRows && sq.k0 + sq.m < p.tk;
+            const bool mend = valid < kTileRows && sq.k0 + sq.m < p.batch.tk;
             const uint32_t full = smem_u32(&full_k[sk]), dst = at_k + sk * Sh::kTileBytes;
             const uint32_t bar = mend ? smem_u32(&bar_raw) : full;
             if (elect_one()) {
@@ -569,10 +572,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const uint32_t dp_at = t_dp + lanes + half * 64;
         const float sl = p.log2_scale;
-        const int limit = seen_keys(i, sq.n, sq.m, p.causal);
-        const int first_limit = seen_keys(row0 + (warp & 3) * 32, sq.n, sq.m, p.causal);
+        const int limit = seen_keys(i, sq.n, sq.m, causal);
+        const int first_limit = seen_keys(row0 + (warp & 3) * 32, sq.n, sq.m, causal);
         float2 row = make_float2(INFINITY, 0.f);
-        if (i < sq.n) row = p.rows[(int64_t)head * p.tq + sq.q0 + i];
+        if (i < sq.n) row = p.rows[(int64_t)head * p.batch.tq + sq.q0 + i];
         bool ok = true;
         for (int j = 0; j < tiles && ok; ++j) {
             const uint32_t s_at = tmem + (j & 1) * 128 + lanes + half * 64;
@@ -632,27 +635,25 @@ struct BwdMaps {
 };
 
 template <int DP>
-cudaError_t launch_dim(const BwdMaps& m, const BwdParams& p, int heads_q, int heads_k,
-                       cudaStream_t st) {
-    const auto tiles = [&](int64_t tokens) {
-        return (unsigned)(p.cu_q ? tokens / kTileRows + p.batch
-                                 : (tokens + kTileRows - 1) / kTileRows);
+cudaError_t launch_dim(const BwdMaps& m, const BwdParams& p, cudaStream_t st) {
+    const auto blocks = [&](int64_t tokens, int heads) {
+        return dim3((unsigned)(tiles_at_most(tokens, kTileRows, p.batch.batch) * heads));
     };
     cudaError_t e = cudaSuccess;
-    if (p.tk > 0) {
+    if (p.batch.tk > 0) {
         e = cudaFuncSetAttribute(attention_dkv_kernel<DP>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)DkvShape<DP>::kSmem);
         if (e == cudaSuccess)
-            e = launch(attention_dkv_kernel<DP>, dim3(tiles(p.tk), (unsigned)heads_k),
+            e = launch(attention_dkv_kernel<DP>, blocks(p.batch.tk, p.heads_k),
                        dim3(kBwdThreads), DkvShape<DP>::kSmem, st, m.q, m.k, m.v, m.d, p);
     }
-    if (e == cudaSuccess && p.tq > 0) {
+    if (e == cudaSuccess && p.batch.tq > 0) {
         e = cudaFuncSetAttribute(attention_dq_kernel<DP>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)DqShape<DP>::kSmem);
         if (e == cudaSuccess)
-            e = launch(attention_dq_kernel<DP>, dim3(tiles(p.tq), (unsigned)heads_q),
+            e = launch(attention_dq_kernel<DP>, blocks(p.batch.tq, p.heads_q),
                        dim3(kBwdThreads), DqShape<DP>::kSmem, st, m.q, m.k, m.v, m.d, p);
     }
     return e;
@@ -670,12 +671,11 @@ cudaError_t launch_attention_bwd(const gs_attention_shape& s, const gs_heads& q,
                                  const gs_heads& dv, const int32_t* cu_q, const int32_t* cu_k,
                                  void* ws, cudaStream_t st) {
     BwdParams p{};
-    p.tq = s.tokens_q;
-    p.tk = s.tokens_k;
-    p.batch = s.batch;
+    p.batch = {cu_q, cu_k, s.tokens_q, s.tokens_k, s.batch, s.causal != 0};
+    p.heads_q = s.heads_q;
+    p.heads_k = s.heads_k;
     p.group = s.heads_q / s.heads_k;
     p.dim = s.head_dim;
-    p.causal = s.causal != 0;
     p.negative = s.scale < 0.f;
     p.scale = s.scale;
     p.log2_scale = fabsf(s.scale) * 1.4426950408889634f;
@@ -686,8 +686,6 @@ cudaError_t launch_attention_bwd(const gs_attention_shape& s, const gs_heads& q,
     p.dv = view(dv);
     p.lse = lse;
     p.rows = static_cast<float2*>(ws);
-    p.cu_q = cu_q;
-    p.cu_k = cu_k;
     cudaError_t e = gave_up_word(&p.gave_up);
     if (e != cudaSuccess) return e;
     BwdMaps m;
@@ -704,15 +702,14 @@ cudaError_t launch_attention_bwd(const gs_attention_shape& s, const gs_heads& q,
     if (s.tokens_q == 0) m.q = m.d = m.k;  // nothing is loaded by them
     if (s.tokens_k == 0) m.k = m.v = m.q;
     if (e != cudaSuccess) return e;
-    if (p.tq > 0) {
-        const int64_t threads = p.tq * s.heads_q * 16;
+    if (p.batch.tq > 0) {
+        const int64_t threads = p.batch.tq * s.heads_q * 16;
         e = launch(attention_delta_kernel,
                    dim3((unsigned)((threads + kDeltaThreads - 1) / kDeltaThreads)),
-                   dim3(kDeltaThreads), 0, st, p, s.heads_q);
+                   dim3(kDeltaThreads), 0, st, p);
         if (e != cudaSuccess) return e;
     }
-    return s.head_dim <= 64 ? launch_dim<64>(m, p, s.heads_q, s.heads_k, st)
-                            : launch_dim<128>(m, p, s.heads_q, s.heads_k, st);
+    return s.head_dim <= 64 ? launch_dim<64>(m, p, st) : launch_dim<128>(m, p, st);
 }
 
 }  // namespace gs

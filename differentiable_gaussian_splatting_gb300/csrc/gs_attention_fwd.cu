@@ -15,6 +15,11 @@
 // rescaling, which has to wait for the last product, is rare.  P is rounded to bfloat16
 // for the product; the sum takes the unrounded values in fp32.
 //
+// Where the blocks are fewer than the SMs, or their last wave would be mostly empty, those
+// blocks' keys are cut into pieces, a block each, which leave normalised outputs and row
+// sums in the workspace for a second kernel to join:
+//   lse = ln sum_z exp(lse_z),  O = sum_z exp(lse_z - lse) O_z.
+//
 // Rows of V beyond the sequence's end are set to zero in shared memory, since their
 // probability 0 times what may lie there (another sequence, NaN) is not 0.
 #include <cuda_bf16.h>
@@ -32,6 +37,7 @@ namespace {
 
 constexpr int kSoftmaxWarps = 8;
 constexpr int kFwdThreads = (kSoftmaxWarps + 2) * 32;
+constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kStale = 8.f;  // powers of two by which a maximum may rise unnoticed
 
 template <int DP>
@@ -44,16 +50,104 @@ struct FwdShape {
     static constexpr uint32_t kSmem = (2 + kSlots) * kTileBytes + 1024;
 };
 
+// How blocks are cut.  Last wave: blocks `whole` .. `whole` + `rest` - 1 are cut into
+// `pieces` of `chunk` key tiles, piece by piece.  Spread: all blocks are cut so that kSms
+// blocks take them all; since the lengths are on the device, the kernels find the chunk.
+constexpr int kSms = 152;
+constexpr int kLeastChunk = 4;  // key tiles; below, joining costs more than it saves
+struct FwdPlan {
+    int64_t whole, rest;
+    int chunk, pieces;
+    bool spread;
+    int slot_rows;  // rows that a piece keeps in the workspace
+    __host__ __device__ int64_t part_rows() const {
+        return spread ? (int64_t)kSms * slot_rows : pieces > 1 ? pieces * rest * slot_rows : 0;
+    }
+};
+
 struct FwdParams {
-    int64_t tq, tk;
-    int batch, group, dim;
-    bool causal, negative, swap_q, swap_k, swap_v;
-    float scale, log2_scale;  // |scale|, and with log2(e)
+    Batch batch;
+    int heads, group, dim;
+    bool negative, swap_q, swap_k, swap_v;
+    float log2_scale;  // |scale| log2(e)
     HeadView o;
     float* lse;
     unsigned int* gave_up;
-    const int32_t *cu_q, *cu_k;
+    FwdPlan plan;
+    float *part_o, *part_lse;  // [pieces][rest][slot_rows][DP], [pieces][rest][slot_rows]
 };
+
+// key tiles that query tile t (128 rows) of the block at row0 walks
+__device__ __forceinline__ int walked(const Sequence& sq, int row0, int t, bool causal) {
+    const int last = min(sq.n, row0 + (t + 1) * kTileRows) - 1;
+    return last >= row0 + t * kTileRows
+               ? (seen_keys(last, sq.n, sq.m, causal) + kTileRows - 1) / kTileRows
+               : 0;
+}
+
+// What a block works on, kept in shared memory: registers are short in the softmax.
+struct FwdWork {
+    Sequence sq;
+    int row0;         // first query of the block in its sequence
+    int head, khead;
+    int key0;         // first key of the block's piece
+    int tiles[2];     // key tiles that each of the two query tiles walks
+    int64_t part;     // first row in the workspace (-1: the block writes the output itself)
+};
+
+// Spread blocks (by one whole warp; lane = sequence): the smallest chunk with which kSms
+// blocks suffice, and the place of block or piece `id`.  Pieces of a block are neighbours.
+struct Spread {
+    int chunk, pieces;  // of the place's sequence
+    int piece;          // with `cut`: which one
+    int first;          // number of the block's first piece
+};
+
+__device__ __forceinline__ bool find_spread(const Batch& v, int heads, int id, bool by_piece,
+                                            Place* at, Spread* sp) {
+    const int lane = threadIdx.x & 31;
+    const unsigned all = 0xffffffffu;
+    int64_t unused;
+    int n = 0, m = 0;
+    if (lane < v.batch) {
+        cut(v.cu_q, lane, v.tq, &unused, &n);
+        cut(v.cu_k, lane, v.tk, &unused, &m);
+    }
+    const int blocks = (n + 2 * kTileRows - 1) / (2 * kTileRows) * heads;
+    const int keys = (m + kTileRows - 1) / kTileRows;
+    int lo = kLeastChunk, hi = max(lo, (int)__reduce_max_sync(all, keys));
+    while (lo < hi) {
+        const int c = (lo + hi) >> 1;
+        if ((int)__reduce_add_sync(all, blocks * max(1, (keys + c - 1) / c)) <= kSms)
+            hi = c;
+        else
+            lo = c + 1;
+    }
+    const int pieces = max(1, (keys + lo - 1) / lo);
+    // blocks (or pieces) up to and with this lane's sequence, and pieces alone
+    int sum = by_piece ? blocks * pieces : blocks, sum_p = blocks * pieces;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(all, sum, o), w = __shfl_up_sync(all, sum_p, o);
+        if (lane >= o) sum += u, sum_p += w;
+    }
+    const unsigned hit = __ballot_sync(all, sum > id);
+    if (!hit) return false;
+    const int l = __ffs(hit) - 1;
+    int within = id - (sum - (by_piece ? blocks * pieces : blocks));
+    const int piece = by_piece ? within % pieces : 0;
+    if (by_piece) within /= pieces;
+    const int first = sum_p - blocks * pieces + within * pieces;
+    at->b = l;
+    at->head = __shfl_sync(all, within % heads, l);
+    at->tile = __shfl_sync(all, within / heads, l);
+    sp->chunk = lo;
+    sp->pieces = __shfl_sync(all, pieces, l);
+    sp->piece = __shfl_sync(all, piece, l);
+    sp->first = __shfl_sync(all, first, l);
+    return sp->first + sp->pieces <= kSms;  // always, unless offsets overlap
+}
+
 
 template <int DP>
 __global__ void __launch_bounds__(kFwdThreads, 1)
@@ -66,33 +160,55 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         bar_empty[Sh::kSlots], bar_raw, bar_drain;
     __shared__ uint32_t tmem_at;
     __shared__ volatile int dead;
-    __shared__ int sh_b, sh_tile, sh_found;
+    __shared__ FwdWork work;
+    __shared__ int found;
 
     grid_dep_sync();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
-        int b = 0, tile = 0;
-        const bool found =
-            find_tile(p.cu_q, p.batch, p.tq, 2 * kTileRows, blockIdx.x, &b, &tile);
-        if (lane == 0) sh_b = b, sh_tile = tile, sh_found = found, dead = 0;
+        Place at{};
+        int piece = 0, chunk = 0;
+        int64_t part = -1;
+        bool ok;
+        if (p.plan.spread) {
+            Spread sp;
+            ok = find_spread(p.batch, p.heads, blockIdx.x, true, &at, &sp);
+            if (ok && sp.pieces > 1) {
+                piece = sp.piece;
+                chunk = sp.chunk;
+                part = (int64_t)blockIdx.x * p.plan.slot_rows;
+            }
+        } else {
+            int64_t id = blockIdx.x;
+            if (id >= p.plan.whole) {  // the cut blocks, piece by piece
+                piece = (int)((id - p.plan.whole) / p.plan.rest);
+                id -= piece * p.plan.rest;
+                chunk = p.plan.chunk;
+                part = ((int64_t)blockIdx.x - p.plan.whole) * p.plan.slot_rows;
+            }
+            ok = find_place<false>(p.batch, 2 * kTileRows, p.heads, (int)id, &at);
+        }
+        if (ok && lane == 0) {
+            FwdWork w;
+            cut(p.batch.cu_q, at.b, p.batch.tq, &w.sq.q0, &w.sq.n);
+            cut(p.batch.cu_k, at.b, p.batch.tk, &w.sq.k0, &w.sq.m);
+            w.row0 = at.tile * 2 * kTileRows;
+            w.head = at.head;
+            w.khead = at.head / p.group;
+            w.key0 = piece * chunk * kTileRows;
+            w.part = part;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                w.tiles[t] = walked(w.sq, w.row0, t, p.batch.causal);
+                if (part >= 0) w.tiles[t] = min(max(w.tiles[t] - piece * chunk, 0), chunk);
+            }
+            if (piece > 0 && w.tiles[0] + w.tiles[1] == 0) ok = false;  // no keys left for it
+            work = w;
+        }
+        if (lane == 0) found = ok, dead = 0;
     }
     __syncthreads();
-    if (!sh_found) return;
-    Sequence sq;
-    cut(p.cu_q, sh_b, p.tq, &sq.q0, &sq.n);
-    cut(p.cu_k, sh_b, p.tk, &sq.k0, &sq.m);
-    const int row0 = sh_tile * 2 * kTileRows;  // first query of the block in its sequence
-    const int head = blockIdx.y, khead = head / p.group;
-    // key tiles that each of the two query tiles walks
-    int tiles[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int last = min(sq.n, row0 + (t + 1) * kTileRows) - 1;
-        tiles[t] = last >= row0 + t * kTileRows
-                       ? (seen_keys(last, sq.n, sq.m, p.causal) + kTileRows - 1) / kTileRows
-                       : 0;
-    }
-    const int most = max(tiles[0], tiles[1]);
+    if (!found) return;
 
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t smem_kv = smem + 2 * Sh::kTileBytes;
@@ -123,12 +239,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     constexpr uint32_t tmem = 0;
     // The score tiles of the block in their order -- key tile by key tile, first and second
     // query tile in turn as long as each has some -- take the buffers in rotation.
-    const auto order = [&](int j, int t) { return min(j + t, tiles[0]) + min(j, tiles[1]); };
     const auto tmem_s = [&](int x) { return tmem + (x % Sh::kScores) * 128; };
     const auto tmem_o = [&](int t) { return tmem + Sh::kScores * 128 + t * DP; };
 
     if (warp == kSoftmaxWarps + 1) {
         // ---- the producer: Q, then K and V tiles in turn ----
+        const int tiles[2] = {work.tiles[0], work.tiles[1]}, most = max(tiles[0], tiles[1]);
+        const int64_t k0 = work.sq.k0 + work.key0;
+        const int left = work.sq.m - work.key0, khead = work.khead;
+        const bool tail = work.sq.k0 + work.sq.m < p.batch.tk;
         if (most > 0) {
             if (elect_one()) {
 #pragma unroll
@@ -136,8 +255,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     if (tiles[t] > 0) {
                         mbar_expect(smem_u32(&bar_q[t]), Sh::kTileBytes);
                         load_tile<Sh::kBlocks>(smem + t * Sh::kTileBytes, &map_q,
-                                               smem_u32(&bar_q[t]), head,
-                                               sq.q0 + row0 + t * kTileRows, p.swap_q);
+                                               smem_u32(&bar_q[t]), work.head,
+                                               work.sq.q0 + work.row0 + t * kTileRows, p.swap_q);
                     }
             }
             __syncwarp();
@@ -148,14 +267,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 const uint32_t dst = smem_kv + slot * Sh::kTileBytes;
                 const uint32_t full = smem_u32(&bar_full[slot]);
                 const bool is_v = i & 1;
-                const int valid = sq.m - j * kTileRows;
+                const int valid = left - j * kTileRows;
                 // values of another sequence behind this one's end: zeros in their place
-                const bool mend = is_v && valid < kTileRows && sq.k0 + sq.m < p.tk;
+                const bool mend = is_v && valid < kTileRows && tail;
                 const uint32_t bar = mend ? smem_u32(&bar_raw) : full;
                 if (elect_one()) {
                     mbar_expect(bar, Sh::kTileBytes);
                     load_tile<Sh::kBlocks>(dst, is_v ? &map_v : &map_k, bar, khead,
-                                           sq.k0 + (int64_t)j * kTileRows,
+                                           k0 + (int64_t)j * kTileRows,
                                            is_v ? p.swap_v : p.swap_k);
                 }
                 __syncwarp();
@@ -184,6 +303,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // us instead of 1,283 on 16,320 tokens x 16 heads x 128).  A step is a key tile and a
         // query tile; scores run kScores steps ahead of the outputs, so that a query tile's
         // softmax finds its next scores ready.
+        const int tiles[2] = {work.tiles[0], work.tiles[1]}, most = max(tiles[0], tiles[1]);
         if (most > 0 && elect_one()) {
             constexpr uint32_t word_o = mma_word(128, DP, false, true);
             const uint32_t word_s = mma_word(128, 128, false, false) | (p.negative ? kNegateA : 0u);
@@ -246,17 +366,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const int t = warp >> 2;
         const int r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's lanes of tensor memory
-        const int i = row0 + t * kTileRows + r;
-        const int limit = seen_keys(i, sq.n, sq.m, p.causal);
-        const int first_limit =
-            seen_keys(row0 + t * kTileRows + (warp & 3) * 32, sq.n, sq.m, p.causal);
-        const float sl = p.log2_scale, tau = kStale / sl;
+        // keys of this piece that the thread's row sees, and the warp's first row
+        const auto keys_of = [&](int row) {
+            return seen_keys(work.row0 + t * kTileRows + row, work.sq.n, work.sq.m,
+                             p.batch.causal) - work.key0;
+        };
+        const int limit = keys_of(r), first_limit = keys_of((warp & 3) * 32);
+        const int tiles_t = work.tiles[t];
+        // the score tiles go by order(j, t) = steps before (j, t)
+        const int tiles_0 = work.tiles[0], tiles_1 = work.tiles[1];
+        const float sl = p.log2_scale;
         const uint32_t o_at = tmem_o(t) + lanes;
         float top = -INFINITY;
         float2 sum = make_float2(0.f, 0.f);
         bool ok = true;
-        for (int j = 0; j < tiles[t]; ++j) {
-            const uint32_t s_at = tmem_s(order(j, t)) + lanes;
+        for (int j = 0; j < tiles_t; ++j) {
+            const uint32_t s_at = tmem_s(min(j + t, tiles_0) + min(j, tiles_1)) + lanes;
             // kScores barriers a query tile: the one of j is used again after P(j) is taken
             ok = mbar_wait(smem_u32(&bar_s[t * Sh::kScores + j % Sh::kScores]),
                            (j / Sh::kScores) & 1, &dead);
@@ -281,7 +406,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 mt[(c >> 1) & 3] = max3(mt[(c >> 1) & 3], __uint_as_float(s[c]),
                                         __uint_as_float(s[c + 1]));
             const float high = max3(fmaxf(mt[0], mt[1]), mt[2], mt[3]);
-            const bool risen = high > top + tau;
+            const bool risen = (high - top) * sl > kStale;
             if (__any_sync(0xffffffffu, risen)) {
                 const float f = risen ? ex2_approx((top - high) * sl) : 1.f;
                 if (risen) top = high;
@@ -325,41 +450,53 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(&bar_p[t * Sh::kScores + j % Sh::kScores]));
         }
         // ---- the row's output ----
-        if (ok && tiles[t] > 0) ok = mbar_wait(smem_u32(&bar_o[t]), (tiles[t] - 1) & 1, &dead);
+        if (ok && tiles_t > 0) ok = mbar_wait(smem_u32(&bar_o[t]), (tiles_t - 1) & 1, &dead);
         if (ok) {
             tmem_fence_after();
             const float l = sum.x + sum.y;
-            const bool valid = i < sq.n;
-            // a row that sees no key: zeros
-            const float f = limit > 0 ? 1.f / l : 0.f;
-            __nv_bfloat16* out = valid ? p.o.row(sq.q0 + i, head) : nullptr;
+            const int slot_row = t * kTileRows + r, i = work.row0 + slot_row;
+            const bool valid = i < work.sq.n, split = work.part >= 0;
+            // a row that sees no key (of this piece): zeros
+            const bool some = limit > 0 && tiles_t > 0;
+            const float f = some ? 1.f / l : 0.f;
+            __nv_bfloat16* out = valid && !split ? p.o.row(work.sq.q0 + i, work.head) : nullptr;
+            float* out32 = valid && split ? p.part_o + (work.part + slot_row) * DP : nullptr;
 #pragma unroll
             for (int c = 0; c < DP; c += 32) {
                 uint32_t o[32];
-                if (tiles[t] > 0) {
+                if (tiles_t > 0) {
                     tmem_ld32(o, o_at + c);
                     tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = 0u;
                 }
-                if (!valid) continue;
 #pragma unroll
-                for (int k = 0; k < 32; k += 8) {
-                    if (c + k >= p.dim) break;
-                    uint32_t w[4];
+                for (int k = 0; k < 32; ++k)
+                    o[k] = some ? __float_as_uint(__uint_as_float(o[k]) * f) : 0u;
+                if (out) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float a = __uint_as_float(o[k + 2 * e]) * f;
-                        const float b = __uint_as_float(o[k + 2 * e + 1]) * f;
-                        w[e] = limit > 0 ? pack_bf16(a, b) : 0u;
+                    for (int k = 0; k < 32; k += 8) {
+                        if (c + k >= p.dim) break;
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack_bf16(__uint_as_float(o[k + 2 * e]),
+                                             __uint_as_float(o[k + 2 * e + 1]));
+                        *reinterpret_cast<uint4*>(out + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    *reinterpret_cast<uint4*>(out + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else if (out32) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4)
+                        *reinterpret_cast<uint4*>(out32 + c + k) =
+                            make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
                 }
             }
-            if (valid)
-                p.lse[(int64_t)head * p.tq + sq.q0 + i] =
-                    limit > 0 ? (fmaf(top, sl, log2f(l))) * 0.69314718055994530942f : -INFINITY;
+            if (valid) {
+                // in powers of two until the pieces are joined
+                const float lse2 = some ? fmaf(top, sl, log2f(l)) : -INFINITY;
+                if (!split)
+                    p.lse[(int64_t)work.head * p.batch.tq + work.sq.q0 + i] = lse2 * kLn2;
+                else
+                    p.part_lse[work.part + slot_row] = lse2;
+            }
         }
     }
     tmem_fence_before();
@@ -372,41 +509,160 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
 }
 
+// A split block's rows from its pieces, in the order of the pieces.  DP / 4 lanes a row.
+constexpr int kJoinThreads = 256;
+
+template <int DP>
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const FwdParams p) {
+    __shared__ Place place;
+    __shared__ Spread spread;
+    __shared__ int found;
+    grid_dep_sync();
+    if (threadIdx.x < 32) {
+        Place at{};
+        Spread sp{p.plan.chunk, p.plan.pieces, 0, (int)blockIdx.x};
+        const bool ok = p.plan.spread
+                            ? find_spread(p.batch, p.heads, blockIdx.x, false, &at, &sp)
+                            : find_place<false>(p.batch, 2 * kTileRows, p.heads,
+                                                (int)(p.plan.whole + blockIdx.x), &at);
+        if (threadIdx.x == 0) place = at, spread = sp, found = ok && sp.pieces > 1;
+    }
+    __syncthreads();
+    if (!found) return;
+    Sequence sq;
+    cut(p.batch.cu_q, place.b, p.batch.tq, &sq.q0, &sq.n);
+    cut(p.batch.cu_k, place.b, p.batch.tk, &sq.k0, &sq.m);
+    const int row0 = place.tile * 2 * kTileRows;
+    constexpr int kLanes = DP / 4;
+    const int lane = threadIdx.x % kLanes;
+    const int rows = min(2 * kTileRows, sq.n - row0);
+    // rows from a piece to the next
+    const int64_t step = (p.plan.spread ? 1 : p.plan.rest) * p.plan.slot_rows;
+    for (int r = blockIdx.y * (kJoinThreads / kLanes) + threadIdx.x / kLanes; r < rows;
+         r += gridDim.y * (kJoinThreads / kLanes)) {
+        // a piece without keys for the row's tile was not walked
+        const int walks = walked(sq, row0, r / kTileRows, p.batch.causal);
+        const int pieces = max(1, (walks + spread.chunk - 1) / spread.chunk);
+        const int64_t at = (int64_t)spread.first * p.plan.slot_rows + r;
+        float top = -INFINITY;
+        bool nan = false;
+        for (int z = 0; z < pieces; ++z) {
+            const float v = p.part_lse[z * step + at];
+            nan |= v != v;
+            top = fmaxf(top, v);
+        }
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+        if (top != -INFINITY) {
+#pragma unroll 4
+            for (int z = 0; z < pieces; ++z) {
+                const float w = ex2_approx(p.part_lse[z * step + at] - top);
+                const float4 v = reinterpret_cast<const float4*>(p.part_o)[(z * step + at) * kLanes + lane];
+                sum += w;
+                o.x = fmaf(w, v.x, o.x);
+                o.y = fmaf(w, v.y, o.y);
+                o.z = fmaf(w, v.z, o.z);
+                o.w = fmaf(w, v.w, o.w);
+            }
+        }
+        const float f = nan ? NAN : (sum > 0.f ? 1.f / sum : 0.f);
+        const int64_t token = sq.q0 + row0 + r;
+        if (lane * 4 < p.dim)
+            *reinterpret_cast<uint2*>(p.o.row(token, place.head) + lane * 4) =
+                make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
+        if (lane == 0)
+            p.lse[(int64_t)place.head * p.batch.tq + token] =
+                nan ? NAN : (sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY);
+    }
+}
+
+// The last wave is cut where a model of the waves says that it pays, in units of one key
+// tile's time: a block costs its tiles and kStart for its start and end, the join kJoin, and
+// less than kGain of the whole is not worth it (at 8,160 tokens x 16 heads x 128 cutting
+// 56 blocks of 512 took 380 -> 362 us; at 16,320 tokens, 112 of 1,024, 1,267 -> 1,274 us).
+constexpr int kStart = 3, kJoin = 4, kMaxPieces = 16;
+constexpr double kGain = 0.05;
+
+FwdPlan plan_fwd(int64_t tq, int64_t tk, int batch, int heads, bool causal) {
+    const int rows = 2 * kTileRows;
+    const int64_t blocks = tiles_at_most(tq, rows, batch) * heads;
+    const int64_t keys = (tk + kTileRows - 1) / kTileRows;
+    FwdPlan plan{};
+    plan.whole = blocks;
+    plan.pieces = 1;
+    plan.slot_rows = (int)(tq < rows ? tq : rows);
+    if (blocks < kSms) {
+        plan.spread = batch <= 32 && keys > kLeastChunk;
+        return plan;
+    }
+    // under the mask, or with sequences of several lengths, the short blocks come last
+    if (causal || batch > 1) return plan;
+    const auto waves = [](int64_t n) { return (n + kSms - 1) / kSms; };
+    const int64_t whole = blocks / kSms * kSms, rest = blocks - whole;
+    if (rest == 0) return plan;
+    double best = (1.0 - kGain) * (double)(waves(blocks) * (keys + kStart));
+    for (int cuts = 2; cuts <= kMaxPieces; ++cuts) {
+        const int64_t chunk = (keys + cuts - 1) / cuts, pieces = (keys + chunk - 1) / chunk;
+        if (chunk < kLeastChunk) break;
+        const double cost = (double)(whole / kSms * (keys + kStart) +
+                                     waves(rest * pieces) * (chunk + kStart) + kJoin);
+        if (cost < best) {
+            best = cost;
+            plan.whole = whole;
+            plan.rest = rest;
+            plan.chunk = (int)chunk;
+            plan.pieces = (int)pieces;
+        }
+    }
+    return plan;
+}
+
 template <int DP>
 cudaError_t launch_dim(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                       const FwdParams& p, int heads, cudaStream_t st) {
-    const cudaError_t e =
+                       const FwdParams& p, cudaStream_t st) {
+    cudaError_t e =
         cudaFuncSetAttribute(attention_fwd_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)FwdShape<DP>::kSmem);
     if (e != cudaSuccess) return e;
-    const int64_t rows = 2 * kTileRows;
-    const int64_t tiles = p.cu_q ? p.tq / rows + p.batch : (p.tq + rows - 1) / rows;
-    return launch(attention_fwd_kernel<DP>, dim3((unsigned)tiles, (unsigned)heads),
-                  dim3(kFwdThreads), FwdShape<DP>::kSmem, st, mq, mk, mv, p);
+    const int64_t blocks = p.plan.spread ? kSms : p.plan.whole + p.plan.rest * p.plan.pieces;
+    e = launch(attention_fwd_kernel<DP>, dim3((unsigned)blocks), dim3(kFwdThreads),
+               FwdShape<DP>::kSmem, st, mq, mk, mv, p);
+    if (e != cudaSuccess || (!p.plan.spread && p.plan.pieces == 1)) return e;
+    const int rows = kJoinThreads / (DP / 4);
+    const unsigned y = (unsigned)((p.plan.slot_rows + 4 * rows - 1) / (4 * rows));
+    const int64_t joined = p.plan.spread ? p.plan.whole : p.plan.rest;
+    return launch(attention_join_kernel<DP>, dim3((unsigned)joined, y), dim3(kJoinThreads), 0, st,
+                  p);
 }
 
 }  // namespace
+
+size_t attention_fwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads,
+                                     int head_dim) {
+    // whatever the mask
+    const int64_t a = plan_fwd(tokens_q, tokens_k, batch, heads, false).part_rows();
+    const int64_t b = plan_fwd(tokens_q, tokens_k, batch, heads, true).part_rows();
+    const int64_t rows = a > b ? a : b;
+    return (size_t)rows * ((head_dim <= 64 ? 64 : 128) + 1) * sizeof(float);
+}
 
 cudaError_t launch_attention_fwd(const gs_attention_shape& s, const gs_heads& q, const gs_heads& k,
                                  const gs_heads& v, const gs_heads& out, float* lse,
                                  const int32_t* cu_q, const int32_t* cu_k, void* ws,
                                  cudaStream_t st) {
-    (void)ws;
     FwdParams p{};
-    p.tq = s.tokens_q;
-    p.tk = s.tokens_k;
-    p.batch = s.batch;
+    p.batch = {cu_q, cu_k, s.tokens_q, s.tokens_k, s.batch, s.causal != 0};
+    p.heads = s.heads_q;
     p.group = s.heads_q / s.heads_k;
     p.dim = s.head_dim;
-    p.causal = s.causal != 0;
     p.negative = s.scale < 0.f;
-    p.scale = fabsf(s.scale);
     // a zero scale as one too small to matter: masked scores of -infinity stay defined
-    p.log2_scale = fmaxf(p.scale * 1.4426950408889634f, 1e-30f);
+    p.log2_scale = fmaxf(fabsf(s.scale) * 1.4426950408889634f, 1e-30f);
     p.o = {static_cast<__nv_bfloat16*>(out.data), out.token_stride, out.head_stride};
     p.lse = lse;
-    p.cu_q = cu_q;
-    p.cu_k = cu_k;
+    p.plan = plan_fwd(s.tokens_q, s.tokens_k, s.batch, s.heads_q, s.causal != 0);
+    p.part_o = static_cast<float*>(ws);
+    p.part_lse = p.part_o + p.plan.part_rows() * (s.head_dim <= 64 ? 64 : 128);
     CUtensorMap mq, mk, mv;
     cudaError_t e = gave_up_word(&p.gave_up);
     if (e != cudaSuccess) return e;
@@ -421,8 +677,7 @@ cudaError_t launch_attention_fwd(const gs_attention_shape& s, const gs_heads& q,
                          s.head_dim, &p.swap_v);
     }
     if (e != cudaSuccess) return e;
-    return s.head_dim <= 64 ? launch_dim<64>(mq, mk, mv, p, s.heads_q, st)
-                            : launch_dim<128>(mq, mk, mv, p, s.heads_q, st);
+    return s.head_dim <= 64 ? launch_dim<64>(mq, mk, mv, p, st) : launch_dim<128>(mq, mk, mv, p, st);
 }
 
 }  // namespace gs

@@ -37,6 +37,8 @@ cudaError_t launch_dropout_add(int64_t n, bool bf16, const void* x, const void* 
 // ---- attention (gs_attention.cu) --------------------------------------------------
 size_t attention_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads_q,
                                  int heads_k, int head_dim);
+size_t attention_fwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads,
+                                     int head_dim);
 cudaError_t launch_attention_fwd(const gs_attention_shape& s, const gs_heads& q, const gs_heads& k,
                                  const gs_heads& v, const gs_heads& out, float* lse,
                                  const int32_t* cu_q, const int32_t* cu_k, void* ws,
