@@ -52,12 +52,11 @@ cudaError_t head_map(CUtensorMap* map, const void* data, int64_t ts, int64_t hs,
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// the forward's pieces, or the backward's (lse, delta) pair of every query row
 size_t attention_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads_q,
                                  int heads_k, int head_dim) {
-    (void)heads_k;
     const size_t fwd = attention_fwd_workspace_bytes(tokens_q, tokens_k, batch, heads_q, head_dim);
-    const size_t bwd = (size_t)tokens_q * heads_q * sizeof(float2);
+    const size_t bwd =
+        attention_bwd_workspace_bytes(tokens_q, tokens_k, batch, heads_q, heads_k, head_dim);
     return (fwd > bwd ? fwd : bwd) / 256 * 256 + 512;
 }
 

@@ -24,6 +24,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -38,6 +39,24 @@ constexpr int kMathWarps = 8;
 constexpr int kBwdThreads = (kMathWarps + 2) * 32;
 constexpr int kDeltaThreads = 256;
 
+// Blocks `whole` .. `whole` + `rest` - 1 are cut into `pieces` of `chunk` tiles of the other
+// side, a block each, piece by piece; a kernel adds the pieces' fp32 results up.
+constexpr int kSms = 152;
+struct BwdPlan {
+    int64_t whole, rest;
+    int chunk, pieces;
+    int slot_rows;  // rows that a piece keeps in the workspace
+};
+
+// What a block works on, kept in shared memory: registers are short in the inner loops.
+struct BwdWork {
+    Sequence sq;
+    int row0;         // first key (dK, dV) or query (dQ) of the block in its sequence
+    int head, khead;
+    int first, items; // tiles of the other side: those of the block's piece
+    int64_t part;     // first row in the workspace (-1: the block writes the output itself)
+};
+
 struct BwdParams {
     Batch batch;
     int heads_q, heads_k, group, dim;
@@ -45,14 +64,67 @@ struct BwdParams {
     float scale, log2_scale;  // scale, and |scale| log2(e)
     HeadView o, dout, dq, dk, dv;
     const float* lse;
-    float2* rows;  // [heads][tokens]: (lse log2(e), delta)
+    float *nlse, *ndelta;  // [heads][tokens]: -lse log2(e) (-infinity: saw no key), -delta
     unsigned int* gave_up;
+    BwdPlan plan;  // of the kernel at hand
+    float* parts;  // [pieces][rest][slot_rows][DP], for dK, then for dV; or for dQ
 };
 
+// query tiles that see a block of keys, for each head of the group: from *first on
+__device__ __forceinline__ int queries_of(const Sequence& sq, int key0, bool causal, int* first) {
+    const int tiles = (sq.n + kTileRows - 1) / kTileRows;
+    *first = causal ? min(tiles, max(0, key0 + sq.n - sq.m) / kTileRows) : 0;
+    return tiles - *first;
+}
+
+// key tiles that a block of queries sees
+__device__ __forceinline__ int keys_of(const Sequence& sq, int row0, bool causal) {
+    const int last = min(sq.n, row0 + kTileRows) - 1;
+    return (seen_keys(last, sq.n, sq.m, causal) + kTileRows - 1) / kTileRows;
+}
+
+__host__ __device__ inline int64_t part_rows(const BwdPlan& plan) {
+    return plan.pieces > 1 ? plan.pieces * plan.rest * plan.slot_rows : 0;
+}
+
+// By one whole warp: the block's work, or false.
+template <bool kKeys>
+__device__ __forceinline__ bool find_work(const BwdParams& p, BwdWork* out) {
+    int64_t id = blockIdx.x, part = -1;
+    int piece = 0;
+    if (id >= p.plan.whole) {  // the cut blocks, piece by piece
+        piece = (int)((id - p.plan.whole) / p.plan.rest);
+        id -= piece * p.plan.rest;
+        part = ((int64_t)blockIdx.x - p.plan.whole) * p.plan.slot_rows;
+    }
+    Place at{};
+    if (!find_place<kKeys>(p.batch, kTileRows, kKeys ? p.heads_k : p.heads_q, (int)id, &at))
+        return false;
+    BwdWork w;
+    cut(p.batch.cu_q, at.b, p.batch.tq, &w.sq.q0, &w.sq.n);
+    cut(p.batch.cu_k, at.b, p.batch.tk, &w.sq.k0, &w.sq.m);
+    w.row0 = at.tile * kTileRows;
+    w.head = at.head;
+    w.khead = kKeys ? at.head : at.head / p.group;
+    int unused;
+    w.items = kKeys ? queries_of(w.sq, w.row0, p.batch.causal, &unused) * p.group
+                    : keys_of(w.sq, w.row0, p.batch.causal);
+    w.first = 0;
+    w.part = part;
+    if (part >= 0) {
+        w.first = piece * p.plan.chunk;
+        w.items = min(max(w.items - w.first, 0), p.plan.chunk);
+        if (piece > 0 && w.items == 0) return false;
+    }
+    if ((threadIdx.x & 31) == 0) *out = w;
+    return true;
+}
+
+
 // ---------------------------------------------------------------------------
-// (lse log2(e), delta) of every query row
+// -lse log2(e) and -delta of every query row
 // ---------------------------------------------------------------------------
-// 16 lanes a row; lse is +infinity for a row that saw no key, so that P comes out 0
+// 16 lanes a row; -infinity for a row that saw no key, so that its P comes out 0
 __global__ void __launch_bounds__(kDeltaThreads) attention_delta_kernel(const BwdParams p) {
     grid_dep_sync();
     const int64_t at = ((int64_t)blockIdx.x * kDeltaThreads + threadIdx.x) >> 4;
@@ -74,8 +146,8 @@ __global__ void __launch_bounds__(kDeltaThreads) attention_delta_kernel(const Bw
     for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (t < p.batch.tq && lane == 0) {
         const float l = p.lse[h * p.batch.tq + t];
-        p.rows[h * p.batch.tq + t] =
-            make_float2(l == -INFINITY ? INFINITY : l * 1.4426950408889634f, s);
+        p.nlse[h * p.batch.tq + t] = l == -INFINITY ? l : l * -1.4426950408889634f;
+        p.ndelta[h * p.batch.tq + t] = -s;
     }
 }
 
@@ -87,10 +159,11 @@ __device__ __forceinline__ void store_half(uint32_t at, const float* v) {
     tmem_st32(at, w);
 }
 
-// kDim columns of a row of tensor memory, times f, to memory in bfloat16
+// kDim columns of a row of tensor memory (or zeros), times f, to memory: in bfloat16 to `out`,
+// or as they are to `part`
 template <int kDim>
-__device__ __forceinline__ void store_row(uint32_t at, __nv_bfloat16* out, int dim, float f,
-                                          bool valid, bool zero) {
+__device__ __forceinline__ void store_row(uint32_t at, __nv_bfloat16* out, float* part, int dim,
+                                          float f, bool zero) {
 #pragma unroll
     for (int c = 0; c < kDim; c += 32) {
         uint32_t o[32];
@@ -98,7 +171,13 @@ __device__ __forceinline__ void store_row(uint32_t at, __nv_bfloat16* out, int d
             tmem_ld32(o, at + c);
             tmem_wait_ld();
         }
-        if (!valid) continue;
+        if (part) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+                *reinterpret_cast<uint4*>(part + c + k) =
+                    zero ? make_uint4(0, 0, 0, 0) : make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+        }
+        if (!out) continue;
 #pragma unroll
         for (int k = 0; k < 32; k += 8) {
             if (c + k < dim) {
@@ -122,6 +201,9 @@ struct DkvShape {
     static constexpr int kBlocks = DP / kBlockCols;
     static constexpr uint32_t kTileBytes = kBlocks * kBlockBytes;
     static constexpr int kSlots = DP == 128 ? 2 : 4;
+    // dO V^T tiles in tensor memory, beside S, dV and dK: with two the next one is formed
+    // before dS of this one is
+    static constexpr int kDp = DP == 128 ? 1 : 2;
     static constexpr uint32_t kSmem = (2 + 2 * kSlots) * kTileBytes + 1024;
 };
 
@@ -133,35 +215,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                          const __grid_constant__ CUtensorMap map_d, const BwdParams p) {
     using Sh = DkvShape<DP>;
     extern __shared__ char smem_raw[];
-    __shared__ uint64_t bar_k, bar_v, bar_s, bar_dp, bar_p, bar_ds, bar_done, bar_raw, bar_drain;
+    __shared__ uint64_t bar_k, bar_v, bar_s, bar_dp[Sh::kDp], bar_p, bar_ds[Sh::kDp], bar_done,
+        bar_raw, bar_drain;
     __shared__ uint64_t full_q[Sh::kSlots], empty_q[Sh::kSlots], full_d[Sh::kSlots],
         empty_d[Sh::kSlots];
-    __shared__ __align__(16) float2 rows[Sh::kSlots][kTileRows];
+    __shared__ __align__(16) float rows[Sh::kSlots][2][kTileRows];  // -lse log2(e), -delta
     __shared__ uint32_t tmem_at;
     __shared__ volatile int dead;
-    __shared__ Place place;
+    __shared__ BwdWork work;
     __shared__ int found;
 
     grid_dep_sync();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
-        Place at{};
-        const bool ok = find_place<true>(p.batch, kTileRows, p.heads_k, blockIdx.x, &at);
-        if (lane == 0) place = at, found = ok, dead = 0;
+        const bool ok = find_work<true>(p, &work);
+        if (lane == 0) found = ok, dead = 0;
     }
     __syncthreads();
     if (!found) return;
-    const bool causal = p.batch.causal;
-    Sequence sq;
-    cut(p.batch.cu_q, place.b, p.batch.tq, &sq.q0, &sq.n);
-    cut(p.batch.cu_k, place.b, p.batch.tk, &sq.k0, &sq.m);
-    const int key0 = place.tile * kTileRows;
-    const int khead = place.head;
-    // the query tiles that see one of these keys, for each head of the group
-    const int q_tiles = (sq.n + kTileRows - 1) / kTileRows;
-    const int q_first =
-        causal ? min(q_tiles, max(0, key0 + sq.n - sq.m) / kTileRows) : 0;
-    const int per_head = q_tiles - q_first, items = per_head * p.group;
+    const int items = work.items;
 
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t at_k = smem, at_v = smem + Sh::kTileBytes;
@@ -169,10 +241,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (warp == kMathWarps) {
         tmem_alloc(smem_u32(&tmem_at), 512);
     } else if (threadIdx.x == 0) {
-        for (uint64_t* b : {&bar_k, &bar_v, &bar_s, &bar_dp, &bar_done, &bar_raw, &bar_drain})
+        for (uint64_t* b : {&bar_k, &bar_v, &bar_s, &bar_done, &bar_raw, &bar_drain})
             mbar_init(smem_u32(b), 1);
         mbar_init(smem_u32(&bar_p), kMathWarps);
-        mbar_init(smem_u32(&bar_ds), kMathWarps);
+        for (int i = 0; i < Sh::kDp; ++i) {
+            mbar_init(smem_u32(&bar_dp[i]), 1);
+            mbar_init(smem_u32(&bar_ds[i]), kMathWarps);
+        }
         for (int i = 0; i < Sh::kSlots; ++i) {
             mbar_init(smem_u32(&full_q[i]), 2);  // the tile, and its rows' lse and delta
             mbar_init(smem_u32(&empty_q[i]), 1);
@@ -184,16 +259,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tmem = tmem_at;
-    const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
+    // all 512 columns are the block's: their addresses start at 0
+    constexpr uint32_t t_s = 0, t_dp = 128, t_dv = t_dp + Sh::kDp * 128, t_dk = t_dv + DP;
 
     if (items > 0 && warp == kMathWarps + 1) {
         // ---- the producer ----
+        const Sequence sq = work.sq;
+        int q_first;
+        const int per_head = queries_of(sq, work.row0, p.batch.causal, &q_first);
         if (elect_one()) {
+            const int64_t key = sq.k0 + work.row0;
             mbar_expect(smem_u32(&bar_k), Sh::kTileBytes);
-            load_tile<Sh::kBlocks>(at_k, &map_k, smem_u32(&bar_k), khead, sq.k0 + key0, p.swap_k);
+            load_tile<Sh::kBlocks>(at_k, &map_k, smem_u32(&bar_k), work.khead, key, p.swap_k);
             mbar_expect(smem_u32(&bar_v), Sh::kTileBytes);
-            load_tile<Sh::kBlocks>(at_v, &map_v, smem_u32(&bar_v), khead, sq.k0 + key0, p.swap_v);
+            load_tile<Sh::kBlocks>(at_v, &map_v, smem_u32(&bar_v), work.khead, key, p.swap_v);
         }
         __syncwarp();
         int i = 0, mends = 0;
@@ -223,7 +302,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             return true;
         };
-        int head = khead * p.group, tile = q_first;
+        int head = work.khead * p.group + work.first / per_head;
+        int tile = q_first + work.first % per_head;
         for (; i < items && ok; ++i) {
             const int slot = i % Sh::kSlots, use = i / Sh::kSlots, i0 = tile * kTileRows;
             if (use > 0) ok = mbar_wait(smem_u32(&empty_q[slot]), (use - 1) & 1, &dead);
@@ -231,18 +311,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const uint32_t full = smem_u32(&full_q[slot]);
             ok = bring(false, at_q + slot * Sh::kTileBytes, full, head, i0);
             if (!ok) break;
-            const float2* src = p.rows + (int64_t)head * p.batch.tq + sq.q0 + i0;
+            const int64_t src = (int64_t)head * p.batch.tq + sq.q0 + i0;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int r = k * 32 + lane;
-                rows[slot][r] = i0 + r < sq.n ? src[r] : make_float2(INFINITY, 0.f);
+                rows[slot][0][r] = i0 + r < sq.n ? p.nlse[src + r] : -INFINITY;
+                rows[slot][1][r] = i0 + r < sq.n ? p.ndelta[src + r] : 0.f;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(full);
             if (use > 0) ok = mbar_wait(smem_u32(&empty_d[slot]), (use - 1) & 1, &dead);
             if (!ok) break;
             ok = bring(true, at_d + slot * Sh::kTileBytes, smem_u32(&full_d[slot]), head, i0);
-            if (++tile == q_tiles) tile = q_first, ++head;
+            if (++tile == q_first + per_head) tile = q_first, ++head;
         }
         if (!ok) {  // gave up: no copy outlives the block
             mbar_drain(smem_u32(&bar_k), 0);
@@ -274,10 +355,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 ok = ok && mbar_wait(smem_u32(&full_d[slot_of(i)]), parity_of(i), &dead);
                 if (!ok) return;
                 tmem_fence_after();
-                product_columns<DP>(t_dp, operand_columns(at_v),
+                const int at = i % Sh::kDp;
+                product_columns<DP>(t_dp + at * 128, operand_columns(at_v),
                                     operand_columns(at_d + slot_of(i) * Sh::kTileBytes), word_dp,
                                     false);
-                mma_commit(smem_u32(&bar_dp));
+                mma_commit(smem_u32(&bar_dp[at]));
             };
             scores(0);
             ok = ok && mbar_wait(smem_u32(&bar_v), 0, &dead);
@@ -291,14 +373,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                              i > 0);
                 mma_commit(smem_u32(&empty_d[slot_of(i)]));
                 if (i + 1 < items) scores(i + 1);
+                if (Sh::kDp == 2 && i + 1 < items) dprobs(i + 1);
                 // while they form P(i + 1): dK, and the next dO V^T
-                ok = ok && mbar_wait(smem_u32(&bar_ds), i & 1, &dead);
+                ok = ok && mbar_wait(smem_u32(&bar_ds[i % Sh::kDp]), (i / Sh::kDp) & 1, &dead);
                 if (!ok) break;
                 tmem_fence_after();
-                product_rows(t_dk, t_dp, 64, operand_rows(at_q + slot_of(i) * Sh::kTileBytes), word_o,
+                product_rows(t_dk, t_dp + i % Sh::kDp * 128, 64, operand_rows(at_q + slot_of(i) * Sh::kTileBytes), word_o,
                              i > 0);
                 mma_commit(smem_u32(&empty_q[slot_of(i)]));
-                if (i + 1 < items) dprobs(i + 1);
+                if (Sh::kDp == 1 && i + 1 < items) dprobs(i + 1);
             }
             if (ok) mma_commit(smem_u32(&bar_done));
             if (!ok) {  // leave no product in flight
@@ -308,20 +391,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
     } else if (warp < kMathWarps) {
         // ---- P and dS: one key a thread, half of the tile's queries ----
-        const int half = warp >> 2, r = (warp & 3) * 32 + lane, key = key0 + r;
+        const int half = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-        const uint32_t s_at = t_s + lanes + half * 64, dp_at = t_dp + lanes + half * 64;
+        const uint32_t s_at = t_s + lanes + half * 64;
         const float sl = p.log2_scale;
+        const int n = work.sq.n;
+        int q_first;
+        const int q_end = queries_of(work.sq, work.row0, p.batch.causal, &q_first) + q_first;
         // the first query that sees this thread's key; the last of the tile's keys' first
-        const int sees = causal ? max(0, key + sq.n - sq.m) : 0;
-        const int all_see = causal ? max(0, key0 + kTileRows - 1 + sq.n - sq.m) : 0;
+        const int ahead = work.row0 + n - work.sq.m;
+        const int sees = p.batch.causal ? max(0, ahead + r) : 0;
+        const int all_see = p.batch.causal ? max(0, ahead + kTileRows - 1) : 0;
         bool ok = true;
-        int tile = q_first;
+        int tile = q_first + (items > 0 ? work.first % (q_end - q_first) : 0);
         for (int i = 0; i < items && ok; ++i) {
             const int slot = i % Sh::kSlots, i0 = tile * kTileRows;
-            if (++tile == q_tiles) tile = q_first;
-            const bool masked = i0 < all_see || i0 + kTileRows > sq.n;
-            const int lo = sees - i0 - half * 64, hi = sq.n - i0 - half * 64;
+            if (++tile == q_end) tile = q_first;
+            const bool masked = i0 < all_see || i0 + kTileRows > n;
+            const int lo = sees - i0 - half * 64, hi = n - i0 - half * 64;
             ok = mbar_wait(smem_u32(&full_q[slot]), (i / Sh::kSlots) & 1, &dead) &&
                  mbar_wait(smem_u32(&bar_s), i & 1, &dead);
             if (!ok) break;
@@ -330,12 +417,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tmem_ld32(reinterpret_cast<uint32_t*>(pr), s_at);
             tmem_ld32(reinterpret_cast<uint32_t*>(pr) + 32, s_at + 32);
             tmem_wait_ld();
-            const float4* rw = reinterpret_cast<const float4*>(rows[slot] + half * 64);
+            const float4* nl = reinterpret_cast<const float4*>(rows[slot][0] + half * 64);
+            const float4* nd = reinterpret_cast<const float4*>(rows[slot][1] + half * 64);
+            const float2 sl2 = make_float2(sl, sl);
 #pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-                const float4 v = rw[c >> 1];
-                pr[c] = ex2_approx(fmaf(pr[c], sl, -v.x));
-                pr[c + 1] = ex2_approx(fmaf(pr[c + 1], sl, -v.z));
+            for (int c = 0; c < 64; c += 4) {
+                const float4 v = nl[c >> 2];
+                const float2 a = __ffma2_rn(make_float2(pr[c], pr[c + 1]), sl2, make_float2(v.x, v.y));
+                const float2 b =
+                    __ffma2_rn(make_float2(pr[c + 2], pr[c + 3]), sl2, make_float2(v.z, v.w));
+                pr[c] = ex2_approx(a.x);
+                pr[c + 1] = ex2_approx(a.y);
+                pr[c + 2] = ex2_approx(b.x);
+                pr[c + 3] = ex2_approx(b.y);
             }
             if (masked) {
 #pragma unroll
@@ -347,7 +441,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tmem_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bar_p));
-            ok = mbar_wait(smem_u32(&bar_dp), i & 1, &dead);
+            const uint32_t dp_at = t_dp + i % Sh::kDp * 128 + lanes + half * 64;
+            ok = mbar_wait(smem_u32(&bar_dp[i % Sh::kDp]), (i / Sh::kDp) & 1, &dead);
             if (!ok) break;
             tmem_fence_after();
             float dp[64];
@@ -355,10 +450,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tmem_ld32(reinterpret_cast<uint32_t*>(dp) + 32, dp_at + 32);
             tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-                const float4 v = rw[c >> 1];
-                dp[c] = pr[c] * (dp[c] - v.y);
-                dp[c + 1] = pr[c + 1] * (dp[c + 1] - v.w);
+            for (int c = 0; c < 64; c += 4) {
+                const float4 v = nd[c >> 2];
+                const float2 a = __fmul2_rn(
+                    make_float2(pr[c], pr[c + 1]),
+                    __fadd2_rn(make_float2(dp[c], dp[c + 1]), make_float2(v.x, v.y)));
+                const float2 b = __fmul2_rn(
+                    make_float2(pr[c + 2], pr[c + 3]),
+                    __fadd2_rn(make_float2(dp[c + 2], dp[c + 3]), make_float2(v.z, v.w)));
+                dp[c] = a.x, dp[c + 1] = a.y, dp[c + 2] = b.x, dp[c + 3] = b.y;
             }
             if (masked) {
 #pragma unroll
@@ -369,15 +469,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tmem_wait_st();
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bar_ds));
+            if (lane == 0) mbar_arrive(smem_u32(&bar_ds[i % Sh::kDp]));
         }
         if (ok && items > 0) ok = mbar_wait(smem_u32(&bar_done), 0, &dead);
         if (ok) {
             tmem_fence_after();
-            const bool valid = key < sq.m, zero = items == 0;
+            const int key = work.row0 + r;
+            const bool valid = key < work.sq.m, split = work.part >= 0;
             const HeadView& g = half ? p.dk : p.dv;
-            store_row<DP>((half ? t_dk : t_dv) + lanes, valid ? g.row(sq.k0 + key, khead) : nullptr,
-                          p.dim, half ? p.scale : 1.f, valid, zero);
+            __nv_bfloat16* out = valid && !split ? g.row(work.sq.k0 + key, work.khead) : nullptr;
+            float* part = valid && split
+                              ? p.parts + (work.part + r + (half ? 0 : part_rows(p.plan))) * DP
+                              : nullptr;
+            store_row<DP>((half ? t_dk : t_dv) + lanes, out, part, p.dim, half ? p.scale : 1.f,
+                          items == 0);
         }
     }
     tmem_fence_before();
@@ -386,7 +491,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (warp == kMathWarps) {
         __syncwarp();
         tmem_fence_after();
-        tmem_free(tmem, 512);
+        tmem_free(tmem_at, 512);
     }
 }
 
@@ -409,31 +514,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         const __grid_constant__ CUtensorMap map_d, const BwdParams p) {
     using Sh = DqShape<DP>;
     extern __shared__ char smem_raw[];
-    __shared__ uint64_t bar_q, bar_d, bar_s[2], bar_dp, bar_ds, bar_done, bar_raw, bar_drain;
+    __shared__ uint64_t bar_q, bar_d, bar_s[2], bar_dp, bar_read, bar_ds[2], bar_done, bar_raw,
+        bar_drain;
     __shared__ uint64_t full_k[Sh::kSlotsK], empty_k[Sh::kSlotsK], full_v[Sh::kSlotsV],
         empty_v[Sh::kSlotsV];
     __shared__ uint32_t tmem_at;
     __shared__ volatile int dead;
-    __shared__ Place place;
+    __shared__ BwdWork work;
     __shared__ int found;
 
     grid_dep_sync();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
-        Place at{};
-        const bool ok = find_place<false>(p.batch, kTileRows, p.heads_q, blockIdx.x, &at);
-        if (lane == 0) place = at, found = ok, dead = 0;
+        const bool ok = find_work<false>(p, &work);
+        if (lane == 0) found = ok, dead = 0;
     }
     __syncthreads();
     if (!found) return;
-    const bool causal = p.batch.causal;
-    Sequence sq;
-    cut(p.batch.cu_q, place.b, p.batch.tq, &sq.q0, &sq.n);
-    cut(p.batch.cu_k, place.b, p.batch.tk, &sq.k0, &sq.m);
-    const int row0 = place.tile * kTileRows;
-    const int head = place.head, khead = head / p.group;
-    const int last = min(sq.n, row0 + kTileRows) - 1;
-    const int tiles = (seen_keys(last, sq.n, sq.m, causal) + kTileRows - 1) / kTileRows;
+    const int tiles = work.items;
 
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t at_q = smem, at_d = smem + Sh::kTileBytes;
@@ -444,7 +542,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (uint64_t* b : {&bar_q, &bar_d, &bar_s[0], &bar_s[1], &bar_dp, &bar_done, &bar_raw,
                             &bar_drain})
             mbar_init(smem_u32(b), 1);
-        mbar_init(smem_u32(&bar_ds), kMathWarps);
+        mbar_init(smem_u32(&bar_ds[0]), kMathWarps);
+        mbar_init(smem_u32(&bar_ds[1]), kMathWarps);
+        mbar_init(smem_u32(&bar_read), kMathWarps);
         for (int i = 0; i < Sh::kSlotsK; ++i) {
             mbar_init(smem_u32(&full_k[i]), 1);
             mbar_init(smem_u32(&empty_k[i]), 1);
@@ -458,16 +558,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tmem = tmem_at;
-    const uint32_t t_dp = tmem + 256, t_dq = tmem + 384;
+    // all 512 columns are the block's: their addresses start at 0
+    constexpr uint32_t tmem = 0, t_dp = 256, t_dq = 384;
 
     if (tiles > 0 && warp == kMathWarps + 1) {
         // ---- the producer ----
+        const int khead = work.khead, left = work.sq.m - work.first * kTileRows;
+        const int64_t k0 = work.sq.k0 + (int64_t)work.first * kTileRows;
+        const bool tail = work.sq.k0 + work.sq.m < p.batch.tk;
         if (elect_one()) {
+            const int64_t q = work.sq.q0 + work.row0;
             mbar_expect(smem_u32(&bar_q), Sh::kTileBytes);
-            load_tile<Sh::kBlocks>(at_q, &map_q, smem_u32(&bar_q), head, sq.q0 + row0, p.swap_q);
+            load_tile<Sh::kBlocks>(at_q, &map_q, smem_u32(&bar_q), work.head, q, p.swap_q);
             mbar_expect(smem_u32(&bar_d), Sh::kTileBytes);
-            load_tile<Sh::kBlocks>(at_d, &map_d, smem_u32(&bar_d), head, sq.q0 + row0, p.swap_d);
+            load_tile<Sh::kBlocks>(at_d, &map_d, smem_u32(&bar_d), work.head, q, p.swap_d);
         }
         __syncwarp();
         int j = 0;
@@ -475,11 +579,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (; j < tiles && ok; ++j) {
             const int sk = j % Sh::kSlotsK, uk = j / Sh::kSlotsK;
             const int sv = j % Sh::kSlotsV, uv = j / Sh::kSlotsV;
-            const int64_t token = sq.k0 + (int64_t)j * kTileRows;
+            const int64_t token = k0 + (int64_t)j * kTileRows;
             if (uk > 0) ok = mbar_wait(smem_u32(&empty_k[sk]), (uk - 1) & 1, &dead);
             if (!ok) break;
-            const int valid = sq.m - j * kTileRows;
-            const bool mend = valid < kTileRows && sq.k0 + sq.m < p.batch.tk;
+            const int valid = left - j * kTileRows;
+            const bool mend = valid < kTileRows && tail;
             const uint32_t full = smem_u32(&full_k[sk]), dst = at_k + sk * Sh::kTileBytes;
             const uint32_t bar = mend ? smem_u32(&bar_raw) : full;
             if (elect_one()) {
@@ -547,13 +651,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             dprobs(0);
             if (tiles > 1) scores(1);
             for (int j = 0; j < tiles && ok; ++j) {
-                ok = mbar_wait(smem_u32(&bar_ds), j & 1, &dead);
+                // the next dO V^T as soon as this one is read, while dS(j) is formed from it
+                if (j + 1 < tiles) {
+                    ok = mbar_wait(smem_u32(&bar_read), j & 1, &dead);
+                    dprobs(j + 1);
+                }
+                // dS(j) comes over S(j); two barriers, since dS(j + 1) may follow at once
+                ok = ok && mbar_wait(smem_u32(&bar_ds[j & 1]), (j >> 1) & 1, &dead);
                 if (!ok) break;
-                // dS(j) lies over S(j), and dP(j) is read: the next dO V^T first, which the
-                // other warps wait for
                 tmem_fence_after();
-                if (j + 1 < tiles) dprobs(j + 1);
-                if (!ok) break;
                 const int sk = j % Sh::kSlotsK;
                 product_rows(t_dq, tmem + (j & 1) * 128, 64,
                              operand_rows(at_k + sk * Sh::kTileBytes), word_o, j > 0);
@@ -568,14 +674,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
     } else if (warp < kMathWarps) {
         // ---- dS: one query a thread, half of the tile's keys ----
-        const int half = warp >> 2, r = (warp & 3) * 32 + lane, i = row0 + r;
+        const int half = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const uint32_t dp_at = t_dp + lanes + half * 64;
         const float sl = p.log2_scale;
-        const int limit = seen_keys(i, sq.n, sq.m, causal);
-        const int first_limit = seen_keys(row0 + (warp & 3) * 32, sq.n, sq.m, causal);
-        float2 row = make_float2(INFINITY, 0.f);
-        if (i < sq.n) row = p.rows[(int64_t)head * p.batch.tq + sq.q0 + i];
+        // keys of this piece that the thread's row sees, and the warp's first row
+        const auto limit_of = [&](int row) {
+            return seen_keys(work.row0 + row, work.sq.n, work.sq.m, p.batch.causal) -
+                   work.first * kTileRows;
+        };
+        const int limit = limit_of(r), first_limit = limit_of((warp & 3) * 32);
+        float nl = -INFINITY, nd = 0.f;
+        if (work.row0 + r < work.sq.n) {
+            const int64_t at = (int64_t)work.head * p.batch.tq + work.sq.q0 + work.row0 + r;
+            nl = p.nlse[at];
+            nd = p.ndelta[at];
+        }
+        const float2 sl2 = make_float2(sl, sl), nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
         bool ok = true;
         for (int j = 0; j < tiles && ok; ++j) {
             const uint32_t s_at = tmem + (j & 1) * 128 + lanes + half * 64;
@@ -587,7 +702,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tmem_ld32(reinterpret_cast<uint32_t*>(pr) + 32, s_at + 32);
             tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 64; ++c) pr[c] = ex2_approx(fmaf(pr[c], sl, -row.x));
+            for (int c = 0; c < 64; c += 2) {
+                const float2 a = __ffma2_rn(make_float2(pr[c], pr[c + 1]), sl2, nl2);
+                pr[c] = ex2_approx(a.x);
+                pr[c + 1] = ex2_approx(a.y);
+            }
             ok = mbar_wait(smem_u32(&bar_dp), j & 1, &dead);
             if (!ok) break;
             tmem_fence_after();
@@ -595,8 +714,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tmem_ld32(reinterpret_cast<uint32_t*>(dp), dp_at);
             tmem_ld32(reinterpret_cast<uint32_t*>(dp) + 32, dp_at + 32);
             tmem_wait_ld();
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar_read));
 #pragma unroll
-            for (int c = 0; c < 64; ++c) dp[c] = pr[c] * (dp[c] - row.y);
+            for (int c = 0; c < 64; c += 2) {
+                const float2 a = __fmul2_rn(make_float2(pr[c], pr[c + 1]),
+                                            __fadd2_rn(make_float2(dp[c], dp[c + 1]), nd2));
+                dp[c] = a.x;
+                dp[c + 1] = a.y;
+            }
             if ((j + 1) * kTileRows > first_limit) {
                 const int left = limit - j * kTileRows - half * 64;
 #pragma unroll
@@ -607,17 +734,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tmem_wait_st();
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bar_ds));
+            if (lane == 0) mbar_arrive(smem_u32(&bar_ds[j & 1]));
         }
         if (ok && tiles > 0) ok = mbar_wait(smem_u32(&bar_done), 0, &dead);
         if (ok) {
             tmem_fence_after();
-            const bool valid = i < sq.n, zero = tiles == 0;
+            const int i = work.row0 + r;
+            const bool valid = i < work.sq.n, split = work.part >= 0;
             // each half of the warps writes half of the columns
             const int c0 = half * (DP / 2);
-            store_row<DP / 2>(t_dq + lanes + c0,
-                              valid ? p.dq.row(sq.q0 + i, head) + c0 : nullptr, p.dim - c0, p.scale,
-                              valid, zero);
+            __nv_bfloat16* out =
+                valid && !split ? p.dq.row(work.sq.q0 + i, work.head) + c0 : nullptr;
+            float* part = valid && split ? p.parts + (work.part + r) * DP + c0 : nullptr;
+            store_row<DP / 2>(t_dq + lanes + c0, out, part, p.dim - c0, p.scale, tiles == 0);
         }
     }
     tmem_fence_before();
@@ -626,35 +755,143 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (warp == kMathWarps) {
         __syncwarp();
         tmem_fence_after();
-        tmem_free(tmem, 512);
+        tmem_free(tmem_at, 512);
     }
+}
+
+// The sum of a cut block's pieces, in their order, times the scale, in bfloat16.  DP / 4
+// lanes a row; blockIdx.z = 1: dV.
+constexpr int kSumThreads = 256;
+
+template <int DP, bool kKeys>
+__global__ void __launch_bounds__(kSumThreads) attention_sum_kernel(const BwdParams p) {
+    __shared__ Place place;
+    __shared__ int found;
+    grid_dep_sync();
+    if (threadIdx.x < 32) {
+        Place at{};
+        const bool ok = find_place<kKeys>(p.batch, kTileRows, kKeys ? p.heads_k : p.heads_q,
+                                          (int)(p.plan.whole + blockIdx.x), &at);
+        if (threadIdx.x == 0) place = at, found = ok;
+    }
+    __syncthreads();
+    if (!found) return;
+    Sequence sq;
+    cut(p.batch.cu_q, place.b, p.batch.tq, &sq.q0, &sq.n);
+    cut(p.batch.cu_k, place.b, p.batch.tk, &sq.k0, &sq.m);
+    const int row0 = place.tile * kTileRows;
+    int unused;
+    const int items = kKeys ? queries_of(sq, row0, p.batch.causal, &unused) * p.group
+                            : keys_of(sq, row0, p.batch.causal);
+    // a piece without work was not begun
+    const int pieces = max(1, (items + p.plan.chunk - 1) / p.plan.chunk);
+    constexpr int kLanes = DP / 4, kRows = kSumThreads / kLanes;
+    const int lane = threadIdx.x % kLanes;
+    const int rows = min(kTileRows, (kKeys ? sq.m : sq.n) - row0);
+    const bool of_v = kKeys && blockIdx.z == 1;
+    const float4* parts = reinterpret_cast<const float4*>(p.parts + (of_v ? part_rows(p.plan) : 0) * DP);
+    const HeadView& g = kKeys ? (of_v ? p.dv : p.dk) : p.dq;
+    const float f = of_v ? 1.f : p.scale;
+    const int64_t step = p.plan.rest * p.plan.slot_rows;  // rows from a piece to the next
+    for (int r = blockIdx.y * kRows + threadIdx.x / kLanes; r < rows; r += gridDim.y * kRows) {
+        const int64_t at = (int64_t)blockIdx.x * p.plan.slot_rows + r;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int z = 0; z < pieces; ++z) {
+            const float4 v = parts[(z * step + at) * kLanes + lane];
+            o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+        }
+        if (lane * 4 < p.dim)
+            *reinterpret_cast<uint2*>(g.row((kKeys ? sq.k0 : sq.q0) + row0 + r, place.head) +
+                                      lane * 4) =
+                make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
+    }
+}
+
+// Cuts the last wave, or all blocks where they are fewer than the SMs, where a model of the
+// waves says that it pays, in units of one tile's time: a block costs its tiles and kStart,
+// the sum kSum; less than kGain of the whole is not worth it.  `items`: tiles that the longest
+// block may meet.  With the mask or several sequences the short blocks come last, and only
+// few blocks are cut.
+constexpr int kStart = 4, kSum = 4, kMaxPieces = 16, kLeastChunk = 2;
+constexpr double kGain = 0.05;
+
+BwdPlan plan_bwd(int64_t blocks, int64_t items, int64_t tokens, bool uniform) {
+    BwdPlan plan{};
+    plan.whole = blocks;
+    plan.pieces = 1;
+    plan.slot_rows = (int)(tokens < kTileRows ? tokens : kTileRows);
+    if (!uniform && blocks >= kSms) return plan;
+    const auto waves = [](int64_t n) { return (n + kSms - 1) / kSms; };
+    const int64_t whole = blocks / kSms * kSms, rest = blocks - whole;
+    if (rest == 0) return plan;
+    double best = (1.0 - kGain) * (double)(waves(blocks) * (items + kStart));
+    for (int cuts = 2; cuts <= kMaxPieces; ++cuts) {
+        const int64_t chunk = (items + cuts - 1) / cuts, pieces = (items + chunk - 1) / chunk;
+        if (chunk < kLeastChunk || rest * pieces > 4 * kSms) break;
+        const double cost = (double)(whole / kSms * (items + kStart) +
+                                     waves(rest * pieces) * (chunk + kStart) + kSum);
+        if (cost < best) {
+            best = cost;
+            plan.whole = whole;
+            plan.rest = rest;
+            plan.chunk = (int)chunk;
+            plan.pieces = (int)pieces;
+        }
+    }
+    return plan;
+}
+
+int64_t tiles_of(int64_t tokens) { return (tokens + kTileRows - 1) / kTileRows; }
+
+BwdPlan plan_dkv(int64_t tq, int64_t tk, int batch, int heads_q, int heads_k, bool causal) {
+    return plan_bwd(tiles_at_most(tk, kTileRows, batch) * heads_k,
+                    tiles_of(tq) * (heads_q / heads_k), tk, batch == 1 && !causal);
+}
+BwdPlan plan_dq(int64_t tq, int64_t tk, int batch, int heads_q, bool causal) {
+    return plan_bwd(tiles_at_most(tq, kTileRows, batch) * heads_q, tiles_of(tk), tq,
+                    batch == 1 && !causal);
 }
 
 struct BwdMaps {
     CUtensorMap q, k, v, d;
 };
 
+template <int DP, bool kKeys>
+cudaError_t launch_sum(const BwdParams& p, cudaStream_t st) {
+    if (p.plan.pieces == 1) return cudaSuccess;
+    const unsigned rows = kSumThreads / (DP / 4);
+    const dim3 grid((unsigned)p.plan.rest, (p.plan.slot_rows + 2 * rows - 1) / (2 * rows),
+                    kKeys ? 2 : 1);
+    return launch(attention_sum_kernel<DP, kKeys>, grid, dim3(kSumThreads), 0, st, p);
+}
+
 template <int DP>
-cudaError_t launch_dim(const BwdMaps& m, const BwdParams& p, cudaStream_t st) {
-    const auto blocks = [&](int64_t tokens, int heads) {
-        return dim3((unsigned)(tiles_at_most(tokens, kTileRows, p.batch.batch) * heads));
-    };
+cudaError_t launch_dim(const BwdMaps& m, BwdParams p, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
+    const auto blocks = [&] {
+        return dim3((unsigned)(p.plan.whole + p.plan.rest * p.plan.pieces));
+    };
     if (p.batch.tk > 0) {
+        p.plan = plan_dkv(p.batch.tq, p.batch.tk, p.batch.batch, p.heads_q, p.heads_k,
+                          p.batch.causal);
         e = cudaFuncSetAttribute(attention_dkv_kernel<DP>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)DkvShape<DP>::kSmem);
         if (e == cudaSuccess)
-            e = launch(attention_dkv_kernel<DP>, blocks(p.batch.tk, p.heads_k),
-                       dim3(kBwdThreads), DkvShape<DP>::kSmem, st, m.q, m.k, m.v, m.d, p);
+            e = launch(attention_dkv_kernel<DP>, blocks(), dim3(kBwdThreads), DkvShape<DP>::kSmem,
+                       st, m.q, m.k, m.v, m.d, p);
+        if (e == cudaSuccess) e = launch_sum<DP, true>(p, st);
     }
     if (e == cudaSuccess && p.batch.tq > 0) {
+        p.plan = plan_dq(p.batch.tq, p.batch.tk, p.batch.batch, p.heads_q, p.batch.causal);
         e = cudaFuncSetAttribute(attention_dq_kernel<DP>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)DqShape<DP>::kSmem);
         if (e == cudaSuccess)
-            e = launch(attention_dq_kernel<DP>, blocks(p.batch.tq, p.heads_q),
-                       dim3(kBwdThreads), DqShape<DP>::kSmem, st, m.q, m.k, m.v, m.d, p);
+            e = launch(attention_dq_kernel<DP>, blocks(), dim3(kBwdThreads), DqShape<DP>::kSmem, st,
+                       m.q, m.k, m.v, m.d, p);
+        if (e == cudaSuccess) e = launch_sum<DP, false>(p, st);
     }
     return e;
 }
@@ -664,6 +901,20 @@ HeadView view(const gs_heads& h) {
 }
 
 }  // namespace
+
+// (-lse, -delta) of every query row, then the pieces of one kernel
+size_t attention_bwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads_q,
+                                     int heads_k, int head_dim) {
+    int64_t rows = 0;
+    for (const bool causal : {false, true}) {
+        const int64_t a =
+            2 * part_rows(plan_dkv(tokens_q, tokens_k, batch, heads_q, heads_k, causal));
+        const int64_t b = part_rows(plan_dq(tokens_q, tokens_k, batch, heads_q, causal));
+        rows = std::max(rows, std::max(a, b));
+    }
+    return ((size_t)tokens_q * heads_q * 2 * sizeof(float) + 255) / 256 * 256 +
+           (size_t)rows * (head_dim <= 64 ? 64 : 128) * sizeof(float);
+}
 
 cudaError_t launch_attention_bwd(const gs_attention_shape& s, const gs_heads& q, const gs_heads& k,
                                  const gs_heads& v, const gs_heads& out, const float* lse,
@@ -685,7 +936,9 @@ cudaError_t launch_attention_bwd(const gs_attention_shape& s, const gs_heads& q,
     p.dk = view(dk);
     p.dv = view(dv);
     p.lse = lse;
-    p.rows = static_cast<float2*>(ws);
+    p.nlse = static_cast<float*>(ws);
+    p.ndelta = p.nlse + s.tokens_q * s.heads_q;
+    p.parts = p.nlse + (s.tokens_q * s.heads_q * 2 + 63) / 64 * 64;
     cudaError_t e = gave_up_word(&p.gave_up);
     if (e != cudaSuccess) return e;
     BwdMaps m;

@@ -43,6 +43,8 @@ cudaError_t launch_attention_fwd(const gs_attention_shape& s, const gs_heads& q,
                                  const gs_heads& v, const gs_heads& out, float* lse,
                                  const int32_t* cu_q, const int32_t* cu_k, void* ws,
                                  cudaStream_t st);
+size_t attention_bwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads_q,
+                                     int heads_k, int head_dim);
 cudaError_t launch_attention_bwd(const gs_attention_shape& s, const gs_heads& q, const gs_heads& k,
                                  const gs_heads& v, const gs_heads& out, const float* lse,
                                  const gs_heads& dout, const gs_heads& dq, const gs_heads& dk,
