@@ -67,6 +67,7 @@ struct BwdParams {
     float *nlse, *ndelta;  // [heads][tokens]: -lse log2(e) (-infinity: saw no key), -delta
     unsigned int* gave_up;
     BwdPlan plan;  // of the kernel at hand
+    bool after_dkv;  // dQ's kernel follows dK and dV's
     float* parts;  // [pieces][rest][slot_rows][DP], for dK, then for dV; or for dQ
 };
 
@@ -523,14 +524,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     __shared__ BwdWork work;
     __shared__ int found;
 
-    grid_dep_sync();
+    // No wait for the kernel before it, dK and dV's, of which it needs nothing: its blocks fill
+    // that one's last wave.  It starts once every block of that kernel has, and thus after the
+    // rows' sums that both read; it waits for it at the end, so that what follows this kernel
+    // on the stream follows both.
+    if (!p.after_dkv) grid_dep_wait();
+    grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
         const bool ok = find_work<false>(p, &work);
         if (lane == 0) found = ok, dead = 0;
     }
     __syncthreads();
-    if (!found) return;
+    if (!found) {
+        if (p.after_dkv) grid_dep_wait();
+        return;
+    }
     const int tiles = work.items;
 
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -757,6 +766,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tmem_fence_after();
         tmem_free(tmem_at, 512);
     }
+    if (p.after_dkv) grid_dep_wait();
 }
 
 // The sum of a cut block's pieces, in their order, times the scale, in bfloat16.  DP / 4
@@ -868,31 +878,34 @@ cudaError_t launch_sum(const BwdParams& p, cudaStream_t st) {
 
 template <int DP>
 cudaError_t launch_dim(const BwdMaps& m, BwdParams p, cudaStream_t st) {
+    const Batch& v = p.batch;
     cudaError_t e = cudaSuccess;
-    const auto blocks = [&] {
-        return dim3((unsigned)(p.plan.whole + p.plan.rest * p.plan.pieces));
+    const auto blocks = [](const BwdPlan& plan) {
+        return dim3((unsigned)(plan.whole + plan.rest * plan.pieces));
     };
-    if (p.batch.tk > 0) {
-        p.plan = plan_dkv(p.batch.tq, p.batch.tk, p.batch.batch, p.heads_q, p.heads_k,
-                          p.batch.causal);
+    BwdParams of_q = p;
+    p.plan = plan_dkv(v.tq, v.tk, v.batch, p.heads_q, p.heads_k, v.causal);
+    of_q.plan = plan_dq(v.tq, v.tk, v.batch, p.heads_q, v.causal);
+    of_q.parts = p.parts + 2 * part_rows(p.plan) * DP;
+    of_q.after_dkv = v.tk > 0;
+    if (v.tk > 0) {
         e = cudaFuncSetAttribute(attention_dkv_kernel<DP>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)DkvShape<DP>::kSmem);
         if (e == cudaSuccess)
-            e = launch(attention_dkv_kernel<DP>, blocks(), dim3(kBwdThreads), DkvShape<DP>::kSmem,
-                       st, m.q, m.k, m.v, m.d, p);
-        if (e == cudaSuccess) e = launch_sum<DP, true>(p, st);
+            e = launch(attention_dkv_kernel<DP>, blocks(p.plan), dim3(kBwdThreads),
+                       DkvShape<DP>::kSmem, st, m.q, m.k, m.v, m.d, p);
     }
-    if (e == cudaSuccess && p.batch.tq > 0) {
-        p.plan = plan_dq(p.batch.tq, p.batch.tk, p.batch.batch, p.heads_q, p.batch.causal);
+    if (e == cudaSuccess && v.tq > 0) {
         e = cudaFuncSetAttribute(attention_dq_kernel<DP>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)DqShape<DP>::kSmem);
         if (e == cudaSuccess)
-            e = launch(attention_dq_kernel<DP>, blocks(), dim3(kBwdThreads), DqShape<DP>::kSmem, st,
-                       m.q, m.k, m.v, m.d, p);
-        if (e == cudaSuccess) e = launch_sum<DP, false>(p, st);
+            e = launch(attention_dq_kernel<DP>, blocks(of_q.plan), dim3(kBwdThreads),
+                       DqShape<DP>::kSmem, st, m.q, m.k, m.v, m.d, of_q);
     }
+    if (e == cudaSuccess && v.tk > 0) e = launch_sum<DP, true>(p, st);
+    if (e == cudaSuccess && v.tq > 0) e = launch_sum<DP, false>(of_q, st);
     return e;
 }
 
@@ -902,7 +915,7 @@ HeadView view(const gs_heads& h) {
 
 }  // namespace
 
-// (-lse, -delta) of every query row, then the pieces of one kernel
+// -lse and -delta of every query row, then the pieces of both kernels
 size_t attention_bwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads_q,
                                      int heads_k, int head_dim) {
     int64_t rows = 0;
@@ -910,7 +923,7 @@ size_t attention_bwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int bat
         const int64_t a =
             2 * part_rows(plan_dkv(tokens_q, tokens_k, batch, heads_q, heads_k, causal));
         const int64_t b = part_rows(plan_dq(tokens_q, tokens_k, batch, heads_q, causal));
-        rows = std::max(rows, std::max(a, b));
+        rows = std::max(rows, a + b);
     }
     return ((size_t)tokens_q * heads_q * 2 * sizeof(float) + 255) / 256 * 256 +
            (size_t)rows * (head_dim <= 64 ? 64 : 128) * sizeof(float);
