@@ -35,7 +35,7 @@ __all__ = [
     "gs_bin_sort_workspace_bytes", "gs_raster_workspace_bytes", "gs_bin_sort_noalloc",
     "gs_raster_stats", "gs_default_settings", "gs_status_string", "gs_num_tiles",
     "gs_qk_norm_rope", "gs_qk_norm_rope_bwd", "gs_qk_norm_rope_workspace_bytes",
-    "gs_attention_fwd", "gs_attention_bwd", "gs_attention_workspace_bytes",
+    "gs_attention_fwd", "gs_attention_bwd", "gs_attention_workspace_bytes", "gs_attention_status",
     "gs_dropout_add", "gs_dropout_add_bwd",
     "Camera", "Settings", "Rasterizer", "library",
     "GSError", "TILE", "GRAD2D", "SPLAT_FLOATS",
@@ -203,6 +203,8 @@ def _declare(lib: C.CDLL) -> None:
     lib.gs_attention_fwd.argtypes = [A, H, H, H, _P, _P, H, _P, _P, C.c_size_t, _P]
     lib.gs_attention_bwd.restype = st
     lib.gs_attention_bwd.argtypes = [A, H, H, H, _P, _P, H, _P, H, H, H, H, _P, C.c_size_t, _P]
+    lib.gs_attention_status.restype = st
+    lib.gs_attention_status.argtypes = [_P]
     lib.gs_dropout_add.restype = st
     lib.gs_dropout_add.argtypes = [_I64, i32, _P, _P, _P, _P, C.c_float, _P]
     lib.gs_dropout_add_bwd.restype = st
@@ -244,11 +246,26 @@ def _ptr(t, name, dtype=None, numel=None, optional=False):
     return t.data_ptr() if t.numel() > 0 else None
 
 
-def _stream(stream):
-    if stream is None:
+_torch = None  # the module, once a call has needed it
+
+
+def _load_torch():
+    global _torch
+    if _torch is None:
         import torch
 
-        return torch.cuda.current_stream().cuda_stream
+        _torch = torch
+    return _torch
+
+
+def _stream(stream):
+    if stream is None:
+        torch = _torch or _load_torch()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            return torch.cuda.current_stream().cuda_stream
+        # the same handle without building a Stream object (0.2 instead of 3 us)
+        return raw(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -500,54 +517,67 @@ def gs_loss_l1_ssim(width, height, image, target, dL_dimage, loss_out, workspace
 # ---------------------------------------------------------------------------
 # token operators
 # ---------------------------------------------------------------------------
-def _heads(t, name, tokens=None, heads=None, dim=None, dtype=None) -> Heads:
+def _heads(t, name, shape=None, dtype=None) -> Heads:
     """A CUDA tensor [tokens, heads, head_dim], contiguous in its last dimension, as gs_heads."""
-    import torch
-
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, (_torch or _load_torch()).Tensor):
         raise TypeError(f"{name}: expected a torch tensor")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name}: expected [tokens, heads, head_dim], got {tuple(t.shape)}")
-    want = (t.shape[0] if tokens is None else tokens, t.shape[1] if heads is None else heads,
-            t.shape[2] if dim is None else dim)
-    if tuple(t.shape) != want:
-        raise ValueError(f"{name}: expected shape {want}, got {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
+    own = t.shape
+    if len(own) != 3:
+        raise ValueError(f"{name}: expected [tokens, heads, head_dim], got {tuple(own)}")
+    if shape is not None and own != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(own)}")
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.numel() > 0 and t.shape[2] > 1 and t.stride(2) != 1:
+    token, head, last = t.stride()
+    if last != 1 and own[2] > 1 and own[0] > 0 and own[1] > 0:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return Heads(t.data_ptr() if t.numel() > 0 else None, t.stride(0), t.stride(1))
+    return Heads(t.data_ptr() or None, token, head)
+
+
+def _flat(t, name, dtype, numel, optional=False):
+    """Address of a contiguous CUDA tensor of at least numel elements (None: left out)."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is required")
+    if not isinstance(t, _torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if not t.is_cuda or t.dtype is not dtype or not t.is_contiguous() or t.numel() < numel:
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor of at least {numel} x {dtype}, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr() or None
 
 
 def _element_type(t, name) -> int:
-    import torch
-
-    types = {torch.float32: 0, torch.bfloat16: 1}
-    if not isinstance(t, torch.Tensor) or t.dtype not in types:
-        raise ValueError(f"{name}: expected a float32 or bfloat16 tensor")
-    return types[t.dtype]
+    torch = _torch or _load_torch()
+    dtype = t.dtype if isinstance(t, torch.Tensor) else None
+    if dtype is torch.bfloat16:
+        return 1
+    if dtype is torch.float32:
+        return 0
+    raise ValueError(f"{name}: expected a float32 or bfloat16 tensor")
 
 
 def _norm_args(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved):
-    import torch
-
+    kind = _element_type(q, "q")
     qh = _heads(q, "q")
     T, hq, D = q.shape
-    kh = _heads(k, "k", tokens=T, dim=D, dtype=q.dtype)
-    rows, rot = (0, 0)
+    kh = _heads(k, "k", None, q.dtype)
+    Tk, hk, Dk = k.shape
+    if Tk != T or Dk != D:
+        raise ValueError(f"k: expected {T} tokens of {D} values a head, got {tuple(k.shape)}")
+    rows = rot = 0
     if cos_sin is not None:
-        if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
+        if not isinstance(cos_sin, _torch.Tensor) or cos_sin.dim() != 2:
             raise ValueError("cos_sin: expected a [rows, rot] tensor")
         rows, rot = cos_sin.shape
-    norm = HeadNorm(_element_type(q, "q"), rot, int(bool(interleaved)), float(eps), rows)
-    f = torch.float32
-    return (T, hq, k.shape[1], D), norm, qh, kh, (
-        _ptr(q_weight, "q_weight", f, D, optional=True),
-        _ptr(k_weight, "k_weight", f, D, optional=True),
-        _ptr(cos_sin, "cos_sin", f, rows * rot, optional=True),
-        _ptr(positions, "positions", torch.int32, T, optional=True))
+    f = _torch.float32
+    return (T, hq, hk, D), HeadNorm(kind, rot, 1 if interleaved else 0, eps, rows), qh, kh, (
+        _flat(q_weight, "q_weight", f, D, True), _flat(k_weight, "k_weight", f, D, True),
+        _flat(cos_sin, "cos_sin", f, 0, True),
+        _flat(positions, "positions", _torch.int32, T, True))
 
 
 def gs_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out, eps=1e-6,
@@ -556,13 +586,13 @@ def gs_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out, 
     q, k, q_out, k_out: [tokens, heads, head_dim] float32 or bfloat16, any strides with a
     contiguous last dimension; cos_sin [rows, rot] float32 (None: no rotation); weights and
     positions may be None."""
-    (T, hq, hk, D), norm, qh, kh, ptrs = _norm_args(q, k, q_weight, k_weight, cos_sin, positions,
-                                                    eps, interleaved)
-    st = library().gs_qk_norm_rope(
-        T, hq, hk, D, C.byref(norm), C.byref(qh), C.byref(kh), *ptrs,
-        C.byref(_heads(q_out, "q_out", T, hq, D, q.dtype)),
-        C.byref(_heads(k_out, "k_out", T, hk, D, q.dtype)), _stream(stream))
-    _check("gs_qk_norm_rope", st)
+    sizes, norm, qh, kh, ptrs = _norm_args(q, k, q_weight, k_weight, cos_sin, positions, eps,
+                                           interleaved)
+    dtype = q.dtype
+    st = library().gs_qk_norm_rope(*sizes, norm, qh, kh, *ptrs, _heads(q_out, "q_out", q.shape, dtype),
+                                   _heads(k_out, "k_out", k.shape, dtype), _stream(stream))
+    if st:
+        _check("gs_qk_norm_rope", st)
 
 
 def gs_qk_norm_rope_workspace_bytes(tokens, heads_q, heads_k, head_dim) -> int:
@@ -574,20 +604,17 @@ def gs_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk
                         dq_weight, dk_weight, workspace, eps=1e-6, interleaved=False, stream=None):
     """Gradient of gs_qk_norm_rope (see gs.h); dq_weight and dk_weight (float32 [head_dim]) may
     be None."""
-    import torch
-
-    (T, hq, hk, D), norm, qh, kh, ptrs = _norm_args(q, k, q_weight, k_weight, cos_sin, positions,
-                                                    eps, interleaved)
-    f = torch.float32
+    sizes, norm, qh, kh, ptrs = _norm_args(q, k, q_weight, k_weight, cos_sin, positions, eps,
+                                           interleaved)
+    f, dtype, of_q, of_k = _torch.float32, q.dtype, q.shape, k.shape
     st = library().gs_qk_norm_rope_bwd(
-        T, hq, hk, D, C.byref(norm), C.byref(qh), C.byref(kh), *ptrs,
-        C.byref(_heads(dq_out, "dq_out", T, hq, D, q.dtype)),
-        C.byref(_heads(dk_out, "dk_out", T, hk, D, q.dtype)),
-        C.byref(_heads(dq, "dq", T, hq, D, q.dtype)), C.byref(_heads(dk, "dk", T, hk, D, q.dtype)),
-        _ptr(dq_weight, "dq_weight", f, D, optional=True),
-        _ptr(dk_weight, "dk_weight", f, D, optional=True),
-        _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
-    _check("gs_qk_norm_rope_bwd", st)
+        *sizes, norm, qh, kh, *ptrs, _heads(dq_out, "dq_out", of_q, dtype),
+        _heads(dk_out, "dk_out", of_k, dtype), _heads(dq, "dq", of_q, dtype),
+        _heads(dk, "dk", of_k, dtype), _flat(dq_weight, "dq_weight", f, sizes[3], True),
+        _flat(dk_weight, "dk_weight", f, sizes[3], True),
+        _flat(workspace, "workspace", _torch.uint8, 0), workspace.numel(), _stream(stream))
+    if st:
+        _check("gs_qk_norm_rope_bwd", st)
 
 
 def gs_attention_workspace_bytes(tokens_q, tokens_k, batch, heads_q, heads_k, head_dim) -> int:
@@ -597,26 +624,24 @@ def gs_attention_workspace_bytes(tokens_q, tokens_k, batch, heads_q, heads_k, he
 
 
 def _attention_args(q, k, v, cu_q, cu_k, causal, scale):
-    import torch
-
-    bf = torch.bfloat16
-    qh = _heads(q, "q", dtype=bf)
+    bf = (_torch or _load_torch()).bfloat16
+    qh, kh = _heads(q, "q", None, bf), _heads(k, "k", None, bf)
+    vh = _heads(v, "v", k.shape, bf)
     Tq, hq, D = q.shape
-    kh = _heads(k, "k", dim=D, dtype=bf)
-    Tk, hk = k.shape[:2]
-    vh = _heads(v, "v", Tk, hk, D, bf)
-    if (cu_q is None) != (cu_k is None):
-        raise ValueError("cu_q and cu_k: give both or neither")
-    batch = 1
-    if cu_q is not None:
+    Tk, hk, Dk = k.shape
+    if Dk != D:
+        raise ValueError(f"k: expected {D} values a head, got {tuple(k.shape)}")
+    batch, cu = 1, (None, None)
+    if cu_q is not None or cu_k is not None:
+        if cu_q is None or cu_k is None:
+            raise ValueError("cu_q and cu_k: give both or neither")
         batch = cu_q.numel() - 1
         if batch < 1 or cu_k.numel() != batch + 1:
             raise ValueError("cu_q and cu_k: expected batch + 1 offsets each")
-    shape = AttentionShape(Tq, Tk, batch, hq, hk, D, int(bool(causal)),
-                           float(D ** -0.5 if scale is None else scale))
-    cu = (_ptr(cu_q, "cu_q", torch.int32, optional=True),
-          _ptr(cu_k, "cu_k", torch.int32, optional=True))
-    return shape, (C.byref(qh), C.byref(kh), C.byref(vh)), cu
+        i = _torch.int32
+        cu = (_flat(cu_q, "cu_q", i, 0), _flat(cu_k, "cu_k", i, 0))
+    return AttentionShape(Tq, Tk, batch, hq, hk, D, 1 if causal else 0,
+                          D ** -0.5 if scale is None else scale), (qh, kh, vh), cu
 
 
 def gs_attention_fwd(q, k, v, out, lse, workspace, cu_q=None, cu_k=None, causal=False, scale=None,
@@ -625,55 +650,55 @@ def gs_attention_fwd(q, k, v, out, lse, workspace, cu_q=None, cu_k=None, causal=
     k, v [tokens_k, heads_k, head_dim] bfloat16, any strides with a contiguous last dimension;
     lse [heads_q, tokens_q] float32; cu_q, cu_k [batch + 1] int32 offsets (None: one sequence);
     scale defaults to head_dim ** -0.5."""
-    import torch
-
     shape, heads, cu = _attention_args(q, k, v, cu_q, cu_k, causal, scale)
-    n = shape.tokens_q * shape.heads_q
     st = library().gs_attention_fwd(
-        C.byref(shape), *heads, *cu,
-        C.byref(_heads(out, "out", *q.shape, torch.bfloat16)), _ptr(lse, "lse", torch.float32, n),
-        _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
-    _check("gs_attention_fwd", st)
+        shape, *heads, *cu, _heads(out, "out", q.shape, _torch.bfloat16),
+        _flat(lse, "lse", _torch.float32, shape.tokens_q * shape.heads_q),
+        _flat(workspace, "workspace", _torch.uint8, 0), workspace.numel(), _stream(stream))
+    if st:
+        _check("gs_attention_fwd", st)
 
 
 def gs_attention_bwd(q, k, v, out, lse, dout, dq, dk, dv, workspace, cu_q=None, cu_k=None,
                      causal=False, scale=None, stream=None):
     """Gradient of gs_attention_fwd from its out and lse (see gs.h)."""
-    import torch
-
     shape, heads, cu = _attention_args(q, k, v, cu_q, cu_k, causal, scale)
-    bf = torch.bfloat16
-    n = shape.tokens_q * shape.heads_q
+    bf, of_q, of_k = _torch.bfloat16, q.shape, k.shape
     st = library().gs_attention_bwd(
-        C.byref(shape), *heads, *cu, C.byref(_heads(out, "out", *q.shape, bf)),
-        _ptr(lse, "lse", torch.float32, n), C.byref(_heads(dout, "dout", *q.shape, bf)),
-        C.byref(_heads(dq, "dq", *q.shape, bf)), C.byref(_heads(dk, "dk", *k.shape, bf)),
-        C.byref(_heads(dv, "dv", *k.shape, bf)), _ptr(workspace, "workspace", torch.uint8),
+        shape, *heads, *cu, _heads(out, "out", of_q, bf),
+        _flat(lse, "lse", _torch.float32, shape.tokens_q * shape.heads_q),
+        _heads(dout, "dout", of_q, bf), _heads(dq, "dq", of_q, bf), _heads(dk, "dk", of_k, bf),
+        _heads(dv, "dv", of_k, bf), _flat(workspace, "workspace", _torch.uint8, 0),
         workspace.numel(), _stream(stream))
-    _check("gs_attention_bwd", st)
+    if st:
+        _check("gs_attention_bwd", st)
+
+
+def gs_attention_status(stream=None) -> None:
+    """Waits for the stream; raises GSError status 4 if a bounded device wait of an attention
+    call on this device has given up since the last such check."""
+    _check("gs_attention_status", library().gs_attention_status(_stream(stream)))
 
 
 def gs_dropout_add(x, residual, out, rng, p, stream=None):
     """out = residual + dropout(x) (see gs.h); residual may be None, out may be x or residual;
     rng: CUDA int64[2], seed and offset."""
-    import torch
-
-    n = x.numel()
+    kind, dtype, n = _element_type(x, "x"), x.dtype, x.numel()
     st = library().gs_dropout_add(
-        n, _element_type(x, "x"), _ptr(x, "x"), _ptr(residual, "residual", x.dtype, n, optional=True),
-        _ptr(out, "out", x.dtype, n), _ptr(rng, "rng", torch.int64, 2), float(p), _stream(stream))
-    _check("gs_dropout_add", st)
+        n, kind, _flat(x, "x", dtype, 0), _flat(residual, "residual", dtype, n, True),
+        _flat(out, "out", dtype, n), _flat(rng, "rng", _torch.int64, 2), p, _stream(stream))
+    if st:
+        _check("gs_dropout_add", st)
 
 
 def gs_dropout_add_bwd(dout, dx, rng, p, stream=None):
     """Gradient of gs_dropout_add by x, with the same rng (the residual's is dout itself)."""
-    import torch
-
-    n = dout.numel()
+    kind, dtype, n = _element_type(dout, "dout"), dout.dtype, dout.numel()
     st = library().gs_dropout_add_bwd(
-        n, _element_type(dout, "dout"), _ptr(dout, "dout"), _ptr(dx, "dx", dout.dtype, n),
-        _ptr(rng, "rng", torch.int64, 2), float(p), _stream(stream))
-    _check("gs_dropout_add_bwd", st)
+        n, kind, _flat(dout, "dout", dtype, 0), _flat(dx, "dx", dtype, n),
+        _flat(rng, "rng", _torch.int64, 2), p, _stream(stream))
+    if st:
+        _check("gs_dropout_add_bwd", st)
 
 
 def gs_raster_stats(workspace, stream=None) -> dict:

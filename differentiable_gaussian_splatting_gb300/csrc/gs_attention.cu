@@ -21,6 +21,16 @@ cudaError_t gave_up_word(unsigned int** word) {
     return e;
 }
 
+cudaError_t attention_gave_up(cudaStream_t st, unsigned int* gave_up) {
+    unsigned int* word = nullptr;
+    cudaError_t e = gave_up_word(&word);
+    if (e == cudaSuccess)
+        e = cudaMemcpyAsync(gave_up, word, sizeof(*word), cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess && *gave_up) e = cudaMemsetAsync(word, 0, sizeof(*word), st);
+    return e;
+}
+
 cudaError_t head_map(CUtensorMap* map, const void* data, int64_t ts, int64_t hs, int64_t tokens,
                      int heads, int dim, bool* swapped) {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,

@@ -543,6 +543,14 @@ gs_status gs_attention_bwd(const gs_attention_shape* shape, const gs_heads* q, c
                            void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * gs_attention_status -- whether a bounded device wait of an attention call has given up on
+ * the current device since the last such query: GS_ERR_TIMEOUT then, and the results of the
+ * calls since are not to be used.  Waits for the stream.  (Every wait inside the attention
+ * kernels gives up after some seconds instead of hanging; none should.)
+ */
+gs_status gs_attention_status(void* stream);
+
+/*
  * gs_dropout_add -- out = residual + x / (1 - p') where an element is kept, residual
  * elsewhere (residual NULL = 0).  gs_dropout_add_bwd -- dx = dout / (1 - p') where it
  * is kept, 0 elsewhere, from the same rng (the residual's gradient is dout itself).
