@@ -156,7 +156,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                          const __grid_constant__ CUtensorMap map_v, const FwdParams p) {
     using Sh = FwdShape<DP>;
     extern __shared__ char smem_raw[];
-    __shared__ uint64_t bar_q[2], bar_s[2 * Sh::kScores], bar_p[2 * Sh::kScores], bar_o[2], bar_full[Sh::kSlots],
+    __shared__ uint64_t bar_q[2], bar_s[2 * Sh::kScores], bar_p[2 * Sh::kScores],
+        bar_o[2 * Sh::kScores], bar_full[Sh::kSlots],
         bar_empty[Sh::kSlots], bar_raw, bar_drain;
     __shared__ uint32_t tmem_at;
     __shared__ volatile int dead;
@@ -218,11 +219,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_u32(&bar_q[t]), 1);
-            mbar_init(smem_u32(&bar_o[t]), 1);
         }
         for (int i = 0; i < 2 * Sh::kScores; ++i) {
             mbar_init(smem_u32(&bar_s[i]), 1);
             mbar_init(smem_u32(&bar_p[i]), 4);
+            mbar_init(smem_u32(&bar_o[i]), 1);
         }
         for (int i = 0; i < Sh::kSlots; ++i) {
             mbar_init(smem_u32(&bar_full[i]), 1);
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 const Step s = at;
                 product_rows(tmem_o(s.t), tmem_s(s.score), 32, op_v + s.slot * kTileStep, word_o,
                              s.j > 0);
-                mma_commit(smem_u32(&bar_o[s.t]));
+                mma_commit(smem_u32(&bar_o[s.t * Sh::kScores + s.bar]));
                 if (ahead.j < most) scores();
                 if (advance(at)) mma_commit(smem_u32(&bar_empty[s.slot + 1]));
             }
@@ -377,6 +378,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const int tiles_0 = work.tiles[0], tiles_1 = work.tiles[1];
         const float sl = p.log2_scale;
         const uint32_t o_at = tmem_o(t) + lanes;
+        // Whether the output has been added to for key tile j.  As for the scores there are
+        // kScores barriers in turn: this warp may be that many steps ahead of the outputs, and
+        // a barrier's phase can be told from the one before it only.
+        const auto output_done = [&](int j) {
+            return mbar_wait(smem_u32(&bar_o[t * Sh::kScores + j % Sh::kScores]),
+                             (j / Sh::kScores) & 1, &dead);
+        };
         float top = -INFINITY;
         float2 sum = make_float2(0.f, 0.f);
         bool ok = true;
@@ -413,7 +421,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 sum.x *= f;
                 sum.y *= f;
                 if (j > 0) {
-                    ok = mbar_wait(smem_u32(&bar_o[t]), (j - 1) & 1, &dead);
+                    ok = output_done(j - 1);
                     if (!ok) break;
                     tmem_fence_after();
 #pragma unroll
@@ -450,7 +458,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(&bar_p[t * Sh::kScores + j % Sh::kScores]));
         }
         // ---- the row's output ----
-        if (ok && tiles_t > 0) ok = mbar_wait(smem_u32(&bar_o[t]), (tiles_t - 1) & 1, &dead);
+        if (ok && tiles_t > 0) ok = output_done(tiles_t - 1);
         if (ok) {
             tmem_fence_after();
             const float l = sum.x + sum.y;

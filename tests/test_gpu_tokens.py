@@ -395,6 +395,26 @@ def test_attention_offsets_out_of_order_stay_inside():
     assert want.shape == (40, 2, 64)
 
 
+@pytest.mark.parametrize("lens_q,lens_k,hq,hk,D,causal", [
+    ([1115, 2215, 0], [1115, 2215, 9], 8, 2, 16, True),   # few blocks: keys in pieces
+    ([3, 700, 1], [4000, 1500, 33], 4, 4, 64, False),
+    ([3, 700, 1], [4000, 1500, 33], 4, 1, 128, True),
+    ([2300], [2300], 17, 1, 64, False),                   # a last wave of 1 block of 153
+    ([1, 1, 1], [6000, 90, 2500], 8, 8, 128, False),
+])
+def test_attention_keys_in_pieces(lens_q, lens_k, hq, hk, D, causal):
+    # scores whose maximum keeps rising, so that rows are rescaled while products are in flight
+    rng, q, k, v = _attention_inputs(sum(lens_q), sum(lens_k), hq, hk, D, seed=77)
+    ramp = np.concatenate([np.linspace(0.1, 1.0, max(n, 1))[:n] for n in lens_k])
+    k = ref.bf16(k * ramp[:, None, None] * 1.9)
+    do = ref.bf16(rng.normal(size=q.shape))
+    got = _check_attention(q, k, v, D ** -0.5, causal, lens_q, lens_k, dout=do)
+    for _ in range(3):
+        again = _run_attention(q, k, v, D ** -0.5, causal, lens_q, lens_k, do)
+        for a, b in ((got[0], again[0]), (got[1], again[1]), *zip(got[2], again[2])):
+            assert bool((a == b).all())
+
+
 def test_attention_strided_heads():
     # [heads, tokens, dim] arrays and a packed projection, gradients into a packed one
     import differentiable_gaussian_splatting_gb300 as gs
