@@ -12,7 +12,7 @@ using namespace gs;
 
 namespace {
 
-constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxTokens = int64_t(1) << 30;  // row and tile numbers stay in 32 bits
 constexpr int64_t kMaxStride = int64_t(1) << 38;  // elements
 constexpr int32_t kMaxHeads = 1024;
 constexpr int32_t kMaxBatch = 1 << 20;

@@ -5,12 +5,28 @@
 #include <cstdint>
 
 #include "gs_attention.cuh"
+#include "gs_internal.h"
 #include "gs_tokens.h"
 
 namespace gs {
 namespace {
 
 __device__ unsigned int g_gave_up;
+
+// test only: a bounded wait for a barrier at which nothing arrives
+__global__ void waiting_kernel(unsigned int* gave_up) {
+    grid_dep_sync();
+    __shared__ uint64_t bar;
+    __shared__ volatile int dead;
+    if (threadIdx.x == 0) {
+        dead = 0;
+        mbar_init(smem_u32(&bar), 1);
+        fence_barrier_init();
+    }
+    __syncthreads();
+    const bool ok = mbar_wait(smem_u32(&bar), 0, &dead);
+    if (!ok && threadIdx.x == 0) *gave_up = 1;
+}
 
 }  // namespace
 
@@ -71,3 +87,13 @@ size_t attention_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, 
 }
 
 }  // namespace gs
+
+// Not part of the C ABI (tests): runs the attention kernels' bounded wait out on the product's
+// own wait, so that gs_attention_status has something to report.
+extern "C" gs_status gs_test_attention_wait(void* stream) {
+    unsigned int* word = nullptr;
+    cudaError_t e = gs::gave_up_word(&word);
+    if (e == cudaSuccess)
+        e = gs::launch(gs::waiting_kernel, dim3(1), dim3(32), 0, (cudaStream_t)stream, word);
+    return e == cudaSuccess ? GS_OK : GS_ERR_CUDA;
+}

@@ -425,7 +425,9 @@ gs_status gs_bin_sort_noalloc(const gs_camera* cam, int64_t n, const float* spla
  *   gs_dropout_add    residual + dropout
  *
  * and back: gs_dropout_add_bwd, gs_attention_bwd, gs_qk_norm_rope_bwd.  Every call
- * is deterministic: the same inputs give the same bits.
+ * is deterministic: the same inputs give the same bits.  At most 2^30 tokens and 1,024
+ * heads.  The first call of each on a device loads its code there: make it before
+ * capturing a stream into a graph.
  *
  * gs_heads: a [tokens][heads][head_dim] array read by strides, so that queries, keys
  * and values may lie in one packed projection or in another order of dimensions.
@@ -510,7 +512,9 @@ gs_status gs_qk_norm_rope_bwd(int64_t tokens, int32_t heads_q, int32_t heads_k, 
  *              (batch = 1).  Offsets beyond the arrays are cut to them; tokens that no
  *              sequence holds are left unwritten
  *   lse        out [heads_q][tokens_q] fp32
- *   workspace  >= gs_attention_workspace_bytes(shape); holds nothing between calls
+ *   workspace  >= gs_attention_workspace_bytes(shape); holds nothing between calls.  The
+ *              size does not depend on causal, scale or whether offsets are given
+ *   out, lse and workspace overlap no input
  *
  * Scores, probabilities' sums and the accumulated outputs are fp32; the probabilities
  * are rounded to bfloat16 (unnormalised, relative to the row's maximum) for the second

@@ -450,6 +450,27 @@ def test_attention_long_rows():
         _close(_np(lse)[:, rows], l, D * U * smag + 4 * U * (1 + np.abs(l)) + 2.0 ** -20, "lse")
 
 
+def test_attention_status_reports_a_wait_that_gave_up():
+    # the kernels' own bounded wait, on a barrier at which nothing arrives (a test-only
+    # launcher): it ends, is reported once, and the context goes on
+    import ctypes as C
+
+    import differentiable_gaussian_splatting_gb300 as gs
+
+    torch = _torch()
+    gs.gs_attention_status()
+    lib = gs.library()
+    lib.gs_test_attention_wait.restype = C.c_int
+    lib.gs_test_attention_wait.argtypes = [C.c_void_p]
+    assert lib.gs_test_attention_wait(torch.cuda.current_stream().cuda_stream) == 0
+    with pytest.raises(gs.GSError) as e:
+        gs.gs_attention_status()
+    assert e.value.status == 4
+    gs.gs_attention_status()
+    rng, q, k, v = _attention_inputs(200, 200, 2, 2, 64, seed=60)
+    _check_attention(q, k, v, 0.125, True)
+
+
 # ---------------------------------------------------------------------------
 # dropout-add
 # ---------------------------------------------------------------------------

@@ -162,7 +162,7 @@ def test_attention_arguments_are_checked_on_the_host(lib):
         return lib.gs_attention_fwd(a, q or _h(), k or _h(ts=128), _h(ts=128), *cu, _h(), lse, wsp,
                                     wsb, None)
 
-    bad = [dict(tokens_q=-1), dict(tokens_k=1 << 31), dict(batch=0), dict(heads_q=0),
+    bad = [dict(tokens_q=-1), dict(tokens_k=(1 << 30) + 1), dict(batch=0), dict(heads_q=0),
            dict(heads_q=7), dict(heads_k=0), dict(heads_q=2048, heads_k=1), dict(head_dim=60),
            dict(head_dim=136), dict(head_dim=0), dict(causal=2), dict(scale=float("inf")),
            dict(batch=2)]  # two sequences without offsets
@@ -183,6 +183,22 @@ def test_attention_arguments_are_checked_on_the_host(lib):
 
     assert bwd(dq=_h(MIS)) == 1 and bwd(dk=_h(None)) == 1 and bwd(lse=None) == 1
     assert bwd(wsb=ws - 1) == 5
+
+
+def test_attention_workspace_covers_every_mask(lib):
+    # one size for a shape, whatever the mask and scale
+    import differentiable_gaussian_splatting_gb300 as gs
+
+    for tq, tk, b, hq, hk, d in ((1, 40000, 1, 16, 16, 64), (8160, 8160, 1, 16, 4, 128),
+                                 (2500, 2500, 1, 8, 8, 64), (3330, 3339, 3, 8, 2, 16),
+                                 (1 << 30, 1 << 30, 1 << 20, 1024, 1, 128)):
+        sizes = {lib.gs_attention_workspace_bytes(C.byref(gs.AttentionShape(tq, tk, b, hq, hk, d, c, s)))
+                 for c in (0, 1) for s in (0.1, -3.0)}
+        assert len(sizes) == 1
+        n = sizes.pop()
+        assert n == gs.gs_attention_workspace_bytes(tq, tk, b, hq, hk, d)
+        # the gradient's two rows of lse and delta, and at most a quarter of a GB of pieces
+        assert 8 * tq * hq <= n <= 8 * tq * hq + (1 << 28)
 
 
 def test_dropout_arguments_are_checked_on_the_host(lib):
