@@ -10,6 +10,17 @@
 // in tensor memory.  While one tile's softmax runs, the tensor cores work on the other's
 // products.
 //
+// What bounds it, at 128 values a head: the tensor cores with the shared memory that feeds
+// them.  A 128 x 128 tile takes 1,024 cycles of products; the first product reads both
+// operands from shared memory at its full 128 bytes a cycle while TMA writes there too, and
+// a tile changes hands twice, so about 1,390 cycles pass (tensor pipe busy 67 % of the
+// active time).  16,320 tokens x 16 heads: 1,260 us, 1,730 TFLOP/s, 0.94 of the measured
+// rate of the library's matrix product, both under the card's power limit.  At 64 values the
+// handshakes weigh twice as much: 8,160 tokens x 16 heads on 4 in 262 us, 1,040 TFLOP/s
+// (289 us with exponentials, 279 without, 209 without any softmax: it is not the
+// exponentials).  Tried and slower: 16 softmax warps with half a row each (1,351 us), a
+// thread for each query tile's products (1,326), a whole warp that walks the steps (1,414).
+//
 // The running maximum is stale on purpose: a row's O and sum are rescaled only once its
 // maximum has risen by more than 8 (in powers of two), so P stays below 2^8 and the
 // rescaling, which has to wait for the last product, is rare.  P is rounded to bfloat16
