@@ -13,7 +13,8 @@ device is present, the calls raise.
 
 Next to the path stand the token operators of a network that predicts Gaussians
 and is trained through it: ``gs_qk_norm_rope``, ``gs_attention_fwd``,
-``gs_dropout_add`` and their gradients.
+``gs_dropout_add`` and their gradients.  They take torch tensors, which a small
+compiled module checks and passes on (``csrc/token_binding.cpp``).
 
 ``Rasterizer`` is a convenience that allocates the outputs and workspaces of
 one view and runs the five calls in order.
@@ -517,67 +518,24 @@ def gs_loss_l1_ssim(width, height, image, target, dL_dimage, loss_out, workspace
 # ---------------------------------------------------------------------------
 # token operators
 # ---------------------------------------------------------------------------
-def _heads(t, name, shape=None, dtype=None) -> Heads:
-    """A CUDA tensor [tokens, heads, head_dim], contiguous in its last dimension, as gs_heads."""
-    if not isinstance(t, (_torch or _load_torch()).Tensor):
-        raise TypeError(f"{name}: expected a torch tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor")
-    own = t.shape
-    if len(own) != 3:
-        raise ValueError(f"{name}: expected [tokens, heads, head_dim], got {tuple(own)}")
-    if shape is not None and own != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(own)}")
-    if dtype is not None and t.dtype is not dtype:
-        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    token, head, last = t.stride()
-    if last != 1 and own[2] > 1 and own[0] > 0 and own[1] > 0:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return Heads(t.data_ptr() or None, token, head)
+_calls = None  # the compiled binding of these calls, once loaded
 
 
-def _flat(t, name, dtype, numel, optional=False):
-    """Address of a contiguous CUDA tensor of at least numel elements (None: left out)."""
-    if t is None:
-        if optional:
-            return None
-        raise ValueError(f"{name} is required")
-    if not isinstance(t, _torch.Tensor):
-        raise TypeError(f"{name}: expected a torch tensor")
-    if not t.is_cuda or t.dtype is not dtype or not t.is_contiguous() or t.numel() < numel:
-        raise ValueError(f"{name}: expected a contiguous CUDA tensor of at least {numel} x {dtype}, "
-                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
-    return t.data_ptr() or None
+def _token_calls():
+    """The compiled binding (csrc/token_binding.cpp): it checks the tensors (TypeError,
+    ValueError), calls the library and returns the status."""
+    global _calls
+    if _calls is None:
+        import importlib.machinery
+        import importlib.util
 
-
-def _element_type(t, name) -> int:
-    torch = _torch or _load_torch()
-    dtype = t.dtype if isinstance(t, torch.Tensor) else None
-    if dtype is torch.bfloat16:
-        return 1
-    if dtype is torch.float32:
-        return 0
-    raise ValueError(f"{name}: expected a float32 or bfloat16 tensor")
-
-
-def _norm_args(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved):
-    kind = _element_type(q, "q")
-    qh = _heads(q, "q")
-    T, hq, D = q.shape
-    kh = _heads(k, "k", None, q.dtype)
-    Tk, hk, Dk = k.shape
-    if Tk != T or Dk != D:
-        raise ValueError(f"k: expected {T} tokens of {D} values a head, got {tuple(k.shape)}")
-    rows = rot = 0
-    if cos_sin is not None:
-        if not isinstance(cos_sin, _torch.Tensor) or cos_sin.dim() != 2:
-            raise ValueError("cos_sin: expected a [rows, rot] tensor")
-        rows, rot = cos_sin.shape
-    f = _torch.float32
-    return (T, hq, hk, D), HeadNorm(kind, rot, 1 if interleaved else 0, eps, rows), qh, kh, (
-        _flat(q_weight, "q_weight", f, D, True), _flat(k_weight, "k_weight", f, D, True),
-        _flat(cos_sin, "cos_sin", f, 0, True),
-        _flat(positions, "positions", _torch.int32, T, True))
+        _load_torch()
+        library()
+        loader = importlib.machinery.ExtensionFileLoader("gs_token_binding", _build.BINDING)
+        spec = importlib.util.spec_from_loader("gs_token_binding", loader)
+        _calls = importlib.util.module_from_spec(spec)
+        loader.exec_module(_calls)
+    return _calls
 
 
 def gs_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out, eps=1e-6,
@@ -586,11 +544,8 @@ def gs_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out, 
     q, k, q_out, k_out: [tokens, heads, head_dim] float32 or bfloat16, any strides with a
     contiguous last dimension; cos_sin [rows, rot] float32 (None: no rotation); weights and
     positions may be None."""
-    sizes, norm, qh, kh, ptrs = _norm_args(q, k, q_weight, k_weight, cos_sin, positions, eps,
-                                           interleaved)
-    dtype = q.dtype
-    st = library().gs_qk_norm_rope(*sizes, norm, qh, kh, *ptrs, _heads(q_out, "q_out", q.shape, dtype),
-                                   _heads(k_out, "k_out", k.shape, dtype), _stream(stream))
+    st = (_calls or _token_calls()).qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions,
+                                                 q_out, k_out, eps, interleaved, stream)
     if st:
         _check("gs_qk_norm_rope", st)
 
@@ -604,15 +559,9 @@ def gs_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk
                         dq_weight, dk_weight, workspace, eps=1e-6, interleaved=False, stream=None):
     """Gradient of gs_qk_norm_rope (see gs.h); dq_weight and dk_weight (float32 [head_dim]) may
     be None."""
-    sizes, norm, qh, kh, ptrs = _norm_args(q, k, q_weight, k_weight, cos_sin, positions, eps,
-                                           interleaved)
-    f, dtype, of_q, of_k = _torch.float32, q.dtype, q.shape, k.shape
-    st = library().gs_qk_norm_rope_bwd(
-        *sizes, norm, qh, kh, *ptrs, _heads(dq_out, "dq_out", of_q, dtype),
-        _heads(dk_out, "dk_out", of_k, dtype), _heads(dq, "dq", of_q, dtype),
-        _heads(dk, "dk", of_k, dtype), _flat(dq_weight, "dq_weight", f, sizes[3], True),
-        _flat(dk_weight, "dk_weight", f, sizes[3], True),
-        _flat(workspace, "workspace", _torch.uint8, 0), workspace.numel(), _stream(stream))
+    st = (_calls or _token_calls()).qk_norm_rope_bwd(
+        q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk_out, dq, dk, dq_weight, dk_weight,
+        workspace, eps, interleaved, stream)
     if st:
         _check("gs_qk_norm_rope_bwd", st)
 
@@ -623,38 +572,14 @@ def gs_attention_workspace_bytes(tokens_q, tokens_k, batch, heads_q, heads_k, he
     return int(library().gs_attention_workspace_bytes(C.byref(shape)))
 
 
-def _attention_args(q, k, v, cu_q, cu_k, causal, scale):
-    bf = (_torch or _load_torch()).bfloat16
-    qh, kh = _heads(q, "q", None, bf), _heads(k, "k", None, bf)
-    vh = _heads(v, "v", k.shape, bf)
-    Tq, hq, D = q.shape
-    Tk, hk, Dk = k.shape
-    if Dk != D:
-        raise ValueError(f"k: expected {D} values a head, got {tuple(k.shape)}")
-    batch, cu = 1, (None, None)
-    if cu_q is not None or cu_k is not None:
-        if cu_q is None or cu_k is None:
-            raise ValueError("cu_q and cu_k: give both or neither")
-        batch = cu_q.numel() - 1
-        if batch < 1 or cu_k.numel() != batch + 1:
-            raise ValueError("cu_q and cu_k: expected batch + 1 offsets each")
-        i = _torch.int32
-        cu = (_flat(cu_q, "cu_q", i, 0), _flat(cu_k, "cu_k", i, 0))
-    return AttentionShape(Tq, Tk, batch, hq, hk, D, 1 if causal else 0,
-                          D ** -0.5 if scale is None else scale), (qh, kh, vh), cu
-
-
 def gs_attention_fwd(q, k, v, out, lse, workspace, cu_q=None, cu_k=None, causal=False, scale=None,
                      stream=None):
     """Softmax attention over a ragged batch (see gs.h).  q, out [tokens_q, heads_q, head_dim],
     k, v [tokens_k, heads_k, head_dim] bfloat16, any strides with a contiguous last dimension;
     lse [heads_q, tokens_q] float32; cu_q, cu_k [batch + 1] int32 offsets (None: one sequence);
     scale defaults to head_dim ** -0.5."""
-    shape, heads, cu = _attention_args(q, k, v, cu_q, cu_k, causal, scale)
-    st = library().gs_attention_fwd(
-        shape, *heads, *cu, _heads(out, "out", q.shape, _torch.bfloat16),
-        _flat(lse, "lse", _torch.float32, shape.tokens_q * shape.heads_q),
-        _flat(workspace, "workspace", _torch.uint8, 0), workspace.numel(), _stream(stream))
+    st = (_calls or _token_calls()).attention_fwd(q, k, v, out, lse, workspace, cu_q, cu_k, causal,
+                                                  scale, stream)
     if st:
         _check("gs_attention_fwd", st)
 
@@ -662,14 +587,8 @@ def gs_attention_fwd(q, k, v, out, lse, workspace, cu_q=None, cu_k=None, causal=
 def gs_attention_bwd(q, k, v, out, lse, dout, dq, dk, dv, workspace, cu_q=None, cu_k=None,
                      causal=False, scale=None, stream=None):
     """Gradient of gs_attention_fwd from its out and lse (see gs.h)."""
-    shape, heads, cu = _attention_args(q, k, v, cu_q, cu_k, causal, scale)
-    bf, of_q, of_k = _torch.bfloat16, q.shape, k.shape
-    st = library().gs_attention_bwd(
-        shape, *heads, *cu, _heads(out, "out", of_q, bf),
-        _flat(lse, "lse", _torch.float32, shape.tokens_q * shape.heads_q),
-        _heads(dout, "dout", of_q, bf), _heads(dq, "dq", of_q, bf), _heads(dk, "dk", of_k, bf),
-        _heads(dv, "dv", of_k, bf), _flat(workspace, "workspace", _torch.uint8, 0),
-        workspace.numel(), _stream(stream))
+    st = (_calls or _token_calls()).attention_bwd(q, k, v, out, lse, dout, dq, dk, dv, workspace,
+                                                  cu_q, cu_k, causal, scale, stream)
     if st:
         _check("gs_attention_bwd", st)
 
@@ -683,20 +602,14 @@ def gs_attention_status(stream=None) -> None:
 def gs_dropout_add(x, residual, out, rng, p, stream=None):
     """out = residual + dropout(x) (see gs.h); residual may be None, out may be x or residual;
     rng: CUDA int64[2], seed and offset."""
-    kind, dtype, n = _element_type(x, "x"), x.dtype, x.numel()
-    st = library().gs_dropout_add(
-        n, kind, _flat(x, "x", dtype, 0), _flat(residual, "residual", dtype, n, True),
-        _flat(out, "out", dtype, n), _flat(rng, "rng", _torch.int64, 2), p, _stream(stream))
+    st = (_calls or _token_calls()).dropout_add(x, residual, out, rng, p, stream)
     if st:
         _check("gs_dropout_add", st)
 
 
 def gs_dropout_add_bwd(dout, dx, rng, p, stream=None):
     """Gradient of gs_dropout_add by x, with the same rng (the residual's is dout itself)."""
-    kind, dtype, n = _element_type(dout, "dout"), dout.dtype, dout.numel()
-    st = library().gs_dropout_add_bwd(
-        n, kind, _flat(dout, "dout", dtype, 0), _flat(dx, "dx", dtype, n),
-        _flat(rng, "rng", _torch.int64, 2), p, _stream(stream))
+    st = (_calls or _token_calls()).dropout_add_bwd(dout, dx, rng, p, stream)
     if st:
         _check("gs_dropout_add_bwd", st)
 

@@ -4,8 +4,9 @@
 
 Each .cu file is compiled in parallel with nvcc, then linked into
 ``_build/libgs.so`` next to this file (static CUDA runtime, no other
-dependency).  A rebuild happens when any source or header is newer than the
-library.
+dependency).  Beside it ``_build/gs_token_binding.so``, the Python binding of
+the token operators, is compiled with g++ against torch's headers.  A rebuild
+happens when any source or header is newer than the libraries.
 """
 
 from __future__ import annotations
@@ -22,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libgs.so")
+BINDING = os.path.join(BUILD, "gs_token_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", *ARCH]
 
@@ -38,15 +40,36 @@ def sources() -> list[str]:
 
 
 def _inputs() -> list[str]:
-    return sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(
-        os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "gs.h")]
+    return sources() + [p for kind in ("*.h", "*.cuh", "*.cpp")
+                        for p in glob.glob(os.path.join(CSRC, kind))] + [
+        os.path.join(INCLUDE, "gs.h")]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _inputs())
+
+
+def _binding_commands(obj: str, tmp: str) -> tuple[list[str], list[str]]:
+    """Compile and link commands of the token operators' binding."""
+    import sysconfig
+
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    lib = os.path.join(base, "lib")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    dirs = [INCLUDE, os.path.join(base, "include"),
+            os.path.join(base, "include", "torch", "csrc", "api", "include"),
+            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    cxx = shutil.which("g++") or "c++"
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return ([cxx, "-O2", "-std=c++17", "-fPIC", "-w", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
+             *[f"-I{d}" for d in dirs], "-c", os.path.join(CSRC, "token_binding.cpp"), "-o", obj],
+            [cxx, "-shared", "-o", tmp, obj, LIB, f"-L{lib}", "-ltorch_python", "-ltorch_cpu",
+             "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}", "-Wl,-rpath,$ORIGIN"])
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -58,23 +81,27 @@ def build(force: bool = False, verbose: bool = False) -> str:
     srcs = sources()
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
 
-    def compile_one(pair):
-        src, obj = pair
-        cmd = [cc, *NVCC_FLAGS, "-I", INCLUDE, "-c", src, "-o", obj]
+    def run(cmd, what):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stderr}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed on {what}:\n{r.stderr}")
         if verbose and r.stderr:
             print(r.stderr, file=sys.stderr)
 
-    with ThreadPoolExecutor(max_workers=max(1, len(srcs))) as ex:
-        list(ex.map(compile_one, zip(srcs, objs)))
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"nvcc link failed:\n{r.stderr}")
+    tmp_binding = BINDING + f".tmp{os.getpid()}"
+    binding_obj = os.path.join(BUILD, "token_binding.o")
+    compile_binding, link_binding = _binding_commands(binding_obj, tmp_binding)
+    jobs = [(compile_binding, "token_binding.cpp")]
+    jobs += [([cc, *NVCC_FLAGS, "-I", INCLUDE, "-c", src, "-o", obj], os.path.basename(src))
+             for src, obj in zip(srcs, objs)]
+    with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
+        list(ex.map(lambda job: run(*job), jobs))
+    # the library's own name inside it, so that the binding finds it beside itself
+    run([cc, *ARCH, "-shared", "-Xlinker", "-soname=libgs.so", "-o", tmp, *objs], "libgs.so")
     os.replace(tmp, LIB)
+    run(link_binding, "gs_token_binding.so")
+    os.replace(tmp_binding, BINDING)
     return LIB
 
 
