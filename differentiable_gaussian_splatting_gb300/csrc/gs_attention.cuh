@@ -31,26 +31,15 @@ struct Sequence {
     int n, m;  // queries, keys
 };
 
-__device__ __forceinline__ void cut(const int32_t* cu, int b, int64_t tokens, int64_t* at, int* n) {
-    if (!cu) {
-        *at = 0;
-        *n = (int)tokens;
-        return;
-    }
-    const int64_t a = min64(max64((int64_t)__ldg(cu + b), 0), tokens);
-    const int64_t e = min64(max64((int64_t)__ldg(cu + b + 1), a), tokens);
-    *at = a;
-    *n = (int)(e - a);
-}
-
 // how many keys query i of a sequence sees
 __device__ __forceinline__ int seen_keys(int i, int n, int m, bool causal) {
     return causal ? min(m, max(0, i + 1 + m - n)) : m;
 }
 
-// A block's place: `rows` queries (or keys) of one sequence and a head.
+// A block's place: `rows` queries (or keys) of one sequence and a head; and the sequence.
 struct Place {
     int b, tile, head;
+    Sequence sq;
 };
 
 struct Batch {
@@ -60,9 +49,31 @@ struct Batch {
     bool causal;
 };
 
+// the bounds of sequence b, cut to the arrays: all four offsets are read at once
+__device__ __forceinline__ Sequence sequence(const Batch& v, int b) {
+    Sequence s{0, 0, (int)v.tq, (int)v.tk};
+    if (v.cu_q) {
+        const int q0 = __ldg(v.cu_q + b), q1 = __ldg(v.cu_q + b + 1);
+        const int k0 = __ldg(v.cu_k + b), k1 = __ldg(v.cu_k + b + 1);
+        s.q0 = min(max(q0, 0), (int)v.tq);
+        s.n = min(max(q1, (int)s.q0), (int)v.tq) - (int)s.q0;
+        s.k0 = min(max(k0, 0), (int)v.tk);
+        s.m = min(max(k1, (int)s.k0), (int)v.tk) - (int)s.k0;
+    }
+    return s;
+}
+
+// a lane's sequence to the whole warp
+__device__ __forceinline__ Sequence from_lane(const Sequence& s, int lane) {
+    const unsigned all = 0xffffffffu;
+    return {__shfl_sync(all, (int)s.q0, lane), __shfl_sync(all, (int)s.k0, lane),
+            __shfl_sync(all, s.n, lane), __shfl_sync(all, s.m, lane)};
+}
+
 // How many of a sequence's tiles cost at least c (c >= 1), cost being the 128-row tiles of
 // the other side that a tile meets.  Tiles of queries cost more towards the sequence's end
-// under the causal mask, tiles of keys towards its start.
+// under the causal mask, tiles of keys towards its start.  (Tokens are at most 2^30: nothing
+// here leaves 32 bits.)
 template <bool kKeys>
 __device__ __forceinline__ int tiles_from(int n, int m, int rows, bool causal, int c) {
     const int of = kKeys ? m : n, other = kKeys ? n : m;
@@ -72,13 +83,12 @@ __device__ __forceinline__ int tiles_from(int n, int m, int rows, bool causal, i
     if (!causal) return tiles;
     if (kKeys) {
         // the tile at `key` meets most - max(0, key + n - m) / 128 tiles of queries
-        const int64_t y = (int64_t)(most - c + 1) * kTileRows + m - n;
-        return y <= 0 ? 0 : (int)min64(tiles, (y + rows - 1) / rows);
+        const int y = (most - c + 1) * kTileRows + m - n;
+        return y <= 0 ? 0 : min(tiles, (y + rows - 1) / rows);
     }
     // the tile up to query e (exclusive) meets ceil((e + m - n) / 128) tiles of keys
-    const int64_t x = (int64_t)(c - 1) * kTileRows + n - m;
-    if (n <= x) return 0;
-    return tiles - (int)max64(0, x / rows);
+    const int x = (c - 1) * kTileRows + n - m;
+    return n <= x ? 0 : tiles - max(0, x) / rows;
 }
 
 // By one whole warp: block `id` of the batch's tiles and heads, costliest first where costs
@@ -87,14 +97,13 @@ __device__ __forceinline__ int tiles_from(int n, int m, int rows, bool causal, i
 template <bool kKeys>
 __device__ __forceinline__ bool find_place(const Batch& v, int rows, int heads, int id, Place* at) {
     if (v.batch == 1) {
-        int64_t unused;
-        int of;
-        cut(kKeys ? v.cu_k : v.cu_q, 0, kKeys ? v.tk : v.tq, &unused, &of);
-        const int tiles = (of + rows - 1) / rows;
+        const Sequence s = sequence(v, 0);
+        const int tiles = ((kKeys ? s.m : s.n) + rows - 1) / rows;
         at->b = 0;
+        at->sq = s;
         if (v.causal) {
-            at->head = id % heads;
             const int rank = id / heads;
+            at->head = id - rank * heads;
             at->tile = kKeys ? rank : tiles - 1 - rank;
             return rank < tiles;
         }
@@ -109,26 +118,23 @@ __device__ __forceinline__ bool find_place(const Batch& v, int rows, int heads, 
     int rank = id / heads;
     at->head = id - rank * heads;
     if (v.batch <= 32) {
-        int64_t unused;
-        int n = 0, m = 0;
-        if (lane < v.batch) {
-            cut(v.cu_q, lane, v.tq, &unused, &n);
-            cut(v.cu_k, lane, v.tk, &unused, &m);
-        }
-        const int tiles = ((kKeys ? m : n) + rows - 1) / rows;
+        Sequence s{};
+        if (lane < v.batch) s = sequence(v, lane);
+        const int tiles = ((kKeys ? s.m : s.n) + rows - 1) / rows;
         if (rank >= (int)__reduce_add_sync(all, tiles)) return false;
         // the largest cost that more than `rank` tiles reach (every tile reaches 0)
-        int lo = 0, hi = (int)__reduce_max_sync(all, ((kKeys ? n : m) + kTileRows - 1) / kTileRows);
+        int lo = 0;
+        int hi = (int)__reduce_max_sync(all, ((kKeys ? s.n : s.m) + kTileRows - 1) / kTileRows);
         while (lo < hi) {
             const int c = (lo + hi + 1) >> 1;
-            const int from = tiles_from<kKeys>(n, m, rows, v.causal, c);
+            const int from = tiles_from<kKeys>(s.n, s.m, rows, v.causal, c);
             if ((int)__reduce_add_sync(all, from) > rank)
                 lo = c;
             else
                 hi = c - 1;
         }
-        const int reach = lo == 0 ? tiles : tiles_from<kKeys>(n, m, rows, v.causal, lo);
-        const int above = tiles_from<kKeys>(n, m, rows, v.causal, lo + 1);
+        const int reach = lo == 0 ? tiles : tiles_from<kKeys>(s.n, s.m, rows, v.causal, lo);
+        const int above = tiles_from<kKeys>(s.n, s.m, rows, v.causal, lo + 1);
         rank -= (int)__reduce_add_sync(all, above);
         int sum = reach - above;
 #pragma unroll
@@ -141,18 +147,15 @@ __device__ __forceinline__ bool find_place(const Batch& v, int rows, int heads, 
         const int tile = kKeys ? above + within : tiles - reach + within;
         at->b = l;
         at->tile = __shfl_sync(all, tile, l);
+        at->sq = from_lane(s, l);
         return true;
     }
     int before = 0;
     for (int base = 0; base < v.batch; base += 32) {
         const int b = v.batch - 1 - base - lane;
-        int tiles = 0;
-        if (b >= 0) {
-            int64_t unused;
-            int n;
-            cut(kKeys ? v.cu_k : v.cu_q, b, kKeys ? v.tk : v.tq, &unused, &n);
-            tiles = (n + rows - 1) / rows;
-        }
+        Sequence s{};
+        if (b >= 0) s = sequence(v, b);
+        const int tiles = ((kKeys ? s.m : s.n) + rows - 1) / rows;
         int sum = tiles;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -166,6 +169,7 @@ __device__ __forceinline__ bool find_place(const Batch& v, int rows, int heads, 
             const int own = __shfl_sync(all, tiles, l);
             at->b = v.batch - 1 - base - l;
             at->tile = kKeys ? rank - (upto - own) : upto - 1 - rank;
+            at->sq = from_lane(s, l);
             return true;
         }
         before += __shfl_sync(all, sum, 31);

@@ -110,8 +110,7 @@ __device__ __forceinline__ bool find_work(const BwdParams& p, BwdWork* out) {
     if (!find_place<kKeys>(p.batch, kTileRows, kKeys ? p.heads_k : p.heads_q, (int)id, &at))
         return false;
     BwdWork w;
-    cut(p.batch.cu_q, at.b, p.batch.tq, &w.sq.q0, &w.sq.n);
-    cut(p.batch.cu_k, at.b, p.batch.tk, &w.sq.k0, &w.sq.m);
+    w.sq = at.sq;
     w.row0 = at.tile * kTileRows;
     w.head = at.head;
     w.khead = kKeys ? at.head : at.head / p.group;
@@ -794,9 +793,7 @@ __global__ void __launch_bounds__(kSumThreads) attention_sum_kernel(const BwdPar
     }
     __syncthreads();
     if (!found) return;
-    Sequence sq;
-    cut(p.batch.cu_q, place.b, p.batch.tq, &sq.q0, &sq.n);
-    cut(p.batch.cu_k, place.b, p.batch.tk, &sq.k0, &sq.m);
+    const Sequence sq = place.sq;
     const int row0 = place.tile * kTileRows;
     int unused;
     const int items = kKeys ? queries_of(sq, row0, p.batch.causal, &unused) * p.group

@@ -118,12 +118,9 @@ __device__ __forceinline__ bool find_spread(const Batch& v, int heads, int id, b
                                             Place* at, Spread* sp) {
     const int lane = threadIdx.x & 31;
     const unsigned all = 0xffffffffu;
-    int64_t unused;
-    int n = 0, m = 0;
-    if (lane < v.batch) {
-        cut(v.cu_q, lane, v.tq, &unused, &n);
-        cut(v.cu_k, lane, v.tk, &unused, &m);
-    }
+    Sequence s{};
+    if (lane < v.batch) s = sequence(v, lane);
+    const int n = s.n, m = s.m;
     const int blocks = (n + 2 * kTileRows - 1) / (2 * kTileRows) * heads;
     const int keys = (m + kTileRows - 1) / kTileRows;
     int lo = kLeastChunk, hi = max(lo, (int)__reduce_max_sync(all, keys));
@@ -150,6 +147,7 @@ __device__ __forceinline__ bool find_spread(const Batch& v, int heads, int id, b
     if (by_piece) within /= pieces;
     const int first = sum_p - blocks * pieces + within * pieces;
     at->b = l;
+    at->sq = from_lane(s, l);
     at->head = __shfl_sync(all, within % heads, l);
     at->tile = __shfl_sync(all, within / heads, l);
     sp->chunk = lo;
@@ -202,8 +200,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         if (ok && lane == 0) {
             FwdWork w;
-            cut(p.batch.cu_q, at.b, p.batch.tq, &w.sq.q0, &w.sq.n);
-            cut(p.batch.cu_k, at.b, p.batch.tk, &w.sq.k0, &w.sq.m);
+            w.sq = at.sq;
             w.row0 = at.tile * 2 * kTileRows;
             w.head = at.head;
             w.khead = at.head / p.group;
@@ -548,9 +545,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const FwdP
     }
     __syncthreads();
     if (!found) return;
-    Sequence sq;
-    cut(p.batch.cu_q, place.b, p.batch.tq, &sq.q0, &sq.n);
-    cut(p.batch.cu_k, place.b, p.batch.tk, &sq.k0, &sq.m);
+    const Sequence sq = place.sq;
     const int row0 = place.tile * 2 * kTileRows;
     constexpr int kLanes = DP / 4;
     const int lane = threadIdx.x % kLanes;
