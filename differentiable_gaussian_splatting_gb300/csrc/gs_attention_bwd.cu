@@ -842,8 +842,10 @@ BwdPlan plan_bwd(int64_t blocks, int64_t items, int64_t tokens, bool uniform) {
     if (rest == 0) return plan;
     double best = (1.0 - kGain) * (double)(waves(blocks) * (items + kStart));
     for (int cuts = 2; cuts <= kMaxPieces; ++cuts) {
-        const int64_t chunk = (items + cuts - 1) / cuts, pieces = (items + chunk - 1) / chunk;
-        if (chunk < kLeastChunk || rest * pieces > 4 * kSms) break;
+        const int64_t chunk = (items + cuts - 1) / cuts;
+        if (chunk < kLeastChunk) break;  // at once where the other side is empty
+        const int64_t pieces = (items + chunk - 1) / chunk;
+        if (rest * pieces > 4 * kSms) break;
         const double cost = (double)(whole / kSms * (items + kStart) +
                                      waves(rest * pieces) * (chunk + kStart) + kSum);
         if (cost < best) {

@@ -616,8 +616,9 @@ FwdPlan plan_fwd(int64_t tq, int64_t tk, int batch, int heads, bool causal) {
     if (rest == 0) return plan;
     double best = (1.0 - kGain) * (double)(waves(blocks) * (keys + kStart));
     for (int cuts = 2; cuts <= kMaxPieces; ++cuts) {
-        const int64_t chunk = (keys + cuts - 1) / cuts, pieces = (keys + chunk - 1) / chunk;
-        if (chunk < kLeastChunk) break;
+        const int64_t chunk = (keys + cuts - 1) / cuts;
+        if (chunk < kLeastChunk) break;  // at once without keys
+        const int64_t pieces = (keys + chunk - 1) / chunk;
         const double cost = (double)(whole / kSms * (keys + kStart) +
                                      waves(rest * pieces) * (chunk + kStart) + kJoin);
         if (cost < best) {

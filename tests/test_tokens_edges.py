@@ -1,0 +1,55 @@
+"""Edges of the token operators that need no GPU: sizes of empty sides, what the sources of the
+kernels must hold, the binding's refusals and the build's parts."""
+
+import os
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from differentiable_gaussian_splatting_gb300 import build
+
+    build.build()
+
+
+def _python(code: str, **kw):
+    return subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True,
+                          timeout=300, **kw)
+
+
+# ---------------------------------------------------------------------------
+# sides without tokens
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("tq,tk,batch", [(5, 0, 1), (0, 7, 2), (0, 0, 2), (100, 0, 1), (0, 100, 1),
+                                         (5000, 0, 1), (0, 5000, 1), (40000, 0, 1), (0, 40000, 3)])
+def test_attention_workspace_of_an_empty_side(tq, tk, batch):
+    # no pieces: the gradient's two fp32 rows per query, in whole 256 bytes, and the slack.  In a
+    # process of its own, since a size that divides by a count of zero ends it.
+    heads = [(4, 2, 64), (16, 16, 128), (16, 1, 40)]
+    r = _python(f"import differentiable_gaussian_splatting_gb300 as gs\n"
+                f"for h in {heads}: print(gs.gs_attention_workspace_bytes({tq}, {tk}, {batch}, *h))")
+    assert r.returncode == 0, (r.returncode, r.stderr[-300:])
+    assert [int(n) for n in r.stdout.split()] == [(8 * tq * hq + 255) // 256 * 256 + 512
+                                                  for hq, _, _ in heads]
+
+
+@pytest.mark.parametrize("tq,tk", [(5, 0), (40000, 0), (0, 7), (0, 40000)])
+def test_attention_calls_with_an_empty_side_check_their_workspace(tq, tk):
+    # both calls plan before they compare the workspace's size (status 5: too small)
+    r = _python(f"""
+import ctypes as C
+import differentiable_gaussian_splatting_gb300 as gs
+lib, P = gs.library(), 0x100000
+h = lambda n: C.byref(gs.Heads(P, n * 64, 64))
+s = C.byref(gs.AttentionShape({tq}, {tk}, 1, 4, 2, 64, 0, 0.125))
+if {tq}:
+    print(lib.gs_attention_fwd(s, h(4), h(2), h(2), None, None, h(4), P, P, 16, None))
+print(lib.gs_attention_bwd(s, h(4), h(2), h(2), None, None, h(4), P, h(4), h(4), h(2), h(2), P, 16,
+                           None))""")
+    assert r.returncode == 0, (r.returncode, r.stderr[-300:])
+    assert set(r.stdout.split()) == {"5"}
