@@ -4,17 +4,18 @@
 //   P = exp(scale Q K^T - lse),  dV = P^T dO,  dS = P (dO V^T - delta),
 //   dQ = scale dS K,  dK = scale dS^T Q,  delta_i = O_i . dO_i
 //
-// Three kernels.  The first makes delta.  The second gives a block 128 keys and walks the
-// queries of every head that shares them: dK and dV stay in tensor memory, so the sum over
-// a group's heads and over queries needs no atomics.  The third gives a block 128 queries
-// and walks the keys, with dQ in tensor memory.  S and dO V^T are formed in both: seven
-// products instead of five.  The other way, dQ added to memory from the second kernel,
+// Two kernels.  The first makes delta.  The second has blocks of two kinds.  One takes 128
+// keys and walks the queries of every head that shares them: dK and dV stay in tensor memory,
+// so the sum over a group's heads and over queries needs no atomics.  The other takes 128
+// queries and walks the keys, with dQ in tensor memory.  S and dO V^T are formed in both:
+// seven products instead of five.  The other way, dQ added to memory from the blocks of keys,
 // moves 64 KB of fp32 additions per 128 x 128 tile, about as many bytes per clock as L2
-// takes, and its result would depend on their order.
+// takes, and its result would depend on their order.  Neither kind needs anything of the
+// other, and in one launch the blocks of queries fill the last wave of the blocks of keys.
 //
-// What bounds them, at 128 values a head: a step of the second kernel is 2,048 cycles of
+// What bounds them, at 128 values a head: a step of a block of keys is 2,048 cycles of
 // products and as many of shared memory at 128 bytes a cycle (192 KB of operands, 64 KB that
-// TMA writes), a step of the third 1,536; the tensor pipe is busy 68 % and 74 % of the
+// TMA writes), a step of a block of queries 1,536; the tensor pipe is busy 68 % and 74 % of the
 // active time, and leaving out all arithmetic between the products saves 7 %.  8,160 tokens
 // x 16 heads on 4: 1,130 us with the row sums, 1,210 TFLOP/s of the gradient's five
 // products, 1,690 of the seven that are done (0.91 of the library's measured rate).  At 64
@@ -22,7 +23,7 @@
 //
 // The transposes come out of the operand descriptors: a tile of rows in shared memory
 // serves both as an operand contracted along its columns and as one contracted along its
-// rows.  P^T and dS^T (second kernel) and dS (third) go back to tensor memory in bfloat16
+// rows.  P^T and dS^T (blocks of keys) and dS (of queries) go back to tensor memory in bfloat16
 // over the scores they came from, as first operands.  P, dP - delta and the sums are fp32;
 // P and dS are rounded to bfloat16 once, for the products.
 //
@@ -74,9 +75,8 @@ struct BwdParams {
     const float* lse;
     float *nlse, *ndelta;  // [heads][tokens]: -lse log2(e) (-infinity: saw no key), -delta
     unsigned int* gave_up;
-    BwdPlan plan;  // of the kernel at hand
-    bool after_dkv;  // dQ's kernel follows dK and dV's
-    float* parts;  // [pieces][rest][slot_rows][DP], for dK, then for dV; or for dQ
+    BwdPlan plan_k, plan_q;     // of the blocks of keys, of queries
+    float *parts_k, *parts_q;   // [pieces][rest][slot_rows][DP]: dK, then dV; dQ
 };
 
 // query tiles that see a block of keys, for each head of the group: from *first on
@@ -96,15 +96,20 @@ __host__ __device__ inline int64_t part_rows(const BwdPlan& plan) {
     return plan.pieces > 1 ? plan.pieces * plan.rest * plan.slot_rows : 0;
 }
 
-// By one whole warp: the block's work, or false.
+__host__ __device__ inline int64_t blocks_of(const BwdPlan& plan) {
+    return plan.whole + plan.rest * plan.pieces;
+}
+
+// By one whole warp: the work of block `id` of its kind, or false.
 template <bool kKeys>
-__device__ __forceinline__ bool find_work(const BwdParams& p, BwdWork* out) {
-    int64_t id = blockIdx.x, part = -1;
+__device__ __forceinline__ bool find_work(const BwdParams& p, int64_t id, BwdWork* out) {
+    const BwdPlan& plan = kKeys ? p.plan_k : p.plan_q;
+    int64_t part = -1;
     int piece = 0;
-    if (id >= p.plan.whole) {  // the cut blocks, piece by piece
-        piece = (int)((id - p.plan.whole) / p.plan.rest);
-        id -= piece * p.plan.rest;
-        part = ((int64_t)blockIdx.x - p.plan.whole) * p.plan.slot_rows;
+    if (id >= plan.whole) {  // the cut blocks, piece by piece
+        part = (id - plan.whole) * plan.slot_rows;
+        piece = (int)((id - plan.whole) / plan.rest);
+        id -= piece * plan.rest;
     }
     Place at{};
     if (!find_place<kKeys>(p.batch, kTileRows, kKeys ? p.heads_k : p.heads_q, (int)id, &at))
@@ -120,8 +125,8 @@ __device__ __forceinline__ bool find_work(const BwdParams& p, BwdWork* out) {
     w.first = 0;
     w.part = part;
     if (part >= 0) {
-        w.first = piece * p.plan.chunk;
-        w.items = min(max(w.items - w.first, 0), p.plan.chunk);
+        w.first = piece * plan.chunk;
+        w.items = min(max(w.items - w.first, 0), plan.chunk);
         if (piece > 0 && w.items == 0) return false;
     }
     if ((threadIdx.x & 31) == 0) *out = w;
@@ -212,31 +217,28 @@ struct DkvShape {
     // dO V^T tiles in tensor memory, beside S, dV and dK: with two the next one is formed
     // before dS of this one is
     static constexpr int kDp = DP == 128 ? 1 : 2;
-    static constexpr uint32_t kSmem = (2 + 2 * kSlots) * kTileBytes + 1024;
+    static constexpr uint32_t kRows = (2 + 2 * kSlots) * kTileBytes;  // behind the tiles
+    static constexpr uint32_t kSmem = kRows + kSlots * 2 * kTileRows * sizeof(float) + 1024;
 };
 
 template <int DP>
-__global__ void __launch_bounds__(kBwdThreads, 1)
-    attention_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
-                         const __grid_constant__ CUtensorMap map_k,
-                         const __grid_constant__ CUtensorMap map_v,
-                         const __grid_constant__ CUtensorMap map_d, const BwdParams p) {
+__device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtensorMap& map_k,
+                                          const CUtensorMap& map_v, const CUtensorMap& map_d,
+                                          const BwdParams& p, int64_t id) {
     using Sh = DkvShape<DP>;
     extern __shared__ char smem_raw[];
     __shared__ uint64_t bar_k, bar_v, bar_s, bar_dp[Sh::kDp], bar_p, bar_ds[Sh::kDp], bar_done,
         bar_raw, bar_drain;
     __shared__ uint64_t full_q[Sh::kSlots], empty_q[Sh::kSlots], full_d[Sh::kSlots],
         empty_d[Sh::kSlots];
-    __shared__ __align__(16) float rows[Sh::kSlots][2][kTileRows];  // -lse log2(e), -delta
     __shared__ uint32_t tmem_at;
     __shared__ volatile int dead;
     __shared__ BwdWork work;
     __shared__ int found;
 
-    grid_dep_sync();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
-        const bool ok = find_work<true>(p, &work);
+        const bool ok = find_work<true>(p, id, &work);
         if (lane == 0) found = ok, dead = 0;
     }
     __syncthreads();
@@ -246,6 +248,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t at_k = smem, at_v = smem + Sh::kTileBytes;
     const uint32_t at_q = smem + 2 * Sh::kTileBytes, at_d = at_q + Sh::kSlots * Sh::kTileBytes;
+    // -lse log2(e) and -delta of each slot's queries
+    auto* rows = reinterpret_cast<float(*)[2][kTileRows]>(
+        smem_raw + (smem + Sh::kRows - smem_u32(smem_raw)));
     if (warp == kMathWarps) {
         tmem_alloc(smem_u32(&tmem_at), 512);
     } else if (threadIdx.x == 0) {
@@ -487,7 +492,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const HeadView& g = half ? p.dk : p.dv;
             __nv_bfloat16* out = valid && !split ? g.row(work.sq.k0 + key, work.khead) : nullptr;
             float* part = valid && split
-                              ? p.parts + (work.part + r + (half ? 0 : part_rows(p.plan))) * DP
+                              ? p.parts_k + (work.part + r + (half ? 0 : part_rows(p.plan_k))) * DP
                               : nullptr;
             store_row<DP>((half ? t_dk : t_dv) + lanes, out, part, p.dim, half ? p.scale : 1.f,
                           items == 0);
@@ -515,11 +520,9 @@ struct DqShape {
 };
 
 template <int DP>
-__global__ void __launch_bounds__(kBwdThreads, 1)
-    attention_dq_kernel(const __grid_constant__ CUtensorMap map_q,
-                        const __grid_constant__ CUtensorMap map_k,
-                        const __grid_constant__ CUtensorMap map_v,
-                        const __grid_constant__ CUtensorMap map_d, const BwdParams p) {
+__device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtensorMap& map_k,
+                                         const CUtensorMap& map_v, const CUtensorMap& map_d,
+                                         const BwdParams& p, int64_t id) {
     using Sh = DqShape<DP>;
     extern __shared__ char smem_raw[];
     __shared__ uint64_t bar_q, bar_d, bar_s[2], bar_dp, bar_read, bar_ds[2], bar_done, bar_raw,
@@ -531,22 +534,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     __shared__ BwdWork work;
     __shared__ int found;
 
-    // No wait for the kernel before it, dK and dV's, of which it needs nothing: its blocks fill
-    // that one's last wave.  It starts once every block of that kernel has, and thus after the
-    // rows' sums that both read; it waits for it at the end, so that what follows this kernel
-    // on the stream follows both.
-    if (!p.after_dkv) grid_dep_wait();
-    grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
-        const bool ok = find_work<false>(p, &work);
+        const bool ok = find_work<false>(p, id, &work);
         if (lane == 0) found = ok, dead = 0;
     }
     __syncthreads();
-    if (!found) {
-        if (p.after_dkv) grid_dep_wait();
-        return;
-    }
+    if (!found) return;
     const int tiles = work.items;
 
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -761,7 +755,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const int c0 = half * (DP / 2);
             __nv_bfloat16* out =
                 valid && !split ? p.dq.row(work.sq.q0 + i, work.head) + c0 : nullptr;
-            float* part = valid && split ? p.parts + (work.part + r) * DP + c0 : nullptr;
+            float* part = valid && split ? p.parts_q + (work.part + r) * DP + c0 : nullptr;
             store_row<DP / 2>(t_dq + lanes + c0, out, part, p.dim - c0, p.scale, tiles == 0);
         }
     }
@@ -773,7 +767,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tmem_fence_after();
         tmem_free(tmem_at, 512);
     }
-    if (p.after_dkv) grid_dep_wait();
+}
+
+// The blocks of keys, then those of queries.
+template <int DP>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    attention_bwd_kernel(const __grid_constant__ CUtensorMap map_q,
+                         const __grid_constant__ CUtensorMap map_k,
+                         const __grid_constant__ CUtensorMap map_v,
+                         const __grid_constant__ CUtensorMap map_d, const BwdParams p) {
+    grid_dep_sync();
+    const int64_t of_keys = blocks_of(p.plan_k), id = blockIdx.x;
+    if (id < of_keys)
+        dkv_block<DP>(map_q, map_k, map_v, map_d, p, id);
+    else
+        dq_block<DP>(map_q, map_k, map_v, map_d, p, id - of_keys);
 }
 
 // The sum of a cut block's pieces, in their order, times the scale, in bfloat16.  DP / 4
@@ -785,10 +793,11 @@ __global__ void __launch_bounds__(kSumThreads) attention_sum_kernel(const BwdPar
     __shared__ Place place;
     __shared__ int found;
     grid_dep_sync();
+    const BwdPlan& plan = kKeys ? p.plan_k : p.plan_q;
     if (threadIdx.x < 32) {
         Place at{};
         const bool ok = find_place<kKeys>(p.batch, kTileRows, kKeys ? p.heads_k : p.heads_q,
-                                          (int)(p.plan.whole + blockIdx.x), &at);
+                                          (int)(plan.whole + blockIdx.x), &at);
         if (threadIdx.x == 0) place = at, found = ok;
     }
     __syncthreads();
@@ -799,17 +808,18 @@ __global__ void __launch_bounds__(kSumThreads) attention_sum_kernel(const BwdPar
     const int items = kKeys ? queries_of(sq, row0, p.batch.causal, &unused) * p.group
                             : keys_of(sq, row0, p.batch.causal);
     // a piece without work was not begun
-    const int pieces = max(1, (items + p.plan.chunk - 1) / p.plan.chunk);
+    const int pieces = max(1, (items + plan.chunk - 1) / plan.chunk);
     constexpr int kLanes = DP / 4, kRows = kSumThreads / kLanes;
     const int lane = threadIdx.x % kLanes;
     const int rows = min(kTileRows, (kKeys ? sq.m : sq.n) - row0);
     const bool of_v = kKeys && blockIdx.z == 1;
-    const float4* parts = reinterpret_cast<const float4*>(p.parts + (of_v ? part_rows(p.plan) : 0) * DP);
+    const float4* parts = reinterpret_cast<const float4*>(
+        (kKeys ? p.parts_k : p.parts_q) + (of_v ? part_rows(plan) : 0) * DP);
     const HeadView& g = kKeys ? (of_v ? p.dv : p.dk) : p.dq;
     const float f = of_v ? 1.f : p.scale;
-    const int64_t step = p.plan.rest * p.plan.slot_rows;  // rows from a piece to the next
+    const int64_t step = plan.rest * plan.slot_rows;  // rows from a piece to the next
     for (int r = blockIdx.y * kRows + threadIdx.x / kLanes; r < rows; r += gridDim.y * kRows) {
-        const int64_t at = (int64_t)blockIdx.x * p.plan.slot_rows + r;
+        const int64_t at = (int64_t)blockIdx.x * plan.slot_rows + r;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int z = 0; z < pieces; ++z) {
@@ -876,9 +886,10 @@ struct BwdMaps {
 
 template <int DP, bool kKeys>
 cudaError_t launch_sum(const BwdParams& p, cudaStream_t st) {
-    if (p.plan.pieces == 1) return cudaSuccess;
+    const BwdPlan& plan = kKeys ? p.plan_k : p.plan_q;
+    if (plan.pieces <= 1) return cudaSuccess;
     const unsigned rows = kSumThreads / (DP / 4);
-    const dim3 grid((unsigned)p.plan.rest, (p.plan.slot_rows + 2 * rows - 1) / (2 * rows),
+    const dim3 grid((unsigned)plan.rest, (plan.slot_rows + 2 * rows - 1) / (2 * rows),
                     kKeys ? 2 : 1);
     return launch(attention_sum_kernel<DP, kKeys>, grid, dim3(kSumThreads), 0, st, p);
 }
@@ -886,33 +897,19 @@ cudaError_t launch_sum(const BwdParams& p, cudaStream_t st) {
 template <int DP>
 cudaError_t launch_dim(const BwdMaps& m, BwdParams p, cudaStream_t st) {
     const Batch& v = p.batch;
-    cudaError_t e = cudaSuccess;
-    const auto blocks = [](const BwdPlan& plan) {
-        return dim3((unsigned)(plan.whole + plan.rest * plan.pieces));
-    };
-    BwdParams of_q = p;
-    p.plan = plan_dkv(v.tq, v.tk, v.batch, p.heads_q, p.heads_k, v.causal);
-    of_q.plan = plan_dq(v.tq, v.tk, v.batch, p.heads_q, v.causal);
-    of_q.parts = p.parts + 2 * part_rows(p.plan) * DP;
-    of_q.after_dkv = v.tk > 0;
-    if (v.tk > 0) {
-        e = cudaFuncSetAttribute(attention_dkv_kernel<DP>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)DkvShape<DP>::kSmem);
-        if (e == cudaSuccess)
-            e = launch(attention_dkv_kernel<DP>, blocks(p.plan), dim3(kBwdThreads),
-                       DkvShape<DP>::kSmem, st, m.q, m.k, m.v, m.d, p);
-    }
-    if (e == cudaSuccess && v.tq > 0) {
-        e = cudaFuncSetAttribute(attention_dq_kernel<DP>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)DqShape<DP>::kSmem);
-        if (e == cudaSuccess)
-            e = launch(attention_dq_kernel<DP>, blocks(of_q.plan), dim3(kBwdThreads),
-                       DqShape<DP>::kSmem, st, m.q, m.k, m.v, m.d, of_q);
-    }
-    if (e == cudaSuccess && v.tk > 0) e = launch_sum<DP, true>(p, st);
-    if (e == cudaSuccess && v.tq > 0) e = launch_sum<DP, false>(of_q, st);
+    // a side without tokens has no blocks
+    if (v.tk > 0) p.plan_k = plan_dkv(v.tq, v.tk, v.batch, p.heads_q, p.heads_k, v.causal);
+    if (v.tq > 0) p.plan_q = plan_dq(v.tq, v.tk, v.batch, p.heads_q, v.causal);
+    p.parts_q = p.parts_k + 2 * part_rows(p.plan_k) * DP;
+    constexpr uint32_t kSmem = std::max(DkvShape<DP>::kSmem, DqShape<DP>::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(
+        attention_bwd_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e == cudaSuccess)
+        e = launch(attention_bwd_kernel<DP>,
+                   dim3((unsigned)(blocks_of(p.plan_k) + blocks_of(p.plan_q))), dim3(kBwdThreads),
+                   kSmem, st, m.q, m.k, m.v, m.d, p);
+    if (e == cudaSuccess) e = launch_sum<DP, true>(p, st);
+    if (e == cudaSuccess) e = launch_sum<DP, false>(p, st);
     return e;
 }
 
@@ -958,7 +955,7 @@ cudaError_t launch_attention_bwd(const gs_attention_shape& s, const gs_heads& q,
     p.lse = lse;
     p.nlse = static_cast<float*>(ws);
     p.ndelta = p.nlse + s.tokens_q * s.heads_q;
-    p.parts = p.nlse + (s.tokens_q * s.heads_q * 2 + 63) / 64 * 64;
+    p.parts_k = p.nlse + (s.tokens_q * s.heads_q * 2 + 63) / 64 * 64;
     cudaError_t e = gave_up_word(&p.gave_up);
     if (e != cudaSuccess) return e;
     BwdMaps m;

@@ -29,14 +29,6 @@ __device__ __forceinline__ bool elect_one() {
     return ok != 0;
 }
 
-// the two halves of grid_dep_sync
-__device__ __forceinline__ void grid_dep_wait() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-__device__ __forceinline__ void grid_dep_launch() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // ---------------------------------------------------------------------------
 // mbarriers
 // ---------------------------------------------------------------------------

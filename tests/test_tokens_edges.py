@@ -2,6 +2,7 @@
 kernels must hold, the binding's refusals and the build's parts."""
 
 import os
+import re
 import subprocess
 import sys
 
@@ -53,3 +54,40 @@ print(lib.gs_attention_bwd(s, h(4), h(2), h(2), None, None, h(4), P, h(4), h(4),
                            None))""")
     assert r.returncode == 0, (r.returncode, r.stderr[-300:])
     assert set(r.stdout.split()) == {"5"}
+
+
+# ---------------------------------------------------------------------------
+# the order of dependent launches
+# ---------------------------------------------------------------------------
+def _kernels():
+    """(file, name, body) of every __global__ function of the library"""
+    csrc = os.path.join(ROOT, "differentiable_gaussian_splatting_gb300", "csrc")
+    for name in sorted(os.listdir(csrc)):
+        if not name.endswith((".cu", ".cuh")):
+            continue
+        with open(os.path.join(csrc, name)) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        for m in re.finditer(r"__global__", text):
+            start = text.index("{", m.end())
+            depth, end = 1, start + 1
+            while depth:
+                depth += {"{": 1, "}": -1}.get(text[end], 0)
+                end += 1
+            head = re.sub(r"__launch_bounds__\([^()]*\)", "", text[m.end():start])
+            yield name, re.search(r"(\w+)\s*\(", head).group(1), text[start + 1:end - 1]
+
+
+def test_every_kernel_waits_for_the_one_before_it():
+    # All kernels are launched with programmatic serialisation: only griddepcontrol.wait orders a
+    # kernel's reads after the writes of those before it, so it comes before anything but
+    # declarations, in every block, and no kernel goes without.
+    declares = re.compile(r"\s*(extern\s+)?(__shared__|constexpr|using|static_assert)\b")
+    seen = []
+    for file, name, body in _kernels():
+        first = body.split("grid_dep_sync();")[0]
+        assert first != body, (file, name, "does not wait")
+        left = [x for x in first.split(";") if x.strip() and not declares.match(x)]
+        assert not left, (file, name, left)
+        seen.append(name)
+    assert {"attention_delta_kernel", "attention_fwd_kernel", "attention_join_kernel",
+            "attention_sum_kernel", "headnorm_kernel", "dropout_add_kernel"} <= set(seen)
