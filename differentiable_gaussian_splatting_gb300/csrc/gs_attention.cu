@@ -13,7 +13,8 @@ namespace {
 
 __device__ unsigned int g_gave_up;
 
-// test only: a bounded wait for a barrier at which nothing arrives
+// test only: a warp's bounded wait in which the last lane alone waits for a phase that does not
+// come, the others for the one before it, which is done; reported if the warp gave up as one
 __global__ void waiting_kernel(unsigned int* gave_up) {
     grid_dep_sync();
     __shared__ uint64_t bar;
@@ -24,7 +25,7 @@ __global__ void waiting_kernel(unsigned int* gave_up) {
         fence_barrier_init();
     }
     __syncthreads();
-    const bool ok = mbar_wait(smem_u32(&bar), 0, &dead);
+    const bool ok = mbar_wait(smem_u32(&bar), threadIdx.x == 31 ? 0 : 1, &dead);
     if (!ok && threadIdx.x == 0) *gave_up = 1;
 }
 

@@ -352,11 +352,11 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
             constexpr uint32_t word_o = mma_word(128, DP, false, true);
             constexpr uint32_t word_dp = mma_word(128, 128, false, false);
             const uint32_t word_s = word_dp | (p.negative ? kNegateA : 0u);
-            bool ok = mbar_wait(smem_u32(&bar_k), 0, &dead);
+            bool ok = mbar_wait_one(smem_u32(&bar_k), 0, &dead);
             const auto slot_of = [&](int i) { return i % Sh::kSlots; };
             const auto parity_of = [&](int i) { return (i / Sh::kSlots) & 1; };
             const auto scores = [&](int i) {
-                ok = ok && mbar_wait(smem_u32(&full_q[slot_of(i)]), parity_of(i), &dead);
+                ok = ok && mbar_wait_one(smem_u32(&full_q[slot_of(i)]), parity_of(i), &dead);
                 if (!ok) return;
                 tmem_fence_after();
                 product_columns<DP>(t_s, operand_columns(at_k),
@@ -365,7 +365,7 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
                 mma_commit(smem_u32(&bar_s));
             };
             const auto dprobs = [&](int i) {
-                ok = ok && mbar_wait(smem_u32(&full_d[slot_of(i)]), parity_of(i), &dead);
+                ok = ok && mbar_wait_one(smem_u32(&full_d[slot_of(i)]), parity_of(i), &dead);
                 if (!ok) return;
                 tmem_fence_after();
                 const int at = i % Sh::kDp;
@@ -375,11 +375,11 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
                 mma_commit(smem_u32(&bar_dp[at]));
             };
             scores(0);
-            ok = ok && mbar_wait(smem_u32(&bar_v), 0, &dead);
+            ok = ok && mbar_wait_one(smem_u32(&bar_v), 0, &dead);
             dprobs(0);
             for (int i = 0; i < items && ok; ++i) {
                 // while the other warps form dS(i): dV, and the next scores
-                ok = mbar_wait(smem_u32(&bar_p), i & 1, &dead);
+                ok = mbar_wait_one(smem_u32(&bar_p), i & 1, &dead);
                 if (!ok) break;
                 tmem_fence_after();
                 product_rows(t_dv, t_s, 64, operand_rows(at_d + slot_of(i) * Sh::kTileBytes), word_o,
@@ -388,7 +388,7 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
                 if (i + 1 < items) scores(i + 1);
                 if (Sh::kDp == 2 && i + 1 < items) dprobs(i + 1);
                 // while they form P(i + 1): dK, and the next dO V^T
-                ok = ok && mbar_wait(smem_u32(&bar_ds[i % Sh::kDp]), (i / Sh::kDp) & 1, &dead);
+                ok = ok && mbar_wait_one(smem_u32(&bar_ds[i % Sh::kDp]), (i / Sh::kDp) & 1, &dead);
                 if (!ok) break;
                 tmem_fence_after();
                 product_rows(t_dk, t_dp + i % Sh::kDp * 128, 64, operand_rows(at_q + slot_of(i) * Sh::kTileBytes), word_o,
@@ -636,10 +636,10 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
             constexpr uint32_t word_o = mma_word(128, DP, false, true);
             constexpr uint32_t word_dp = mma_word(128, 128, false, false);
             const uint32_t word_s = word_dp | (p.negative ? kNegateA : 0u);
-            bool ok = mbar_wait(smem_u32(&bar_q), 0, &dead);
+            bool ok = mbar_wait_one(smem_u32(&bar_q), 0, &dead);
             const auto scores = [&](int j) {
                 const int sk = j % Sh::kSlotsK;
-                ok = ok && mbar_wait(smem_u32(&full_k[sk]), (j / Sh::kSlotsK) & 1, &dead);
+                ok = ok && mbar_wait_one(smem_u32(&full_k[sk]), (j / Sh::kSlotsK) & 1, &dead);
                 if (!ok) return;
                 tmem_fence_after();
                 product_columns<DP>(tmem + (j & 1) * 128, operand_columns(at_q),
@@ -648,7 +648,7 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
             };
             const auto dprobs = [&](int j) {
                 const int sv = j % Sh::kSlotsV;
-                ok = ok && mbar_wait(smem_u32(&full_v[sv]), (j / Sh::kSlotsV) & 1, &dead);
+                ok = ok && mbar_wait_one(smem_u32(&full_v[sv]), (j / Sh::kSlotsV) & 1, &dead);
                 if (!ok) return;
                 tmem_fence_after();
                 product_columns<DP>(t_dp, operand_columns(at_d),
@@ -657,17 +657,17 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
                 mma_commit(smem_u32(&empty_v[sv]));
             };
             scores(0);
-            ok = ok && mbar_wait(smem_u32(&bar_d), 0, &dead);
+            ok = ok && mbar_wait_one(smem_u32(&bar_d), 0, &dead);
             dprobs(0);
             if (tiles > 1) scores(1);
             for (int j = 0; j < tiles && ok; ++j) {
                 // the next dO V^T as soon as this one is read, while dS(j) is formed from it
                 if (j + 1 < tiles) {
-                    ok = mbar_wait(smem_u32(&bar_read), j & 1, &dead);
+                    ok = mbar_wait_one(smem_u32(&bar_read), j & 1, &dead);
                     dprobs(j + 1);
                 }
                 // dS(j) comes over S(j); two barriers, since dS(j + 1) may follow at once
-                ok = ok && mbar_wait(smem_u32(&bar_ds[j & 1]), (j >> 1) & 1, &dead);
+                ok = ok && mbar_wait_one(smem_u32(&bar_ds[j & 1]), (j >> 1) & 1, &dead);
                 if (!ok) break;
                 tmem_fence_after();
                 const int sk = j % Sh::kSlotsK;

@@ -341,8 +341,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             };
             Step ahead{0, tiles[0] > 0 ? 0 : 1, 0, 0, 0, 0, 0}, at = ahead;
             const auto scores = [&]() {
-                ok = ok && mbar_wait(smem_u32(&bar_full[ahead.slot]), ahead.phase, &dead);
-                if (ahead.j == 0) ok = ok && mbar_wait(smem_u32(&bar_q[ahead.t]), 0, &dead);
+                ok = ok && mbar_wait_one(smem_u32(&bar_full[ahead.slot]), ahead.phase, &dead);
+                if (ahead.j == 0) ok = ok && mbar_wait_one(smem_u32(&bar_q[ahead.t]), 0, &dead);
                 if (!ok) return;
                 tmem_fence_after();
                 const Step s = ahead;
@@ -354,8 +354,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             };
             for (int k = 0; k < Sh::kScores && ahead.j < most; ++k) scores();
             while (at.j < most && ok) {
-                ok = mbar_wait(smem_u32(&bar_full[at.slot + 1]), at.phase, &dead) &&
-                     mbar_wait(smem_u32(&bar_p[at.t * Sh::kScores + at.bar]), at.turn, &dead);
+                ok = mbar_wait_one(smem_u32(&bar_full[at.slot + 1]), at.phase, &dead) &&
+                     mbar_wait_one(smem_u32(&bar_p[at.t * Sh::kScores + at.bar]), at.turn, &dead);
                 if (!ok) break;
                 tmem_fence_after();
                 const Step s = at;

@@ -70,8 +70,14 @@ __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, vo
     }
     return true;
 }
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+// by one thread
+__device__ __forceinline__ bool mbar_wait_one(uint32_t bar, uint32_t parity, volatile int* dead) {
     return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, dead);
+}
+// By a whole warp, whose lanes go on or give up together: a lane may find the phase done just as
+// another's limit runs out, and what follows is in step.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+    return __all_sync(0xffffffffu, mbar_wait_one(bar, parity, dead));
 }
 
 // after a wait has given up: waits again, with the same limit, for what is in flight
