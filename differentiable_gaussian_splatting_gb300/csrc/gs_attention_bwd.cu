@@ -288,7 +288,7 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
             load_tile<Sh::kBlocks>(at_v, &map_v, smem_u32(&bar_v), work.khead, key, p.swap_v);
         }
         __syncwarp();
-        int i = 0, mends = 0;
+        int mends = 0, tiles_q = 0, tiles_d = 0;  // tiles brought into the rings
         bool ok = true;
         // one tile of queries (which = 0) or of output gradients (1) into slot `slot`
         const auto bring = [&](bool of_d, uint32_t dst, uint32_t full, int head, int i0) {
@@ -317,7 +317,7 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
         };
         int head = work.khead * p.group + work.first / per_head;
         int tile = q_first + work.first % per_head;
-        for (; i < items && ok; ++i) {
+        for (int i = 0; i < items; ++i) {
             const int slot = i % Sh::kSlots, use = i / Sh::kSlots, i0 = tile * kTileRows;
             if (use > 0) ok = mbar_wait(smem_u32(&empty_q[slot]), (use - 1) & 1, &dead);
             if (!ok) break;
@@ -333,19 +333,18 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(full);
+            ++tiles_q;
             if (use > 0) ok = mbar_wait(smem_u32(&empty_d[slot]), (use - 1) & 1, &dead);
             if (!ok) break;
             ok = bring(true, at_d + slot * Sh::kTileBytes, smem_u32(&full_d[slot]), head, i0);
+            if (!ok) break;
+            ++tiles_d;
             if (++tile == q_first + per_head) tile = q_first, ++head;
         }
-        if (!ok) {  // gave up: no copy outlives the block
-            mbar_drain(smem_u32(&bar_k), 0);
-            mbar_drain(smem_u32(&bar_v), 0);
-            for (int u = max(0, i + 1 - Sh::kSlots); u <= i; ++u) {
-                mbar_drain(smem_u32(&full_q[u % Sh::kSlots]), (u / Sh::kSlots) & 1);
-                mbar_drain(smem_u32(&full_d[u % Sh::kSlots]), (u / Sh::kSlots) & 1);
-            }
-        }
+        mbar_drain(smem_u32(&bar_k), 0);
+        mbar_drain(smem_u32(&bar_v), 0);
+        drain_ring<Sh::kSlots>(full_q, tiles_q);
+        drain_ring<Sh::kSlots>(full_d, tiles_d);
     } else if (items > 0 && warp == kMathWarps) {
         // ---- the products ----
         if (elect_one()) {
@@ -397,10 +396,8 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
                 if (Sh::kDp == 1 && i + 1 < items) dprobs(i + 1);
             }
             if (ok) mma_commit(smem_u32(&bar_done));
-            if (!ok) {  // leave no product in flight
-                mma_commit(smem_u32(&bar_drain));
-                mbar_drain(smem_u32(&bar_drain), 0);
-            }
+            mma_commit(smem_u32(&bar_drain));
+            mbar_drain(smem_u32(&bar_drain), 0);
         }
     } else if (warp < kMathWarps) {
         // ---- P and dS: one key a thread, half of the tile's queries ----
@@ -584,9 +581,9 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
             load_tile<Sh::kBlocks>(at_d, &map_d, smem_u32(&bar_d), work.head, q, p.swap_d);
         }
         __syncwarp();
-        int j = 0;
+        int tiles_k = 0, tiles_v = 0;  // tiles brought into the rings
         bool ok = true;
-        for (; j < tiles && ok; ++j) {
+        for (int j = 0; j < tiles; ++j) {
             const int sk = j % Sh::kSlotsK, uk = j / Sh::kSlotsK;
             const int sv = j % Sh::kSlotsV, uv = j / Sh::kSlotsV;
             const int64_t token = k0 + (int64_t)j * kTileRows;
@@ -613,6 +610,7 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
                 if (elect_one()) mbar_arrive(full);
                 __syncwarp();
             }
+            ++tiles_k;
             if (uv > 0) ok = mbar_wait(smem_u32(&empty_v[sv]), (uv - 1) & 1, &dead);
             if (!ok) break;
             if (elect_one()) {
@@ -620,16 +618,13 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
                 load_tile<Sh::kBlocks>(at_v + sv * Sh::kTileBytes, &map_v, smem_u32(&full_v[sv]),
                                        khead, token, p.swap_v);
             }
+            ++tiles_v;
             __syncwarp();
         }
-        if (!ok) {  // gave up: no copy outlives the block
-            mbar_drain(smem_u32(&bar_q), 0);
-            mbar_drain(smem_u32(&bar_d), 0);
-            for (int u = max(0, j + 1 - Sh::kSlotsK); u <= j; ++u)
-                mbar_drain(smem_u32(&full_k[u % Sh::kSlotsK]), (u / Sh::kSlotsK) & 1);
-            for (int u = max(0, j - Sh::kSlotsV); u < j; ++u)
-                mbar_drain(smem_u32(&full_v[u % Sh::kSlotsV]), (u / Sh::kSlotsV) & 1);
-        }
+        mbar_drain(smem_u32(&bar_q), 0);
+        mbar_drain(smem_u32(&bar_d), 0);
+        drain_ring<Sh::kSlotsK>(full_k, tiles_k);
+        drain_ring<Sh::kSlotsV>(full_v, tiles_v);
     } else if (tiles > 0 && warp == kMathWarps) {
         // ---- the products ----
         if (elect_one()) {
@@ -677,10 +672,8 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
                 if (j + 2 < tiles) scores(j + 2);
             }
             if (ok) mma_commit(smem_u32(&bar_done));
-            if (!ok) {  // leave no product in flight
-                mma_commit(smem_u32(&bar_drain));
-                mbar_drain(smem_u32(&bar_drain), 0);
-            }
+            mma_commit(smem_u32(&bar_drain));
+            mbar_drain(smem_u32(&bar_drain), 0);
         }
     } else if (warp < kMathWarps) {
         // ---- dS: one query a thread, half of the tile's keys ----

@@ -299,12 +299,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 }
                 __syncwarp();
             }
-            if (i < 2 * most) {  // gave up: no copy outlives the block
-                for (int t = 0; t < 2; ++t)
-                    if (tiles[t] > 0) mbar_drain(smem_u32(&bar_q[t]), 0);
-                for (int u = max(0, i - Sh::kSlots); u < i; ++u)
-                    mbar_drain(smem_u32(&bar_full[u % Sh::kSlots]), (u / Sh::kSlots) & 1);
-            }
+            for (int t = 0; t < 2; ++t)
+                if (tiles[t] > 0) mbar_drain(smem_u32(&bar_q[t]), 0);
+            drain_ring<Sh::kSlots>(bar_full, i);
         }
     } else if (warp == kSoftmaxWarps) {
         // ---- the products ----
@@ -365,10 +362,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 if (ahead.j < most) scores();
                 if (advance(at)) mma_commit(smem_u32(&bar_empty[s.slot + 1]));
             }
-            if (!ok) {  // leave no product in flight
-                mma_commit(smem_u32(&bar_drain));
-                mbar_drain(smem_u32(&bar_drain), 0);
-            }
+            mma_commit(smem_u32(&bar_drain));
+            mbar_drain(smem_u32(&bar_drain), 0);
         }
     } else {
         // ---- softmax: one row a thread ----

@@ -80,11 +80,18 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     return __all_sync(0xffffffffu, mbar_wait_one(bar, parity, dead));
 }
 
-// after a wait has given up: waits again, with the same limit, for what is in flight
+// A block ends when its own copies and products have: whoever issued them waits for them last
+// of all, with the same limit, whether or not a wait of the block has given up.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
     const long long t0 = clock64();
     while (!mbar_try(bar, parity) && clock64() - t0 < kWaitClocks) {
     }
+}
+// the last of `items` copies that went round a ring of kSlots barriers
+template <int kSlots>
+__device__ __forceinline__ void drain_ring(const uint64_t* full, int items) {
+    for (int u = max(0, items - kSlots); u < items; ++u)
+        mbar_drain(smem_u32(&full[u % kSlots]), (u / kSlots) & 1);
 }
 
 // writes of ordinary stores become visible to TMA and the tensor cores

@@ -91,3 +91,28 @@ def test_every_kernel_waits_for_the_one_before_it():
         seen.append(name)
     assert {"attention_delta_kernel", "attention_fwd_kernel", "attention_join_kernel",
             "attention_sum_kernel", "headnorm_kernel", "dropout_add_kernel"} <= set(seen)
+
+
+def _source(name):
+    path = os.path.join(ROOT, "differentiable_gaussian_splatting_gb300", "csrc", name)
+    with open(path) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+@pytest.mark.parametrize("file,roles", [("gs_attention_fwd.cu", 1), ("gs_attention_bwd.cu", 2)])
+def test_no_copy_or_product_outlives_a_block(file, roles):
+    # Whoever issued asynchronous work waits for it last of all, in every case: a producer that
+    # has issued its last tile may find that another warp has given up.  (What such a block does
+    # cannot be run: here the sources are held to it.)
+    text = _source(file)
+    guards = re.findall(r"if \(([^{}]*)\) \{([^{}]*)\}", text)
+    for condition, body in guards:
+        if "drain_ring" in body or "&bar_drain" in body:
+            raise AssertionError(("waited for under a condition", condition))
+    assert len(re.findall(r"mma_commit\(smem_u32\(&bar_drain\)\);\s*"
+                          r"mbar_drain\(smem_u32\(&bar_drain\), 0\);", text)) == roles
+    rings = set(re.findall(r"drain_ring<Sh::\w+>\((\w+), \w+\)", text))
+    assert rings == ({"bar_full"} if roles == 1 else {"full_q", "full_d", "full_k", "full_v"})
+    # tiles that are loaded once, outside the rings
+    once = set(re.findall(r"mbar_drain\(smem_u32\(&(bar_[qkvd])", text))
+    assert once == ({"bar_q"} if roles == 1 else {"bar_q", "bar_k", "bar_v", "bar_d"})
