@@ -114,5 +114,5 @@ def test_no_copy_or_product_outlives_a_block(file, roles):
     rings = set(re.findall(r"drain_ring<Sh::\w+>\((\w+), \w+\)", text))
     assert rings == ({"bar_full"} if roles == 1 else {"full_q", "full_d", "full_k", "full_v"})
     # tiles that are loaded once, outside the rings
-    once = set(re.findall(r"mbar_drain\(smem_u32\(&(bar_[qkvd])", text))
+    once = set(re.findall(r"mbar_drain\(smem_u32\(&(bar_[qkvd])\b", text))
     assert once == ({"bar_q"} if roles == 1 else {"bar_q", "bar_k", "bar_v", "bar_d"})
