@@ -595,7 +595,8 @@ def gs_attention_bwd(q, k, v, out, lse, dout, dq, dk, dv, workspace, cu_q=None, 
 
 def gs_attention_status(stream=None) -> None:
     """Waits for the stream; raises GSError status 4 if a bounded device wait of an attention
-    call on this device has given up since the last such check."""
+    call on this device has given up since this thread's last such check (or ever, at its
+    first)."""
     _check("gs_attention_status", library().gs_attention_status(_stream(stream)))
 
 

@@ -222,7 +222,7 @@ gs_status gs_attention_bwd(const gs_attention_shape* shape, const gs_heads* q, c
 }
 
 gs_status gs_attention_status(void* stream) {
-    unsigned int gave_up = 0;
+    bool gave_up = false;
     const cudaError_t e = attention_gave_up((cudaStream_t)stream, &gave_up);
     if (e != cudaSuccess) return GS_ERR_CUDA;
     return gave_up ? GS_ERR_TIMEOUT : GS_OK;

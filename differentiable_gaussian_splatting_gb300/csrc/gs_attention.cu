@@ -1,5 +1,5 @@
 // gs_attention.cu -- host parts that the attention kernels share: tensor maps, the size of
-// the workspace, and the word that reports a wait that gave up.
+// the workspace, and the count of blocks in which a wait gave up.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -11,7 +11,7 @@
 namespace gs {
 namespace {
 
-__device__ unsigned int g_gave_up;
+__device__ unsigned int g_gave_up;  // only ever counted up: every thread of the host compares
 
 // test only: a warp's bounded wait in which the last lane alone waits for a phase that does not
 // come, the others for the one before it, which is done; reported if the warp gave up as one
@@ -26,7 +26,7 @@ __global__ void waiting_kernel(unsigned int* gave_up) {
     }
     __syncthreads();
     const bool ok = mbar_wait(smem_u32(&bar), threadIdx.x == 31 ? 0 : 1, &dead);
-    if (!ok && threadIdx.x == 0) *gave_up = 1;
+    if (!ok && threadIdx.x == 0) atomicAdd(gave_up, 1u);
 }
 
 }  // namespace
@@ -38,14 +38,22 @@ cudaError_t gave_up_word(unsigned int** word) {
     return e;
 }
 
-cudaError_t attention_gave_up(cudaStream_t st, unsigned int* gave_up) {
-    unsigned int* word = nullptr;
-    cudaError_t e = gave_up_word(&word);
+cudaError_t attention_gave_up(cudaStream_t st, bool* gave_up) {
+    // what this thread has been told of: a report to one thread takes it from no other
+    constexpr int kDevices = 64;
+    static thread_local unsigned int told[kDevices];
+    unsigned int *word = nullptr, count = 0;
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess && device >= kDevices) e = cudaErrorInvalidDevice;
+    if (e == cudaSuccess) e = gave_up_word(&word);
     if (e == cudaSuccess)
-        e = cudaMemcpyAsync(gave_up, word, sizeof(*word), cudaMemcpyDeviceToHost, st);
+        e = cudaMemcpyAsync(&count, word, sizeof(count), cudaMemcpyDeviceToHost, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e == cudaSuccess && *gave_up) e = cudaMemsetAsync(word, 0, sizeof(*word), st);
-    return e;
+    if (e != cudaSuccess) return e;
+    *gave_up = count != told[device];
+    told[device] = count;
+    return cudaSuccess;
 }
 
 cudaError_t head_map(CUtensorMap* map, const void* data, int64_t ts, int64_t hs, int64_t tokens,

@@ -194,7 +194,7 @@ __device__ __forceinline__ void zero_rows(char* tile, int first) {
                 make_uint4(0, 0, 0, 0);
 }
 
-// Device address of the word that is set when a bounded wait of an attention kernel gave up.
+// Device address of the count of blocks in which a bounded wait of an attention kernel gave up.
 cudaError_t gave_up_word(unsigned int** word);
 
 // Tensor map of a [tokens][heads][dim] array: tiles of 128 tokens of one head, 64 values

@@ -497,7 +497,7 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
     }
     tmem_fence_before();
     __syncthreads();
-    if (dead && threadIdx.x == 0) *p.gave_up = 1;
+    if (dead && threadIdx.x == 0) atomicAdd(p.gave_up, 1u);
     if (warp == kMathWarps) {
         __syncwarp();
         tmem_fence_after();
@@ -754,7 +754,7 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
     }
     tmem_fence_before();
     __syncthreads();
-    if (dead && threadIdx.x == 0) *p.gave_up = 1;
+    if (dead && threadIdx.x == 0) atomicAdd(p.gave_up, 1u);
     if (warp == kMathWarps) {
         __syncwarp();
         tmem_fence_after();

@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
     tmem_fence_before();
     __syncthreads();
-    if (dead && threadIdx.x == 0) *p.gave_up = 1;
+    if (dead && threadIdx.x == 0) atomicAdd(p.gave_up, 1u);
     if (warp == kSoftmaxWarps) {
         __syncwarp();
         tmem_fence_after();

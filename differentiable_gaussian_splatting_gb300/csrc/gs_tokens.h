@@ -51,7 +51,7 @@ cudaError_t launch_attention_bwd(const gs_attention_shape& s, const gs_heads& q,
                                  const gs_heads& dv, const int32_t* cu_q, const int32_t* cu_k,
                                  void* ws, cudaStream_t st);
 
-// whether a wait of an attention kernel has given up since the last call (waits for st)
-cudaError_t attention_gave_up(cudaStream_t st, unsigned int* gave_up);
+// whether a wait of an attention kernel has given up since this thread's last call (waits for st)
+cudaError_t attention_gave_up(cudaStream_t st, bool* gave_up);
 
 }  // namespace gs

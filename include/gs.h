@@ -547,10 +547,11 @@ gs_status gs_attention_bwd(const gs_attention_shape* shape, const gs_heads* q, c
                            void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * gs_attention_status -- whether a bounded device wait of an attention call has given up on
- * the current device since the last such query: GS_ERR_TIMEOUT then, and the results of the
- * calls since are not to be used.  Waits for the stream.  (Every wait inside the attention
- * kernels gives up after some seconds instead of hanging; none should.)
+ * gs_attention_status -- whether a bounded device wait of an attention call, of any thread and
+ * stream, has given up on the current device since the calling thread's last such query there
+ * (or ever, at its first): GS_ERR_TIMEOUT then, and the results of the calls since are not to
+ * be used.  Waits for the stream.  (Every wait inside the attention kernels gives up after some
+ * seconds instead of hanging; none should.)
  */
 gs_status gs_attention_status(void* stream);
 
