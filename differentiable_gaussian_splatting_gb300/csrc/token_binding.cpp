@@ -112,6 +112,15 @@ void* stream_of(PyObject* o) {
     return p;
 }
 
+// The library's call, without the interpreter's lock: a launch may wait for room in the queue.
+template <typename F, typename... A>
+gs_status unlocked(F* call, const A&... args) {
+    PyThreadState* thread = PyEval_SaveThread();
+    const gs_status st = call(args...);
+    PyEval_RestoreThread(thread);
+    return st;
+}
+
 struct Norm {
     int64_t tokens;
     int32_t hq, hk, dim;
@@ -156,8 +165,8 @@ Norm norm_of(PyObject* const* a, PyObject* eps, PyObject* interleaved) {
 gs_status qk_norm_rope(PyObject* const* a) {
     const Norm n = norm_of(a, a[8], a[9]);
     const gs_heads qo = heads(a[6], "q_out", n.type, n.tq), ko = heads(a[7], "k_out", n.type, n.tk);
-    return gs_qk_norm_rope(n.tokens, n.hq, n.hk, n.dim, &n.norm, &n.q, &n.k, n.qw, n.kw, n.table,
-                           n.positions, &qo, &ko, stream_of(a[10]));
+    return unlocked(gs_qk_norm_rope, n.tokens, n.hq, n.hk, n.dim, &n.norm, &n.q, &n.k, n.qw, n.kw,
+                    n.table, n.positions, &qo, &ko, stream_of(a[10]));
 }
 
 gs_status qk_norm_rope_bwd(PyObject* const* a) {
@@ -167,9 +176,9 @@ gs_status qk_norm_rope_bwd(PyObject* const* a) {
     float* dqw = static_cast<float*>(flat(a[10], "dq_weight", ScalarType::Float, n.dim, true));
     float* dkw = static_cast<float*>(flat(a[11], "dk_weight", ScalarType::Float, n.dim, true));
     const Bytes ws = workspace(a[12]);
-    return gs_qk_norm_rope_bwd(n.tokens, n.hq, n.hk, n.dim, &n.norm, &n.q, &n.k, n.qw, n.kw, n.table,
-                               n.positions, &yq, &yk, &dq, &dk, dqw, dkw, ws.p, ws.n,
-                               stream_of(a[15]));
+    return unlocked(gs_qk_norm_rope_bwd, n.tokens, n.hq, n.hk, n.dim, &n.norm, &n.q, &n.k, n.qw, n.kw,
+                    n.table, n.positions, &yq, &yk, &dq, &dk, dqw, dkw, ws.p, ws.n,
+                    stream_of(a[15]));
 }
 
 struct Attention {
@@ -218,8 +227,8 @@ gs_status attention_fwd(PyObject* const* a) {
     float* lse = static_cast<float*>(
         flat(a[4], "lse", ScalarType::Float, t.shape.tokens_q * t.shape.heads_q));
     const Bytes ws = workspace(a[5]);
-    return gs_attention_fwd(&t.shape, &t.q, &t.k, &t.v, t.cu_q, t.cu_k, &out, lse, ws.p, ws.n,
-                            stream_of(a[10]));
+    return unlocked(gs_attention_fwd, &t.shape, &t.q, &t.k, &t.v, t.cu_q, t.cu_k, &out, lse, ws.p,
+                    ws.n, stream_of(a[10]));
 }
 
 gs_status attention_bwd(PyObject* const* a) {
@@ -231,8 +240,8 @@ gs_status attention_bwd(PyObject* const* a) {
     const float* lse = static_cast<float*>(
         flat(a[4], "lse", ScalarType::Float, t.shape.tokens_q * t.shape.heads_q));
     const Bytes ws = workspace(a[9]);
-    return gs_attention_bwd(&t.shape, &t.q, &t.k, &t.v, t.cu_q, t.cu_k, &out, lse, &dout, &dq, &dk,
-                            &dv, ws.p, ws.n, stream_of(a[14]));
+    return unlocked(gs_attention_bwd, &t.shape, &t.q, &t.k, &t.v, t.cu_q, t.cu_k, &out, lse, &dout,
+                    &dq, &dk, &dv, ws.p, ws.n, stream_of(a[14]));
 }
 
 const int64_t* rng_of(PyObject* o) {
@@ -246,7 +255,8 @@ gs_status dropout_add(PyObject* const* a) {
     const int64_t n = THPVariable_Unpack(a[0]).numel();
     const void* residual = flat(a[1], "residual", type, n, true);
     void* out = flat(a[2], "out", type, n);
-    return gs_dropout_add(n, kind, x, residual, out, rng_of(a[3]), number(a[4]), stream_of(a[5]));
+    return unlocked(gs_dropout_add, n, kind, x, residual, out, rng_of(a[3]), number(a[4]),
+                    stream_of(a[5]));
 }
 
 gs_status dropout_add_bwd(PyObject* const* a) {
@@ -255,7 +265,7 @@ gs_status dropout_add_bwd(PyObject* const* a) {
     const void* dout = flat(a[0], "dout", type, 0);
     const int64_t n = THPVariable_Unpack(a[0]).numel();
     void* dx = flat(a[1], "dx", type, n);
-    return gs_dropout_add_bwd(n, kind, dout, dx, rng_of(a[2]), number(a[3]), stream_of(a[4]));
+    return unlocked(gs_dropout_add_bwd, n, kind, dout, dx, rng_of(a[2]), number(a[3]), stream_of(a[4]));
 }
 
 // a call with its number of arguments; no C++ exception leaves it

@@ -3,6 +3,7 @@ kernels must hold, the binding's refusals and the build's parts."""
 
 import os
 import re
+import shutil
 import subprocess
 import sys
 
@@ -116,3 +117,76 @@ def test_no_copy_or_product_outlives_a_block(file, roles):
     # tiles that are loaded once, outside the rings
     once = set(re.findall(r"mbar_drain\(smem_u32\(&(bar_[qkvd])\b", text))
     assert once == ({"bar_q"} if roles == 1 else {"bar_q", "bar_k", "bar_v", "bar_d"})
+
+
+# ---------------------------------------------------------------------------
+# the binding, on tensors that have a shape and a CUDA device but no memory
+# ---------------------------------------------------------------------------
+@pytest.fixture
+def fake():
+    import torch
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    def make(*shape, dtype=torch.bfloat16):
+        with FakeTensorMode():
+            return torch.empty(shape, dtype=dtype, device="cuda")
+
+    return make
+
+
+SLOW_LIBRARY = """
+#include <unistd.h>
+extern "C" {
+int gs_qk_norm_rope(...) { return 0; }
+int gs_qk_norm_rope_bwd(...) { return 0; }
+int gs_attention_fwd(...) { return 0; }
+int gs_attention_bwd(...) { return 0; }
+int gs_dropout_add(...) { usleep(500000); return 0; }
+int gs_dropout_add_bwd(...) { return 0; }
+}
+"""
+
+SLOW_CALL = """
+import importlib.machinery, importlib.util, threading, time, sys
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+
+loader = importlib.machinery.ExtensionFileLoader("gs_token_binding", sys.argv[1])
+calls = importlib.util.module_from_spec(importlib.util.spec_from_loader("gs_token_binding", loader))
+loader.exec_module(calls)
+with FakeTensorMode():
+    x = torch.empty(0, device="cuda")
+    rng = torch.empty(2, dtype=torch.int64, device="cuda")
+calls.dropout_add(x, None, x, rng, 0.1, 0)
+stop, ticks = False, []
+
+def tick():
+    while not stop:
+        ticks.append(time.monotonic())
+        time.sleep(0.01)
+
+t = threading.Thread(target=tick)
+t.start()
+time.sleep(0.05)
+a = time.monotonic()
+calls.dropout_add(x, None, x, rng, 0.1, 0)
+b = time.monotonic()
+stop = True
+t.join()
+print(sum(a < x < b for x in ticks), b - a)
+"""
+
+
+def test_a_call_that_waits_lets_other_threads_run(tmp_path):
+    # a launch that waits for room in the queue: here a library whose call takes half a second
+    from differentiable_gaussian_splatting_gb300 import build
+
+    (tmp_path / "slow.cpp").write_text(SLOW_LIBRARY)
+    subprocess.run(["g++", "-shared", "-fPIC", "-Wl,-soname,libgs.so", "-o",
+                    str(tmp_path / "libgs.so"), str(tmp_path / "slow.cpp")], check=True)
+    copy = shutil.copy(build.BINDING, tmp_path)
+    r = subprocess.run([sys.executable, "-c", SLOW_CALL, copy], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stderr[-500:]
+    ticks, seconds = r.stdout.split()
+    assert float(seconds) > 0.4 and int(ticks) >= 5, r.stdout
