@@ -601,8 +601,8 @@ def gs_attention_status(stream=None) -> None:
 
 
 def gs_dropout_add(x, residual, out, rng, p, stream=None):
-    """out = residual + dropout(x) (see gs.h); residual may be None, out may be x or residual;
-    rng: CUDA int64[2], seed and offset."""
+    """out = residual + dropout(x) (see gs.h), all of one shape; residual may be None, out may be
+    x or residual; rng: CUDA int64[2], seed and offset."""
     st = (_calls or _token_calls()).dropout_add(x, residual, out, rng, p, stream)
     if st:
         _check("gs_dropout_add", st)

@@ -76,6 +76,24 @@ void* flat(PyObject* o, const char* name, ScalarType type, int64_t n, bool optio
     return address(t);
 }
 
+// a contiguous tensor of exactly the shape of `like`, or null where it may be None
+void* alike(PyObject* o, const char* name, const Tensor& like, bool optional = false) {
+    void* p = flat(o, name, like.scalar_type(), 0, optional);
+    if (o != Py_None && THPVariable_Unpack(o).sizes() != like.sizes())
+        throw ValueError(text(name, ": expected shape ", like.sizes(), ", got ",
+                              THPVariable_Unpack(o).sizes()));
+    return p;
+}
+
+// head_dim values of fp32 (weights, which all heads share, or their gradient), or null for None
+float* weights(PyObject* o, const char* name, int64_t dim) {
+    void* p = flat(o, name, ScalarType::Float, dim, true);
+    if (o != Py_None && THPVariable_Unpack(o).numel() != dim)
+        throw ValueError(text(name, ": expected ", dim, " values, got ",
+                              THPVariable_Unpack(o).sizes()));
+    return static_cast<float*>(p);
+}
+
 struct Bytes {
     void* p;
     size_t n;
@@ -147,8 +165,8 @@ Norm norm_of(PyObject* const* a, PyObject* eps, PyObject* interleaved) {
     if (r.tk->size(0) != r.tokens || r.tk->size(2) != r.dim)
         throw ValueError(text("k: expected ", r.tokens, " tokens of ", r.dim,
                               " values a head, got ", r.tk->sizes()));
-    r.qw = static_cast<float*>(flat(a[2], "q_weight", ScalarType::Float, r.dim, true));
-    r.kw = static_cast<float*>(flat(a[3], "k_weight", ScalarType::Float, r.dim, true));
+    r.qw = weights(a[2], "q_weight", r.dim);
+    r.kw = weights(a[3], "k_weight", r.dim);
     if (a[4] != Py_None) {
         if (!THPVariable_Check(a[4]) || THPVariable_Unpack(a[4]).dim() != 2)
             throw ValueError("cos_sin: expected a [rows, rot] tensor");
@@ -173,8 +191,7 @@ gs_status qk_norm_rope_bwd(PyObject* const* a) {
     const Norm n = norm_of(a, a[13], a[14]);
     const gs_heads yq = heads(a[6], "dq_out", n.type, n.tq), yk = heads(a[7], "dk_out", n.type, n.tk),
                    dq = heads(a[8], "dq", n.type, n.tq), dk = heads(a[9], "dk", n.type, n.tk);
-    float* dqw = static_cast<float*>(flat(a[10], "dq_weight", ScalarType::Float, n.dim, true));
-    float* dkw = static_cast<float*>(flat(a[11], "dk_weight", ScalarType::Float, n.dim, true));
+    float *dqw = weights(a[10], "dq_weight", n.dim), *dkw = weights(a[11], "dk_weight", n.dim);
     const Bytes ws = workspace(a[12]);
     return unlocked(gs_qk_norm_rope_bwd, n.tokens, n.hq, n.hk, n.dim, &n.norm, &n.q, &n.k, n.qw, n.kw,
                     n.table, n.positions, &yq, &yk, &dq, &dk, dqw, dkw, ws.p, ws.n,
@@ -252,9 +269,10 @@ gs_status dropout_add(PyObject* const* a) {
     ScalarType type;
     const int32_t kind = element_type(a[0], "x", &type);
     const void* x = flat(a[0], "x", type, 0);
-    const int64_t n = THPVariable_Unpack(a[0]).numel();
-    const void* residual = flat(a[1], "residual", type, n, true);
-    void* out = flat(a[2], "out", type, n);
+    const Tensor& t = THPVariable_Unpack(a[0]);
+    const int64_t n = t.numel();
+    const void* residual = alike(a[1], "residual", t, true);
+    void* out = alike(a[2], "out", t);
     return unlocked(gs_dropout_add, n, kind, x, residual, out, rng_of(a[3]), number(a[4]),
                     stream_of(a[5]));
 }
@@ -263,8 +281,9 @@ gs_status dropout_add_bwd(PyObject* const* a) {
     ScalarType type;
     const int32_t kind = element_type(a[0], "dout", &type);
     const void* dout = flat(a[0], "dout", type, 0);
-    const int64_t n = THPVariable_Unpack(a[0]).numel();
-    void* dx = flat(a[1], "dx", type, n);
+    const Tensor& t = THPVariable_Unpack(a[0]);
+    const int64_t n = t.numel();
+    void* dx = alike(a[1], "dx", t);
     return unlocked(gs_dropout_add_bwd, n, kind, dout, dx, rng_of(a[2]), number(a[3]), stream_of(a[4]));
 }
 

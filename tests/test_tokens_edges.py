@@ -190,3 +190,39 @@ def test_a_call_that_waits_lets_other_threads_run(tmp_path):
     assert r.returncode == 0, r.stderr[-500:]
     ticks, seconds = r.stdout.split()
     assert float(seconds) > 0.4 and int(ticks) >= 5, r.stdout
+
+
+def test_dropout_arrays_have_one_shape(fake):
+    # elements are taken by flat index: another shape would be added in the wrong places
+    import torch
+
+    import differentiable_gaussian_splatting_gb300 as gs
+
+    f32 = torch.float32
+    x, rng = fake(4, 6, dtype=f32), fake(2, dtype=torch.int64)
+    for bad in (fake(4, 8, dtype=f32), fake(8, 6, dtype=f32), fake(6, 4, dtype=f32),
+                fake(24, dtype=f32), fake(25, dtype=f32), fake(1, 6, dtype=f32)):
+        with pytest.raises(ValueError, match="residual"):
+            gs.gs_dropout_add(x, bad, x, rng, 0.1, stream=0)
+        with pytest.raises(ValueError, match="out"):
+            gs.gs_dropout_add(x, None, bad, rng, 0.1, stream=0)
+        with pytest.raises(ValueError, match="dx"):
+            gs.gs_dropout_add_bwd(x, bad, rng, 0.1, stream=0)
+    with pytest.raises(ValueError, match="residual"):
+        gs.gs_dropout_add(x, fake(4, 6), x, rng, 0.1, stream=0)
+
+
+def test_head_norm_weights_are_those_of_one_head(fake):
+    import torch
+
+    import differentiable_gaussian_splatting_gb300 as gs
+
+    x, ws = fake(0, 2, 64), fake(1, dtype=torch.uint8)
+    good, bad = fake(64, dtype=torch.float32), fake(2, 64, dtype=torch.float32)
+    for name, args in (("q_weight", (bad, None)), ("k_weight", (good, bad))):
+        with pytest.raises(ValueError, match=name):
+            gs.gs_qk_norm_rope(x, x, *args, None, None, x, x, stream=0)
+    for name, args in (("dq_weight", (bad, None)), ("dk_weight", (good, bad))):
+        with pytest.raises(ValueError, match=name):
+            gs.gs_qk_norm_rope_bwd(x, x, good, good, None, None, x, x, x, x, *args, ws, stream=0)
+    gs.gs_qk_norm_rope(x, x, good, good, None, None, x, x, stream=0)  # no tokens: nothing to do
