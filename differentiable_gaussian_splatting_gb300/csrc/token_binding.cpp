@@ -118,11 +118,17 @@ float number(PyObject* o) {
     return (float)v;
 }
 
+// what an object is as a condition; one that has no truth value raises
+int32_t truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw TypeError("");
+    return v;
+}
+
 // None: torch's current stream; an address; or an object with cuda_stream
 void* stream_of(PyObject* o) {
     if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
-    if (PyLong_Check(o)) return PyLong_AsVoidPtr(o);
-    PyObject* v = PyObject_GetAttrString(o, "cuda_stream");
+    PyObject* v = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
     if (!v) throw TypeError("");
     void* p = PyLong_AsVoidPtr(v);
     Py_DECREF(v);
@@ -176,7 +182,7 @@ Norm norm_of(PyObject* const* a, PyObject* eps, PyObject* interleaved) {
     }
     r.positions = static_cast<int32_t*>(flat(a[5], "positions", ScalarType::Int, r.tokens, true));
     r.norm.eps = number(eps);
-    r.norm.interleaved = PyObject_IsTrue(interleaved);
+    r.norm.interleaved = truth(interleaved);
     return r;
 }
 
@@ -233,7 +239,7 @@ Attention attention_of(PyObject* q, PyObject* k, PyObject* v, PyObject* cu_q, Py
     r.shape.heads_q = (int32_t)r.tq->size(1);
     r.shape.heads_k = (int32_t)r.tk->size(1);
     r.shape.head_dim = (int32_t)dim;
-    r.shape.causal = PyObject_IsTrue(causal);
+    r.shape.causal = truth(causal);
     r.shape.scale = scale == Py_None ? (float)(1.0 / std::sqrt((double)dim)) : number(scale);
     return r;
 }

@@ -226,3 +226,28 @@ def test_head_norm_weights_are_those_of_one_head(fake):
         with pytest.raises(ValueError, match=name):
             gs.gs_qk_norm_rope_bwd(x, x, good, good, None, None, x, x, x, x, *args, ws, stream=0)
     gs.gs_qk_norm_rope(x, x, good, good, None, None, x, x, stream=0)  # no tokens: nothing to do
+
+
+class _NoTruth:
+    def __bool__(self):
+        raise ZeroDivisionError("no truth value")
+
+
+def test_conditions_and_streams_that_raise(fake):
+    # the caller's own error comes out, and nothing is called with what was left in its place
+    import torch
+
+    import differentiable_gaussian_splatting_gb300 as gs
+
+    x, ws = fake(0, 2, 64), fake(1, dtype=torch.uint8)
+    lse, rng = fake(2, 0, dtype=torch.float32), fake(2, dtype=torch.int64)
+    with pytest.raises(ZeroDivisionError):
+        gs.gs_qk_norm_rope(x, x, None, None, None, None, x, x, interleaved=_NoTruth(), stream=0)
+    with pytest.raises(ZeroDivisionError):
+        gs.gs_attention_fwd(x, x, x, x, lse, ws, causal=_NoTruth(), stream=0)
+    with pytest.raises(OverflowError):
+        gs.gs_dropout_add(x, None, x, rng, 0.1, stream=1 << 80)
+    with pytest.raises(TypeError):
+        gs.gs_dropout_add(x, None, x, rng, "half", stream=0)
+    with pytest.raises(AttributeError):
+        gs.gs_dropout_add(x, None, x, rng, 0.1, stream="main")
