@@ -9,6 +9,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <cstdint>
 #include <exception>
 #include <sstream>
 #include <stdexcept>
@@ -125,6 +126,12 @@ int32_t truth(PyObject* o) {
     return v;
 }
 
+// a tensor's size where the library takes 32 bits
+int32_t small(int64_t n, const char* name) {
+    if (n > INT32_MAX) throw ValueError(text(name, ": a dimension of ", n, " is too large"));
+    return (int32_t)n;
+}
+
 // None: torch's current stream; an address; or an object with cuda_stream
 void* stream_of(PyObject* o) {
     if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
@@ -165,9 +172,9 @@ Norm norm_of(PyObject* const* a, PyObject* eps, PyObject* interleaved) {
     r.tq = &THPVariable_Unpack(a[0]);
     r.tk = &THPVariable_Unpack(a[1]);
     r.tokens = r.tq->size(0);
-    r.hq = (int32_t)r.tq->size(1);
-    r.hk = (int32_t)r.tk->size(1);
-    r.dim = (int32_t)r.tq->size(2);
+    r.hq = small(r.tq->size(1), "q");
+    r.hk = small(r.tk->size(1), "k");
+    r.dim = small(r.tq->size(2), "q");
     if (r.tk->size(0) != r.tokens || r.tk->size(2) != r.dim)
         throw ValueError(text("k: expected ", r.tokens, " tokens of ", r.dim,
                               " values a head, got ", r.tk->sizes()));
@@ -178,7 +185,7 @@ Norm norm_of(PyObject* const* a, PyObject* eps, PyObject* interleaved) {
             throw ValueError("cos_sin: expected a [rows, rot] tensor");
         r.table = static_cast<float*>(flat(a[4], "cos_sin", ScalarType::Float, 0));
         r.norm.table_rows = THPVariable_Unpack(a[4]).size(0);
-        r.norm.rot = (int32_t)THPVariable_Unpack(a[4]).size(1);
+        r.norm.rot = small(THPVariable_Unpack(a[4]).size(1), "cos_sin");
     }
     r.positions = static_cast<int32_t*>(flat(a[5], "positions", ScalarType::Int, r.tokens, true));
     r.norm.eps = number(eps);
@@ -232,13 +239,13 @@ Attention attention_of(PyObject* q, PyObject* k, PyObject* v, PyObject* cu_q, Py
         r.cu_k = static_cast<int32_t*>(flat(cu_k, "cu_k", ScalarType::Int, n));
         if (THPVariable_Unpack(cu_k).numel() != n)
             throw ValueError("cu_q and cu_k: expected batch + 1 offsets each");
-        r.shape.batch = (int32_t)(n - 1);
+        r.shape.batch = small(n - 1, "cu_q");
     }
     r.shape.tokens_q = r.tq->size(0);
     r.shape.tokens_k = r.tk->size(0);
-    r.shape.heads_q = (int32_t)r.tq->size(1);
-    r.shape.heads_k = (int32_t)r.tk->size(1);
-    r.shape.head_dim = (int32_t)dim;
+    r.shape.heads_q = small(r.tq->size(1), "q");
+    r.shape.heads_k = small(r.tk->size(1), "k");
+    r.shape.head_dim = small(dim, "q");
     r.shape.causal = truth(causal);
     r.shape.scale = scale == Py_None ? (float)(1.0 / std::sqrt((double)dim)) : number(scale);
     return r;

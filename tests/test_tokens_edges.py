@@ -251,3 +251,25 @@ def test_conditions_and_streams_that_raise(fake):
         gs.gs_dropout_add(x, None, x, rng, "half", stream=0)
     with pytest.raises(AttributeError):
         gs.gs_dropout_add(x, None, x, rng, 0.1, stream="main")
+
+
+def test_dimensions_beyond_32_bits(fake):
+    # 2^32 + 8 heads are not 8
+    import torch
+
+    import differentiable_gaussian_splatting_gb300 as gs
+
+    n = 2 ** 32 + 8
+    x, wide, long = fake(0, 2, 64), fake(0, n, 64), fake(0, 2, n)
+    lse, ws = fake(2, 0, dtype=torch.float32), fake(1, dtype=torch.uint8)
+    for a, b in ((wide, x), (x, wide), (long, long)):
+        with pytest.raises(ValueError, match="too large"):
+            gs.gs_qk_norm_rope(a, b, None, None, None, None, a, b, stream=0)
+        with pytest.raises(ValueError, match="too large"):
+            gs.gs_attention_fwd(a, b, b, a, lse, ws, stream=0)
+    table = fake(4, n, dtype=torch.float32)
+    with pytest.raises(ValueError, match="too large"):
+        gs.gs_qk_norm_rope(x, x, None, None, table, None, x, x, stream=0)
+    cu = fake(n, dtype=torch.int32)
+    with pytest.raises(ValueError, match="too large"):
+        gs.gs_attention_fwd(x, x, x, x, lse, ws, cu_q=cu, cu_k=cu, stream=0)
