@@ -140,8 +140,8 @@ def library() -> C.CDLL:
     with _lib_lock:
         if _lib is None:
             path = _build.LIB
-            if not _build.up_to_date():
-                _build.build()
+            if not _build.library_up_to_date():
+                _build.build_library()
             if not os.path.exists(path):
                 raise RuntimeError("libgs.so is not built; run differentiable_gaussian_splatting_gb300.build")
             lib = C.CDLL(path)
@@ -523,7 +523,8 @@ _calls = None  # the compiled binding of these calls, once loaded
 
 def _token_calls():
     """The compiled binding (csrc/token_binding.cpp): it checks the tensors (TypeError,
-    ValueError), calls the library and returns the status."""
+    ValueError), calls the library and returns the status.  Built when a call first needs it, if
+    it is not there or was made for another torch or Python."""
     global _calls
     if _calls is None:
         import importlib.machinery
@@ -531,10 +532,14 @@ def _token_calls():
 
         _load_torch()
         library()
-        loader = importlib.machinery.ExtensionFileLoader("gs_token_binding", _build.BINDING)
-        spec = importlib.util.spec_from_loader("gs_token_binding", loader)
-        _calls = importlib.util.module_from_spec(spec)
-        loader.exec_module(_calls)
+        with _lib_lock:
+            if _calls is None:
+                loader = importlib.machinery.ExtensionFileLoader("gs_token_binding",
+                                                                 _build.build_binding())
+                spec = importlib.util.spec_from_loader("gs_token_binding", loader)
+                calls = importlib.util.module_from_spec(spec)
+                loader.exec_module(calls)
+                _calls = calls
     return _calls
 
 

@@ -273,3 +273,73 @@ def test_dimensions_beyond_32_bits(fake):
     cu = fake(n, dtype=torch.int32)
     with pytest.raises(ValueError, match="too large"):
         gs.gs_attention_fwd(x, x, x, x, lse, ws, cu_q=cu, cu_k=cu, stream=0)
+
+
+# ---------------------------------------------------------------------------
+# the build's two parts
+# ---------------------------------------------------------------------------
+@pytest.fixture
+def scratch_build(tmp_path, monkeypatch):
+    """The build module with its results in a scratch folder and compilers that write empty
+    files: (module, list of what was run, set of what shall fail)"""
+    from differentiable_gaussian_splatting_gb300 import build
+
+    ran, fails = [], set()
+
+    def run(cmd, what, verbose):
+        if what in fails:
+            raise RuntimeError(f"{what} failed")
+        ran.append(what)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "libgs.so"))
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "gs_token_binding.so"))
+    monkeypatch.setattr(build, "_run", run)
+    return build, ran, fails
+
+
+def test_library_builds_without_torch(scratch_build, monkeypatch):
+    build, ran, _ = scratch_build
+    monkeypatch.setitem(sys.modules, "torch", None)
+    build.build()
+    assert os.path.exists(build.LIB) and not os.path.exists(build.BINDING)
+    assert "libgs.so" in ran and "token_binding.cpp" not in ran
+    assert build.up_to_date()
+    with pytest.raises(RuntimeError, match="torch"):
+        build.build_binding()
+
+
+@pytest.mark.parametrize("part", ["token_binding.cpp", "gs_token_binding.so"])
+def test_library_builds_beside_a_binding_that_fails(scratch_build, part):
+    build, ran, fails = scratch_build
+    fails.add(part)
+    with pytest.raises(RuntimeError, match=part):
+        build.build()
+    assert os.path.exists(build.LIB) and build.library_up_to_date()
+    assert not os.path.exists(build.BINDING) and not build.up_to_date()
+    fails.clear()
+    ran.clear()
+    build.build()
+    assert ran == ["token_binding.cpp", "gs_token_binding.so"] and build.up_to_date()
+
+
+def test_binding_of_another_torch_is_built_anew(scratch_build, monkeypatch):
+    build, ran, _ = scratch_build
+    build.build()
+    ran.clear()
+    build.build()
+    assert ran == []
+    for name, value in (("torch", "9.9"), ("at", "/elsewhere"), ("changed", 1.0), ("python", ".x")):
+        made_for = build._torch_of_binding()
+        assert name in made_for
+        with monkeypatch.context() as m:
+            m.setattr(build, "_torch_of_binding", lambda: {**made_for, name: value})
+            assert build.library_up_to_date() and not build.binding_up_to_date()
+            ran.clear()
+            build.build()
+            assert ran == ["token_binding.cpp", "gs_token_binding.so"]
+        assert not build.binding_up_to_date()
+        build.build()
+    os.remove(build.BINDING + ".json")  # from before it was recorded
+    assert not build.binding_up_to_date()
