@@ -93,7 +93,8 @@ __device__ __forceinline__ int tiles_from(int n, int m, int rows, bool causal, i
 
 // By one whole warp: block `id` of the batch's tiles and heads, costliest first where costs
 // differ, so that the last blocks to start are short.  False beyond the last one.  Batches
-// of more than 32 sequences go sequence by sequence instead, from the last.
+// of more than 32 sequences go sequence by sequence instead, from the last; blocks in between
+// may be left without a tile.
 template <bool kKeys>
 __device__ __forceinline__ bool find_place(const Batch& v, int rows, int heads, int id, Place* at) {
     if (v.batch == 1) {
@@ -150,34 +151,29 @@ __device__ __forceinline__ bool find_place(const Batch& v, int rows, int heads, 
         at->sq = from_lane(s, l);
         return true;
     }
-    int before = 0;
-    for (int base = 0; base < v.batch; base += 32) {
-        const int b = v.batch - 1 - base - lane;
-        Sequence s{};
-        if (b >= 0) s = sequence(v, b);
-        const int tiles = ((kKeys ? s.m : s.n) + rows - 1) / rows;
-        int sum = tiles;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(all, sum, o);
-            if (lane >= o) sum += u;
-        }
-        const unsigned hit = __ballot_sync(all, before + sum > rank);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            const int upto = before + __shfl_sync(all, sum, l);
-            const int own = __shfl_sync(all, tiles, l);
-            at->b = v.batch - 1 - base - l;
-            at->tile = kKeys ? rank - (upto - own) : upto - 1 - rank;
-            at->sq = from_lane(s, l);
-            return true;
-        }
-        before += __shfl_sync(all, sum, 31);
+    // A sequence that starts at token t has the slots from t / rows + b on.  They hold its tiles:
+    // ceil(n / rows) <= (t + n) / rows + 1 - t / rows.  So a slot's sequence is found without the
+    // lengths of those before it, in as many rounds as the batch has powers of 32.
+    const int32_t* cu = kKeys ? v.cu_k : v.cu_q;
+    const int most = (int)(kKeys ? v.tk : v.tq);
+    const auto first_slot = [&](int b) { return min(max(__ldg(cu + b), 0), most) / rows + b; };
+    const int slot = most / rows + v.batch - 1 - rank;
+    int lo = 0, hi = v.batch;  // the last sequence that starts at the slot or before
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) >> 5, b = lo + lane * step;
+        const unsigned upto = __ballot_sync(all, b < hi && first_slot(b) <= slot);
+        if (upto) lo += (31 - __clz(upto)) * step;
+        hi = min(hi, lo + step);
     }
-    return false;
+    const Sequence s = sequence(v, lo);
+    const int tiles = ((kKeys ? s.m : s.n) + rows - 1) / rows, within = slot - first_slot(lo);
+    at->b = lo;
+    at->tile = kKeys ? tiles - 1 - within : within;
+    at->sq = s;
+    return within >= 0 && within < tiles;
 }
 
-// an upper bound of the tiles of a batch
+// an upper bound of the tiles of a batch (of several sequences: the slots of find_place)
 inline int64_t tiles_at_most(int64_t tokens, int rows, int batch) {
     return batch > 1 ? tokens / rows + batch : (tokens + rows - 1) / rows;
 }
