@@ -130,3 +130,169 @@ def test_attention_of_many_lone_tokens():
     assert ((dq.double()).abs() <= noise * k.double().abs()).all()
     assert ((dk.double()).abs() <= noise * q.double().abs()).all()
     assert times[1] < 200.0, times
+
+
+# ---------------------------------------------------------------------------
+# what lies around the arrays
+# ---------------------------------------------------------------------------
+class Guarded:
+    """A tensor inside a larger one of known bytes, with gaps between its rows where it has
+    three dimensions; `intact` tells whether the call left them as they were."""
+
+    def __init__(self, shape, dtype, gaps=True):
+        torch = _torch()
+        size = torch.empty((), dtype=dtype).element_size()
+        self.shape, self.dtype, self.gaps = tuple(shape), dtype, gaps and len(shape) == 3
+        full = self.shape
+        if self.gaps:
+            full = (full[0], full[1] + 1, full[2] + 16 // size)
+        self.full, self.bytes = full, int(np.prod(full)) * size
+        self.all = (torch.arange(self.bytes + 8192, device="cuda") * 37 % 251 + 1).to(torch.uint8)
+        self.before = self.all.clone()
+        self.t = self._view(self.all)
+
+    def _view(self, raw):
+        t = raw[4096:4096 + self.bytes].view(self.dtype).view(self.full)
+        return t[:, :self.shape[1], :self.shape[2]] if self.gaps else t
+
+    def rest(self):
+        """the bytes around the tensor: as they are, and as they were"""
+        after, before = self.all.clone(), self.before.clone()
+        self._view(after).zero_()
+        self._view(before).zero_()
+        return after, before
+
+    def intact(self):
+        return _torch().equal(*self.rest())
+
+    def kept(self, rows):
+        """whether these rows of t are as before the call"""
+        torch = _torch()
+        return torch.equal(self.t[rows].contiguous().view(torch.uint8),
+                           self._view(self.before)[rows].contiguous().view(torch.uint8))
+
+
+def _guarded_attention(q, k, v, do, cu_q, cu_k, causal, scale):
+    """({name: Guarded}) of both calls"""
+    import differentiable_gaussian_splatting_gb300 as gs
+
+    torch = _torch()
+    (Tq, hq, D), (Tk, hk, _) = q.shape, k.shape
+    bf = torch.bfloat16
+    n = gs.gs_attention_workspace_bytes(Tq, Tk, len(cu_q) - 1, hq, hk, D)
+    g = {"out": Guarded(q.shape, bf), "dq": Guarded(q.shape, bf), "dk": Guarded(k.shape, bf),
+         "dv": Guarded(v.shape, bf), "lse": Guarded((hq, Tq), torch.float32),
+         "ws": Guarded((n,), torch.uint8)}
+    t = {name: x.t for name, x in g.items()}
+    qkv = [_dev(x, "bf16") for x in (q, k, v)]
+    cu = dict(cu_q=torch.tensor(cu_q, dtype=torch.int32, device="cuda"),
+              cu_k=torch.tensor(cu_k, dtype=torch.int32, device="cuda"))
+    gs.gs_attention_fwd(*qkv, t["out"], t["lse"], t["ws"], causal=causal, scale=scale, **cu)
+    gs.gs_attention_bwd(*qkv, t["out"], t["lse"], _dev(do, "bf16"), t["dq"], t["dk"], t["dv"],
+                        t["ws"], causal=causal, scale=scale, **cu)
+    torch.cuda.synchronize()
+    for name, x in g.items():
+        assert x.intact(), name
+    return g
+
+
+@pytest.mark.parametrize("D", [40, 64, 128])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("cu_q,cu_k", [
+    ([0, 60, 1000], [0, 70, 2 ** 31 - 1]),       # beyond the arrays: cut
+    ([0, 0, 30, 150], [0, 40, 40, 90]),          # short of their end: the rest is left
+    ([10, 150, 160], [30, 200, 300]),            # from behind their start
+    ([-5, 64, 200], [-2 ** 31, 128, 256]),
+    ([0] * 38 + [7, 200], [0] * 38 + [200, 333]),  # more than 32 sequences
+    ([13] + [20] * 37 + [190], [5] + [9] * 37 + [290]),
+])
+def test_attention_touches_nothing_else(D, causal, cu_q, cu_k):
+    Tq, Tk, hq, hk = 200, 333, 4, 2
+    rng, q, k, v = _attention_inputs(Tq, Tk, hq, hk, D, seed=len(cu_q))
+    do = ref.bf16(rng.normal(size=q.shape))
+    scale = D ** -0.5
+    g = _guarded_attention(q, k, v, do, cu_q, cu_k, causal, scale)
+    cq, ck = np.clip(cu_q, 0, Tq), np.clip(cu_k, 0, Tk)
+    torch = _torch()
+    for names, c, T in ((("out", "dq"), cq, Tq), (("dk", "dv"), ck, Tk)):
+        free = torch.tensor([i for i in range(T) if not c[0] <= i < c[-1]], device="cuda",
+                            dtype=torch.long)
+        for name in names:
+            assert g[name].kept(free), name
+    lse = g["lse"]
+    free = [i for i in range(Tq) if not cq[0] <= i < cq[-1]]
+    assert torch.equal(lse.t[:, free].view(torch.int32), lse._view(lse.before)[:, free].view(torch.int32))
+    # and what the sequences hold is right
+    q_rows, k_rows = slice(cq[0], cq[-1]), slice(ck[0], ck[-1])
+    out, l, mag, smag = ref.attention(q, k, v, scale, causal, cq, ck)
+    got = _np(g["out"].t)
+    _close(got[q_rows], out[q_rows], ((2 * H + 2.0 ** -12) * mag)[q_rows], "out")
+    got_l, l, smag = (x[:, q_rows] for x in (_np(lse.t), l, smag))
+    fin = np.isfinite(l)
+    assert np.array_equal(np.isneginf(got_l), ~fin)
+    _close(got_l[fin], l[fin], (D * U * smag + 4 * U * (1 + np.abs(l)) + 2.0 ** -20)[fin], "lse")
+    safe = np.zeros((hq, Tq))
+    safe[:, q_rows] = got_l
+    want = ref.attention_bwd(q, k, v, got, safe, do, scale, causal, cq, ck)
+    for n, name, rows in (("q", "dq", q_rows), ("k", "dk", k_rows), ("v", "dv", k_rows)):
+        w, b = want[n]
+        _close(_np(g[name].t)[rows], w[rows], (b + H * np.abs(w) + 1e-30)[rows], name)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_offsets_that_fall(D):
+    # no sequence of the batch has a defined result where two of them overlap, but nothing
+    # outside is touched, a negative length is none, and rows of one sequence alone are right
+    T, h = 100, 2
+    rng, q, k, v = _attention_inputs(T, T, h, h, D, seed=40)
+    do = ref.bf16(rng.normal(size=q.shape))
+    cu = [0, 60, 40, 1000]                      # 0..59, none, 40..99
+    g = _guarded_attention(q, k, v, do, cu, cu, False, 0.125)
+    got = _np(g["out"].t)
+    for rows, keys in ((slice(0, 40), slice(0, 60)), (slice(60, 100), slice(40, 100))):
+        want, _, mag, _ = ref.attention(q[rows], k[keys], v[keys], 0.125)
+        _close(got[rows], want, (2 * H + 2.0 ** -12) * mag, "out")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,hq,hk,D,rot,inter", [(5, 3, 1, 40, 20, False), (33, 2, 2, 72, 36, False),
+                                                 (129, 5, 3, 64, 48, True), (1, 1, 1, 8, 0, False),
+                                                 (700, 16, 4, 128, 128, False)])
+def test_head_norm_touches_nothing_else(T, hq, hk, D, rot, inter, dtype):
+    import differentiable_gaussian_splatting_gb300 as gs
+
+    torch = _torch()
+    ty = torch.bfloat16 if dtype == "bf16" else torch.float32
+    q, k, dq, dk = (torch.randn((T, h, D), device="cuda").to(ty) for h in (hq, hk, hq, hk))
+    w = torch.randn(D, device="cuda")
+    table = torch.randn((T, rot), device="cuda") if rot else None
+    n = gs.gs_qk_norm_rope_workspace_bytes(T, hq, hk, D)
+    g = {name: Guarded((T, h, D), ty) for name, h in (("qo", hq), ("ko", hk), ("gq", hq), ("gk", hk))}
+    g |= {"dqw": Guarded((D,), torch.float32), "dkw": Guarded((D,), torch.float32),
+          "ws": Guarded((n,), torch.uint8)}
+    t = {name: x.t for name, x in g.items()}
+    gs.gs_qk_norm_rope(q, k, w, w, table, None, t["qo"], t["ko"], interleaved=inter)
+    gs.gs_qk_norm_rope_bwd(q, k, w, w, table, None, dq, dk, t["gq"], t["gk"], t["dqw"], t["dkw"],
+                           t["ws"], interleaved=inter)
+    for name, x in g.items():
+        assert x.intact(), name
+    plain = torch.empty_like(q), torch.empty_like(k)
+    gs.gs_qk_norm_rope(q, k, w, w, table, None, *plain, interleaved=inter)
+    assert torch.equal(plain[0], t["qo"]) and torch.equal(plain[1], t["ko"])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [1, 7, 8, 9, 2049, 4095])
+def test_dropout_touches_nothing_else(n, dtype):
+    import differentiable_gaussian_splatting_gb300 as gs
+
+    torch = _torch()
+    ty = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x, r = (torch.randn(n, device="cuda").to(ty) for _ in range(2))
+    state = torch.tensor([5, 6], dtype=torch.int64, device="cuda")
+    out, dx = Guarded((n,), ty), Guarded((n,), ty)
+    gs.gs_dropout_add(x, r, out.t, state, 0.3)
+    gs.gs_dropout_add_bwd(x, dx.t, state, 0.3)
+    assert out.intact() and dx.intact()
+    keep, _ = ref.kept(n, 5, 6, 0.3)
+    assert np.array_equal(_np(dx.t) != 0, keep & (_np(x) != 0))
