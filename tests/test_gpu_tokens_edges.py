@@ -296,3 +296,68 @@ def test_dropout_touches_nothing_else(n, dtype):
     assert out.intact() and dx.intact()
     keep, _ = ref.kept(n, 5, 6, 0.3)
     assert np.array_equal(_np(dx.t) != 0, keep & (_np(x) != 0))
+
+
+# ---------------------------------------------------------------------------
+# long sequences: sampled rows of the outputs and of every gradient
+# ---------------------------------------------------------------------------
+def _sample(rng, n):
+    edge = [0, 1, 63, 127, 128, n // 2, n - 129, n - 2, n - 1]
+    return np.unique(np.concatenate([edge, rng.choice(n, 32, replace=False)]))
+
+
+@pytest.mark.parametrize("n,m,hq,hk,D,causal", [
+    (8160, 8160, 2, 1, 64, False), (8160, 8160, 2, 1, 64, True), (8160, 8160, 2, 1, 128, False),
+    (8160, 8160, 2, 1, 128, True), (4346, 8160, 2, 2, 72, True), (16320, 16320, 1, 1, 128, False),
+])
+def test_attention_long_gradients(n, m, hq, hk, D, causal):
+    # As test_gpu_tokens.py's bounds; the sums run over up to n rows here, in fp32: n u of their
+    # terms' magnitudes besides.
+    from test_gpu_tokens import _run_attention
+
+    rng, q, k, v = _attention_inputs(n, m, hq, hk, D, seed=n + D)
+    do = ref.bf16(rng.normal(size=q.shape))
+    scale, E = D ** -0.5, 2.0 ** -12
+    out, lse, (dq, dk, dv) = _run_attention(q, k, v, scale, causal, dout=do)
+    out, lse, dq, dk, dv = (_np(x) for x in (out, lse, dq, dk, dv))
+    q, k, v, do = (x.astype(np.float64) for x in (q, k, v, do))
+    delta, delta_m = (do * out).sum(-1), np.abs(do * out).sum(-1)
+    A = max(n, m) * U
+
+    def parts(h, rows, keys):
+        """p, dS and the bound of dS's error, of these queries and keys"""
+        i, j = np.arange(n)[rows][:, None], np.arange(m)[keys][None]
+        kk, vv = k[keys, h // (hq // hk)], v[keys, h // (hq // hk)]
+        s = scale * q[rows, h] @ kk.T
+        p = np.exp(s - lse[h, rows][:, None]) * ((j <= i + m - n) if causal else 1.0)
+        ds = p * (do[rows, h] @ vv.T - delta[rows, h][:, None])
+        err = (H + A) * np.abs(ds) + E * p * (np.abs(do[rows, h]) @ np.abs(vv).T +
+                                              delta_m[rows, h][:, None])
+        return p, ds, err
+
+    rows, keys, every = _sample(rng, n), _sample(rng, m), slice(None)
+    for h in range(hq):
+        kk, vv = k[:, h // (hq // hk)], v[:, h // (hq // hk)]
+        p, ds, err = parts(h, rows, every)
+        w = scale * ds @ kk
+        _close(dq[rows, h], w, scale * err @ np.abs(kk) + H * np.abs(w) + 1e-30, "dq")
+        # the forward's rows: probabilities by its own lse
+        s = scale * q[rows, h] @ kk.T
+        if causal:
+            s = np.where(np.arange(m)[None] <= rows[:, None] + m - n, s, -np.inf)
+        top = s.max(-1, keepdims=True)
+        e = np.exp(s - top)
+        true_lse = (top + np.log(e.sum(-1, keepdims=True)))[:, 0]
+        smag = scale * (np.abs(q[rows, h]) @ np.abs(kk).T).max(-1)
+        _close(lse[h, rows], true_lse,
+               D * U * smag + 4 * U * (1 + np.abs(true_lse)) + 2.0 ** -20, "lse")
+        e /= e.sum(-1, keepdims=True)
+        _close(out[rows, h], e @ vv, (2 * H + E + A) * (e @ np.abs(vv)), "out")
+    for g in range(hk):
+        wk = wv = bk = bv = 0.0
+        for h in range(g * (hq // hk), (g + 1) * (hq // hk)):
+            p, ds, err = parts(h, every, keys)
+            wk, bk = wk + scale * ds.T @ q[:, h], bk + scale * err.T @ np.abs(q[:, h])
+            wv, bv = wv + p.T @ do[:, h], bv + (H + E + A) * (p.T @ np.abs(do[:, h]))
+        _close(dk[keys, g], wk, bk + H * np.abs(wk) + 1e-30, "dk")
+        _close(dv[keys, g], wv, bv + H * np.abs(wv) + 1e-30, "dv")
