@@ -412,16 +412,14 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
         const int ahead = work.row0 + n - work.sq.m;
         const int sees = p.batch.causal ? max(0, ahead + r) : 0;
         const int all_see = p.batch.causal ? max(0, ahead + kTileRows - 1) : 0;
-        bool ok = true;
         int tile = q_first + (items > 0 ? work.first % (q_end - q_first) : 0);
-        for (int i = 0; i < items && ok; ++i) {
+        for (int i = 0; i < items; ++i) {
             const int slot = i % Sh::kSlots, i0 = tile * kTileRows;
             if (++tile == q_end) tile = q_first;
             const bool masked = i0 < all_see || i0 + kTileRows > n;
             const int lo = sees - i0 - half * 64, hi = n - i0 - half * 64;
-            ok = mbar_wait(smem_u32(&full_q[slot]), (i / Sh::kSlots) & 1, &dead) &&
-                 mbar_wait(smem_u32(&bar_s), i & 1, &dead);
-            if (!ok) break;
+            mbar_pass(smem_u32(&full_q[slot]), (i / Sh::kSlots) & 1, &dead);
+            mbar_pass(smem_u32(&bar_s), i & 1, &dead);
             tmem_fence_after();
             float pr[64];
             tmem_ld32(reinterpret_cast<uint32_t*>(pr), s_at);
@@ -452,8 +450,7 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bar_p));
             const uint32_t dp_at = t_dp + i % Sh::kDp * 128 + lanes + half * 64;
-            ok = mbar_wait(smem_u32(&bar_dp[i % Sh::kDp]), (i / Sh::kDp) & 1, &dead);
-            if (!ok) break;
+            mbar_pass(smem_u32(&bar_dp[i % Sh::kDp]), (i / Sh::kDp) & 1, &dead);
             tmem_fence_after();
             float dp[64];
             tmem_ld32(reinterpret_cast<uint32_t*>(dp), dp_at);
@@ -481,8 +478,8 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bar_ds[i % Sh::kDp]));
         }
-        if (ok && items > 0) ok = mbar_wait(smem_u32(&bar_done), 0, &dead);
-        if (ok) {
+        if (items > 0) mbar_pass(smem_u32(&bar_done), 0, &dead);
+        if (!any_dead(&dead)) {
             tmem_fence_after();
             const int key = work.row0 + r;
             const bool valid = key < work.sq.m, split = work.part >= 0;
@@ -694,11 +691,9 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
             nd = p.ndelta[at];
         }
         const float2 sl2 = make_float2(sl, sl), nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
-        bool ok = true;
-        for (int j = 0; j < tiles && ok; ++j) {
+        for (int j = 0; j < tiles; ++j) {
             const uint32_t s_at = tmem + (j & 1) * 128 + lanes + half * 64;
-            ok = mbar_wait(smem_u32(&bar_s[j & 1]), (j >> 1) & 1, &dead);
-            if (!ok) break;
+            mbar_pass(smem_u32(&bar_s[j & 1]), (j >> 1) & 1, &dead);
             tmem_fence_after();
             float pr[64];
             tmem_ld32(reinterpret_cast<uint32_t*>(pr), s_at);
@@ -710,8 +705,7 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
                 pr[c] = ex2_approx(a.x);
                 pr[c + 1] = ex2_approx(a.y);
             }
-            ok = mbar_wait(smem_u32(&bar_dp), j & 1, &dead);
-            if (!ok) break;
+            mbar_pass(smem_u32(&bar_dp), j & 1, &dead);
             tmem_fence_after();
             float dp[64];
             tmem_ld32(reinterpret_cast<uint32_t*>(dp), dp_at);
@@ -739,8 +733,8 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bar_ds[j & 1]));
         }
-        if (ok && tiles > 0) ok = mbar_wait(smem_u32(&bar_done), 0, &dead);
-        if (ok) {
+        if (tiles > 0) mbar_pass(smem_u32(&bar_done), 0, &dead);
+        if (!any_dead(&dead)) {
             tmem_fence_after();
             const int i = work.row0 + r;
             const bool valid = i < work.sq.n, split = work.part >= 0;

@@ -385,18 +385,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // kScores barriers in turn: this warp may be that many steps ahead of the outputs, and
         // a barrier's phase can be told from the one before it only.
         const auto output_done = [&](int j) {
-            return mbar_wait(smem_u32(&bar_o[t * Sh::kScores + j % Sh::kScores]),
-                             (j / Sh::kScores) & 1, &dead);
+            mbar_pass(smem_u32(&bar_o[t * Sh::kScores + j % Sh::kScores]), (j / Sh::kScores) & 1,
+                      &dead);
         };
         float top = -INFINITY;
         float2 sum = make_float2(0.f, 0.f);
-        bool ok = true;
         for (int j = 0; j < tiles_t; ++j) {
             const uint32_t s_at = tmem_s(min(j + t, tiles_0) + min(j, tiles_1)) + lanes;
             // kScores barriers a query tile: the one of j is used again after P(j) is taken
-            ok = mbar_wait(smem_u32(&bar_s[t * Sh::kScores + j % Sh::kScores]),
-                           (j / Sh::kScores) & 1, &dead);
-            if (!ok) break;
+            mbar_pass(smem_u32(&bar_s[t * Sh::kScores + j % Sh::kScores]), (j / Sh::kScores) & 1,
+                      &dead);
             tmem_fence_after();
             uint32_t s[128];
 #pragma unroll
@@ -424,8 +422,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 sum.x *= f;
                 sum.y *= f;
                 if (j > 0) {
-                    ok = output_done(j - 1);
-                    if (!ok) break;
+                    output_done(j - 1);
                     tmem_fence_after();
 #pragma unroll
                     for (int c = 0; c < DP; c += 16) {
@@ -461,8 +458,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(&bar_p[t * Sh::kScores + j % Sh::kScores]));
         }
         // ---- the row's output ----
-        if (ok && tiles_t > 0) ok = output_done(tiles_t - 1);
-        if (ok) {
+        if (tiles_t > 0) output_done(tiles_t - 1);
+        if (!any_dead(&dead)) {
             tmem_fence_after();
             const float l = sum.x + sum.y;
             const int slot_row = t * kTileRows + r, i = work.row0 + slot_row;
