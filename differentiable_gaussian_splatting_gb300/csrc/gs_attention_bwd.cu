@@ -15,17 +15,22 @@
 //
 // What bounds them, at 128 values a head: a step of a block of keys is 2,048 cycles of
 // products and as many of shared memory at 128 bytes a cycle (192 KB of operands, 64 KB that
-// TMA writes), a step of a block of queries 1,536; the tensor pipe is busy 68 % and 74 % of the
-// active time, and leaving out all arithmetic between the products saves 7 %.  8,160 tokens
-// x 16 heads on 4: 1,130 us with the row sums, 1,210 TFLOP/s of the gradient's five
-// products, 1,690 of the seven that are done (0.91 of the library's measured rate).  At 64
-// values: 860 us; there the handshakes bound it.
+// TMA writes), a step of a block of queries 1,536; the tensor pipe is busy 72 % of the active
+// time, and leaving out all arithmetic between the products saves 7 %.  8,160 tokens x 16 heads
+// on 4, called one by one: 1,127 us with the row sums, 1,210 TFLOP/s of the gradient's
+// five products, 1,694 of the seven that are done (0.91 of the rate that the library's matrix
+// product reaches in single calls); back to back, under the power limit: 1,183 to 1,205 us from
+// card to card (0.92 to 0.94 of the library's rate under it).  At 64 values: 846 us one by one;
+// there the handshakes bound it.
 //
 // The transposes come out of the operand descriptors: a tile of rows in shared memory
 // serves both as an operand contracted along its columns and as one contracted along its
 // rows.  P^T and dS^T (blocks of keys) and dS (of queries) go back to tensor memory in bfloat16
-// over the scores they came from, as first operands.  P, dP - delta and the sums are fp32;
-// P and dS are rounded to bfloat16 once, for the products.
+// over the scores they came from, as first operands.  P, dP - delta and the sums are fp32; P
+// and dS are rounded to bfloat16 once, for the products, whose other operands are the caller's
+// bfloat16 dO, Q and K.  By norms the gradients stand 0.0023 to 0.0025 from the exact ones, where
+// rounding the exact ones to bfloat16 alone gives 0.0016 to 0.0018; exact arithmetic with P and
+// dS rounded gives the same as the kernel.
 //
 // Rows of a tile that lie beyond the sequence and are contracted over are zeroed in shared
 // memory, and P and dS are set to zero there by selection, so that what lies behind a
@@ -906,7 +911,7 @@ HeadView view(const gs_heads& h) {
 
 }  // namespace
 
-// -lse and -delta of every query row, then the pieces of both kernels
+// -lse and -delta of every query row, then the pieces of both kinds of blocks
 size_t attention_bwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads_q,
                                      int heads_k, int head_dim) {
     int64_t rows = 0;

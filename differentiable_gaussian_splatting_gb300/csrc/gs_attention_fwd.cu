@@ -2,7 +2,8 @@
 //
 //   S = scale Q K^T,  P = exp(S - row maximum),  O = P V / row sum
 //
-// in one pass over the keys with a running maximum and sum.  A block takes 256 queries of
+// in one pass over the keys with a running maximum and sum (Milakov and Gimelshein, "Online
+// normalizer calculation for softmax", 2018).  A block takes 256 queries of
 // one head as two tiles of 128 rows, with the key and value tiles (128 rows) shared by
 // both.  A producer warp brings tiles by TMA into a ring, one thread issues the products,
 // and four warps per query tile do its softmax, one row a thread: S comes from tensor
@@ -13,18 +14,26 @@
 // What bounds it, at 128 values a head: the tensor cores with the shared memory that feeds
 // them.  A 128 x 128 tile takes 1,024 cycles of products; the first product reads both
 // operands from shared memory at its full 128 bytes a cycle while TMA writes there too, and
-// a tile changes hands twice, so about 1,390 cycles pass (tensor pipe busy 67 % of the
-// active time).  16,320 tokens x 16 heads: 1,260 us, 1,730 TFLOP/s, 0.94 of the measured
-// rate of the library's matrix product, both under the card's power limit.  At 64 values the
-// handshakes weigh twice as much: 8,160 tokens x 16 heads on 4 in 262 us, 1,040 TFLOP/s
-// (289 us with exponentials, 279 without, 209 without any softmax: it is not the
-// exponentials).  Tried and slower: 16 softmax warps with half a row each (1,351 us), a
-// thread for each query tile's products (1,326), a whole warp that walks the steps (1,414).
+// a tile changes hands twice, so about 1,390 cycles pass (tensor pipe busy 68 % of the
+// active time).  16,320 tokens x 16 heads, called one by one: 1,250 us, 1,745 TFLOP/s, 0.94 of
+// the rate that the library's matrix product reaches in single calls; back to back, under the
+// power limit: 1,340 to 1,375 us from card to card, 0.92 to 0.94 of the library's rate under it.
+// At 64 values the handshakes weigh twice as much: 8,160 tokens x 16 heads on 4 in 265 us,
+// 1,030 TFLOP/s (243 us without the exponentials, 215 without any softmax: more than half of
+// what it stands above its products' 147 is the exchange).  Tried and slower, each against the
+// kernel of its time: 16 softmax warps with half a row each (1,260 -> 1,351 us at 16,320 tokens),
+// a thread for each query tile's products (1,255 -> 1,326), a whole warp that walks the steps
+// (1,283 -> 1,414).
 //
-// The running maximum is stale on purpose: a row's O and sum are rescaled only once its
-// maximum has risen by more than 8 (in powers of two), so P stays below 2^8 and the
-// rescaling, which has to wait for the last product, is rare.  P is rounded to bfloat16
-// for the product; the sum takes the unrounded values in fp32.
+// The running maximum is stale on purpose, as in published attention kernels for tensor memory:
+// a row's O and sum are rescaled only once its maximum has risen by more than 8 (in powers of
+// two), so P stays below 2^8 and the rescaling, which has to wait for the last product, is rare.
+//
+// P is rounded to bfloat16 for the second product, whose other operand is the caller's bfloat16
+// V (both operands of a product have one type, and a product of P's high and low parts would
+// double its time); the sum takes the unrounded values in fp32.  By norms the outputs stand
+// 0.0020 to 0.0024 from the exact ones, where rounding the exact ones to bfloat16 alone gives
+// 0.0016 to 0.0017; exact arithmetic with P rounded gives the same as the kernel.
 //
 // Where the blocks are fewer than the SMs, or their last wave would be mostly empty, those
 // blocks' keys are cut into pieces, a block each, which leave normalised outputs and row

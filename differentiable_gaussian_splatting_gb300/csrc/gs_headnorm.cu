@@ -48,7 +48,9 @@ constexpr int kSms = 152;
 constexpr int kFwdBlocks = 4 * kSms, kBwdBlocks = 3 * kSms;  // resident at once
 constexpr int kFinishCols = 32, kFinishThreads = 1024;
 
-// how the pairs lie: halves in whole groups of 4 pairs, halves otherwise, neighbours
+// How the pairs lie: halves in whole groups of 4 pairs, halves otherwise, neighbours.  Halves
+// whose columns no 4 pairs hold are read and written one by one: 32,400 tokens x (16 + 4) heads x
+// 72 in bfloat16 take 126 us with 36 values rotated, 57 with all 72.
 enum Pairing : int { kHalves4 = 0, kHalves = 1, kNeighbours = 2 };
 
 struct Rows {

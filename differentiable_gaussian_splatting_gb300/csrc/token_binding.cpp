@@ -2,8 +2,8 @@
 // passes plain pointers to the calls of include/gs.h.  What the package's Python code does
 // for the other calls through ctypes is done here in C++, because these are called many
 // times a training step on few tokens: on the GB300's Grace a call's host time is 3 to 4 us
-// (8 for attention's gradient with its three launches) instead of 6 to 23.  Errors are those of the Python code: TypeError and
-// ValueError for tensors; the status of the call is returned.
+// (6 for attention's gradient with its two launches) instead of 6 to 23.  Errors are those of
+// the Python code: TypeError and ValueError for tensors; the status of the call is returned.
 #include <Python.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>

@@ -524,7 +524,9 @@ gs_status gs_qk_norm_rope_bwd(int64_t tokens, int32_t heads_q, int32_t heads_k, 
  *   P = exp(s - lse), delta_i = out_i . dout_i, dV = P^T dout,
  *   dS = P (dout V^T - delta), dQ = scale dS K, dK = scale dS^T Q,
  * keys' gradients summed over the query heads that share them.  Queries that see no
- * key, and keys that no query sees, get zeros.  dq, dk and dv overlap no input.
+ * key, and keys that no query sees, get zeros.  As in the forward, everything inside a
+ * sequence must be finite where the mask hides it from some token of the other side: keys
+ * and values, and the queries, out and dout of queries too.  dq, dk and dv overlap no input.
  */
 typedef struct {
     int64_t tokens_q, tokens_k;
