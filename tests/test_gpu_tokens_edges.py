@@ -361,3 +361,43 @@ def test_attention_long_gradients(n, m, hq, hk, D, causal):
             wv, bv = wv + p.T @ do[:, h], bv + (H + E + A) * (p.T @ np.abs(do[:, h]))
         _close(dk[keys, g], wk, bk + H * np.abs(wk) + 1e-30, "dk")
         _close(dv[keys, g], wv, bv + H * np.abs(wv) + 1e-30, "dv")
+
+
+@pytest.mark.parametrize("n,m,D,causal", [(300, 300, 64, True), (700, 520, 128, False),
+                                          (1, 5000, 64, False)])
+def test_attention_in_a_captured_graph(n, m, D, causal):
+    # the chain of dependent launches replayed, on new inputs: the bits of the calls one by one
+    import differentiable_gaussian_splatting_gb300 as gs
+
+    torch = _torch()
+    hq, hk = 4, 2
+    new = lambda t, h: torch.empty((t, h, D), dtype=torch.bfloat16, device="cuda")
+    q, k, v, do = new(n, hq), new(m, hk), new(m, hk), new(n, hq)
+    out, dq, dk, dv = new(n, hq), new(n, hq), new(m, hk), new(m, hk)
+    lse = torch.empty((hq, n), device="cuda")
+    ws = torch.empty(gs.gs_attention_workspace_bytes(n, m, 1, hq, hk, D), dtype=torch.uint8,
+                     device="cuda")
+
+    def calls():
+        gs.gs_attention_fwd(q, k, v, out, lse, ws, causal=causal)
+        gs.gs_attention_bwd(q, k, v, out, lse, do, dq, dk, dv, ws, causal=causal)
+
+    for t in (q, k, v, do):
+        t.normal_()
+    calls()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    for _ in range(3):
+        for t in (q, k, v, do):
+            t.normal_()
+        results = []
+        for run in (calls, g.replay):
+            ws.fill_(255)
+            for t in (out, lse, dq, dk, dv):
+                t.fill_(float("nan"))
+            run()
+            results.append([t.clone() for t in (out, lse, dq, dk, dv)])
+        assert all(torch.equal(a, b) for a, b in zip(*results))
+        assert all(torch.isfinite(t).all() for t in results[0])
