@@ -13,8 +13,9 @@ device is present, the calls raise.
 
 Next to the path stand the token operators of a network that predicts Gaussians
 and is trained through it: ``gs_qk_norm_rope``, ``gs_attention_fwd``,
-``gs_dropout_add`` and their gradients.  They take torch tensors, which a small
-compiled module checks and passes on (``csrc/token_binding.cpp``).
+``gs_dropout_add``, ``gs_residual_norm`` and their gradients, and
+``gs_clip_grad_norm``.  They take torch tensors, which a small compiled module
+checks and passes on (``csrc/token_binding.cpp``).
 
 ``Rasterizer`` is a convenience that allocates the outputs and workspaces of
 one view and runs the five calls in order.
@@ -38,6 +39,8 @@ __all__ = [
     "gs_qk_norm_rope", "gs_qk_norm_rope_bwd", "gs_qk_norm_rope_workspace_bytes",
     "gs_attention_fwd", "gs_attention_bwd", "gs_attention_workspace_bytes", "gs_attention_status",
     "gs_dropout_add", "gs_dropout_add_bwd",
+    "gs_residual_norm", "gs_residual_norm_bwd", "gs_residual_norm_workspace_bytes",
+    "gs_clip_grad_norm", "gs_clip_grad_norm_workspace_bytes",
     "Camera", "Settings", "Rasterizer", "library",
     "GSError", "TILE", "GRAD2D", "SPLAT_FLOATS",
 ]
@@ -128,6 +131,28 @@ class AttentionShape(C.Structure):
                 ("causal", C.c_int32), ("scale", C.c_float)]
 
 
+class Rows(C.Structure):
+    """gs_rows: a [tokens, width] array by its row stride (in elements)."""
+    _fields_ = [("data", C.c_void_p), ("row_stride", C.c_int64)]
+
+
+class BlockNorm(C.Structure):
+    """gs_block_norm: element type, kinds of the norms, rows of the gate, alpha, beta, eps."""
+    _fields_ = [("type", C.c_int32), ("pre", C.c_int32), ("post", C.c_int32), ("batch", C.c_int32),
+                ("alpha", C.c_float), ("beta", C.c_float), ("eps", C.c_float)]
+
+
+class NormParams(C.Structure):
+    """gs_norm_params and gs_norm_grads: weights and biases of both norms, gate."""
+    _fields_ = [(n, C.c_void_p) for n in ("pre_weight", "pre_bias", "post_weight", "post_bias",
+                                          "gate")]
+
+
+class Array(C.Structure):
+    """gs_array: a contiguous array of gradients."""
+    _fields_ = [("data", C.c_void_p), ("elements", C.c_int64), ("type", C.c_int32)]
+
+
 _lib = None
 _lib_lock = threading.Lock()
 _P = C.c_void_p
@@ -210,6 +235,17 @@ def _declare(lib: C.CDLL) -> None:
     lib.gs_dropout_add.argtypes = [_I64, i32, _P, _P, _P, _P, C.c_float, _P]
     lib.gs_dropout_add_bwd.restype = st
     lib.gs_dropout_add_bwd.argtypes = [_I64, i32, _P, _P, _P, C.c_float, _P]
+    lib.gs_residual_norm.restype = st
+    B, R, W = C.POINTER(BlockNorm), C.POINTER(Rows), C.POINTER(NormParams)
+    lib.gs_residual_norm.argtypes = [_I64, i32, B, R, R, W, _P, R, R, _P]
+    lib.gs_residual_norm_workspace_bytes.restype = C.c_size_t
+    lib.gs_residual_norm_workspace_bytes.argtypes = [_I64, i32, i32]
+    lib.gs_residual_norm_bwd.restype = st
+    lib.gs_residual_norm_bwd.argtypes = [_I64, i32, B, R, R, W, _P, R, R, R, R, W, _P, C.c_size_t, _P]
+    lib.gs_clip_grad_norm_workspace_bytes.restype = C.c_size_t
+    lib.gs_clip_grad_norm_workspace_bytes.argtypes = [i32]
+    lib.gs_clip_grad_norm.restype = st
+    lib.gs_clip_grad_norm.argtypes = [i32, C.POINTER(Array), C.POINTER(Array), C.c_float, _P, _P, C.c_size_t, _P]
     lib.gs_bin_sort_noalloc.restype = st
     lib.gs_bin_sort_noalloc.argtypes = [C.POINTER(Camera), _I64, _P, _P, _P, _P, _I64, _P, _P, _P,
                                         _P, _P]
@@ -618,6 +654,61 @@ def gs_dropout_add_bwd(dout, dx, rng, p, stream=None):
     st = (_calls or _token_calls()).dropout_add_bwd(dout, dx, rng, p, stream)
     if st:
         _check("gs_dropout_add_bwd", st)
+
+
+_NORMS = {"none": 0, "rms": 1, "layer": 2}
+
+
+def _norm_kind(name, kind) -> int:
+    if kind not in _NORMS:
+        raise ValueError(f"{name}: expected 'none', 'rms' or 'layer', got {kind!r}")
+    return _NORMS[kind]
+
+
+def gs_residual_norm(x, y, r_out, h_out, pre_weight=None, pre_bias=None, post_weight=None,
+                     post_bias=None, gate=None, cu=None, pre="rms", post="none", alpha=1.0, beta=1.0,
+                     eps=1e-6, stream=None):
+    """r = alpha x + beta gate post(y), h = pre(r) (see gs.h).  x, y, r_out, h_out: [tokens, width]
+    float32 or bfloat16, any row stride; y and r_out may be None, h_out is None with pre "none".
+    pre and post: "none", "rms" or "layer"; weights, biases and gate float32 or None; gate [width],
+    or [batch, width] with cu, the int32 offsets [batch + 1] of its sequences."""
+    st = (_calls or _token_calls()).residual_norm(
+        x, y, r_out, h_out, pre_weight, pre_bias, post_weight, post_bias, gate, cu,
+        _norm_kind("pre", pre), _norm_kind("post", post), alpha, beta, eps, stream)
+    if st:
+        _check("gs_residual_norm", st)
+
+
+def gs_residual_norm_workspace_bytes(tokens, width, batch=1) -> int:
+    return int(library().gs_residual_norm_workspace_bytes(int(tokens), int(width), int(batch)))
+
+
+def gs_residual_norm_bwd(x, y, dr_out, dh_out, dx, dy, workspace, pre_weight=None, pre_bias=None,
+                         post_weight=None, post_bias=None, gate=None, cu=None, pre="rms",
+                         post="none", alpha=1.0, beta=1.0, eps=1e-6, dpre_weight=None,
+                         dpre_bias=None, dpost_weight=None, dpost_bias=None, dgate=None,
+                         stream=None):
+    """Gradient of gs_residual_norm from its inputs x and y and the gradients of r_out (None = 0)
+    and h_out (see gs.h); gradients of weights, biases and gate that are None are not wanted."""
+    st = (_calls or _token_calls()).residual_norm_bwd(
+        x, y, dr_out, dh_out, dx, dy, workspace, pre_weight, pre_bias, post_weight, post_bias, gate,
+        cu, _norm_kind("pre", pre), _norm_kind("post", post), alpha, beta, eps, dpre_weight,
+        dpre_bias, dpost_weight, dpost_bias, dgate, stream)
+    if st:
+        _check("gs_residual_norm_bwd", st)
+
+
+def gs_clip_grad_norm_workspace_bytes(count) -> int:
+    return int(library().gs_clip_grad_norm_workspace_bytes(int(count)))
+
+
+def gs_clip_grad_norm(grads, max_norm, norm, workspace, outs=None, stream=None):
+    """The norm over all of grads, a list of contiguous float32 or bfloat16 tensors, into norm
+    (float32 [1]), and the gradients scaled to at most max_norm into outs, tensors of the same
+    sizes and types (None: in place); see gs.h."""
+    st = (_calls or _token_calls()).clip_grad_norm(grads, max_norm, norm, workspace, outs, stream)
+    if st:
+        _check("gs_clip_grad_norm", st)
 
 
 def gs_raster_stats(workspace, stream=None) -> dict:

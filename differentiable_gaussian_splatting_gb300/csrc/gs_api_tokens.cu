@@ -257,4 +257,137 @@ gs_status gs_dropout_add_bwd(int64_t n, int32_t type, const void* dout, void* dx
     return gs_dropout_add(n, type, dout, nullptr, dx, rng, p, stream);
 }
 
+namespace {
+
+constexpr int32_t kMaxWidth = 8192;
+constexpr int32_t kMaxArrays = 65536;
+
+bool aligned(const void* p, int size) { return reinterpret_cast<uintptr_t>(p) % size == 0; }
+
+// a [tokens][width] array by rows that do not overlap; with `optional` it may be missing
+bool rows_ok(const gs_rows* r, int64_t tokens, int width, int size, bool optional) {
+    if (!r || !r->data) return optional || tokens == 0;
+    return aligned(r->data, size) &&
+           (tokens <= 1 || (r->row_stride >= width && r->row_stride <= kMaxStride));
+}
+
+// with a missing array's pointer null, and the stride of a single row set to something valid
+gs_rows normal(const gs_rows* r, int64_t tokens, int width) {
+    gs_rows n = r ? *r : gs_rows{nullptr, 0};
+    if (tokens <= 1) n.row_stride = (width + 7) / 8 * 8;
+    return n;
+}
+
+bool block_norm_ok(int64_t tokens, int32_t width, const gs_block_norm* n, const gs_rows* y,
+                   const gs_norm_params* w, const int32_t* cu) {
+    if (!n || !w || tokens < 0 || tokens > kMaxTokens || width < 1 || width > kMaxWidth) return false;
+    if (n->type != GS_TYPE_F32 && n->type != GS_TYPE_BF16) return false;
+    if (n->pre < GS_NORM_NONE || n->pre > GS_NORM_LAYER || n->post < GS_NORM_NONE ||
+        n->post > GS_NORM_LAYER)
+        return false;
+    if (!std::isfinite(n->alpha) || !std::isfinite(n->beta) || !(n->eps > 0.f) ||
+        !std::isfinite(n->eps))
+        return false;
+    if (n->pre == GS_NORM_NONE && (w->pre_weight || w->pre_bias)) return false;
+    if (n->post == GS_NORM_NONE && (w->post_weight || w->post_bias)) return false;
+    if ((!y || !y->data) && tokens > 0 && (n->post != GS_NORM_NONE || w->gate)) return false;
+    if (n->batch < 1 || n->batch > kMaxBatch || (!cu && n->batch != 1) || (cu && !w->gate)) return false;
+    for (const void* p : {(const void*)w->pre_weight, (const void*)w->pre_bias,
+                          (const void*)w->post_weight, (const void*)w->post_bias,
+                          (const void*)w->gate, (const void*)cu})
+        if (!aligned16(p)) return false;
+    return true;
+}
+
+ResidualNormArgs norm_args(int64_t tokens, int32_t width, const gs_block_norm& n,
+                           const gs_norm_params& w, const int32_t* cu) {
+    return {tokens,  width,  n.batch, n.type == GS_TYPE_BF16, n.pre, n.post,
+            n.alpha, n.beta, n.eps,   w,                      cu};
+}
+
+}  // namespace
+
+gs_status gs_residual_norm(int64_t tokens, int32_t width, const gs_block_norm* norm,
+                           const gs_rows* x, const gs_rows* y, const gs_norm_params* params,
+                           const int32_t* cu, const gs_rows* r_out, const gs_rows* h_out,
+                           void* stream) {
+    if (!block_norm_ok(tokens, width, norm, y, params, cu)) return GS_ERR_INVALID_ARG;
+    if (tokens == 0) return GS_OK;
+    const int size = norm->type == GS_TYPE_BF16 ? 2 : 4;
+    const bool pre = norm->pre != GS_NORM_NONE;
+    if (!rows_ok(x, tokens, width, size, false) || !rows_ok(y, tokens, width, size, true) ||
+        !rows_ok(r_out, tokens, width, size, true) || !rows_ok(h_out, tokens, width, size, !pre) ||
+        (!pre && h_out && h_out->data))
+        return GS_ERR_INVALID_ARG;
+    return status_of(launch_residual_norm(norm_args(tokens, width, *norm, *params, cu),
+                                          normal(x, tokens, width), normal(y, tokens, width),
+                                          normal(r_out, tokens, width),
+                                          normal(h_out, tokens, width), (cudaStream_t)stream));
+}
+
+size_t gs_residual_norm_workspace_bytes(int64_t tokens, int32_t width, int32_t batch) {
+    if (tokens < 0 || tokens > kMaxTokens || width < 1 || width > kMaxWidth || batch < 1 ||
+        batch > kMaxBatch)
+        return 0;
+    return residual_norm_workspace_bytes(width);
+}
+
+gs_status gs_residual_norm_bwd(int64_t tokens, int32_t width, const gs_block_norm* norm,
+                               const gs_rows* x, const gs_rows* y, const gs_norm_params* params,
+                               const int32_t* cu, const gs_rows* dr_out, const gs_rows* dh_out,
+                               const gs_rows* dx, const gs_rows* dy, const gs_norm_grads* grads,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+    if (!block_norm_ok(tokens, width, norm, y, params, cu) || !grads) return GS_ERR_INVALID_ARG;
+    const int size = norm->type == GS_TYPE_BF16 ? 2 : 4;
+    const bool pre = norm->pre != GS_NORM_NONE, post = norm->post != GS_NORM_NONE;
+    const bool of_y = y && y->data;
+    if (!rows_ok(x, tokens, width, size, false) || !rows_ok(y, tokens, width, size, true) ||
+        !rows_ok(dr_out, tokens, width, size, true) ||
+        !rows_ok(dh_out, tokens, width, size, !pre) || (!pre && dh_out && dh_out->data) ||
+        !rows_ok(dx, tokens, width, size, false) || !rows_ok(dy, tokens, width, size, !of_y) ||
+        (tokens > 0 && !of_y && dy && dy->data))
+        return GS_ERR_INVALID_ARG;
+    if ((!pre && (grads->pre_weight || grads->pre_bias)) ||
+        (!post && (grads->post_weight || grads->post_bias)) || (grads->gate && !params->gate))
+        return GS_ERR_INVALID_ARG;
+    for (const float* g : {grads->pre_weight, grads->pre_bias, grads->post_weight, grads->post_bias,
+                           grads->gate})
+        if (!aligned16(g)) return GS_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace)) return GS_ERR_INVALID_ARG;
+    if (workspace_bytes < residual_norm_workspace_bytes(width)) return GS_ERR_WORKSPACE;
+    return status_of(launch_residual_norm_bwd(
+        norm_args(tokens, width, *norm, *params, cu), normal(x, tokens, width),
+        normal(y, tokens, width), normal(dr_out, tokens, width), normal(dh_out, tokens, width),
+        normal(dx, tokens, width), normal(dy, tokens, width), *grads, workspace,
+        (cudaStream_t)stream));
+}
+
+size_t gs_clip_grad_norm_workspace_bytes(int32_t count) {
+    return count < 0 || count > kMaxArrays ? 0 : clip_workspace_bytes(count);
+}
+
+gs_status gs_clip_grad_norm(int32_t count, const gs_array* grads, const gs_array* outs,
+                            float max_norm, float* norm, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+    if (count < 0 || count > kMaxArrays || (count > 0 && !grads) || !(max_norm >= 0.f) || !norm ||
+        !aligned(norm, 4) || !workspace || !aligned16(workspace))
+        return GS_ERR_INVALID_ARG;
+    if (!outs) outs = grads;
+    int64_t all = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        const gs_array &g = grads[i], &o = outs[i];
+        if ((g.type != GS_TYPE_F32 && g.type != GS_TYPE_BF16) || o.type != g.type ||
+            g.elements < 0 || g.elements > (int64_t(1) << 40) || o.elements != g.elements)
+            return GS_ERR_INVALID_ARG;
+        const int size = g.type == GS_TYPE_BF16 ? 2 : 4;
+        if (g.elements > 0 && (!g.data || !o.data || !aligned(g.data, size) || !aligned(o.data, size)))
+            return GS_ERR_INVALID_ARG;
+        all += g.elements;
+    }
+    if (all > (int64_t(1) << 42)) return GS_ERR_INVALID_ARG;
+    if (workspace_bytes < clip_workspace_bytes(count)) return GS_ERR_WORKSPACE;
+    return status_of(launch_clip(count, grads, outs, (double)max_norm, norm, workspace,
+                                 (cudaStream_t)stream));
+}
+
 }  // extern "C"

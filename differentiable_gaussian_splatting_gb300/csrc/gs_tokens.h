@@ -1,6 +1,6 @@
-// gs_tokens.h -- launch declarations of the token operators (head norms with
-// rotation, attention, dropout-add), shared by their translation units and the
-// entry points in gs_api_tokens.cu.  Not part of the C ABI.
+// gs_tokens.h -- launch declarations of the token operators (head norms with rotation,
+// attention, dropout-add, residual norms, gradient clipping), shared by their translation
+// units and the entry points in gs_api_tokens.cu.  Not part of the C ABI.
 #pragma once
 
 #include <cstddef>
@@ -50,6 +50,29 @@ cudaError_t launch_attention_bwd(const gs_attention_shape& s, const gs_heads& q,
                                  const gs_heads& dout, const gs_heads& dq, const gs_heads& dk,
                                  const gs_heads& dv, const int32_t* cu_q, const int32_t* cu_k,
                                  void* ws, cudaStream_t st);
+
+// ---- norms around a block with its gate and residual (gs_residual_norm.cu) ----------
+struct ResidualNormArgs {
+    int64_t tokens;
+    int width, batch;
+    bool bf16;
+    int pre, post;  // GS_NORM_*
+    float alpha, beta, eps;
+    gs_norm_params w;
+    const int32_t* cu;
+};
+cudaError_t launch_residual_norm(const ResidualNormArgs& a, const gs_rows& x, const gs_rows& y,
+                                 const gs_rows& r, const gs_rows& h, cudaStream_t st);
+size_t residual_norm_workspace_bytes(int width);
+cudaError_t launch_residual_norm_bwd(const ResidualNormArgs& a, const gs_rows& x, const gs_rows& y,
+                                     const gs_rows& dr, const gs_rows& dh, const gs_rows& dx,
+                                     const gs_rows& dy, const gs_norm_grads& g, void* ws,
+                                     cudaStream_t st);
+
+// ---- gradient norm and clipping (gs_clip.cu) ------------------------------------------
+size_t clip_workspace_bytes(int count);
+cudaError_t launch_clip(int count, const gs_array* in, const gs_array* out, double max_norm,
+                        float* norm, void* ws, cudaStream_t st);
 
 // whether a wait of an attention kernel has given up since this thread's last call (waits for st)
 cudaError_t attention_gave_up(cudaStream_t st, bool* gave_up);

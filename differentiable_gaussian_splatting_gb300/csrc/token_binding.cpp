@@ -14,8 +14,15 @@
 #include <sstream>
 #include <stdexcept>
 #include <string>
+#include <vector>
 
 #include "../../include/gs.h"
+
+// The calls that came after the first ones are looked for weakly: the binding loads beside a
+// library without them, which then says so.
+#pragma weak gs_residual_norm
+#pragma weak gs_residual_norm_bwd
+#pragma weak gs_clip_grad_norm
 
 namespace {
 
@@ -146,6 +153,7 @@ void* stream_of(PyObject* o) {
 // The library's call, without the interpreter's lock: a launch may wait for room in the queue.
 template <typename F, typename... A>
 gs_status unlocked(F* call, const A&... args) {
+    if (!call) throw std::runtime_error("libgs.so does not have this call: build it anew");
     PyThreadState* thread = PyEval_SaveThread();
     const gs_status st = call(args...);
     PyEval_RestoreThread(thread);
@@ -300,6 +308,116 @@ gs_status dropout_add_bwd(PyObject* const* a) {
     return unlocked(gs_dropout_add_bwd, n, kind, dout, dx, rng_of(a[2]), number(a[3]), stream_of(a[4]));
 }
 
+// [tokens][width], contiguous in its last dimension, of the shape of `like`; or none
+gs_rows rows(PyObject* o, const char* name, ScalarType type, const Tensor* like) {
+    if (o == Py_None) return {nullptr, 0};
+    const Tensor& t = tensor(o, name);
+    if (t.dim() != 2) throw ValueError(text(name, ": expected [tokens, width], got ", t.sizes()));
+    if (like && t.sizes() != like->sizes())
+        throw ValueError(text(name, ": expected shape ", like->sizes(), ", got ", t.sizes()));
+    want_type(t, name, type);
+    if (t.stride(1) != 1 && t.size(1) > 1 && t.numel() > 0)
+        throw ValueError(text(name, ": the last dimension must be contiguous"));
+    return {address(t), t.stride(0)};
+}
+
+// n values of fp32, or null for None
+float* vector(PyObject* o, const char* name, int64_t n) {
+    void* p = flat(o, name, ScalarType::Float, n, true);
+    if (o != Py_None && THPVariable_Unpack(o).numel() != n)
+        throw ValueError(text(name, ": expected ", n, " values, got ", THPVariable_Unpack(o).sizes()));
+    return static_cast<float*>(p);
+}
+
+struct BlockNorm {
+    int64_t tokens, width;
+    ScalarType type;
+    gs_block_norm norm;
+    gs_rows x, y;
+    gs_norm_params w;
+    const int32_t* cu;
+    const Tensor* tx;
+};
+
+// a: pre_weight, pre_bias, post_weight, post_bias, gate, cu, pre, post, alpha, beta, eps
+BlockNorm block_norm_of(PyObject* x, PyObject* y, PyObject* const* a) {
+    BlockNorm r{};
+    r.norm.type = element_type(x, "x", &r.type);
+    r.x = rows(x, "x", r.type, nullptr);
+    r.tx = &THPVariable_Unpack(x);
+    r.y = rows(y, "y", r.type, r.tx);
+    r.tokens = r.tx->size(0);
+    r.width = small(r.tx->size(1), "x");
+    r.norm.batch = 1;
+    if (a[5] != Py_None) {
+        r.cu = static_cast<int32_t*>(flat(a[5], "cu", ScalarType::Int, 2));
+        r.norm.batch = small(THPVariable_Unpack(a[5]).numel() - 1, "cu");
+    }
+    r.w = {vector(a[0], "pre_weight", r.width), vector(a[1], "pre_bias", r.width),
+           vector(a[2], "post_weight", r.width), vector(a[3], "post_bias", r.width),
+           vector(a[4], "gate", r.norm.batch * r.width)};
+    if (r.cu && a[4] == Py_None) throw ValueError("cu: the offsets of a gate, which is None");
+    r.norm.pre = (int32_t)number(a[6]);
+    r.norm.post = (int32_t)number(a[7]);
+    r.norm.alpha = number(a[8]);
+    r.norm.beta = number(a[9]);
+    r.norm.eps = number(a[10]);
+    return r;
+}
+
+gs_status residual_norm(PyObject* const* a) {
+    const BlockNorm n = block_norm_of(a[0], a[1], a + 4);
+    const gs_rows r = rows(a[2], "r_out", n.type, n.tx), h = rows(a[3], "h_out", n.type, n.tx);
+    return unlocked(gs_residual_norm, n.tokens, (int32_t)n.width, &n.norm, &n.x, &n.y, &n.w, n.cu, &r,
+                    &h, stream_of(a[15]));
+}
+
+gs_status residual_norm_bwd(PyObject* const* a) {
+    const BlockNorm n = block_norm_of(a[0], a[1], a + 7);
+    const gs_rows dr = rows(a[2], "dr_out", n.type, n.tx), dh = rows(a[3], "dh_out", n.type, n.tx),
+                  dx = rows(a[4], "dx", n.type, n.tx), dy = rows(a[5], "dy", n.type, n.tx);
+    const Bytes ws = workspace(a[6]);
+    const gs_norm_grads g{vector(a[18], "dpre_weight", n.width), vector(a[19], "dpre_bias", n.width),
+                          vector(a[20], "dpost_weight", n.width),
+                          vector(a[21], "dpost_bias", n.width),
+                          vector(a[22], "dgate", n.norm.batch * n.width)};
+    return unlocked(gs_residual_norm_bwd, n.tokens, (int32_t)n.width, &n.norm, &n.x, &n.y, &n.w, n.cu,
+                    &dr, &dh, &dx, &dy, &g, ws.p, ws.n, stream_of(a[23]));
+}
+
+// the tensors of a list or tuple, contiguous, float32 or bfloat16
+std::vector<gs_array> arrays(PyObject* o, const char* name, const std::vector<gs_array>* like) {
+    if (!PyList_Check(o) && !PyTuple_Check(o))
+        throw TypeError(text(name, ": expected a list or tuple of tensors"));
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(o);
+    if (like && n != (Py_ssize_t)like->size())
+        throw ValueError(text(name, ": expected ", like->size(), " tensors, got ", n));
+    std::vector<gs_array> r((size_t)n);
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        const Tensor& t = tensor(PySequence_Fast_GET_ITEM(o, i), name);
+        const ScalarType type = t.scalar_type();
+        if (type != ScalarType::Float && type != ScalarType::BFloat16)
+            throw ValueError(text(name, "[", i, "]: expected float32 or bfloat16, got ", type));
+        if (!t.is_contiguous()) throw ValueError(text(name, "[", i, "]: must be contiguous"));
+        r[i] = {address(t), t.numel(), type == ScalarType::BFloat16 ? GS_TYPE_BF16 : GS_TYPE_F32};
+        if (like && (r[i].elements != (*like)[i].elements || r[i].type != (*like)[i].type))
+            throw ValueError(text(name, "[", i, "]: expected ", (*like)[i].elements,
+                                  " elements of its gradient's type, got ", t.sizes(), " of ", type));
+    }
+    return r;
+}
+
+gs_status clip_grad_norm(PyObject* const* a) {
+    const std::vector<gs_array> g = arrays(a[0], "grads", nullptr);
+    float* norm = static_cast<float*>(flat(a[2], "norm", ScalarType::Float, 1));
+    const Bytes ws = workspace(a[3]);
+    std::vector<gs_array> o;
+    if (a[4] != Py_None) o = arrays(a[4], "outs", &g);
+    return unlocked(gs_clip_grad_norm, small((int64_t)g.size(), "grads"), g.data(),
+                    a[4] != Py_None ? o.data() : nullptr, number(a[1]), norm, ws.p, ws.n,
+                    stream_of(a[5]));
+}
+
 // a call with its number of arguments; no C++ exception leaves it
 template <gs_status (*kCall)(PyObject* const*), Py_ssize_t kArgs>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -331,6 +449,9 @@ PyMethodDef methods[] = {method<qk_norm_rope, 11>("qk_norm_rope"),
                          method<attention_bwd, 15>("attention_bwd"),
                          method<dropout_add, 6>("dropout_add"),
                          method<dropout_add_bwd, 5>("dropout_add_bwd"),
+                         method<residual_norm, 16>("residual_norm"),
+                         method<residual_norm_bwd, 24>("residual_norm_bwd"),
+                         method<clip_grad_norm, 6>("clip_grad_norm"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "gs_token_binding", nullptr, -1, methods,

@@ -18,7 +18,8 @@
  * the backward), gs_project_bwd_adam (the chain rule fused with one Adam
  * step), bfloat16-SH variants of the projection and its chain rule,
  * gs_bin_sort_noalloc, and the token operators of a network that predicts the
- * Gaussians (gs_qk_norm_rope, gs_attention_fwd, gs_dropout_add, their gradients).
+ * Gaussians (gs_qk_norm_rope, gs_attention_fwd, gs_dropout_add, gs_residual_norm, their
+ * gradients, gs_clip_grad_norm).
  *
  * Sources (page title, section / equation):
  *   [RY]  Ryu & Yoo, "Mitigating SM-Level Load Imbalance in 3D Gaussian
@@ -578,6 +579,101 @@ gs_status gs_dropout_add(int64_t n, int32_t type, const void* x, const void* res
 
 gs_status gs_dropout_add_bwd(int64_t n, int32_t type, const void* dout, void* dx,
                              const int64_t* rng, float p, void* stream);
+
+/*
+ * gs_residual_norm -- what stands between two blocks, per token over its `width` values:
+ *   u = post(y),  r = alpha x + beta gate u,  h = pre(r)
+ * x the residual stream, y a block's output, post and pre each nothing (GS_NORM_NONE),
+ * the RMS norm v (mean(v^2) + eps)^(-1/2) or the layer norm, the same of v less its mean, times a
+ * weight and plus a bias.  r is rounded once for r_out; h is made of the unrounded r.
+ *
+ *   tokens >= 0; width 1..8192; norm.type: of all [tokens][width] arrays
+ *   x, y       y NULL: r = alpha x (post GS_NORM_NONE, no gate)
+ *   params     fp32 [width] weights (NULL = 1) and biases (NULL = 0), of post only with post and
+ *              of pre only with pre; gate fp32 [batch][width] (NULL = 1)
+ *   cu         with a gate: int32 [batch + 1] offsets of the sequences' tokens, ascending from
+ *              0 to tokens, lengths may be 0; tokens of sequence b take row b of the gate.  Offsets
+ *              beyond the tokens are cut to them; rows that no sequence holds are left unwritten
+ *              and count for no gradient.  NULL: batch = 1, all tokens
+ *   r_out      NULL = not wanted
+ *   h_out      required with pre, NULL without
+ *
+ * gs_residual_norm_bwd -- the gradient, from that of r_out (dr_out, NULL = 0) and of h_out
+ * (dh_out, required with pre, NULL without); the statistics are formed again from x and y:
+ *   dR = dr_out + pre's,  dx = alpha dR,  dy = post's of beta gate dR
+ *   dy         required with y, NULL without
+ *   grads      fp32 out, sums over all tokens (gate: over each sequence's); NULL = not wanted,
+ *              which those of a norm that is not there must be
+ *   workspace  >= gs_residual_norm_workspace_bytes(...); holds nothing between calls
+ *
+ * Rows may be those of a wider array (row_stride in elements, >= width); widths that are a multiple
+ * of 8 in rows of whole 16-byte words go faster.  Outputs may be inputs (same data and stride),
+ * but not overlap them otherwise, nor each other.  All sums are fp32.
+ */
+#define GS_NORM_NONE 0
+#define GS_NORM_RMS 1
+#define GS_NORM_LAYER 2
+
+typedef struct {
+    void* data; /* device, aligned to an element */
+    int64_t row_stride;
+} gs_rows;
+
+typedef struct {
+    int32_t type; /* GS_TYPE_F32 or GS_TYPE_BF16 */
+    int32_t pre, post;
+    int32_t batch; /* rows of the gate */
+    float alpha, beta, eps;
+} gs_block_norm;
+
+typedef struct {
+    const float *pre_weight, *pre_bias, *post_weight, *post_bias, *gate;
+} gs_norm_params;
+
+typedef struct {
+    float *pre_weight, *pre_bias, *post_weight, *post_bias, *gate;
+} gs_norm_grads;
+
+gs_status gs_residual_norm(int64_t tokens, int32_t width, const gs_block_norm* norm,
+                           const gs_rows* x, const gs_rows* y, const gs_norm_params* params,
+                           const int32_t* cu, const gs_rows* r_out, const gs_rows* h_out,
+                           void* stream);
+
+size_t gs_residual_norm_workspace_bytes(int64_t tokens, int32_t width, int32_t batch);
+
+gs_status gs_residual_norm_bwd(int64_t tokens, int32_t width, const gs_block_norm* norm,
+                               const gs_rows* x, const gs_rows* y, const gs_norm_params* params,
+                               const int32_t* cu, const gs_rows* dr_out, const gs_rows* dh_out,
+                               const gs_rows* dx, const gs_rows* dy, const gs_norm_grads* grads,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gs_clip_grad_norm -- the norm over all values of a step's gradients, and the gradients scaled to
+ * a norm of at most max_norm:
+ *   norm = (sum over all arrays of g^2)^(1/2),  out = g min(1, max_norm / norm)
+ * Where norm is not finite (a gradient is infinite or NaN; finite ones do not overflow: squares
+ * are summed in fp64 where they would) the factor is 0 and every out value 0.
+ *
+ *   count      0..65536 arrays of at most 2^40 elements each, 2^42 in all
+ *   grads      host array: device data (aligned to an element; at 16 bytes it goes faster, NULL
+ *              where elements = 0), elements, and type
+ *   outs       host array of the same elements and types; an out may be its gradient itself.  NULL:
+ *              all are, and where norm <= max_norm nothing is written
+ *   max_norm   >= 0; infinity: the norm alone is wanted, outs as grads (NULL: nothing is written)
+ *   norm       out, device float: the norm before clipping
+ *   workspace  >= gs_clip_grad_norm_workspace_bytes(count); holds nothing between calls
+ */
+typedef struct {
+    void* data;
+    int64_t elements;
+    int32_t type; /* GS_TYPE_F32 or GS_TYPE_BF16 */
+} gs_array;
+
+size_t gs_clip_grad_norm_workspace_bytes(int32_t count);
+
+gs_status gs_clip_grad_norm(int32_t count, const gs_array* grads, const gs_array* outs,
+                            float max_norm, float* norm, void* workspace, size_t workspace_bytes,
+                            void* stream);
 
 #ifdef __cplusplus
 }
