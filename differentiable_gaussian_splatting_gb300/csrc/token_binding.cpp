@@ -356,7 +356,7 @@ BlockNorm block_norm_of(PyObject* x, PyObject* y, PyObject* const* a) {
     r.w = {vector(a[0], "pre_weight", r.width), vector(a[1], "pre_bias", r.width),
            vector(a[2], "post_weight", r.width), vector(a[3], "post_bias", r.width),
            vector(a[4], "gate", r.norm.batch * r.width)};
-    if (r.cu && a[4] == Py_None) throw ValueError("cu: the offsets of a gate, which is None");
+    if (a[5] != Py_None && a[4] == Py_None) throw ValueError("cu: the offsets of a gate, which is None");
     r.norm.pre = (int32_t)number(a[6]);
     r.norm.post = (int32_t)number(a[7]);
     r.norm.alpha = number(a[8]);
