@@ -39,6 +39,7 @@ __all__ = [
     "gs_qk_norm_rope", "gs_qk_norm_rope_bwd", "gs_qk_norm_rope_workspace_bytes",
     "gs_attention_fwd", "gs_attention_bwd", "gs_attention_workspace_bytes", "gs_attention_status",
     "gs_dropout_add", "gs_dropout_add_bwd",
+    "gs_attention_window_fwd", "gs_attention_window_bwd", "gs_attention_window_workspace_bytes",
     "gs_residual_norm", "gs_residual_norm_bwd", "gs_residual_norm_workspace_bytes",
     "gs_clip_grad_norm", "gs_clip_grad_norm_workspace_bytes",
     "Camera", "Settings", "Rasterizer", "library",
@@ -129,6 +130,11 @@ class AttentionShape(C.Structure):
     _fields_ = [("tokens_q", C.c_int64), ("tokens_k", C.c_int64), ("batch", C.c_int32),
                 ("heads_q", C.c_int32), ("heads_k", C.c_int32), ("head_dim", C.c_int32),
                 ("causal", C.c_int32), ("scale", C.c_float)]
+
+
+class Window(C.Structure):
+    """gs_window: keys that a query sees before and behind its own, and first keys that all see."""
+    _fields_ = [("left", C.c_int32), ("right", C.c_int32), ("sinks", C.c_int32)]
 
 
 class Rows(C.Structure):
@@ -229,6 +235,14 @@ def _declare(lib: C.CDLL) -> None:
     lib.gs_attention_fwd.argtypes = [A, H, H, H, _P, _P, H, _P, _P, C.c_size_t, _P]
     lib.gs_attention_bwd.restype = st
     lib.gs_attention_bwd.argtypes = [A, H, H, H, _P, _P, H, _P, H, H, H, H, _P, C.c_size_t, _P]
+    V = C.POINTER(Window)
+    lib.gs_attention_window_workspace_bytes.restype = C.c_size_t
+    lib.gs_attention_window_workspace_bytes.argtypes = [A, V]
+    lib.gs_attention_window_fwd.restype = st
+    lib.gs_attention_window_fwd.argtypes = [A, V, H, H, H, _P, _P, H, _P, _P, C.c_size_t, _P]
+    lib.gs_attention_window_bwd.restype = st
+    lib.gs_attention_window_bwd.argtypes = [A, V, H, H, H, _P, _P, H, _P, H, H, H, H, _P,
+                                            C.c_size_t, _P]
     lib.gs_attention_status.restype = st
     lib.gs_attention_status.argtypes = [_P]
     lib.gs_dropout_add.restype = st
@@ -632,6 +646,34 @@ def gs_attention_bwd(q, k, v, out, lse, dout, dq, dk, dv, workspace, cu_q=None, 
                                                   cu_q, cu_k, causal, scale, stream)
     if st:
         _check("gs_attention_bwd", st)
+
+
+def gs_attention_window_workspace_bytes(tokens_q, tokens_k, batch, heads_q, heads_k, head_dim, left,
+                                        right=0, sinks=0) -> int:
+    shape = AttentionShape(int(tokens_q), int(tokens_k), int(batch), int(heads_q), int(heads_k),
+                           int(head_dim), 0, 1.0)
+    window = Window(*[min(int(n), 2 ** 31 - 1) for n in (left, right, sinks)])
+    return int(library().gs_attention_window_workspace_bytes(C.byref(shape), C.byref(window)))
+
+
+def gs_attention_window_fwd(q, k, v, out, lse, workspace, left, right=0, sinks=0, cu_q=None,
+                            cu_k=None, causal=False, scale=None, stream=None):
+    """gs_attention_fwd over the `left` keys before a query's own, the `right` ones behind it and the
+    first `sinks` of its sequence (see gs.h)."""
+    st = (_calls or _token_calls()).attention_window_fwd(
+        q, k, v, out, lse, workspace, left, right, sinks, cu_q, cu_k, causal, scale, stream)
+    if st:
+        _check("gs_attention_window_fwd", st)
+
+
+def gs_attention_window_bwd(q, k, v, out, lse, dout, dq, dk, dv, workspace, left, right=0, sinks=0,
+                            cu_q=None, cu_k=None, causal=False, scale=None, stream=None):
+    """Gradient of gs_attention_window_fwd from its out and lse (see gs.h)."""
+    st = (_calls or _token_calls()).attention_window_bwd(
+        q, k, v, out, lse, dout, dq, dk, dv, workspace, left, right, sinks, cu_q, cu_k, causal,
+        scale, stream)
+    if st:
+        _check("gs_attention_window_bwd", st)
 
 
 def gs_attention_status(stream=None) -> None:

@@ -17,6 +17,7 @@ constexpr int64_t kMaxStride = int64_t(1) << 38;  // elements
 constexpr int32_t kMaxHeads = 1024;
 constexpr int32_t kMaxBatch = 1 << 20;
 constexpr int32_t kMaxNormDim = 256, kMaxAttentionDim = 128;
+constexpr int32_t kMaxSinks = 128;  // of one key tile
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -171,11 +172,13 @@ size_t gs_attention_workspace_bytes(const gs_attention_shape* shape) {
                                      shape->heads_q, shape->heads_k, shape->head_dim);
 }
 
-gs_status gs_attention_fwd(const gs_attention_shape* shape, const gs_heads* q, const gs_heads* k,
-                           const gs_heads* v, const int32_t* cu_q, const int32_t* cu_k,
-                           const gs_heads* out, float* lse, void* workspace,
-                           size_t workspace_bytes, void* stream) {
-    if (!shape_ok(shape)) return GS_ERR_INVALID_ARG;
+namespace {
+
+// window: null without one
+gs_status attention_fwd(const gs_attention_shape* shape, const gs_window* window, const gs_heads* q,
+                        const gs_heads* k, const gs_heads* v, const int32_t* cu_q,
+                        const int32_t* cu_k, const gs_heads* out, float* lse, void* workspace,
+                        size_t workspace_bytes, size_t needed, void* stream) {
     const gs_attention_shape& s = *shape;
     if (s.tokens_q == 0) return GS_OK;
     if (!offsets_ok(s, cu_q, cu_k) || !lse || !aligned16(lse) || !workspace ||
@@ -184,20 +187,20 @@ gs_status gs_attention_fwd(const gs_attention_shape* shape, const gs_heads* q, c
         !heads_ok(v, s.tokens_k, s.heads_k, s.head_dim, 2) ||
         !heads_ok(out, s.tokens_q, s.heads_q, s.head_dim, 2))
         return GS_ERR_INVALID_ARG;
-    if (workspace_bytes < gs_attention_workspace_bytes(shape)) return GS_ERR_WORKSPACE;
+    if (workspace_bytes < needed) return GS_ERR_WORKSPACE;
     return status_of(launch_attention_fwd(
         s, normal(q, s.tokens_q, s.heads_q, s.head_dim),
         normal(k, s.tokens_k, s.heads_k, s.head_dim), normal(v, s.tokens_k, s.heads_k, s.head_dim),
-        normal(out, s.tokens_q, s.heads_q, s.head_dim), lse, cu_q, cu_k, workspace,
+        normal(out, s.tokens_q, s.heads_q, s.head_dim), lse, cu_q, cu_k, window, workspace,
         (cudaStream_t)stream));
 }
 
-gs_status gs_attention_bwd(const gs_attention_shape* shape, const gs_heads* q, const gs_heads* k,
-                           const gs_heads* v, const int32_t* cu_q, const int32_t* cu_k,
-                           const gs_heads* out, const float* lse, const gs_heads* dout,
-                           const gs_heads* dq, const gs_heads* dk, const gs_heads* dv,
-                           void* workspace, size_t workspace_bytes, void* stream) {
-    if (!shape_ok(shape)) return GS_ERR_INVALID_ARG;
+gs_status attention_bwd(const gs_attention_shape* shape, const gs_window* window, const gs_heads* q,
+                        const gs_heads* k, const gs_heads* v, const int32_t* cu_q,
+                        const int32_t* cu_k, const gs_heads* out, const float* lse,
+                        const gs_heads* dout, const gs_heads* dq, const gs_heads* dk,
+                        const gs_heads* dv, void* workspace, size_t workspace_bytes, size_t needed,
+                        void* stream) {
     const gs_attention_shape& s = *shape;
     if (s.tokens_q == 0 && s.tokens_k == 0) return GS_OK;
     if (!offsets_ok(s, cu_q, cu_k) || (s.tokens_q > 0 && (!lse || !aligned16(lse))) || !workspace ||
@@ -209,7 +212,7 @@ gs_status gs_attention_bwd(const gs_attention_shape* shape, const gs_heads* q, c
         if (!heads_ok(h, s.tokens_q, s.heads_q, s.head_dim, 2)) return GS_ERR_INVALID_ARG;
     for (const gs_heads* h : of_k)
         if (!heads_ok(h, s.tokens_k, s.heads_k, s.head_dim, 2)) return GS_ERR_INVALID_ARG;
-    if (workspace_bytes < gs_attention_workspace_bytes(shape)) return GS_ERR_WORKSPACE;
+    if (workspace_bytes < needed) return GS_ERR_WORKSPACE;
     const auto nq = [&](const gs_heads* h) {
         return normal(h, s.tokens_q, s.heads_q, s.head_dim);
     };
@@ -217,8 +220,62 @@ gs_status gs_attention_bwd(const gs_attention_shape* shape, const gs_heads* q, c
         return normal(h, s.tokens_k, s.heads_k, s.head_dim);
     };
     return status_of(launch_attention_bwd(s, nq(q), nk(k), nk(v), nq(out), lse, nq(dout), nq(dq),
-                                          nk(dk), nk(dv), cu_q, cu_k, workspace,
+                                          nk(dk), nk(dv), cu_q, cu_k, window, workspace,
                                           (cudaStream_t)stream));
+}
+
+bool window_ok(const gs_window* w) {
+    return w && w->left >= 0 && w->right >= 0 && w->sinks >= 0 && w->sinks <= kMaxSinks;
+}
+
+}  // namespace
+
+gs_status gs_attention_fwd(const gs_attention_shape* shape, const gs_heads* q, const gs_heads* k,
+                           const gs_heads* v, const int32_t* cu_q, const int32_t* cu_k,
+                           const gs_heads* out, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    if (!shape_ok(shape)) return GS_ERR_INVALID_ARG;
+    return attention_fwd(shape, nullptr, q, k, v, cu_q, cu_k, out, lse, workspace, workspace_bytes,
+                         gs_attention_workspace_bytes(shape), stream);
+}
+
+gs_status gs_attention_bwd(const gs_attention_shape* shape, const gs_heads* q, const gs_heads* k,
+                           const gs_heads* v, const int32_t* cu_q, const int32_t* cu_k,
+                           const gs_heads* out, const float* lse, const gs_heads* dout,
+                           const gs_heads* dq, const gs_heads* dk, const gs_heads* dv,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+    if (!shape_ok(shape)) return GS_ERR_INVALID_ARG;
+    return attention_bwd(shape, nullptr, q, k, v, cu_q, cu_k, out, lse, dout, dq, dk, dv, workspace,
+                         workspace_bytes, gs_attention_workspace_bytes(shape), stream);
+}
+
+size_t gs_attention_window_workspace_bytes(const gs_attention_shape* shape,
+                                           const gs_window* window) {
+    if (!shape_ok(shape) || !window_ok(window)) return 0;
+    return attention_workspace_bytes(shape->tokens_q, shape->tokens_k, shape->batch,
+                                     shape->heads_q, shape->heads_k, shape->head_dim, *window);
+}
+
+gs_status gs_attention_window_fwd(const gs_attention_shape* shape, const gs_window* window,
+                                  const gs_heads* q, const gs_heads* k, const gs_heads* v,
+                                  const int32_t* cu_q, const int32_t* cu_k, const gs_heads* out,
+                                  float* lse, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+    if (!shape_ok(shape) || !window_ok(window)) return GS_ERR_INVALID_ARG;
+    return attention_fwd(shape, window, q, k, v, cu_q, cu_k, out, lse, workspace, workspace_bytes,
+                         gs_attention_window_workspace_bytes(shape, window), stream);
+}
+
+gs_status gs_attention_window_bwd(const gs_attention_shape* shape, const gs_window* window,
+                                  const gs_heads* q, const gs_heads* k, const gs_heads* v,
+                                  const int32_t* cu_q, const int32_t* cu_k, const gs_heads* out,
+                                  const float* lse, const gs_heads* dout, const gs_heads* dq,
+                                  const gs_heads* dk, const gs_heads* dv, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+    if (!shape_ok(shape) || !window_ok(window)) return GS_ERR_INVALID_ARG;
+    return attention_bwd(shape, window, q, k, v, cu_q, cu_k, out, lse, dout, dq, dk, dv, workspace,
+                         workspace_bytes, gs_attention_window_workspace_bytes(shape, window),
+                         stream);
 }
 
 gs_status gs_attention_status(void* stream) {

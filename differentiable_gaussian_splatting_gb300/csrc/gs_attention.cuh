@@ -10,6 +10,7 @@
 
 #include "gs_device.cuh"
 #include "gs_tensor.cuh"
+#include "../../include/gs.h"
 
 namespace gs {
 
@@ -34,6 +35,62 @@ struct Sequence {
 // how many keys query i of a sequence sees
 __device__ __forceinline__ int seen_keys(int i, int n, int m, bool causal) {
     return causal ? min(m, max(0, i + 1 + m - n)) : m;
+}
+
+// A window on the keys (gs_attention_window_*): query i stands at key i + m - n and sees `left`
+// keys before it, `right` behind it and, wherever it stands, the first `sinks`; under the causal
+// mask none behind it.
+struct Window {
+    int left, right, sinks;
+    bool causal;
+};
+
+// What a query sees: keys lo..hi - 1 and 0..sinks - 1.  All three rise with the query.
+struct Seen {
+    int lo, hi, sinks;
+};
+
+__device__ __forceinline__ int cut(int64_t x, int lo, int hi) {
+    return (int)min64(max64(x, lo), hi);
+}
+
+__device__ __forceinline__ Seen seen_by(const Window& w, int i, int n, int m) {
+    const int64_t at = (int64_t)i + m - n;  // 64 bits: windows may be as wide as all keys
+    Seen s;
+    s.hi = cut(at + w.right + 1, 0, m);
+    s.lo = cut(at - w.left, 0, s.hi);
+    s.sinks = min(w.sinks, m);
+    if (w.causal) s.sinks = cut(at + 1, 0, s.sinks);
+    return s;
+}
+
+// The queries that see key j: first .. end - 1.
+__device__ __forceinline__ void seers_of(const Window& w, int j, int n, int m, int* first,
+                                         int* end) {
+    const int64_t at = (int64_t)j + n - m;  // the query that stands at the key
+    const bool sink = j < w.sinks;
+    *first = sink && !w.causal ? 0 : cut(at - (sink ? 0 : w.right), 0, n);
+    *end = sink ? n : cut(at + w.left + 1, 0, n);
+}
+
+// The key tiles that rows a..b of a sequence walk: the window's, and before them (extra = 1) that of
+// the sinks, tile 0, where the window begins behind it.
+struct Walk {
+    int first, extra, tiles;
+    __device__ __forceinline__ int tile(int v) const { return v < extra ? 0 : first + v - extra; }
+};
+
+__device__ __forceinline__ int walk_end(const Seen& s) {
+    return s.hi > 0 ? (s.hi + kTileRows - 1) / kTileRows : (s.sinks > 0 ? 1 : 0);
+}
+
+__device__ __forceinline__ Walk walk_of(const Window& w, const Sequence& sq, int a, int b) {
+    const Seen last = seen_by(w, b, sq.n, sq.m);
+    Walk k;
+    k.first = seen_by(w, a, sq.n, sq.m).lo / kTileRows;
+    k.extra = k.first > 0 && last.sinks > 0 ? 1 : 0;
+    k.tiles = max(0, walk_end(last) - k.first) + k.extra;
+    return k;
 }
 
 // A block's place: `rows` queries (or keys) of one sequence and a head; and the sequence.
@@ -192,6 +249,11 @@ __device__ __forceinline__ void zero_rows(char* tile, int first) {
 
 // Device address of the count of blocks in which a bounded wait of an attention kernel gave up.
 cudaError_t gave_up_word(unsigned int** word);
+
+// the window as the kernels take it
+inline Window window_of(const gs_window& w, bool causal) {
+    return {w.left, causal ? 0 : w.right, w.sinks, causal};
+}
 
 // Tensor map of a [tokens][heads][dim] array: tiles of 128 tokens of one head, 64 values
 // wide under the 128-byte swizzle; zeros beyond the array.  The map's outer dimensions go

@@ -69,6 +69,10 @@ struct BwdWork {
     int head, khead;
     int first, items; // tiles of the other side: those of the block's piece
     int64_t part;     // first row in the workspace (-1: the block writes the output itself)
+    // with a window
+    int q_first, per_head;  // block of keys: its query tiles, of each head
+    int key_first, key_end; // block of keys: those it writes, less row0
+    Walk walk;              // block of queries
 };
 
 struct BwdParams {
@@ -82,13 +86,46 @@ struct BwdParams {
     unsigned int* gave_up;
     BwdPlan plan_k, plan_q;     // of the blocks of keys, of queries
     float *parts_k, *parts_q;   // [pieces][rest][slot_rows][DP]: dK, then dV; dQ
+    // With a window (batch.causal is not set then).  Every query may see the sinks: their blocks
+    // take `sink_rows` queries each, `sink_blocks` in all, before the other blocks of keys, which
+    // leave the sinks out.  Sequences of more queries keep the pieces' sums in
+    // parts_s [slots][heads_k][dK, dV][sinks][DP].
+    Window window;
+    int sink_rows;
+    int64_t sink_blocks;
+    float* parts_s;
 };
+
+// A sequence's first slot: there are sink_slots of them, and of sequences with more than `rows`
+// queries no two meet (they have floor(2 n / rows) >= ceil(n / rows) slots each).
+__host__ __device__ inline int64_t sink_slot(int64_t q0, int rows) { return 2 * q0 / rows; }
+__host__ __device__ inline int64_t sink_slots(int64_t tq, int rows) { return sink_slot(tq, rows) + 2; }
 
 // query tiles that see a block of keys, for each head of the group: from *first on
 __device__ __forceinline__ int queries_of(const Sequence& sq, int key0, bool causal, int* first) {
     const int tiles = (sq.n + kTileRows - 1) / kTileRows;
     *first = causal ? min(tiles, max(0, key0 + sq.n - sq.m) / kTileRows) : 0;
     return tiles - *first;
+}
+
+// the same with a window, for keys first..end - 1 of the sequence: (first tile, tiles)
+__device__ __forceinline__ int queries_of(const Window& w, const Sequence& sq, int first, int end,
+                                          int* tile) {
+    *tile = 0;
+    if (first >= end) return 0;
+    int q0, q1, unused;
+    seers_of(w, first, sq.n, sq.m, &q0, &unused);
+    seers_of(w, end - 1, sq.n, sq.m, &unused, &q1);
+    if (q0 >= q1) return 0;
+    *tile = q0 / kTileRows;
+    return (q1 + kTileRows - 1) / kTileRows - *tile;
+}
+
+// keys of the block at row0 that are no sinks: first..end - 1
+__device__ __forceinline__ void window_keys(const Window& w, const Sequence& sq, int row0, int* first,
+                                            int* end) {
+    *end = min(sq.m, row0 + kTileRows);
+    *first = min(max(row0, w.sinks), *end);
 }
 
 // key tiles that a block of queries sees
@@ -105,8 +142,31 @@ __host__ __device__ inline int64_t blocks_of(const BwdPlan& plan) {
     return plan.whole + plan.rest * plan.pieces;
 }
 
+// By one whole warp: the work of block `id` of the sinks' blocks, or false.
+__device__ __forceinline__ bool find_sink_work(const BwdParams& p, int64_t id, BwdWork* out) {
+    Place at{};
+    if (!find_place<false>(p.batch, p.sink_rows, p.heads_k, (int)id, &at)) return false;
+    BwdWork w;
+    w.sq = at.sq;
+    w.row0 = 0;
+    w.head = w.khead = at.head;
+    w.key_first = 0;
+    w.key_end = min(p.window.sinks, w.sq.m);
+    if (w.key_end == 0) return false;
+    w.q_first = at.tile * (p.sink_rows / kTileRows);
+    w.per_head = min((w.sq.n + kTileRows - 1) / kTileRows - w.q_first, p.sink_rows / kTileRows);
+    w.first = 0;
+    w.items = w.per_head * p.group;
+    w.part = -1;
+    if (w.sq.n > p.sink_rows)
+        w.part = ((sink_slot(w.sq.q0, p.sink_rows) + at.tile) * p.heads_k + at.head) * 2 *
+                 p.window.sinks;
+    if ((threadIdx.x & 31) == 0) *out = w;
+    return true;
+}
+
 // By one whole warp: the work of block `id` of its kind, or false.
-template <bool kKeys>
+template <bool kKeys, bool kWindow>
 __device__ __forceinline__ bool find_work(const BwdParams& p, int64_t id, BwdWork* out) {
     const BwdPlan& plan = kKeys ? p.plan_k : p.plan_q;
     int64_t part = -1;
@@ -125,8 +185,20 @@ __device__ __forceinline__ bool find_work(const BwdParams& p, int64_t id, BwdWor
     w.head = at.head;
     w.khead = kKeys ? at.head : at.head / p.group;
     int unused;
-    w.items = kKeys ? queries_of(w.sq, w.row0, p.batch.causal, &unused) * p.group
-                    : keys_of(w.sq, w.row0, p.batch.causal);
+    if constexpr (kWindow && kKeys) {
+        int first, end;
+        window_keys(p.window, w.sq, w.row0, &first, &end);
+        w.per_head = queries_of(p.window, w.sq, first, end, &w.q_first);
+        w.key_first = first - w.row0;
+        w.key_end = end - w.row0;
+        w.items = w.per_head * p.group;
+    } else if constexpr (kWindow) {
+        w.walk = walk_of(p.window, w.sq, w.row0, min(w.sq.n, w.row0 + kTileRows) - 1);
+        w.items = w.walk.tiles;
+    } else {
+        w.items = kKeys ? queries_of(w.sq, w.row0, p.batch.causal, &unused) * p.group
+                        : keys_of(w.sq, w.row0, p.batch.causal);
+    }
     w.first = 0;
     w.part = part;
     if (part >= 0) {
@@ -226,7 +298,8 @@ struct DkvShape {
     static constexpr uint32_t kSmem = kRows + kSlots * 2 * kTileRows * sizeof(float) + 1024;
 };
 
-template <int DP>
+// kSinks: a block of the sinks (with a window)
+template <int DP, bool kWindow, bool kSinks>
 __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtensorMap& map_k,
                                           const CUtensorMap& map_v, const CUtensorMap& map_d,
                                           const BwdParams& p, int64_t id) {
@@ -243,7 +316,11 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
-        const bool ok = find_work<true>(p, id, &work);
+        bool ok;
+        if constexpr (kSinks)
+            ok = find_sink_work(p, id, &work);
+        else
+            ok = find_work<true, kWindow>(p, id, &work);
         if (lane == 0) found = ok, dead = 0;
     }
     __syncthreads();
@@ -283,8 +360,9 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
     if (items > 0 && warp == kMathWarps + 1) {
         // ---- the producer ----
         const Sequence sq = work.sq;
-        int q_first;
-        const int per_head = queries_of(sq, work.row0, p.batch.causal, &q_first);
+        int q_first = work.q_first;
+        const int per_head =
+            kWindow ? work.per_head : queries_of(sq, work.row0, p.batch.causal, &q_first);
         if (elect_one()) {
             const int64_t key = sq.k0 + work.row0;
             mbar_expect(smem_u32(&bar_k), Sh::kTileBytes);
@@ -411,18 +489,28 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
         const uint32_t s_at = t_s + lanes + half * 64;
         const float sl = p.log2_scale;
         const int n = work.sq.n;
-        int q_first;
-        const int q_end = queries_of(work.sq, work.row0, p.batch.causal, &q_first) + q_first;
+        int q_first = work.q_first;
+        const int q_end =
+            (kWindow ? work.per_head : queries_of(work.sq, work.row0, p.batch.causal, &q_first)) +
+            q_first;
         // the first query that sees this thread's key; the last of the tile's keys' first
         const int ahead = work.row0 + n - work.sq.m;
-        const int sees = p.batch.causal ? max(0, ahead + r) : 0;
-        const int all_see = p.batch.causal ? max(0, ahead + kTileRows - 1) : 0;
+        int sees = p.batch.causal ? max(0, ahead + r) : 0;
+        int all_see = p.batch.causal ? max(0, ahead + kTileRows - 1) : 0;
+        // the query behind the last that sees it; the first of the tile's keys'
+        int sees_end = n, all_end = n;
+        if constexpr (kWindow) {
+            int unused;
+            seers_of(p.window, work.row0 + r, n, work.sq.m, &sees, &sees_end);
+            seers_of(p.window, work.row0 + work.key_first, n, work.sq.m, &unused, &all_end);
+            seers_of(p.window, work.row0 + work.key_end - 1, n, work.sq.m, &all_see, &unused);
+        }
         int tile = q_first + (items > 0 ? work.first % (q_end - q_first) : 0);
         for (int i = 0; i < items; ++i) {
             const int slot = i % Sh::kSlots, i0 = tile * kTileRows;
             if (++tile == q_end) tile = q_first;
-            const bool masked = i0 < all_see || i0 + kTileRows > n;
-            const int lo = sees - i0 - half * 64, hi = n - i0 - half * 64;
+            const bool masked = i0 < all_see || i0 + kTileRows > all_end;
+            const int lo = sees - i0 - half * 64, hi = sees_end - i0 - half * 64;
             mbar_pass(smem_u32(&full_q[slot]), (i / Sh::kSlots) & 1, &dead);
             mbar_pass(smem_u32(&bar_s), i & 1, &dead);
             tmem_fence_after();
@@ -487,12 +575,15 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
         if (!any_dead(&dead)) {
             tmem_fence_after();
             const int key = work.row0 + r;
-            const bool valid = key < work.sq.m, split = work.part >= 0;
+            const bool valid = kWindow ? r >= work.key_first && r < work.key_end : key < work.sq.m;
+            const bool split = work.part >= 0;
             const HeadView& g = half ? p.dk : p.dv;
             __nv_bfloat16* out = valid && !split ? g.row(work.sq.k0 + key, work.khead) : nullptr;
-            float* part = valid && split
-                              ? p.parts_k + (work.part + r + (half ? 0 : part_rows(p.plan_k))) * DP
-                              : nullptr;
+            float* part = nullptr;
+            if (valid && split)
+                part = kSinks ? p.parts_s + (work.part + r + (half ? 0 : p.window.sinks)) * DP
+                              : p.parts_k +
+                                    (work.part + r + (half ? 0 : part_rows(p.plan_k))) * DP;
             store_row<DP>((half ? t_dk : t_dv) + lanes, out, part, p.dim, half ? p.scale : 1.f,
                           items == 0);
         }
@@ -518,7 +609,7 @@ struct DqShape {
     static constexpr uint32_t kSmem = (2 + kSlotsK + kSlotsV) * kTileBytes + 1024;
 };
 
-template <int DP>
+template <int DP, bool kWindow>
 __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtensorMap& map_k,
                                          const CUtensorMap& map_v, const CUtensorMap& map_d,
                                          const BwdParams& p, int64_t id) {
@@ -535,7 +626,7 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
-        const bool ok = find_work<false>(p, id, &work);
+        const bool ok = find_work<false, kWindow>(p, id, &work);
         if (lane == 0) found = ok, dead = 0;
     }
     __syncthreads();
@@ -572,8 +663,9 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
 
     if (tiles > 0 && warp == kMathWarps + 1) {
         // ---- the producer ----
-        const int khead = work.khead, left = work.sq.m - work.first * kTileRows;
-        const int64_t k0 = work.sq.k0 + (int64_t)work.first * kTileRows;
+        const int khead = work.khead;
+        const int left = work.sq.m - (kWindow ? 0 : work.first * kTileRows);
+        const int64_t k0 = work.sq.k0 + (kWindow ? 0 : (int64_t)work.first * kTileRows);
         const bool tail = work.sq.k0 + work.sq.m < p.batch.tk;
         if (elect_one()) {
             const int64_t q = work.sq.q0 + work.row0;
@@ -588,10 +680,11 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
         for (int j = 0; j < tiles; ++j) {
             const int sk = j % Sh::kSlotsK, uk = j / Sh::kSlotsK;
             const int sv = j % Sh::kSlotsV, uv = j / Sh::kSlotsV;
-            const int64_t token = k0 + (int64_t)j * kTileRows;
+            const int tile = kWindow ? work.walk.tile(work.first + j) : j;
+            const int64_t token = k0 + (int64_t)tile * kTileRows;
             if (uk > 0) ok = mbar_wait(smem_u32(&empty_k[sk]), (uk - 1) & 1, &dead);
             if (!ok) break;
-            const int valid = left - j * kTileRows;
+            const int valid = left - tile * kTileRows;
             const bool mend = valid < kTileRows && tail;
             const uint32_t full = smem_u32(&full_k[sk]), dst = at_k + sk * Sh::kTileBytes;
             const uint32_t bar = mend ? smem_u32(&bar_raw) : full;
@@ -688,7 +781,18 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
             return seen_keys(work.row0 + row, work.sq.n, work.sq.m, p.batch.causal) -
                    work.first * kTileRows;
         };
-        const int limit = limit_of(r), first_limit = limit_of((warp & 3) * 32);
+        const int limit = kWindow ? 0 : limit_of(r);
+        const int first_limit = kWindow ? 0 : limit_of((warp & 3) * 32);
+        // with a window: what the row sees, the end of the warp's first row's keys and the start of
+        // its last one's
+        Seen see{};
+        int first_hi = 0, last_lo = 0;
+        if constexpr (kWindow) {
+            const int row = work.row0 + (warp & 3) * 32;
+            see = seen_by(p.window, row + lane, work.sq.n, work.sq.m);
+            first_hi = seen_by(p.window, row, work.sq.n, work.sq.m).hi;
+            last_lo = seen_by(p.window, row + 31, work.sq.n, work.sq.m).lo;
+        }
         float nl = -INFINITY, nd = 0.f;
         if (work.row0 + r < work.sq.n) {
             const int64_t at = (int64_t)work.head * p.batch.tq + work.sq.q0 + work.row0 + r;
@@ -726,7 +830,17 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
                 dp[c] = a.x;
                 dp[c + 1] = a.y;
             }
-            if ((j + 1) * kTileRows > first_limit) {
+            if constexpr (kWindow) {
+                const int key = work.walk.tile(work.first + j) * kTileRows;
+                if (key + kTileRows > first_hi || key < last_lo) {
+                    const int at = key + half * 64;
+                    const int lo = see.lo - at, hi = see.hi - at, sinks = see.sinks - at;
+#pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        if (c >= hi || c < lo)
+                            if (c >= sinks) dp[c] = 0.f;
+                }
+            } else if ((j + 1) * kTileRows > first_limit) {
                 const int left = limit - j * kTileRows - half * 64;
 #pragma unroll
                 for (int c = 0; c < 64; ++c)
@@ -761,26 +875,34 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
     }
 }
 
-// The blocks of keys, then those of queries.
-template <int DP>
+// The blocks of keys, with a window those of the sinks first, then those of queries.
+template <int DP, bool kWindow>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     attention_bwd_kernel(const __grid_constant__ CUtensorMap map_q,
                          const __grid_constant__ CUtensorMap map_k,
                          const __grid_constant__ CUtensorMap map_v,
                          const __grid_constant__ CUtensorMap map_d, const BwdParams p) {
     grid_dep_sync();
-    const int64_t of_keys = blocks_of(p.plan_k), id = blockIdx.x;
+    const int64_t of_keys = blocks_of(p.plan_k);
+    int64_t id = blockIdx.x;
+    if constexpr (kWindow) {
+        if (id < p.sink_blocks) {
+            dkv_block<DP, true, true>(map_q, map_k, map_v, map_d, p, id);
+            return;
+        }
+        id -= p.sink_blocks;
+    }
     if (id < of_keys)
-        dkv_block<DP>(map_q, map_k, map_v, map_d, p, id);
+        dkv_block<DP, kWindow, false>(map_q, map_k, map_v, map_d, p, id);
     else
-        dq_block<DP>(map_q, map_k, map_v, map_d, p, id - of_keys);
+        dq_block<DP, kWindow>(map_q, map_k, map_v, map_d, p, id - of_keys);
 }
 
 // The sum of a cut block's pieces, in their order, times the scale, in bfloat16.  DP / 4
 // lanes a row; blockIdx.z = 1: dV.
 constexpr int kSumThreads = 256;
 
-template <int DP, bool kKeys>
+template <int DP, bool kKeys, bool kWindow>
 __global__ void __launch_bounds__(kSumThreads) attention_sum_kernel(const BwdParams p) {
     __shared__ Place place;
     __shared__ int found;
@@ -796,9 +918,18 @@ __global__ void __launch_bounds__(kSumThreads) attention_sum_kernel(const BwdPar
     if (!found) return;
     const Sequence sq = place.sq;
     const int row0 = place.tile * kTileRows;
-    int unused;
-    const int items = kKeys ? queries_of(sq, row0, p.batch.causal, &unused) * p.group
-                            : keys_of(sq, row0, p.batch.causal);
+    int unused, items, first_row = 0;
+    if constexpr (kWindow && kKeys) {
+        int first, end;
+        window_keys(p.window, sq, row0, &first, &end);
+        items = queries_of(p.window, sq, first, end, &unused) * p.group;
+        first_row = first - row0;
+    } else if constexpr (kWindow) {
+        items = walk_of(p.window, sq, row0, min(sq.n, row0 + kTileRows) - 1).tiles;
+    } else {
+        items = kKeys ? queries_of(sq, row0, p.batch.causal, &unused) * p.group
+                      : keys_of(sq, row0, p.batch.causal);
+    }
     // a piece without work was not begun
     const int pieces = max(1, (items + plan.chunk - 1) / plan.chunk);
     constexpr int kLanes = DP / 4, kRows = kSumThreads / kLanes;
@@ -811,6 +942,7 @@ __global__ void __launch_bounds__(kSumThreads) attention_sum_kernel(const BwdPar
     const float f = of_v ? 1.f : p.scale;
     const int64_t step = plan.rest * plan.slot_rows;  // rows from a piece to the next
     for (int r = blockIdx.y * kRows + threadIdx.x / kLanes; r < rows; r += gridDim.y * kRows) {
+        if (r < first_row) continue;  // sinks
         const int64_t at = (int64_t)blockIdx.x * plan.slot_rows + r;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -822,6 +954,36 @@ __global__ void __launch_bounds__(kSumThreads) attention_sum_kernel(const BwdPar
             *reinterpret_cast<uint2*>(g.row((kKeys ? sq.k0 : sq.q0) + row0 + r, place.head) +
                                       lane * 4) =
                 make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
+    }
+}
+
+// dK and dV of the sinks of sequences that several blocks took, in their order; zeros where there
+// are no queries.  DP / 4 lanes a row; blockIdx.y = key head.
+template <int DP>
+__global__ void __launch_bounds__(kSumThreads) attention_sink_kernel(const BwdParams p) {
+    grid_dep_sync();
+    constexpr int kLanes = DP / 4, kRows = kSumThreads / kLanes;
+    const int lane = threadIdx.x % kLanes, head = blockIdx.y, sinks = p.window.sinks;
+    for (int b = blockIdx.x; b < p.batch.batch; b += gridDim.x) {
+        const Sequence sq = sequence(p.batch, b);
+        const int pieces = (sq.n + p.sink_rows - 1) / p.sink_rows, rows = min(sinks, sq.m);
+        if (pieces == 1) continue;  // its block has written them
+        const int64_t slot = sink_slot(sq.q0, p.sink_rows);
+        for (int r = threadIdx.x / kLanes; r < 2 * rows; r += kRows) {
+            const bool of_v = r >= rows;
+            const int key = of_v ? r - rows : r;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int z = 0; z < pieces; ++z) {
+                const int64_t row = ((slot + z) * p.heads_k + head) * 2 * sinks + (of_v ? sinks : 0) + key;
+                const float4 v = reinterpret_cast<const float4*>(p.parts_s)[row * kLanes + lane];
+                o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+            }
+            const float f = of_v ? 1.f : p.scale;
+            if (lane * 4 < p.dim)
+                *reinterpret_cast<uint2*>((of_v ? p.dv : p.dk).row(sq.k0 + key, head) + lane * 4) =
+                    make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
+        }
     }
 }
 
@@ -863,45 +1025,74 @@ BwdPlan plan_bwd(int64_t blocks, int64_t items, int64_t tokens, bool uniform) {
 
 int64_t tiles_of(int64_t tokens) { return (tokens + kTileRows - 1) / kTileRows; }
 
-BwdPlan plan_dkv(int64_t tq, int64_t tk, int batch, int heads_q, int heads_k, bool causal) {
-    return plan_bwd(tiles_at_most(tk, kTileRows, batch) * heads_k,
-                    tiles_of(tq) * (heads_q / heads_k), tk, batch == 1 && !causal);
+// `window`: the width that a tile of the other side meets, 0 without a window
+BwdPlan plan_dkv(int64_t tq, int64_t tk, int batch, int heads_q, int heads_k, bool causal,
+                 int64_t window) {
+    const int64_t most = window > 0 ? std::min(tiles_of(tq), tiles_of(window)) : tiles_of(tq);
+    return plan_bwd(tiles_at_most(tk, kTileRows, batch) * heads_k, most * (heads_q / heads_k), tk,
+                    batch == 1 && !causal && window == 0);
 }
-BwdPlan plan_dq(int64_t tq, int64_t tk, int batch, int heads_q, bool causal) {
-    return plan_bwd(tiles_at_most(tq, kTileRows, batch) * heads_q, tiles_of(tk), tq,
-                    batch == 1 && !causal);
+BwdPlan plan_dq(int64_t tq, int64_t tk, int batch, int heads_q, bool causal, int64_t window) {
+    const int64_t most = window > 0 ? std::min(tiles_of(tk), tiles_of(window)) : tiles_of(tk);
+    return plan_bwd(tiles_at_most(tq, kTileRows, batch) * heads_q, most, tq,
+                    batch == 1 && !causal && window == 0);
+}
+
+// a tile's own rows, a part of a tile at either end, and the sinks' tile
+int64_t meets(const gs_window& w) { return (int64_t)w.left + w.right + 1 + 4 * kTileRows; }
+
+// Queries that a block of the sinks takes: about what another block of keys meets.
+int sink_rows_of(const gs_window& w, int64_t tq) {
+    const int64_t tiles = (w.left + (int64_t)w.right) / kTileRows + 2;
+    return (int)std::max<int64_t>(1, std::min(tiles, tiles_of(tq))) * kTileRows;
+}
+int64_t sink_floats(const gs_window& w, int64_t tq, int heads_k, int dp) {
+    return sink_slots(tq, sink_rows_of(w, tq)) * heads_k * 2 * w.sinks * dp;
 }
 
 struct BwdMaps {
     CUtensorMap q, k, v, d;
 };
 
-template <int DP, bool kKeys>
+template <int DP, bool kKeys, bool kWindow>
 cudaError_t launch_sum(const BwdParams& p, cudaStream_t st) {
     const BwdPlan& plan = kKeys ? p.plan_k : p.plan_q;
     if (plan.pieces <= 1) return cudaSuccess;
     const unsigned rows = kSumThreads / (DP / 4);
     const dim3 grid((unsigned)plan.rest, (plan.slot_rows + 2 * rows - 1) / (2 * rows),
                     kKeys ? 2 : 1);
-    return launch(attention_sum_kernel<DP, kKeys>, grid, dim3(kSumThreads), 0, st, p);
+    return launch(attention_sum_kernel<DP, kKeys, kWindow>, grid, dim3(kSumThreads), 0, st, p);
 }
 
-template <int DP>
-cudaError_t launch_dim(const BwdMaps& m, BwdParams p, cudaStream_t st) {
+template <int DP, bool kWindow>
+cudaError_t launch_dim(const BwdMaps& m, BwdParams p, const gs_window* w, cudaStream_t st) {
     const Batch& v = p.batch;
+    const int64_t width = kWindow ? meets(*w) : 0;
     // a side without tokens has no blocks
-    if (v.tk > 0) p.plan_k = plan_dkv(v.tq, v.tk, v.batch, p.heads_q, p.heads_k, v.causal);
-    if (v.tq > 0) p.plan_q = plan_dq(v.tq, v.tk, v.batch, p.heads_q, v.causal);
+    if (v.tk > 0) p.plan_k = plan_dkv(v.tq, v.tk, v.batch, p.heads_q, p.heads_k, v.causal, width);
+    if (v.tq > 0) p.plan_q = plan_dq(v.tq, v.tk, v.batch, p.heads_q, v.causal, width);
     p.parts_q = p.parts_k + 2 * part_rows(p.plan_k) * DP;
+    const bool sinks = kWindow && w->sinks > 0 && v.tk > 0;
+    if (sinks) {
+        p.parts_s = p.parts_q + part_rows(p.plan_q) * DP;
+        p.sink_rows = sink_rows_of(*w, v.tq);
+        if (v.tq > 0) p.sink_blocks = tiles_at_most(v.tq, p.sink_rows, v.batch) * p.heads_k;
+    }
     constexpr uint32_t kSmem = std::max(DkvShape<DP>::kSmem, DqShape<DP>::kSmem);
     cudaError_t e = cudaFuncSetAttribute(
-        attention_bwd_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        attention_bwd_kernel<DP, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e == cudaSuccess)
-        e = launch(attention_bwd_kernel<DP>,
-                   dim3((unsigned)(blocks_of(p.plan_k) + blocks_of(p.plan_q))), dim3(kBwdThreads),
-                   kSmem, st, m.q, m.k, m.v, m.d, p);
-    if (e == cudaSuccess) e = launch_sum<DP, true>(p, st);
-    if (e == cudaSuccess) e = launch_sum<DP, false>(p, st);
+        e = launch(attention_bwd_kernel<DP, kWindow>,
+                   dim3((unsigned)(p.sink_blocks + blocks_of(p.plan_k) + blocks_of(p.plan_q))),
+                   dim3(kBwdThreads), kSmem, st, m.q, m.k, m.v, m.d, p);
+    if (e == cudaSuccess) e = launch_sum<DP, true, kWindow>(p, st);
+    if (e == cudaSuccess) e = launch_sum<DP, false, kWindow>(p, st);
+    if constexpr (kWindow)
+        // one sequence that one block takes: nothing is left to do
+        if (e == cudaSuccess && sinks && (v.batch > 1 || v.tq == 0 || v.tq > p.sink_rows))
+            e = launch(attention_sink_kernel<DP>,
+                       dim3((unsigned)std::min(v.batch, 8 * kSms), (unsigned)p.heads_k),
+                       dim3(kSumThreads), 0, st, p);
     return e;
 }
 
@@ -917,21 +1108,32 @@ size_t attention_bwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int bat
     int64_t rows = 0;
     for (const bool causal : {false, true}) {
         const int64_t a =
-            2 * part_rows(plan_dkv(tokens_q, tokens_k, batch, heads_q, heads_k, causal));
-        const int64_t b = part_rows(plan_dq(tokens_q, tokens_k, batch, heads_q, causal));
+            2 * part_rows(plan_dkv(tokens_q, tokens_k, batch, heads_q, heads_k, causal, 0));
+        const int64_t b = part_rows(plan_dq(tokens_q, tokens_k, batch, heads_q, causal, 0));
         rows = std::max(rows, a + b);
     }
     return ((size_t)tokens_q * heads_q * 2 * sizeof(float) + 255) / 256 * 256 +
            (size_t)rows * (head_dim <= 64 ? 64 : 128) * sizeof(float);
 }
 
+size_t attention_bwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads_q,
+                                     int heads_k, int head_dim, const gs_window& w) {
+    const int64_t dp = head_dim <= 64 ? 64 : 128, width = meets(w);
+    const int64_t rows =
+        2 * part_rows(plan_dkv(tokens_q, tokens_k, batch, heads_q, heads_k, false, width)) +
+        part_rows(plan_dq(tokens_q, tokens_k, batch, heads_q, false, width));
+    return ((size_t)tokens_q * heads_q * 2 * sizeof(float) + 255) / 256 * 256 +
+           (size_t)(rows * dp + sink_floats(w, tokens_q, heads_k, (int)dp)) * sizeof(float);
+}
+
 cudaError_t launch_attention_bwd(const gs_attention_shape& s, const gs_heads& q, const gs_heads& k,
                                  const gs_heads& v, const gs_heads& out, const float* lse,
                                  const gs_heads& dout, const gs_heads& dq, const gs_heads& dk,
                                  const gs_heads& dv, const int32_t* cu_q, const int32_t* cu_k,
-                                 void* ws, cudaStream_t st) {
+                                 const gs_window* window, void* ws, cudaStream_t st) {
     BwdParams p{};
-    p.batch = {cu_q, cu_k, s.tokens_q, s.tokens_k, s.batch, s.causal != 0};
+    p.batch = {cu_q, cu_k, s.tokens_q, s.tokens_k, s.batch, s.causal != 0 && !window};
+    if (window) p.window = window_of(*window, s.causal != 0);
     p.heads_q = s.heads_q;
     p.heads_k = s.heads_k;
     p.group = s.heads_q / s.heads_k;
@@ -971,7 +1173,11 @@ cudaError_t launch_attention_bwd(const gs_attention_shape& s, const gs_heads& q,
                    dim3(kDeltaThreads), 0, st, p);
         if (e != cudaSuccess) return e;
     }
-    return s.head_dim <= 64 ? launch_dim<64>(m, p, st) : launch_dim<128>(m, p, st);
+    if (window)
+        return s.head_dim <= 64 ? launch_dim<64, true>(m, p, window, st)
+                                : launch_dim<128, true>(m, p, window, st);
+    return s.head_dim <= 64 ? launch_dim<64, false>(m, p, nullptr, st)
+                            : launch_dim<128, false>(m, p, nullptr, st);
 }
 
 }  // namespace gs

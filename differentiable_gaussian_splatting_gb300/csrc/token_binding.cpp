@@ -8,6 +8,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <exception>
@@ -20,6 +21,8 @@
 
 // The calls that came after the first ones are looked for weakly: the binding loads beside a
 // library without them, which then says so.
+#pragma weak gs_attention_window_fwd
+#pragma weak gs_attention_window_bwd
 #pragma weak gs_residual_norm
 #pragma weak gs_residual_norm_bwd
 #pragma weak gs_clip_grad_norm
@@ -282,6 +285,42 @@ gs_status attention_bwd(PyObject* const* a) {
                     &dq, &dk, &dv, ws.p, ws.n, stream_of(a[14]));
 }
 
+// left, right, sinks; windows wider than 32 bits hold are as wide as all keys
+gs_window window_of(PyObject* const* a) {
+    const auto whole = [](PyObject* o, const char* name) {
+        const long long v = PyLong_AsLongLong(o);
+        if (v == -1 && PyErr_Occurred()) throw TypeError("");
+        if (v < 0) throw ValueError(text(name, ": expected a number from 0 on, got ", v));
+        return (int32_t)std::min<long long>(v, INT32_MAX);
+    };
+    return {whole(a[0], "left"), whole(a[1], "right"), whole(a[2], "sinks")};
+}
+
+gs_status attention_window_fwd(PyObject* const* a) {
+    const Attention t = attention_of(a[0], a[1], a[2], a[9], a[10], a[11], a[12]);
+    const gs_window w = window_of(a + 6);
+    const gs_heads out = heads(a[3], "out", ScalarType::BFloat16, t.tq);
+    float* lse = static_cast<float*>(
+        flat(a[4], "lse", ScalarType::Float, t.shape.tokens_q * t.shape.heads_q));
+    const Bytes ws = workspace(a[5]);
+    return unlocked(gs_attention_window_fwd, &t.shape, &w, &t.q, &t.k, &t.v, t.cu_q, t.cu_k, &out, lse,
+                    ws.p, ws.n, stream_of(a[13]));
+}
+
+gs_status attention_window_bwd(PyObject* const* a) {
+    const ScalarType bf = ScalarType::BFloat16;
+    const Attention t = attention_of(a[0], a[1], a[2], a[13], a[14], a[15], a[16]);
+    const gs_window w = window_of(a + 10);
+    const gs_heads out = heads(a[3], "out", bf, t.tq), dout = heads(a[5], "dout", bf, t.tq),
+                   dq = heads(a[6], "dq", bf, t.tq), dk = heads(a[7], "dk", bf, t.tk),
+                   dv = heads(a[8], "dv", bf, t.tk);
+    const float* lse = static_cast<float*>(
+        flat(a[4], "lse", ScalarType::Float, t.shape.tokens_q * t.shape.heads_q));
+    const Bytes ws = workspace(a[9]);
+    return unlocked(gs_attention_window_bwd, &t.shape, &w, &t.q, &t.k, &t.v, t.cu_q, t.cu_k, &out, lse,
+                    &dout, &dq, &dk, &dv, ws.p, ws.n, stream_of(a[17]));
+}
+
 const int64_t* rng_of(PyObject* o) {
     return static_cast<int64_t*>(flat(o, "rng", ScalarType::Long, 2));
 }
@@ -449,6 +488,8 @@ PyMethodDef methods[] = {method<qk_norm_rope, 11>("qk_norm_rope"),
                          method<attention_bwd, 15>("attention_bwd"),
                          method<dropout_add, 6>("dropout_add"),
                          method<dropout_add_bwd, 5>("dropout_add_bwd"),
+                         method<attention_window_fwd, 14>("attention_window_fwd"),
+                         method<attention_window_bwd, 18>("attention_window_bwd"),
                          method<residual_norm, 16>("residual_norm"),
                          method<residual_norm_bwd, 24>("residual_norm_bwd"),
                          method<clip_grad_norm, 6>("clip_grad_norm"),

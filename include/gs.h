@@ -18,8 +18,8 @@
  * the backward), gs_project_bwd_adam (the chain rule fused with one Adam
  * step), bfloat16-SH variants of the projection and its chain rule,
  * gs_bin_sort_noalloc, and the token operators of a network that predicts the
- * Gaussians (gs_qk_norm_rope, gs_attention_fwd, gs_dropout_add, gs_residual_norm, their
- * gradients, gs_clip_grad_norm).
+ * Gaussians (gs_qk_norm_rope, gs_attention_fwd, gs_attention_window_fwd,
+ * gs_dropout_add, gs_residual_norm, their gradients, gs_clip_grad_norm).
  *
  * Sources (page title, section / equation):
  *   [RY]  Ryu & Yoo, "Mitigating SM-Level Load Imbalance in 3D Gaussian
@@ -548,6 +548,38 @@ gs_status gs_attention_bwd(const gs_attention_shape* shape, const gs_heads* q, c
                            const gs_heads* out, const float* lse, const gs_heads* dout,
                            const gs_heads* dq, const gs_heads* dk, const gs_heads* dv,
                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gs_attention_window_fwd, gs_attention_window_bwd -- gs_attention_fwd and gs_attention_bwd over the
+ * keys near a query and the sequence's first few (sinks), which stay visible.  Query i of n stands at
+ * key c = i + m - n of m (the last query at the last key) and sees key j iff
+ *   c - left <= j <= c + right  or  j < sinks,  and with causal: j <= c.
+ * Work and time go with the pairs seen, not with n m.  Everything else is as there; what the window
+ * hides must be finite as what the mask hides.
+ *
+ *   left, right  >= 0; as large as the sequences: all keys on that side
+ *   sinks        0..128
+ *   workspace    >= gs_attention_window_workspace_bytes(shape, window)
+ */
+typedef struct {
+    int32_t left, right, sinks;
+} gs_window;
+
+size_t gs_attention_window_workspace_bytes(const gs_attention_shape* shape,
+                                           const gs_window* window);
+
+gs_status gs_attention_window_fwd(const gs_attention_shape* shape, const gs_window* window,
+                                  const gs_heads* q, const gs_heads* k, const gs_heads* v,
+                                  const int32_t* cu_q, const int32_t* cu_k, const gs_heads* out,
+                                  float* lse, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+gs_status gs_attention_window_bwd(const gs_attention_shape* shape, const gs_window* window,
+                                  const gs_heads* q, const gs_heads* k, const gs_heads* v,
+                                  const int32_t* cu_q, const int32_t* cu_k, const gs_heads* out,
+                                  const float* lse, const gs_heads* dout, const gs_heads* dq,
+                                  const gs_heads* dk, const gs_heads* dv, void* workspace,
+                                  size_t workspace_bytes, void* stream);
 
 /*
  * gs_attention_status -- whether a bounded device wait of an attention call, of any thread and
