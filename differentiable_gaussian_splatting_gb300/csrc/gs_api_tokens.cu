@@ -188,11 +188,14 @@ gs_status attention_fwd(const gs_attention_shape* shape, const gs_window* window
         !heads_ok(out, s.tokens_q, s.heads_q, s.head_dim, 2))
         return GS_ERR_INVALID_ARG;
     if (workspace_bytes < needed) return GS_ERR_WORKSPACE;
-    return status_of(launch_attention_fwd(
-        s, normal(q, s.tokens_q, s.heads_q, s.head_dim),
-        normal(k, s.tokens_k, s.heads_k, s.head_dim), normal(v, s.tokens_k, s.heads_k, s.head_dim),
-        normal(out, s.tokens_q, s.heads_q, s.head_dim), lse, cu_q, cu_k, window, workspace,
-        (cudaStream_t)stream));
+    const gs_heads nq = normal(q, s.tokens_q, s.heads_q, s.head_dim),
+                   nk = normal(k, s.tokens_k, s.heads_k, s.head_dim),
+                   nv = normal(v, s.tokens_k, s.heads_k, s.head_dim),
+                   no = normal(out, s.tokens_q, s.heads_q, s.head_dim);
+    return status_of(window ? launch_attention_window_fwd(s, *window, nq, nk, nv, no, lse, cu_q, cu_k,
+                                                          workspace, (cudaStream_t)stream)
+                            : launch_attention_fwd(s, nq, nk, nv, no, lse, cu_q, cu_k, workspace,
+                                                   (cudaStream_t)stream));
 }
 
 gs_status attention_bwd(const gs_attention_shape* shape, const gs_window* window, const gs_heads* q,
@@ -252,8 +255,9 @@ gs_status gs_attention_bwd(const gs_attention_shape* shape, const gs_heads* q, c
 size_t gs_attention_window_workspace_bytes(const gs_attention_shape* shape,
                                            const gs_window* window) {
     if (!shape_ok(shape) || !window_ok(window)) return 0;
-    return attention_workspace_bytes(shape->tokens_q, shape->tokens_k, shape->batch,
-                                     shape->heads_q, shape->heads_k, shape->head_dim, *window);
+    return attention_window_workspace_bytes(shape->tokens_q, shape->tokens_k, shape->batch,
+                                            shape->heads_q, shape->heads_k, shape->head_dim,
+                                            *window);
 }
 
 gs_status gs_attention_window_fwd(const gs_attention_shape* shape, const gs_window* window,

@@ -95,12 +95,12 @@ size_t attention_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, 
     return (fwd > bwd ? fwd : bwd) / 256 * 256 + 512;
 }
 
-size_t attention_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads_q,
-                                 int heads_k, int head_dim, const gs_window& window) {
+size_t attention_window_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads_q,
+                                        int heads_k, int head_dim, const gs_window& window) {
     const size_t fwd =
-        attention_fwd_workspace_bytes(tokens_q, tokens_k, batch, heads_q, head_dim, window);
-    const size_t bwd = attention_bwd_workspace_bytes(tokens_q, tokens_k, batch, heads_q, heads_k,
-                                                     head_dim, window);
+        attention_window_fwd_workspace_bytes(tokens_q, tokens_k, batch, heads_q, head_dim, window);
+    const size_t bwd = attention_window_bwd_workspace_bytes(tokens_q, tokens_k, batch, heads_q,
+                                                            heads_k, head_dim, window);
     return (fwd > bwd ? fwd : bwd) / 256 * 256 + 512;
 }
 

@@ -532,7 +532,10 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
                 pr[c + 2] = ex2_approx(b.x);
                 pr[c + 3] = ex2_approx(b.y);
             }
-            if (masked) {
+            if (kWindow && masked) {
+                mask_by_bits(pr, seen_bits(lo, hi, 0), 0.f);
+                mask_by_bits(pr + 32, seen_bits(lo - 32, hi - 32, 0), 0.f);
+            } else if (masked) {
 #pragma unroll
                 for (int c = 0; c < 64; ++c)
                     if (c < lo || c >= hi) pr[c] = 0.f;
@@ -560,7 +563,10 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
                     __fadd2_rn(make_float2(dp[c + 2], dp[c + 3]), make_float2(v.z, v.w)));
                 dp[c] = a.x, dp[c + 1] = a.y, dp[c + 2] = b.x, dp[c + 3] = b.y;
             }
-            if (masked) {
+            if (kWindow && masked) {
+                mask_by_bits(dp, seen_bits(lo, hi, 0), 0.f);
+                mask_by_bits(dp + 32, seen_bits(lo - 32, hi - 32, 0), 0.f);
+            } else if (masked) {
 #pragma unroll
                 for (int c = 0; c < 64; ++c)
                     if (c < lo || c >= hi) dp[c] = 0.f;
@@ -833,12 +839,11 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
             if constexpr (kWindow) {
                 const int key = work.walk.tile(work.first + j) * kTileRows;
                 if (key + kTileRows > first_hi || key < last_lo) {
-                    const int at = key + half * 64;
-                    const int lo = see.lo - at, hi = see.hi - at, sinks = see.sinks - at;
 #pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        if (c >= hi || c < lo)
-                            if (c >= sinks) dp[c] = 0.f;
+                    for (int c = 0; c < 64; c += 32) {
+                        const int at = key + half * 64 + c;
+                        mask_by_bits(dp + c, seen_bits(see.lo - at, see.hi - at, see.sinks - at), 0.f);
+                    }
                 }
             } else if ((j + 1) * kTileRows > first_limit) {
                 const int left = limit - j * kTileRows - half * 64;
@@ -1116,8 +1121,9 @@ size_t attention_bwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int bat
            (size_t)rows * (head_dim <= 64 ? 64 : 128) * sizeof(float);
 }
 
-size_t attention_bwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads_q,
-                                     int heads_k, int head_dim, const gs_window& w) {
+size_t attention_window_bwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch,
+                                            int heads_q, int heads_k, int head_dim,
+                                            const gs_window& w) {
     const int64_t dp = head_dim <= 64 ? 64 : 128, width = meets(w);
     const int64_t rows =
         2 * part_rows(plan_dkv(tokens_q, tokens_k, batch, heads_q, heads_k, false, width)) +

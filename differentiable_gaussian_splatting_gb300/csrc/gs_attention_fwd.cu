@@ -48,85 +48,14 @@
 #include <cmath>
 #include <cstdint>
 
-#include "gs_attention.cuh"
+#include "gs_attention_fwd.cuh"
 #include "gs_internal.h"
 #include "gs_tokens.h"
 
 namespace gs {
 namespace {
 
-constexpr int kSoftmaxWarps = 8;
 constexpr int kFwdThreads = (kSoftmaxWarps + 2) * 32;
-constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kStale = 8.f;  // powers of two by which a maximum may rise unnoticed
-
-template <int DP>
-struct FwdShape {
-    static constexpr int kBlocks = DP / kBlockCols;
-    static constexpr uint32_t kTileBytes = kBlocks * kBlockBytes;
-    static constexpr int kSlots = DP == 128 ? 4 : 8;
-    // score tiles in tensor memory beside the two outputs: 512 columns hold 3 or 2
-    static constexpr int kScores = DP == 128 ? 2 : 3;
-    static constexpr uint32_t kSmem = (2 + kSlots) * kTileBytes + 1024;
-};
-
-// How blocks are cut.  Last wave: blocks `whole` .. `whole` + `rest` - 1 are cut into
-// `pieces` of `chunk` key tiles, piece by piece.  Spread: all blocks are cut so that kSms
-// blocks take them all; since the lengths are on the device, the kernels find the chunk.
-constexpr int kSms = 152;
-constexpr int kLeastChunk = 4;  // key tiles; below, joining costs more than it saves
-struct FwdPlan {
-    int64_t whole, rest;
-    int chunk, pieces;
-    bool spread;
-    int most_keys;  // key tiles that a block may walk
-    int slot_rows;  // rows that a piece keeps in the workspace
-    __host__ __device__ int64_t part_rows() const {
-        return spread ? (int64_t)kSms * slot_rows : pieces > 1 ? pieces * rest * slot_rows : 0;
-    }
-};
-
-struct FwdParams {
-    Batch batch;
-    int heads, group, dim;
-    bool negative, swap_q, swap_k, swap_v;
-    float log2_scale;  // |scale| log2(e)
-    HeadView o;
-    float* lse;
-    unsigned int* gave_up;
-    FwdPlan plan;
-    Window window;  // batch.causal is not set with one: its blocks cost about the same
-    float *part_o, *part_lse;  // [pieces][rest][slot_rows][DP], [pieces][rest][slot_rows]
-};
-
-// key tiles that query tile t (128 rows) of the block at row0 walks
-__device__ __forceinline__ int walked(const Sequence& sq, int row0, int t, bool causal) {
-    const int last = min(sq.n, row0 + (t + 1) * kTileRows) - 1;
-    return last >= row0 + t * kTileRows
-               ? (seen_keys(last, sq.n, sq.m, causal) + kTileRows - 1) / kTileRows
-               : 0;
-}
-
-// With a window: the walk of both query tiles, each tile's end in it, and the step that the
-// second leaves out (-1: none), since it sees no key of the first's first tile.
-struct FwdWalk {
-    Walk walk;
-    int end[2], skip;
-};
-
-__device__ __forceinline__ FwdWalk walk_of_block(const Window& w, const Sequence& sq, int row0) {
-    FwdWalk f;
-    const int last = min(sq.n, row0 + 2 * kTileRows) - 1;
-    f.walk = walk_of(w, sq, row0, last);
-    const Seen s = seen_by(w, min(last, row0 + kTileRows - 1), sq.n, sq.m);
-    f.end[0] = max(0, walk_end(s) - f.walk.first) + f.walk.extra;
-    f.end[1] = row0 + kTileRows < sq.n ? f.walk.tiles : 0;
-    f.skip = -1;
-    if (f.end[1] > 0 && (f.walk.first > 0 || w.sinks == 0) &&  // the sinks lie in tile 0
-        seen_by(w, row0 + kTileRows, sq.n, sq.m).lo / kTileRows > f.walk.first)
-        f.skip = f.walk.extra;
-    return f;
-}
 
 // What a block works on, kept in shared memory: registers are short in the softmax.
 struct FwdWork {
@@ -136,65 +65,9 @@ struct FwdWork {
     int key0;         // first key of the block's piece
     int tiles[2];     // key tiles that each of the two query tiles walks
     int64_t part;     // first row in the workspace (-1: the block writes the output itself)
-    // with a window: steps are those of the walk from `step0` on; the second query tile's end
-    // among them and the one it leaves out (-1)
-    Walk walk;
-    int step0, end1, skip;
 };
 
-// Spread blocks (by one whole warp; lane = sequence): the smallest chunk with which kSms
-// blocks suffice, and the place of block or piece `id`.  Pieces of a block are neighbours.
-struct Spread {
-    int chunk, pieces;  // of the place's sequence
-    int piece;          // with `cut`: which one
-    int first;          // number of the block's first piece
-};
-
-__device__ __forceinline__ bool find_spread(const Batch& v, int heads, int id, bool by_piece,
-                                            int most_keys, Place* at, Spread* sp) {
-    const int lane = threadIdx.x & 31;
-    const unsigned all = 0xffffffffu;
-    Sequence s{};
-    if (lane < v.batch) s = sequence(v, lane);
-    const int n = s.n, m = s.m;
-    const int blocks = (n + 2 * kTileRows - 1) / (2 * kTileRows) * heads;
-    const int keys = min((m + kTileRows - 1) / kTileRows, most_keys);
-    int lo = kLeastChunk, hi = max(lo, (int)__reduce_max_sync(all, keys));
-    while (lo < hi) {
-        const int c = (lo + hi) >> 1;
-        if ((int)__reduce_add_sync(all, blocks * max(1, (keys + c - 1) / c)) <= kSms)
-            hi = c;
-        else
-            lo = c + 1;
-    }
-    const int pieces = max(1, (keys + lo - 1) / lo);
-    // blocks (or pieces) up to and with this lane's sequence, and pieces alone
-    int sum = by_piece ? blocks * pieces : blocks, sum_p = blocks * pieces;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(all, sum, o), w = __shfl_up_sync(all, sum_p, o);
-        if (lane >= o) sum += u, sum_p += w;
-    }
-    const unsigned hit = __ballot_sync(all, sum > id);
-    if (!hit) return false;
-    const int l = __ffs(hit) - 1;
-    int within = id - (sum - (by_piece ? blocks * pieces : blocks));
-    const int piece = by_piece ? within % pieces : 0;
-    if (by_piece) within /= pieces;
-    const int first = sum_p - blocks * pieces + within * pieces;
-    at->b = l;
-    at->sq = from_lane(s, l);
-    at->head = __shfl_sync(all, within % heads, l);
-    at->tile = __shfl_sync(all, within / heads, l);
-    sp->chunk = lo;
-    sp->pieces = __shfl_sync(all, pieces, l);
-    sp->piece = __shfl_sync(all, piece, l);
-    sp->first = __shfl_sync(all, first, l);
-    return sp->first + sp->pieces <= kSms;  // always, unless offsets overlap
-}
-
-
-template <int DP, bool kWindow>
+template <int DP>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     attention_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
                          const __grid_constant__ CUtensorMap map_k,
@@ -242,29 +115,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             w.khead = at.head / p.group;
             w.key0 = piece * chunk * kTileRows;
             w.part = part;
-            if constexpr (kWindow) {
-                const FwdWalk f = walk_of_block(p.window, w.sq, w.row0);
-                int end[2] = {f.end[0], f.end[1]};
-                w.walk = f.walk;
-                w.step0 = 0;
-                w.skip = f.skip;
-                if (part >= 0) {
-                    w.step0 = piece * chunk;
-                    end[0] = min(max(end[0] - w.step0, 0), chunk);
-                    end[1] = min(max(end[1] - w.step0, 0), chunk);
-                    w.skip -= f.skip >= 0 ? w.step0 : 0;
-                }
-                if (w.skip >= end[1]) w.skip = -1;
-                w.skip = max(w.skip, -1);
-                w.end1 = end[1];
-                w.tiles[0] = end[0];
-                w.tiles[1] = end[1] - (w.skip >= 0 ? 1 : 0);
-            } else {
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    w.tiles[t] = walked(w.sq, w.row0, t, p.batch.causal);
-                    if (part >= 0) w.tiles[t] = min(max(w.tiles[t] - piece * chunk, 0), chunk);
-                }
+            for (int t = 0; t < 2; ++t) {
+                w.tiles[t] = walked(w.sq, w.row0, t, p.batch.causal);
+                if (part >= 0) w.tiles[t] = min(max(w.tiles[t] - piece * chunk, 0), chunk);
             }
             if (piece > 0 && w.tiles[0] + w.tiles[1] == 0) ok = false;  // no keys left for it
             work = w;
@@ -308,10 +162,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
     if (warp == kSoftmaxWarps + 1) {
         // ---- the producer: Q, then K and V tiles in turn ----
-        const int tiles[2] = {work.tiles[0], work.tiles[1]};
-        const int most = max(tiles[0], kWindow ? work.end1 : tiles[1]);
-        const int64_t k0 = work.sq.k0 + (kWindow ? 0 : work.key0);
-        const int left = work.sq.m - (kWindow ? 0 : work.key0), khead = work.khead;
+        const int tiles[2] = {work.tiles[0], work.tiles[1]}, most = max(tiles[0], tiles[1]);
+        const int64_t k0 = work.sq.k0 + work.key0;
+        const int left = work.sq.m - work.key0, khead = work.khead;
         const bool tail = work.sq.k0 + work.sq.m < p.batch.tk;
         if (most > 0) {
             if (elect_one()) {
@@ -327,8 +180,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             __syncwarp();
             int i = 0;  // items issued
             for (; i < 2 * most; ++i) {
-                const int slot = i % Sh::kSlots, use = i / Sh::kSlots;
-                const int j = kWindow ? work.walk.tile(work.step0 + (i >> 1)) : i >> 1;
+                const int slot = i % Sh::kSlots, use = i / Sh::kSlots, j = i >> 1;
                 if (use > 0 && !mbar_wait(smem_u32(&bar_empty[slot]), (use - 1) & 1, &dead)) break;
                 const uint32_t dst = smem_kv + slot * Sh::kTileBytes;
                 const uint32_t full = smem_u32(&bar_full[slot]);
@@ -366,9 +218,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // us instead of 1,283 on 16,320 tokens x 16 heads x 128).  A step is a key tile and a
         // query tile; scores run kScores steps ahead of the outputs, so that a query tile's
         // softmax finds its next scores ready.
-        const int tiles[2] = {work.tiles[0], work.tiles[1]};
-        const int end1 = kWindow ? work.end1 : tiles[1], skip = kWindow ? work.skip : -1;
-        const int most = max(tiles[0], end1);
+        const int tiles[2] = {work.tiles[0], work.tiles[1]}, most = max(tiles[0], tiles[1]);
         if (most > 0 && elect_one()) {
             constexpr uint32_t word_o = mma_word(128, DP, false, true);
             const uint32_t word_s = mma_word(128, 128, false, false) | (p.negative ? kNegateA : 0u);
@@ -381,16 +231,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 int slot, phase;   // of K in the ring, V behind it
                 int bar, turn;     // j % kScores and the barrier's phase
                 int score;         // score tile
-                // with a window, the same of the second query tile's own count of key tiles
-                int bar1, turn1, j1;
             };
             const auto advance = [&](Step& s) {
                 s.score = s.score + 1 == Sh::kScores ? 0 : s.score + 1;
-                if (kWindow && s.t == 1) {
-                    ++s.j1;
-                    if (++s.bar1 == Sh::kScores) s.bar1 = 0, s.turn1 ^= 1;
-                }
-                if (s.t == 0 && (kWindow ? s.j < end1 && s.j != skip : tiles[1] > 0)) {
+                if (s.t == 0 && tiles[1] > 0) {
                     s.t = 1;
                     return false;
                 }
@@ -401,39 +245,29 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 if (++s.bar == Sh::kScores) s.bar = 0, s.turn ^= 1;
                 return true;  // on to another key tile
             };
-            const auto bar_of = [&](const Step& s) {
-                return s.t * Sh::kScores + (kWindow && s.t == 1 ? s.bar1 : s.bar);
-            };
-            const auto turn_of = [&](const Step& s) {
-                return kWindow && s.t == 1 ? s.turn1 : s.turn;
-            };
-            // whether it is the query tile's first key tile
-            const auto begins = [&](const Step& s) {
-                return (kWindow && s.t == 1 ? s.j1 : s.j) == 0;
-            };
-            Step ahead{0, tiles[0] > 0 ? 0 : 1, 0, 0, 0, 0, 0, 0, 0, 0}, at = ahead;
+            Step ahead{0, tiles[0] > 0 ? 0 : 1, 0, 0, 0, 0, 0}, at = ahead;
             const auto scores = [&]() {
                 ok = ok && mbar_wait_one(smem_u32(&bar_full[ahead.slot]), ahead.phase, &dead);
-                if (begins(ahead)) ok = ok && mbar_wait_one(smem_u32(&bar_q[ahead.t]), 0, &dead);
+                if (ahead.j == 0) ok = ok && mbar_wait_one(smem_u32(&bar_q[ahead.t]), 0, &dead);
                 if (!ok) return;
                 tmem_fence_after();
                 const Step s = ahead;
                 // over a tile of P: products are carried out in the order of their issue
                 product_columns<DP>(tmem_s(s.score), op_q + s.t * kTileStep,
                                     op_k + s.slot * kTileStep, word_s, false);
-                mma_commit(smem_u32(&bar_s[bar_of(s)]));
+                mma_commit(smem_u32(&bar_s[s.t * Sh::kScores + s.bar]));
                 if (advance(ahead)) mma_commit(smem_u32(&bar_empty[s.slot]));
             };
             for (int k = 0; k < Sh::kScores && ahead.j < most; ++k) scores();
             while (at.j < most && ok) {
                 ok = mbar_wait_one(smem_u32(&bar_full[at.slot + 1]), at.phase, &dead) &&
-                     mbar_wait_one(smem_u32(&bar_p[bar_of(at)]), turn_of(at), &dead);
+                     mbar_wait_one(smem_u32(&bar_p[at.t * Sh::kScores + at.bar]), at.turn, &dead);
                 if (!ok) break;
                 tmem_fence_after();
                 const Step s = at;
                 product_rows(tmem_o(s.t), tmem_s(s.score), 32, op_v + s.slot * kTileStep, word_o,
-                             !begins(s));
-                mma_commit(smem_u32(&bar_o[bar_of(s)]));
+                             s.j > 0);
+                mma_commit(smem_u32(&bar_o[s.t * Sh::kScores + s.bar]));
                 if (ahead.j < most) scores();
                 if (advance(at)) mma_commit(smem_u32(&bar_empty[s.slot + 1]));
             }
@@ -450,19 +284,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             return seen_keys(work.row0 + t * kTileRows + row, work.sq.n, work.sq.m,
                              p.batch.causal) - work.key0;
         };
-        const int limit = kWindow ? 0 : keys_of(r);
-        const int first_limit = kWindow ? 0 : keys_of((warp & 3) * 32);
-        // with a window: what the row sees, the end of the warp's first row's keys and the start of
-        // its last one's
-        Seen see{};
-        int first_hi = 0, last_lo = 0;
-        if constexpr (kWindow) {
-            const int row = work.row0 + t * kTileRows + (warp & 3) * 32;
-            see = seen_by(p.window, row + lane, work.sq.n, work.sq.m);
-            first_hi = seen_by(p.window, row, work.sq.n, work.sq.m).hi;
-            last_lo = seen_by(p.window, row + 31, work.sq.n, work.sq.m).lo;
-        }
-        const int skip = kWindow ? work.skip : -1;
+        const int limit = keys_of(r), first_limit = keys_of((warp & 3) * 32);
         const int tiles_t = work.tiles[t];
         // the score tiles go by order(j, t) = steps before (j, t)
         const int tiles_0 = work.tiles[0], tiles_1 = work.tiles[1];
@@ -478,13 +300,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         float top = -INFINITY;
         float2 sum = make_float2(0.f, 0.f);
         for (int j = 0; j < tiles_t; ++j) {
-            // key tile of the block's order, and the score tiles before this one
-            const int v = kWindow && t == 1 && skip >= 0 && j >= skip ? j + 1 : j;
-            const int before =
-                kWindow ? (t == 1 ? min(v + 1, tiles_0) + j
-                                  : j + min(j - (skip >= 0 && j > skip ? 1 : 0), tiles_1))
-                        : min(j + t, tiles_0) + min(j, tiles_1);
-            const uint32_t s_at = tmem_s(before) + lanes;
+            const uint32_t s_at = tmem_s(min(j + t, tiles_0) + min(j, tiles_1)) + lanes;
             // kScores barriers a query tile: the one of j is used again after P(j) is taken
             mbar_pass(smem_u32(&bar_s[t * Sh::kScores + j % Sh::kScores]), (j / Sh::kScores) & 1,
                       &dead);
@@ -493,16 +309,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
             for (int c = 0; c < 128; c += 32) tmem_ld32(s + c, s_at + c);
             tmem_wait_ld();
-            if constexpr (kWindow) {
-                const int key = work.walk.tile(work.step0 + v) * kTileRows;
-                if (key + kTileRows > first_hi || key < last_lo) {
-                    const int lo = see.lo - key, hi = see.hi - key, sinks = see.sinks - key;
-#pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c >= hi || c < lo)
-                            if (c >= sinks) s[c] = 0xff800000u;  // -infinity
-                }
-            } else if ((j + 1) * kTileRows > first_limit) {  // some row of the warp ends in this tile
+            if ((j + 1) * kTileRows > first_limit) {  // some row of the warp ends in this tile
                 const int left = limit - j * kTileRows;
 #pragma unroll
                 for (int c = 0; c < 128; ++c)
@@ -567,7 +374,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const int slot_row = t * kTileRows + r, i = work.row0 + slot_row;
             const bool valid = i < work.sq.n, split = work.part >= 0;
             // a row that sees no key (of this piece): zeros
-            const bool some = (kWindow ? l != 0.f : limit > 0) && tiles_t > 0;
+            const bool some = limit > 0 && tiles_t > 0;
             const float f = some ? 1.f / l : 0.f;
             __nv_bfloat16* out = valid && !split ? p.o.row(work.sq.q0 + i, work.head) : nullptr;
             float* out32 = valid && split ? p.part_o + (work.part + slot_row) * DP : nullptr;
@@ -619,73 +426,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
 }
 
-// A split block's rows from its pieces, in the order of the pieces.  DP / 4 lanes a row.
-constexpr int kJoinThreads = 256;
-
-template <int DP, bool kWindow>
-__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const FwdParams p) {
-    __shared__ Place place;
-    __shared__ Spread spread;
-    __shared__ int found;
-    grid_dep_sync();
-    if (threadIdx.x < 32) {
-        Place at{};
-        Spread sp{p.plan.chunk, p.plan.pieces, 0, (int)blockIdx.x};
-        const bool ok = p.plan.spread
-                            ? find_spread(p.batch, p.heads, blockIdx.x, false, p.plan.most_keys, &at,
-                                          &sp)
-                            : find_place<false>(p.batch, 2 * kTileRows, p.heads,
-                                                (int)(p.plan.whole + blockIdx.x), &at);
-        if (threadIdx.x == 0) place = at, spread = sp, found = ok && sp.pieces > 1;
-    }
-    __syncthreads();
-    if (!found) return;
-    const Sequence sq = place.sq;
-    const int row0 = place.tile * 2 * kTileRows;
-    constexpr int kLanes = DP / 4;
-    const int lane = threadIdx.x % kLanes;
-    const int rows = min(2 * kTileRows, sq.n - row0);
-    // rows from a piece to the next
-    const int64_t step = (p.plan.spread ? 1 : p.plan.rest) * p.plan.slot_rows;
-    for (int r = blockIdx.y * (kJoinThreads / kLanes) + threadIdx.x / kLanes; r < rows;
-         r += gridDim.y * (kJoinThreads / kLanes)) {
-        // a piece without keys for the row's tile was not walked
-        const int walks = kWindow ? walk_of_block(p.window, sq, row0).end[r / kTileRows]
-                                  : walked(sq, row0, r / kTileRows, p.batch.causal);
-        const int pieces = max(1, (walks + spread.chunk - 1) / spread.chunk);
-        const int64_t at = (int64_t)spread.first * p.plan.slot_rows + r;
-        float top = -INFINITY;
-        bool nan = false;
-        for (int z = 0; z < pieces; ++z) {
-            const float v = p.part_lse[z * step + at];
-            nan |= v != v;
-            top = fmaxf(top, v);
-        }
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-        if (top != -INFINITY) {
-#pragma unroll 4
-            for (int z = 0; z < pieces; ++z) {
-                const float w = ex2_approx(p.part_lse[z * step + at] - top);
-                const float4 v = reinterpret_cast<const float4*>(p.part_o)[(z * step + at) * kLanes + lane];
-                sum += w;
-                o.x = fmaf(w, v.x, o.x);
-                o.y = fmaf(w, v.y, o.y);
-                o.z = fmaf(w, v.z, o.z);
-                o.w = fmaf(w, v.w, o.w);
-            }
-        }
-        const float f = nan ? NAN : (sum > 0.f ? 1.f / sum : 0.f);
-        const int64_t token = sq.q0 + row0 + r;
-        if (lane * 4 < p.dim)
-            *reinterpret_cast<uint2*>(p.o.row(token, place.head) + lane * 4) =
-                make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
-        if (lane == 0)
-            p.lse[(int64_t)place.head * p.batch.tq + token] =
-                nan ? NAN : (sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY);
-    }
-}
-
 // The last wave is cut where a model of the waves says that it pays, in units of one key
 // tile's time: a block costs its tiles and kStart for its start and end, the join kJoin, and
 // less than kGain of the whole is not worth it (at 8,160 tokens x 16 heads x 128 cutting
@@ -693,12 +433,10 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const FwdP
 constexpr int kStart = 3, kJoin = 4, kMaxPieces = 16;
 constexpr double kGain = 0.05;
 
-// `window`: the window's and the queries' width, the sinks' tile included (0: no window).
-FwdPlan plan_fwd(int64_t tq, int64_t tk, int batch, int heads, bool causal, int64_t window) {
+FwdPlan plan_fwd(int64_t tq, int64_t tk, int batch, int heads, bool causal) {
     const int rows = 2 * kTileRows;
     const int64_t blocks = tiles_at_most(tq, rows, batch) * heads;
-    int64_t keys = (tk + kTileRows - 1) / kTileRows;
-    if (window > 0) keys = std::min(keys, (window + kTileRows - 1) / kTileRows);
+    const int64_t keys = (tk + kTileRows - 1) / kTileRows;
     FwdPlan plan{};
     plan.most_keys = (int)keys;
     plan.whole = blocks;
@@ -709,7 +447,7 @@ FwdPlan plan_fwd(int64_t tq, int64_t tk, int batch, int heads, bool causal, int6
         return plan;
     }
     // under the mask, or with sequences of several lengths, the short blocks come last
-    if (causal || batch > 1 || window > 0) return plan;
+    if (causal || batch > 1) return plan;
     const auto waves = [](int64_t n) { return (n + kSms - 1) / kSms; };
     const int64_t whole = blocks / kSms * kSms, rest = blocks - whole;
     if (rest == 0) return plan;
@@ -731,29 +469,22 @@ FwdPlan plan_fwd(int64_t tq, int64_t tk, int batch, int heads, bool causal, int6
     return plan;
 }
 
-template <int DP, bool kWindow>
+template <int DP>
 cudaError_t launch_dim(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                        const FwdParams& p, cudaStream_t st) {
     cudaError_t e =
-        cudaFuncSetAttribute(attention_fwd_kernel<DP, kWindow>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FwdShape<DP>::kSmem);
+        cudaFuncSetAttribute(attention_fwd_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)FwdShape<DP>::kSmem);
     if (e != cudaSuccess) return e;
     const int64_t blocks = p.plan.spread ? kSms : p.plan.whole + p.plan.rest * p.plan.pieces;
-    e = launch(attention_fwd_kernel<DP, kWindow>, dim3((unsigned)blocks), dim3(kFwdThreads),
+    e = launch(attention_fwd_kernel<DP>, dim3((unsigned)blocks), dim3(kFwdThreads),
                FwdShape<DP>::kSmem, st, mq, mk, mv, p);
     if (e != cudaSuccess || (!p.plan.spread && p.plan.pieces == 1)) return e;
     const int rows = kJoinThreads / (DP / 4);
     const unsigned y = (unsigned)((p.plan.slot_rows + 4 * rows - 1) / (4 * rows));
     const int64_t joined = p.plan.spread ? p.plan.whole : p.plan.rest;
-    return launch(attention_join_kernel<DP, kWindow>, dim3((unsigned)joined, y), dim3(kJoinThreads),
-                  0, st, p);
-}
-
-// Key tiles' worth of keys that a block may walk: its rows' windows, a tile's part at either end,
-// and the sinks' tile.
-int64_t walk_width(const gs_window& w) {
-    return (int64_t)w.left + w.right + 1 + 2 * kTileRows + 2 * kTileRows +
-           (w.sinks > 0 ? kTileRows : 0);
+    return launch(attention_join_kernel<DP, false>, dim3((unsigned)joined, y), dim3(kJoinThreads), 0, st,
+                  p);
 }
 
 }  // namespace
@@ -761,26 +492,18 @@ int64_t walk_width(const gs_window& w) {
 size_t attention_fwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads,
                                      int head_dim) {
     // whatever the mask
-    const int64_t a = plan_fwd(tokens_q, tokens_k, batch, heads, false, 0).part_rows();
-    const int64_t b = plan_fwd(tokens_q, tokens_k, batch, heads, true, 0).part_rows();
+    const int64_t a = plan_fwd(tokens_q, tokens_k, batch, heads, false).part_rows();
+    const int64_t b = plan_fwd(tokens_q, tokens_k, batch, heads, true).part_rows();
     const int64_t rows = a > b ? a : b;
-    return (size_t)rows * ((head_dim <= 64 ? 64 : 128) + 1) * sizeof(float);
-}
-
-size_t attention_fwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads,
-                                     int head_dim, const gs_window& window) {
-    const int64_t rows =
-        plan_fwd(tokens_q, tokens_k, batch, heads, false, walk_width(window)).part_rows();
     return (size_t)rows * ((head_dim <= 64 ? 64 : 128) + 1) * sizeof(float);
 }
 
 cudaError_t launch_attention_fwd(const gs_attention_shape& s, const gs_heads& q, const gs_heads& k,
                                  const gs_heads& v, const gs_heads& out, float* lse,
-                                 const int32_t* cu_q, const int32_t* cu_k, const gs_window* window,
-                                 void* ws, cudaStream_t st) {
+                                 const int32_t* cu_q, const int32_t* cu_k, void* ws,
+                                 cudaStream_t st) {
     FwdParams p{};
-    p.batch = {cu_q, cu_k, s.tokens_q, s.tokens_k, s.batch, s.causal != 0 && !window};
-    if (window) p.window = window_of(*window, s.causal != 0);
+    p.batch = {cu_q, cu_k, s.tokens_q, s.tokens_k, s.batch, s.causal != 0};
     p.heads = s.heads_q;
     p.group = s.heads_q / s.heads_k;
     p.dim = s.head_dim;
@@ -789,8 +512,7 @@ cudaError_t launch_attention_fwd(const gs_attention_shape& s, const gs_heads& q,
     p.log2_scale = fmaxf(fabsf(s.scale) * 1.4426950408889634f, 1e-30f);
     p.o = {static_cast<__nv_bfloat16*>(out.data), out.token_stride, out.head_stride};
     p.lse = lse;
-    p.plan = plan_fwd(s.tokens_q, s.tokens_k, s.batch, s.heads_q, s.causal != 0,
-                      window ? walk_width(*window) : 0);
+    p.plan = plan_fwd(s.tokens_q, s.tokens_k, s.batch, s.heads_q, s.causal != 0);
     p.part_o = static_cast<float*>(ws);
     p.part_lse = p.part_o + p.plan.part_rows() * (s.head_dim <= 64 ? 64 : 128);
     CUtensorMap mq, mk, mv;
@@ -807,11 +529,7 @@ cudaError_t launch_attention_fwd(const gs_attention_shape& s, const gs_heads& q,
                          s.head_dim, &p.swap_v);
     }
     if (e != cudaSuccess) return e;
-    if (window)
-        return s.head_dim <= 64 ? launch_dim<64, true>(mq, mk, mv, p, st)
-                                : launch_dim<128, true>(mq, mk, mv, p, st);
-    return s.head_dim <= 64 ? launch_dim<64, false>(mq, mk, mv, p, st)
-                            : launch_dim<128, false>(mq, mk, mv, p, st);
+    return s.head_dim <= 64 ? launch_dim<64>(mq, mk, mv, p, st) : launch_dim<128>(mq, mk, mv, p, st);
 }
 
 }  // namespace gs

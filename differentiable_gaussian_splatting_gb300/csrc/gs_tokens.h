@@ -41,8 +41,8 @@ size_t attention_fwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int bat
                                      int head_dim);
 cudaError_t launch_attention_fwd(const gs_attention_shape& s, const gs_heads& q, const gs_heads& k,
                                  const gs_heads& v, const gs_heads& out, float* lse,
-                                 const int32_t* cu_q, const int32_t* cu_k, const gs_window* window,
-                                 void* ws, cudaStream_t st);
+                                 const int32_t* cu_q, const int32_t* cu_k, void* ws,
+                                 cudaStream_t st);
 size_t attention_bwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads_q,
                                      int heads_k, int head_dim);
 cudaError_t launch_attention_bwd(const gs_attention_shape& s, const gs_heads& q, const gs_heads& k,
@@ -50,13 +50,18 @@ cudaError_t launch_attention_bwd(const gs_attention_shape& s, const gs_heads& q,
                                  const gs_heads& dout, const gs_heads& dq, const gs_heads& dk,
                                  const gs_heads& dv, const int32_t* cu_q, const int32_t* cu_k,
                                  const gs_window* window, void* ws, cudaStream_t st);
-// the same with a window (window null above: none)
-size_t attention_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads_q,
-                                 int heads_k, int head_dim, const gs_window& window);
-size_t attention_fwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads,
-                                     int head_dim, const gs_window& window);
-size_t attention_bwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads_q,
-                                     int heads_k, int head_dim, const gs_window& window);
+// the same over a window (window null in the gradient above: none)
+size_t attention_window_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads_q,
+                                        int heads_k, int head_dim, const gs_window& window);
+size_t attention_window_fwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads,
+                                            int head_dim, const gs_window& window);
+size_t attention_window_bwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch,
+                                            int heads_q, int heads_k, int head_dim,
+                                            const gs_window& window);
+cudaError_t launch_attention_window_fwd(const gs_attention_shape& s, const gs_window& window,
+                                        const gs_heads& q, const gs_heads& k, const gs_heads& v,
+                                        const gs_heads& out, float* lse, const int32_t* cu_q,
+                                        const int32_t* cu_k, void* ws, cudaStream_t st);
 
 // ---- norms around a block with its gate and residual (gs_residual_norm.cu) ----------
 struct ResidualNormArgs {
