@@ -173,19 +173,48 @@ __global__ void __launch_bounds__(kClipThreads, 6)
     if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
-// One value times the factor.  A factor below fp32's normal range has lost bits: fp64 then.
-struct Factor {
-    float f;
-    double d;
-    bool tiny;
-    __device__ __forceinline__ float of(float v) const {
-        return tiny ? (float)((double)v * d) : v * f;
-    }
-};
+// A value times the factor.  A factor below fp32's normal range has lost bits: fp64 then (kTiny; not
+// chosen value by value, which would cost the fp64 units' time always).
+template <bool kTiny>
+__device__ __forceinline__ float scaled(float v, double d) {
+    return kTiny ? (float)((double)v * d) : v * (float)d;
+}
 
 __device__ __forceinline__ uint32_t pair_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <bool kTiny>
+__device__ __forceinline__ void scale_chunk(const Chunk& c, double d) {
+    const bool whole = c.elements * (c.bf16 ? 2 : 4) == kChunkBytes && words16(c.in) && words16(c.out);
+    if (whole) {
+        const uint4* in = reinterpret_cast<const uint4*>(c.in) + threadIdx.x;
+        uint4* out = reinterpret_cast<uint4*>(c.out) + threadIdx.x;
+        uint4 w[kVecs];
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k)
+            w[k] = d != 0.0 ? __ldcs(in + k * kClipThreads) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+            uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                u[e] = c.bf16 ? pair_bf16(scaled<kTiny>(lo16(u[e]), d), scaled<kTiny>(hi16(u[e]), d))
+                              : __float_as_uint(scaled<kTiny>(__uint_as_float(u[e]), d));
+            __stcs(out + k * kClipThreads, make_uint4(u[0], u[1], u[2], u[3]));
+        }
+        return;
+    }
+    for (int e = threadIdx.x; e < c.elements; e += kClipThreads) {
+        if (c.bf16) {
+            const float v = d != 0.0 ? lo16(reinterpret_cast<const uint16_t*>(c.in)[e]) : 0.f;
+            reinterpret_cast<__nv_bfloat16*>(c.out)[e] = __float2bfloat16_rn(scaled<kTiny>(v, d));
+        } else {
+            const float v = d != 0.0 ? reinterpret_cast<const float*>(c.in)[e] : 0.f;
+            reinterpret_cast<float*>(c.out)[e] = scaled<kTiny>(v, d);
+        }
+    }
 }
 
 // A table without arrays gives the norm alone.
@@ -198,47 +227,22 @@ __global__ void __launch_bounds__(kClipThreads, 6)
     double sum = 0.0;
     for (int i = threadIdx.x; i < parts; i += kClipThreads) sum += __ldg(part + i);
     sum = block_sum(sum);
-    if (threadIdx.x == 0) total = sum;
+    if (threadIdx.x == 0) {
+        const double norm = sqrt(sum);
+        if (norm_out && blockIdx.x == 0) *norm_out = (float)norm;
+        // 0 where the norm is not finite: nothing is read then
+        total = !(norm < INFINITY) ? 0.0 : norm > max_norm ? max_norm / norm : 1.0;
+    }
     __syncthreads();
-    const double norm = sqrt(total);
-    if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
-    const bool finite = norm < INFINITY;
-    const double d = !finite ? 0.0 : norm > max_norm ? max_norm / norm : 1.0;
-    const Factor f{(float)d, d, d < 0x1p-126};
+    const double d = total;
     const int chunks = t.chunk0[t.count];
     for (int i = blockIdx.x; i < chunks; i += gridDim.x) {
         const Chunk c = chunk_of(t, chunks - 1 - i);
         if (c.in == c.out && d == 1.0) continue;
-        const bool whole = c.elements * (c.bf16 ? 2 : 4) == kChunkBytes && words16(c.in) &&
-                           words16(c.out);
-        if (whole) {
-            uint4 w[kVecs];
-#pragma unroll
-            for (int k = 0; k < kVecs; ++k)
-                w[k] = finite ? __ldcs(reinterpret_cast<const uint4*>(c.in) + k * kClipThreads +
-                                       threadIdx.x)
-                              : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int k = 0; k < kVecs; ++k) {
-                uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    u[e] = c.bf16 ? pair_bf16(f.of(lo16(u[e])), f.of(hi16(u[e])))
-                                  : __float_as_uint(f.of(__uint_as_float(u[e])));
-                __stcs(reinterpret_cast<uint4*>(c.out) + k * kClipThreads + threadIdx.x,
-                       make_uint4(u[0], u[1], u[2], u[3]));
-            }
-            continue;
-        }
-        for (int e = threadIdx.x; e < c.elements; e += kClipThreads) {
-            if (c.bf16) {
-                const float v = finite ? lo16(reinterpret_cast<const uint16_t*>(c.in)[e]) : 0.f;
-                reinterpret_cast<__nv_bfloat16*>(c.out)[e] = __float2bfloat16_rn(f.of(v));
-            } else {
-                const float v = finite ? reinterpret_cast<const float*>(c.in)[e] : 0.f;
-                reinterpret_cast<float*>(c.out)[e] = f.of(v);
-            }
-        }
+        if (d == 0.0 || d >= 0x1p-126)
+            scale_chunk<false>(c, d);
+        else
+            scale_chunk<true>(c, d);
     }
 }
 
