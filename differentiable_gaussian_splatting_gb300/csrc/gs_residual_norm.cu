@@ -41,7 +41,7 @@ constexpr int kSms = 152;
 constexpr int kPer = 8;             // values a thread
 constexpr int kMostThreads = 1024;  // width <= 8,192
 constexpr int kFwdWarps = 32, kBwdWarps = 16;  // resident on an SM
-constexpr int kSumThreads = 256;
+constexpr int kMostGates = 256;     // sequences at once when the gates' gradients are added up
 
 struct NormRows {
     char* p;
@@ -63,6 +63,30 @@ struct RnParams {
     float *part, *part_gate;
 };
 
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
+// A thread's values of a row, in pairs (two operations an instruction).
+constexpr int kPairs = kPer / 2;
+struct Values {
+    float2 v[kPairs];
+};
+
+__device__ __forceinline__ float dot(const Values& a, const Values& b) {
+    float2 s = mul(a.v[0], b.v[0]);
+#pragma unroll
+    for (int k = 1; k < kPairs; ++k) s = fma2(a.v[k], b.v[k], s);
+    return s.x + s.y;
+}
+__device__ __forceinline__ float total(const Values& a) {
+    float2 s = a.v[0];
+#pragma unroll
+    for (int k = 1; k < kPairs; ++k) s = add(s, a.v[k]);
+    return s.x + s.y;
+}
+
 // A thread's eight columns: neighbours, or (odd widths and strides) every blockDim-th.
 template <bool kVec>
 struct Columns {
@@ -72,10 +96,13 @@ struct Columns {
         step = kVec ? 1 : (int)blockDim.x;
         n = first >= width ? 0 : kVec ? kPer : min(kPer, (width - 1 - first) / step + 1);
     }
-    __device__ __forceinline__ void weights(float (&v)[kPer], const float* w, float other) const {
+    // values of fp32 from w, `other` where there are none
+    __device__ __forceinline__ Values weights(const float* w, float other) const {
+        Values r;
+        float* v = &r.v[0].x;
 #pragma unroll
         for (int k = 0; k < kPer; ++k) v[k] = other;
-        if (!w || n == 0) return;
+        if (!w || n == 0) return r;
         if (kVec) {
             const float4 a = __ldg(reinterpret_cast<const float4*>(w + first));
             const float4 b = __ldg(reinterpret_cast<const float4*>(w + first) + 1);
@@ -86,9 +113,11 @@ struct Columns {
             for (int k = 0; k < kPer; ++k)
                 if (k < n) v[k] = __ldg(w + first + k * step);
         }
+        return r;
     }
-    __device__ __forceinline__ void store(float* w, const float (&v)[kPer]) const {
+    __device__ __forceinline__ void store(float* w, const Values& r) const {
         if (n == 0) return;
+        const float* v = &r.v[0].x;
         if (kVec) {
             reinterpret_cast<float4*>(w + first)[0] = make_float4(v[0], v[1], v[2], v[3]);
             reinterpret_cast<float4*>(w + first)[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -98,6 +127,14 @@ struct Columns {
                 if (k < n) w[first + k * step] = v[k];
         }
     }
+    // zero where there is no column
+    __device__ __forceinline__ void trim(Values& r) const {
+        if (kVec ? n > 0 : n == kPer) return;
+        float* v = &r.v[0].x;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+            if (k >= n) v[k] = 0.f;
+    }
 };
 
 // A thread's values of a row as they lie in memory, zeros where there is none.
@@ -106,8 +143,9 @@ struct RawRow;
 
 template <bool kVec>
 struct RawRow<float, kVec> {
-    float v[kPer];
+    Values r;
     __device__ __forceinline__ void load(const char* row, const Columns<kVec>& c) {
+        float* v = &r.v[0].x;
 #pragma unroll
         for (int k = 0; k < kPer; ++k) v[k] = 0.f;
         if (!row || c.n == 0) return;
@@ -123,22 +161,18 @@ struct RawRow<float, kVec> {
                 if (k < c.n) v[k] = p[k * c.step];
         }
     }
-    __device__ __forceinline__ void get(float (&f)[kPer]) const {
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) f[k] = v[k];
-    }
-    __device__ static __forceinline__ void store(char* row, const float (&f)[kPer],
-                                                 const Columns<kVec>& c) {
+    __device__ __forceinline__ Values get() const { return r; }
+    __device__ static __forceinline__ void store(char* row, const Values& f, const Columns<kVec>& c) {
         c.store(reinterpret_cast<float*>(row), f);
     }
 };
 
 template <bool kVec>
 struct RawRow<__nv_bfloat16, kVec> {
-    uint32_t w[kPer / 2];
+    uint32_t w[kPairs];
     __device__ __forceinline__ void load(const char* row, const Columns<kVec>& c) {
 #pragma unroll
-        for (int k = 0; k < kPer / 2; ++k) w[k] = 0;
+        for (int k = 0; k < kPairs; ++k) w[k] = 0;
         if (!row || c.n == 0) return;
         const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + c.first;
         if (kVec) {
@@ -150,92 +184,84 @@ struct RawRow<__nv_bfloat16, kVec> {
                 if (k < c.n) w[k / 2] |= (uint32_t)p[k * c.step] << (16 * (k & 1));
         }
     }
-    __device__ __forceinline__ void get(float (&f)[kPer]) const {
+    __device__ __forceinline__ Values get() const {
+        Values r;
 #pragma unroll
-        for (int k = 0; k < kPer / 2; ++k) {
-            f[2 * k] = __uint_as_float(w[k] << 16);
-            f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-        }
+        for (int k = 0; k < kPairs; ++k)
+            r.v[k] = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+        return r;
     }
-    __device__ static __forceinline__ void store(char* row, const float (&f)[kPer],
-                                                 const Columns<kVec>& c) {
+    __device__ static __forceinline__ void store(char* row, const Values& f, const Columns<kVec>& c) {
         if (c.n == 0) return;
         __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(row) + c.first;
         if (kVec) {
-            __nv_bfloat162 h[4];
+            __nv_bfloat162 h[kPairs];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) h[k] = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+            for (int k = 0; k < kPairs; ++k) h[k] = __floats2bfloat162_rn(f.v[k].x, f.v[k].y);
             *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
         } else {
+            const float* v = &f.v[0].x;
 #pragma unroll
             for (int k = 0; k < kPer; ++k)
-                if (k < c.n) p[k * c.step] = __float2bfloat16_rn(f[k]);
+                if (k < c.n) p[k * c.step] = __float2bfloat16_rn(v[k]);
         }
     }
 };
 
-// Sums over the row: lanes, then the row's warps in order.  Two buffers in turn, so that one
-// barrier a sum is enough: who writes a buffer again has passed the barrier behind which all had
-// read it.
-constexpr int kMostSums = 3;
+// Means over the row: across lanes, then over the row's warps in order.  Two buffers in turn, so that
+// one barrier is enough: who writes a buffer again has passed the barrier behind which all had read
+// it.
 struct RowSum {
-    float (*buffer)[kMostSums][kMostThreads / 32];
+    float4 (*buffer)[kMostThreads / 32];
     int turn, warps;
     float inv_width;
 
-    template <int kN>
-    __device__ __forceinline__ void mean(float (&v)[kN]) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-            for (int k = 0; k < kN; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-        if (warps > 1) {
-            float(*to)[kMostThreads / 32] = buffer[turn];
-            turn ^= 1;
-            if ((threadIdx.x & 31) == 0)
-#pragma unroll
-                for (int k = 0; k < kN; ++k) to[k][threadIdx.x >> 5] = v[k];
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < kN; ++k) v[k] = to[k][0];
-            for (int w = 1; w < warps; ++w)
-#pragma unroll
-                for (int k = 0; k < kN; ++k) v[k] += to[k][w];
+    __device__ __forceinline__ float4 over_warps(bool writes, float v, int at) {
+        float4* to = buffer[turn];
+        turn ^= 1;
+        if (writes) (&to[threadIdx.x >> 5].x)[at] = v;
+        __syncthreads();
+        float4 s = to[0];
+        for (int w = 1; w < warps; ++w) {
+            const float4 o = to[w];
+            s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
         }
+        return s;
+    }
+    __device__ __forceinline__ float mean(float v) {
 #pragma unroll
-        for (int k = 0; k < kN; ++k) v[k] *= inv_width;
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (warps > 1) v = over_warps((threadIdx.x & 31) == 0, v, 0).x;
+        return v * inv_width;
+    }
+    // Of four values: the halves of the warp take two of them each, their halves one: six steps
+    // across lanes instead of twenty.
+    __device__ __forceinline__ float4 mean(float a, float b, float c, float d) {
+        const unsigned all = 0xffffffffu;
+        const int lane = threadIdx.x & 31;
+        const bool upper = lane & 16, odd = lane & 8;
+        const float p = (upper ? c : a) + __shfl_xor_sync(all, upper ? a : c, 16);
+        const float q = (upper ? d : b) + __shfl_xor_sync(all, upper ? b : d, 16);
+        float v = (odd ? q : p) + __shfl_xor_sync(all, odd ? p : q, 8);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(all, v, o);
+        float4 s;
+        if (warps > 1)
+            s = over_warps((lane & 7) == 0, v, lane >> 3);
+        else
+            s = make_float4(__shfl_sync(all, v, 0), __shfl_sync(all, v, 8), __shfl_sync(all, v, 16),
+                            __shfl_sync(all, v, 24));
+        return make_float4(s.x * inv_width, s.y * inv_width, s.z * inv_width, s.w * inv_width);
     }
 };
 
 // the values less their mean (layer norms), zero where there is none
-__device__ __forceinline__ void centre(float (&v)[kPer], int n, int kind, RowSum& sums) {
-    if (kind != GS_NORM_LAYER) return;
-    float m[1] = {0.f};
+template <bool kVec>
+__device__ __forceinline__ void centre(Values& a, const Columns<kVec>& c, RowSum& sums) {
+    const float m = sums.mean(total(a));
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) m[0] += v[k];
-    sums.mean(m);
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) v[k] = k < n ? v[k] - m[0] : 0.f;
-}
-
-__device__ __forceinline__ float square_sum(const float (&v)[kPer]) {
-    float s = 0.f;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) s = fmaf(v[k], v[k], s);
-    return s;
-}
-
-// values to those of the norm, without weight and bias; returns the factor
-__device__ __forceinline__ float normalise(float (&v)[kPer], int n, int kind, float eps,
-                                           RowSum& sums) {
-    if (kind == GS_NORM_NONE) return 1.f;
-    centre(v, n, kind, sums);
-    float s[1] = {square_sum(v)};
-    sums.mean(s);
-    const float f = rsqrtf(s[0] + eps);
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) v[k] *= f;
-    return f;
+    for (int k = 0; k < kPairs; ++k) a.v[k] = add(a.v[k], both(-m));
+    c.trim(a);
 }
 
 // The rows of block k of `blocks`, and the sequence of a token: consecutive.
@@ -270,10 +296,12 @@ __device__ __forceinline__ Part part_of(const RnParams& p, int64_t t) {
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-template <typename T, bool kVec>
+// kLayer: one of the norms is a layer norm.  Without, the mean square of the next row's y is formed
+// with a sum of this row.
+template <typename T, bool kVec, bool kLayer>
 __global__ void __launch_bounds__(kMostThreads) residual_norm_kernel(const RnParams p) {
     grid_dep_sync();
-    __shared__ float buffer[2][kMostSums][kMostThreads / 32];
+    __shared__ float4 buffer[2][kMostThreads / 32];
     RowSum sums{buffer, 0, (int)blockDim.x / 32, 1.f / (float)p.width};
     const Columns<kVec> c(p.width);
     const int64_t end = first_row(p.tokens, gridDim.x, blockIdx.x + 1);
@@ -285,49 +313,67 @@ __global__ void __launch_bounds__(kMostThreads) residual_norm_kernel(const RnPar
         y.load(row < end && p.y.p ? p.y.row(row) : nullptr, c);
     };
     load(t);
+    const bool ahead = !kLayer && p.post != GS_NORM_NONE && p.pre != GS_NORM_NONE;
+    float square = 0.f;  // mean of y^2 where it is formed ahead
+    if (ahead) square = sums.mean(dot(y.get(), y.get()));
     for (; t < end; ++t) {
-        float v[kPer], u[kPer], w[kPer];
-        x.get(v);
-        y.get(u);
+        Values v = x.get(), u = y.get();
         load(t + 1);
         if (t >= at.end) at = part_of(p, t);
-        if (at.b < 0) continue;
-        normalise(u, c.n, p.post, p.eps, sums);
-        c.weights(w, p.gate ? p.gate + (int64_t)at.b * p.width : nullptr, 1.f);
-        float a[kPer], b[kPer];
-        c.weights(a, p.qw, 1.f);
-        c.weights(b, p.qb, 0.f);
+        if (p.post != GS_NORM_NONE) {
+            if (kLayer && p.post == GS_NORM_LAYER) centre(u, c, sums);
+            if (!ahead) square = sums.mean(dot(u, u));
+            const float2 f = both(rsqrtf(square + p.eps));
 #pragma unroll
-        for (int k = 0; k < kPer; ++k)
-            v[k] = fmaf(p.alpha, v[k], p.beta * w[k] * fmaf(u[k], a[k], b[k]));
-        if (p.r.p) RawRow<T, kVec>::store(p.r.row(t), v, c);
+            for (int k = 0; k < kPairs; ++k) u.v[k] = mul(u.v[k], f);
+        }
+        {
+            const Values g = c.weights(p.gate ? p.gate + (int64_t)max(at.b, 0) * p.width : nullptr, 1.f);
+            const Values a = c.weights(p.qw, 1.f), b = c.weights(p.qb, 0.f);
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k)
+                v.v[k] = fma2(both(p.alpha), v.v[k],
+                              mul(mul(both(p.beta), g.v[k]), fma2(u.v[k], a.v[k], b.v[k])));
+        }
+        if (p.r.p && at.b >= 0) RawRow<T, kVec>::store(p.r.row(t), v, c);
         if (p.pre == GS_NORM_NONE) continue;
-        normalise(v, c.n, p.pre, p.eps, sums);
-        c.weights(a, p.pw, 1.f);
-        c.weights(b, p.pb, 0.f);
+        c.trim(v);
+        float s;
+        if (ahead) {
+            const Values next = y.get();
+            const float4 m = sums.mean(dot(v, v), dot(next, next), 0.f, 0.f);
+            s = m.x;
+            square = m.y;
+        } else {
+            if (kLayer && p.pre == GS_NORM_LAYER) centre(v, c, sums);
+            s = sums.mean(dot(v, v));
+        }
+        const float2 f = both(rsqrtf(s + p.eps));
+        const Values a = c.weights(p.pw, 1.f), b = c.weights(p.pb, 0.f);
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) v[k] = fmaf(v[k], a[k], b[k]);
-        RawRow<T, kVec>::store(p.h.row(t), v, c);
+        for (int k = 0; k < kPairs; ++k) v.v[k] = fma2(mul(v.v[k], f), a.v[k], b.v[k]);
+        if (at.b >= 0) RawRow<T, kVec>::store(p.h.row(t), v, c);
     }
 }
 
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
-// The sums of du un and of du over rows of one sequence share the gate: kept without it, they
-// give the gate's gradient too.
-template <typename T, bool kVec, int kThreads>
+// The sums of dR un and of dR over rows of one sequence share the gate: kept without it, they give
+// the gate's gradient and, with it, those of post's weight and bias.  kBias: there are biases or
+// their gradients are wanted.  kLayer as above.
+template <typename T, bool kVec, bool kLayer, bool kBias, int kThreads>
 __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnParams p) {
     grid_dep_sync();
-    __shared__ float buffer[2][kMostSums][kMostThreads / 32];
+    __shared__ float4 buffer[2][kMostThreads / 32];
     RowSum sums{buffer, 0, (int)blockDim.x / 32, 1.f / (float)p.width};
     const Columns<kVec> c(p.width);
     const int64_t begin = first_row(p.tokens, gridDim.x, blockIdx.x);
     const int64_t end = first_row(p.tokens, gridDim.x, blockIdx.x + 1);
     int64_t t = begin;
     Part at{-1, 0, 0};
-    float dpw[kPer]{}, dpb[kPer]{}, dqw[kPer]{}, dqb[kPer]{};  // over all rows
-    float su[kPer]{}, s1[kPer]{};  // sums of dR un and of dR over the sequence's rows
+    Values dpw{}, dpb{}, dqw{}, dqb{};  // over all rows
+    Values su{}, s1{};                  // of dR un and of dR over the sequence's rows
     RawRow<T, kVec> x, y, dr, dh;
     const auto load = [&](int64_t row) {
         const bool some = row < end;
@@ -336,19 +382,29 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
         dr.load(some && p.dr.p ? p.dr.row(row) : nullptr, c);
         dh.load(some && p.dh.p ? p.dh.row(row) : nullptr, c);
     };
+    const auto gate_of = [&]() {  // beta gate
+        Values g = c.weights(p.gate ? p.gate + (int64_t)max(at.b, 0) * p.width : nullptr, 1.f);
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) g.v[k] = mul(both(p.beta), g.v[k]);
+        return g;
+    };
     // the sequence's sums to those of all rows, and to its gate's gradient
     const auto leave = [&]() {
         if (at.b < 0) return;
-        float g[kPer], a[kPer], b[kPer], d[kPer];
-        c.weights(g, p.gate ? p.gate + (int64_t)at.b * p.width : nullptr, 1.f);
-        c.weights(a, p.qw, 1.f);
-        c.weights(b, p.qb, 0.f);
+        const Values g = gate_of(), a = c.weights(p.qw, 1.f);
+        Values b{}, d;
+        if (kBias) b = c.weights(p.qb, 0.f);
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            dqw[k] = fmaf(p.beta * g[k], su[k], dqw[k]);
-            dqb[k] = fmaf(p.beta * g[k], s1[k], dqb[k]);
-            d[k] = p.beta * fmaf(a[k], su[k], b[k] * s1[k]);
-            su[k] = s1[k] = 0.f;
+        for (int k = 0; k < kPairs; ++k) {
+            dqw.v[k] = fma2(g.v[k], su.v[k], dqw.v[k]);
+            d.v[k] = mul(a.v[k], su.v[k]);
+            if (kBias) {
+                dqb.v[k] = fma2(g.v[k], s1.v[k], dqb.v[k]);
+                d.v[k] = fma2(b.v[k], s1.v[k], d.v[k]);
+                s1.v[k] = both(0.f);
+            }
+            d.v[k] = mul(both(p.beta), d.v[k]);
+            su.v[k] = both(0.f);
         }
         if (!p.dgate) return;
         const bool from_before = at.begin < begin, goes_on = at.end > end;
@@ -358,135 +414,166 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
             c.store(p.part_gate + ((int64_t)blockIdx.x * 2 + (from_before ? 0 : 1)) * p.width, d);
     };
     load(t);
+    const bool ahead = !kLayer && p.post != GS_NORM_NONE;
+    float square = 0.f;  // mean of y^2 where it is formed ahead
+    if (ahead) square = sums.mean(dot(y.get(), y.get()));
     for (; t < end; ++t) {
-        float v[kPer], u[kPer], g[kPer], w[kPer], d[kPer];
-        x.get(v);
-        y.get(u);
-        dr.get(d);
-        dh.get(g);
+        Values v = x.get(), u = y.get(), d = dr.get();
+        const Values g = dh.get();
         load(t + 1);
         if (t >= at.end) {
             leave();
             at = part_of(p, t);
         }
-        if (at.b < 0) continue;
-        const float fu = normalise(u, c.n, p.post, p.eps, sums);  // un
-        float bg[kPer], qw[kPer];
-        c.weights(bg, p.gate ? p.gate + (int64_t)at.b * p.width : nullptr, 1.f);
-        c.weights(qw, p.qw, 1.f);
+        // a row that no sequence holds is gone through like the others, but for the results
+        const bool held = at.b >= 0;
+        float fu = 1.f;
+        if (p.post != GS_NORM_NONE) {
+            if (kLayer && p.post == GS_NORM_LAYER) centre(u, c, sums);
+            if (!ahead) square = sums.mean(dot(u, u));
+            fu = rsqrtf(square + p.eps);
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) bg[k] *= p.beta;
+            for (int k = 0; k < kPairs; ++k) u.v[k] = mul(u.v[k], both(fu));  // un
+        }
         if (p.pre != GS_NORM_NONE) {
-            c.weights(w, p.qb, 0.f);
+            {
+                const Values bg = gate_of(), a = c.weights(p.qw, 1.f);
+                Values b{};
+                if (kBias) b = c.weights(p.qb, 0.f);
 #pragma unroll
-            for (int k = 0; k < kPer; ++k)
-                v[k] = k < c.n ? fmaf(p.alpha, v[k], bg[k] * fmaf(u[k], qw[k], w[k])) : 0.f;
-            centre(v, c.n, p.pre, sums);
-            c.weights(w, p.pw, 1.f);
-            float s[3] = {square_sum(v), 0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                w[k] *= g[k];
-                s[1] = fmaf(w[k], v[k], s[1]);
-                s[2] += w[k];
+                for (int k = 0; k < kPairs; ++k)
+                    v.v[k] = fma2(both(p.alpha), v.v[k],
+                                  mul(bg.v[k], kBias ? fma2(u.v[k], a.v[k], b.v[k])
+                                                     : mul(u.v[k], a.v[k])));
             }
-            sums.mean(s);
-            const float f = rsqrtf(s[0] + p.eps), along = s[1] * f;
-            const float mean = p.pre == GS_NORM_LAYER ? s[2] : 0.f;
+            c.trim(v);
+            if (kLayer && p.pre == GS_NORM_LAYER) centre(v, c, sums);
+            Values w = c.weights(p.pw, 1.f);
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                const float vn = v[k] * f;
-                dpw[k] = fmaf(g[k], vn, dpw[k]);
-                dpb[k] += g[k];
-                d[k] = fmaf(f, (w[k] - mean) - vn * along, d[k]);
+            for (int k = 0; k < kPairs; ++k) w.v[k] = mul(w.v[k], g.v[k]);
+            const float4 s = sums.mean(dot(v, v), dot(w, v), kLayer ? total(w) : 0.f, 0.f);
+            const float f = rsqrtf(s.x + p.eps);
+            const float2 f2 = both(f), along = both(-s.y * f * f);
+            const float2 mean = both(kLayer && p.pre == GS_NORM_LAYER ? -s.z : 0.f);
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k) {
+                if (held) {
+                    dpw.v[k] = fma2(g.v[k], mul(v.v[k], f2), dpw.v[k]);
+                    if (kBias) dpb.v[k] = add(dpb.v[k], g.v[k]);
+                }
+                if (kLayer) w.v[k] = add(w.v[k], mean);
+                d.v[k] = fma2(f2, fma2(v.v[k], along, w.v[k]), d.v[k]);
             }
         }
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) v[k] = p.alpha * d[k];
-        RawRow<T, kVec>::store(p.dx.row(t), v, c);
+        for (int k = 0; k < kPairs; ++k) v.v[k] = mul(both(p.alpha), d.v[k]);
+        if (held) RawRow<T, kVec>::store(p.dx.row(t), v, c);
         if (!p.y.p) continue;
+        if (held)
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            su[k] = fmaf(d[k], u[k], su[k]);
-            s1[k] += d[k];
-            d[k] *= bg[k];
+            for (int k = 0; k < kPairs; ++k) {
+                su.v[k] = fma2(d.v[k], u.v[k], su.v[k]);
+                if (kBias) s1.v[k] = add(s1.v[k], d.v[k]);
+            }
+        {
+            const Values bg = gate_of();
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k) d.v[k] = mul(d.v[k], bg.v[k]);
         }
         if (p.post != GS_NORM_NONE) {
-            float s[2] = {0.f, 0.f};
+            const Values a = c.weights(p.qw, 1.f);
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                d[k] = k < c.n ? d[k] * qw[k] : 0.f;
-                s[0] = fmaf(d[k], u[k], s[0]);
-                s[1] += d[k];
+            for (int k = 0; k < kPairs; ++k) d.v[k] = mul(d.v[k], a.v[k]);
+            c.trim(d);
+            float4 s;
+            if (ahead) {
+                const Values next = y.get();
+                s = sums.mean(dot(d, u), dot(next, next), 0.f, 0.f);
+                square = s.y;
+            } else {
+                s = sums.mean(dot(d, u), total(d), 0.f, 0.f);
             }
-            sums.mean(s);
-            const float mean = p.post == GS_NORM_LAYER ? s[1] : 0.f;
+            const float2 along = both(-s.x), mean = both(p.post == GS_NORM_LAYER ? -s.y : 0.f);
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) d[k] = fu * ((d[k] - mean) - u[k] * s[0]);
+            for (int k = 0; k < kPairs; ++k) {
+                if (kLayer) d.v[k] = add(d.v[k], mean);
+                d.v[k] = mul(both(fu), fma2(u.v[k], along, d.v[k]));
+            }
         }
-        RawRow<T, kVec>::store(p.dy.row(t), d, c);
+        if (held) RawRow<T, kVec>::store(p.dy.row(t), d, c);
     }
     leave();
     float* part = p.part + (int64_t)blockIdx.x * 4 * p.width;
     c.store(part, dpw);
-    c.store(part + p.width, dpb);
+    if (kBias) c.store(part + p.width, dpb);
     c.store(part + 2 * p.width, dqw);
-    c.store(part + 3 * p.width, dqb);
+    if (kBias) c.store(part + 3 * p.width, dqb);
 }
 
 // The blocks' sums of a column: 32 threads take every 32nd block, and their sums are added in
-// order.  blockIdx.y: which of the four gradients.
-constexpr int kFinishCols = 32, kFinishThreads = 1024;
+// order.  blockIdx.y: which of the four gradients, or behind them a sequence's gate (and every
+// gridDim.y - 4 th from it on): of those that several blocks met, and zeros for empty ones.
+constexpr int kFinishCols = 32, kFinishThreads = 1024, kFinishOf = kFinishThreads / kFinishCols;
 struct FourGradients {
     float* g[4];
 };
-__global__ void __launch_bounds__(kFinishThreads)
-    residual_norm_sum_kernel(const float* __restrict__ part, int blocks, int width,
-                             FourGradients out) {
-    grid_dep_sync();
-    if (!out.g[blockIdx.y]) return;
-    constexpr int kOf = kFinishThreads / kFinishCols;
-    __shared__ float s[kOf][kFinishCols];
+
+__device__ __forceinline__ void sum_blocks(float (*s)[kFinishCols], const float* part, int first,
+                                           int count, int64_t step, bool has, float* out) {
     const int col = threadIdx.x % kFinishCols, row = threadIdx.x / kFinishCols;
-    const int i = blockIdx.x * kFinishCols + col;
     float a = 0.f;
-    if (i < width)
-#pragma unroll 8
-        for (int b = row; b < blocks; b += kOf)
-            a += __ldg(part + ((int64_t)b * 4 + blockIdx.y) * width + i);
+    if (has)
+#pragma unroll 4
+        for (int b = row; b < count; b += kFinishOf) a += __ldg(part + (first + b) * step);
     s[row][col] = a;
     __syncthreads();
-    if (row != 0 || i >= width) return;
-    for (int r = 1; r < kOf; ++r) a += s[r][col];
-    out.g[blockIdx.y][i] = a;
+    if (row == 0 && has) {
+        for (int r = 1; r < kFinishOf; ++r) a += s[r][col];
+        *out = a;
+    }
 }
 
-// The gate's gradient of sequences that several blocks met, in the blocks' order, and of empty ones.
-__global__ void __launch_bounds__(kSumThreads) residual_norm_gate_kernel(const RnParams p, int blocks) {
+__global__ void __launch_bounds__(kFinishThreads)
+    residual_norm_finish_kernel(const RnParams p, int blocks, FourGradients out) {
     grid_dep_sync();
-    for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+    __shared__ float s[kFinishOf][kFinishCols];
+    const int col = blockIdx.x * kFinishCols + threadIdx.x % kFinishCols;
+    const bool has = col < p.width;
+    if (blockIdx.y < 4) {
+        float* to = out.g[blockIdx.y];
+        if (to)
+            sum_blocks(s, p.part + (int64_t)blockIdx.y * p.width + col, 0, blocks, 4 * (int64_t)p.width,
+                       has, to + col);
+        return;
+    }
+    const int64_t w = p.width;
+    for (int b = blockIdx.y - 4; b < p.batch; b += gridDim.y - 4) {
         const int64_t begin = p.cu ? offset(p, b) : 0, end = p.cu ? offset(p, b + 1) : p.tokens;
+        float* to = p.dgate + b * w + col;
+        if (end <= begin) {
+            if (has && threadIdx.x < kFinishCols) *to = 0.f;
+            continue;
+        }
         const auto block_of = [&](int64_t t) {
-            int64_t k = t * blocks / p.tokens;  // its first row may lie before t, or one block on
+            int64_t k = t * blocks / p.tokens;  // or one off
             while (k + 1 < blocks && first_row(p.tokens, blocks, k + 1) <= t) ++k;
             while (k > 0 && first_row(p.tokens, blocks, k) > t) --k;
             return (int)k;
         };
-        const bool some = end > begin;
-        const int first = some ? block_of(begin) : 0, last = some ? block_of(end - 1) : 0;
-        if (some && first == last) continue;
-        for (int i = blockIdx.y * kSumThreads + threadIdx.x; i < p.width; i += gridDim.y * kSumThreads) {
-            float a = 0.f;
-            if (some) {
-                // the first block's last sequence -- unless it is its first one too
-                const bool before = first_row(p.tokens, blocks, first) > begin;
-                a = __ldg(p.part_gate + ((int64_t)first * 2 + (before ? 0 : 1)) * p.width + i);
-#pragma unroll 8
-                for (int k = first + 1; k <= last; ++k)
-                    a += __ldg(p.part_gate + (int64_t)k * 2 * p.width + i);
-            }
-            p.dgate[(int64_t)b * p.width + i] = a;
-        }
+        const int first = block_of(begin), last = block_of(end - 1);
+        if (first == last) continue;  // the block has written it
+        // The first block keeps it as its last sequence: in the second of its places, unless it
+        // began before the block, which only offsets out of order make it; the others in the first.
+        __syncthreads();
+        const float* part = p.part_gate + col;
+        const bool here = first_row(p.tokens, blocks, first) <= begin;
+        if (threadIdx.x < kFinishCols && has)
+            s[0][threadIdx.x] = __ldg(part + ((int64_t)first * 2 + (here ? 1 : 0)) * w);
+        __syncthreads();
+        const float head = s[0][threadIdx.x % kFinishCols];
+        __syncthreads();
+        sum_blocks(s, part, first + 1, last - first, 2 * w, has, to);
+        if (threadIdx.x < kFinishCols && has) *to += head;
     }
 }
 
@@ -532,17 +619,26 @@ bool whole_words(int width, std::initializer_list<NormRows> arrays) {
 
 template <typename T, bool kVec>
 cudaError_t launch_fwd(const RnParams& p, int blocks, cudaStream_t st) {
-    return launch(residual_norm_kernel<T, kVec>, dim3((unsigned)blocks),
-                  dim3((unsigned)warps_of(p.width) * 32), 0, st, p);
+    const bool layer = p.pre == GS_NORM_LAYER || p.post == GS_NORM_LAYER;
+    return launch(layer ? residual_norm_kernel<T, kVec, true> : residual_norm_kernel<T, kVec, false>,
+                  dim3((unsigned)blocks), dim3((unsigned)warps_of(p.width) * 32), 0, st, p);
 }
 
 // Up to 4,096 values a row its threads may have 128 registers each; beyond, 64 and spills.
 template <typename T, bool kVec>
-cudaError_t launch_bwd(const RnParams& p, int blocks, cudaStream_t st) {
+cudaError_t launch_bwd(const RnParams& p, bool bias, int blocks, cudaStream_t st) {
     const unsigned threads = (unsigned)warps_of(p.width) * 32;
-    return launch(threads <= 512 ? residual_norm_bwd_kernel<T, kVec, 512>
-                                 : residual_norm_bwd_kernel<T, kVec, kMostThreads>,
-                  dim3((unsigned)blocks), dim3(threads), 0, st, p);
+    const bool layer = p.pre == GS_NORM_LAYER || p.post == GS_NORM_LAYER;
+    void (*kernel)(const RnParams);
+    if (threads > 512)
+        kernel = residual_norm_bwd_kernel<T, kVec, true, true, kMostThreads>;
+    else if (layer)
+        kernel = bias ? residual_norm_bwd_kernel<T, kVec, true, true, 512>
+                      : residual_norm_bwd_kernel<T, kVec, true, false, 512>;
+    else
+        kernel = bias ? residual_norm_bwd_kernel<T, kVec, false, true, 512>
+                      : residual_norm_bwd_kernel<T, kVec, false, false, 512>;
+    return launch(kernel, dim3((unsigned)blocks), dim3(threads), 0, st, p);
 }
 
 }  // namespace
@@ -581,22 +677,21 @@ cudaError_t launch_residual_norm_bwd(const ResidualNormArgs& a, const gs_rows& x
     p.part = static_cast<float*>(ws);
     p.part_gate = p.part + ((int64_t)blocks * 4 * a.width + 3) / 4 * 4;
     const bool vec = whole_words(a.width, {p.x, p.y, p.dr, p.dh, p.dx, p.dy});
+    const bool bias = p.pb || p.qb || g.pre_bias || g.post_bias;
     cudaError_t e = cudaSuccess;
     if (a.tokens > 0 && a.bf16)
-        e = vec ? launch_bwd<__nv_bfloat16, true>(p, blocks, st)
-                : launch_bwd<__nv_bfloat16, false>(p, blocks, st);
+        e = vec ? launch_bwd<__nv_bfloat16, true>(p, bias, blocks, st)
+                : launch_bwd<__nv_bfloat16, false>(p, bias, blocks, st);
     else if (a.tokens > 0)
-        e = vec ? launch_bwd<float, true>(p, blocks, st) : launch_bwd<float, false>(p, blocks, st);
+        e = vec ? launch_bwd<float, true>(p, bias, blocks, st)
+                : launch_bwd<float, false>(p, bias, blocks, st);
     const FourGradients out{{g.pre_weight, g.pre_bias, g.post_weight, g.post_bias}};
-    if (e == cudaSuccess && (g.pre_weight || g.pre_bias || g.post_weight || g.post_bias))
-        e = launch(residual_norm_sum_kernel,
-                   dim3((a.width + kFinishCols - 1) / kFinishCols, 4), dim3(kFinishThreads), 0, st,
-                   (const float*)p.part, blocks, a.width, out);
-    if (e == cudaSuccess && g.gate)
-        e = launch(residual_norm_gate_kernel,
-                   dim3((unsigned)std::min(a.batch, 4 * kSms),
-                        (unsigned)((a.width + kSumThreads - 1) / kSumThreads)),
-                   dim3(kSumThreads), 0, st, p, blocks);
+    const bool sums = g.pre_weight || g.pre_bias || g.post_weight || g.post_bias;
+    if (e == cudaSuccess && (sums || g.gate))
+        e = launch(residual_norm_finish_kernel,
+                   dim3((unsigned)((a.width + kFinishCols - 1) / kFinishCols),
+                        4u + (g.gate ? (unsigned)std::min(a.batch, kMostGates) : 0u)),
+                   dim3(kFinishThreads), 0, st, p, blocks, out);
     return e;
 }
 
