@@ -38,15 +38,14 @@ namespace gs {
 namespace {
 
 constexpr int kSms = 152;
-constexpr int kPer = 8;             // values a thread
 constexpr int kMostThreads = 1024;  // width <= 8,192
+constexpr int kFourUpTo = 2048;  // odd widths whose threads take four values instead of eight
 constexpr int kFwdWarps = 32, kBwdWarps = 16;  // resident on an SM
 constexpr int kMostGates = 256;     // sequences at once when the gates' gradients are added up
 
 struct NormRows {
     char* p;
     int64_t stride;  // bytes
-    __device__ __forceinline__ char* row(int64_t t) const { return p + t * stride; }
 };
 
 struct RnParams {
@@ -69,67 +68,92 @@ __device__ __forceinline__ float2 add(float2 a, float2 b) { return __fadd2_rn(a,
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
 // A thread's values of a row, in pairs (two operations an instruction).
-constexpr int kPairs = kPer / 2;
+template <int kPairs>
 struct Values {
     float2 v[kPairs];
 };
 
-__device__ __forceinline__ float dot(const Values& a, const Values& b) {
+template <int kPairs>
+__device__ __forceinline__ float dot(const Values<kPairs>& a, const Values<kPairs>& b) {
     float2 s = mul(a.v[0], b.v[0]);
 #pragma unroll
     for (int k = 1; k < kPairs; ++k) s = fma2(a.v[k], b.v[k], s);
     return s.x + s.y;
 }
-__device__ __forceinline__ float total(const Values& a) {
+template <int kPairs>
+__device__ __forceinline__ float total(const Values<kPairs>& a) {
     float2 s = a.v[0];
 #pragma unroll
     for (int k = 1; k < kPairs; ++k) s = add(s, a.v[k]);
     return s.x + s.y;
 }
 
-// A thread's eight columns: neighbours, or (odd widths and strides) every blockDim-th.
-template <bool kVec>
+// A thread's columns: neighbours, or (odd widths and strides) every 32nd of its warp's.
+template <bool kVec, int kPairs>
 struct Columns {
-    int first, step, n;  // n: those that exist
+    static constexpr int kPer = 2 * kPairs, kStep = kVec ? 1 : 32;
+    using V = Values<kPairs>;
+    int first, n;  // n: those that exist
+    bool full;     // the whole warp's do
+
     __device__ __forceinline__ Columns(int width) {
-        first = kVec ? (int)threadIdx.x * kPer : (int)threadIdx.x;
-        step = kVec ? 1 : (int)blockDim.x;
-        n = first >= width ? 0 : kVec ? kPer : min(kPer, (width - 1 - first) / step + 1);
+        if (kVec) {
+            first = (int)threadIdx.x * kPer;
+            n = first >= width ? 0 : kPer;
+            full = n > 0;
+        } else {
+            const int lane = threadIdx.x & 31, of_warp = ((int)threadIdx.x - lane) * kPer;
+            first = of_warp + lane;
+            n = first >= width ? 0 : min(kPer, (width - 1 - first) / kStep + 1);
+            full = of_warp + 32 * kPer <= width;
+        }
+    }
+    // values k of the lane, by f, where there are such columns
+    template <typename F>
+    __device__ __forceinline__ void each(const F& f) const {
+        if (full) {
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) f(k);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kPer; ++k)
+                if (k < n) f(k);
+        }
     }
     // values of fp32 from w, `other` where there are none
-    __device__ __forceinline__ Values weights(const float* w, float other) const {
-        Values r;
+    __device__ __forceinline__ V weights(const float* w, float other) const {
+        V r;
         float* v = &r.v[0].x;
 #pragma unroll
         for (int k = 0; k < kPer; ++k) v[k] = other;
         if (!w || n == 0) return r;
+        const float* p = w + first;
         if (kVec) {
-            const float4 a = __ldg(reinterpret_cast<const float4*>(w + first));
-            const float4 b = __ldg(reinterpret_cast<const float4*>(w + first) + 1);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        } else {
 #pragma unroll
-            for (int k = 0; k < kPer; ++k)
-                if (k < n) v[k] = __ldg(w + first + k * step);
+            for (int k = 0; k < kPer; k += 4) {
+                const float4 a = __ldg(reinterpret_cast<const float4*>(p + k));
+                v[k] = a.x, v[k + 1] = a.y, v[k + 2] = a.z, v[k + 3] = a.w;
+            }
+        } else {
+            each([&](int k) { v[k] = __ldg(p + k * kStep); });
         }
         return r;
     }
-    __device__ __forceinline__ void store(float* w, const Values& r) const {
+    __device__ __forceinline__ void store(float* w, const V& r) const { store_at(w + first, r); }
+    __device__ __forceinline__ void store_at(float* p, const V& r) const {  // p: at the first column
         if (n == 0) return;
         const float* v = &r.v[0].x;
         if (kVec) {
-            reinterpret_cast<float4*>(w + first)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4*>(w + first)[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
 #pragma unroll
-            for (int k = 0; k < kPer; ++k)
-                if (k < n) w[first + k * step] = v[k];
+            for (int k = 0; k < kPer; k += 4)
+                *reinterpret_cast<float4*>(p + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+        } else {
+            each([&](int k) { p[k * kStep] = v[k]; });
         }
     }
     // zero where there is no column
-    __device__ __forceinline__ void trim(Values& r) const {
-        if (kVec ? n > 0 : n == kPer) return;
+    __device__ __forceinline__ void trim(V& r) const {
+        if (full) return;
         float* v = &r.v[0].x;
 #pragma unroll
         for (int k = 0; k < kPer; ++k)
@@ -138,72 +162,82 @@ struct Columns {
 };
 
 // A thread's values of a row as they lie in memory, zeros where there is none.
-template <typename T, bool kVec>
+template <typename T, bool kVec, int kPairs>
 struct RawRow;
 
-template <bool kVec>
-struct RawRow<float, kVec> {
-    Values r;
-    __device__ __forceinline__ void load(const char* row, const Columns<kVec>& c) {
+template <bool kVec, int kPairs>
+struct RawRow<float, kVec, kPairs> {
+    using C = Columns<kVec, kPairs>;
+    using V = Values<kPairs>;
+    V r;
+    __device__ __forceinline__ void clear() { r = V{}; }
+    __device__ __forceinline__ void load(const char* at, const C& c) {
         float* v = &r.v[0].x;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) v[k] = 0.f;
-        if (!row || c.n == 0) return;
-        const float* p = reinterpret_cast<const float*>(row) + c.first;
+        const float* p = reinterpret_cast<const float*>(at);
         if (kVec) {
-            const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-            const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        } else {
 #pragma unroll
-            for (int k = 0; k < kPer; ++k)
-                if (k < c.n) v[k] = p[k * c.step];
+            for (int k = 0; k < C::kPer; k += 4) {
+                const float4 a = __ldcs(reinterpret_cast<const float4*>(p + k));
+                v[k] = a.x, v[k + 1] = a.y, v[k + 2] = a.z, v[k + 3] = a.w;
+            }
+        } else {
+            c.each([&](int k) { v[k] = p[k * C::kStep]; });
         }
     }
-    __device__ __forceinline__ Values get() const { return r; }
-    __device__ static __forceinline__ void store(char* row, const Values& f, const Columns<kVec>& c) {
-        c.store(reinterpret_cast<float*>(row), f);
+    __device__ __forceinline__ V get() const { return r; }
+    __device__ static __forceinline__ void store(char* at, const V& f, const C& c) {
+        c.store_at(reinterpret_cast<float*>(at), f);
     }
 };
 
-template <bool kVec>
-struct RawRow<__nv_bfloat16, kVec> {
+template <bool kVec, int kPairs>
+struct RawRow<__nv_bfloat16, kVec, kPairs> {
+    using C = Columns<kVec, kPairs>;
+    using V = Values<kPairs>;
     uint32_t w[kPairs];
-    __device__ __forceinline__ void load(const char* row, const Columns<kVec>& c) {
+    __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) w[k] = 0;
-        if (!row || c.n == 0) return;
-        const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + c.first;
-        if (kVec) {
+    }
+    __device__ __forceinline__ void load(const char* at, const C& c) {
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(at);
+        if constexpr (kVec && kPairs == 4) {
             const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
             w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+        } else if constexpr (kVec) {
+            const uint2 a = __ldcs(reinterpret_cast<const uint2*>(p));
+            w[0] = a.x, w[1] = a.y;
         } else {
+            uint32_t half[C::kPer]{};
+            c.each([&](int k) { half[k] = p[k * C::kStep]; });
 #pragma unroll
-            for (int k = 0; k < kPer; ++k)
-                if (k < c.n) w[k / 2] |= (uint32_t)p[k * c.step] << (16 * (k & 1));
+            for (int k = 0; k < kPairs; ++k) w[k] = half[2 * k] | half[2 * k + 1] << 16;
         }
     }
-    __device__ __forceinline__ Values get() const {
-        Values r;
+    __device__ __forceinline__ V get() const {
+        V r;
 #pragma unroll
         for (int k = 0; k < kPairs; ++k)
             r.v[k] = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
         return r;
     }
-    __device__ static __forceinline__ void store(char* row, const Values& f, const Columns<kVec>& c) {
+    __device__ static __forceinline__ void store(char* at, const V& f, const C& c) {
         if (c.n == 0) return;
-        __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(row) + c.first;
+        __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(at);
         if (kVec) {
-            __nv_bfloat162 h[kPairs];
+            uint32_t h[kPairs];
 #pragma unroll
-            for (int k = 0; k < kPairs; ++k) h[k] = __floats2bfloat162_rn(f.v[k].x, f.v[k].y);
-            *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
+            for (int k = 0; k < kPairs; ++k) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(f.v[k].x, f.v[k].y);
+                h[k] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            if constexpr (kPairs == 4)
+                *reinterpret_cast<uint4*>(p) = make_uint4(h[0], h[1], h[2], h[3]);
+            else
+                *reinterpret_cast<uint2*>(p) = make_uint2(h[0], h[1]);
         } else {
             const float* v = &f.v[0].x;
-#pragma unroll
-            for (int k = 0; k < kPer; ++k)
-                if (k < c.n) p[k * c.step] = __float2bfloat16_rn(v[k]);
+            c.each([&](int k) { p[k * C::kStep] = __float2bfloat16_rn(v[k]); });
         }
     }
 };
@@ -222,9 +256,14 @@ struct RowSum {
         if (writes) (&to[threadIdx.x >> 5].x)[at] = v;
         __syncthreads();
         float4 s = to[0];
-        for (int w = 1; w < warps; ++w) {
+        const auto plus = [&](int w) {
             const float4 o = to[w];
             s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
+        };
+        if (warps == 4) {
+            plus(1), plus(2), plus(3);
+        } else {
+            for (int w = 1; w < warps; ++w) plus(w);
         }
         return s;
     }
@@ -256,13 +295,23 @@ struct RowSum {
 };
 
 // the values less their mean (layer norms), zero where there is none
-template <bool kVec>
-__device__ __forceinline__ void centre(Values& a, const Columns<kVec>& c, RowSum& sums) {
+template <bool kVec, int kPairs>
+__device__ __forceinline__ void centre(Values<kPairs>& a, const Columns<kVec, kPairs>& c,
+                                       RowSum& sums) {
     const float m = sums.mean(total(a));
 #pragma unroll
     for (int k = 0; k < kPairs; ++k) a.v[k] = add(a.v[k], both(-m));
     c.trim(a);
 }
+
+// Rows one after the other, from column `first` on.
+struct Walk {
+    char* p;
+    int64_t stride;
+    __device__ __forceinline__ Walk(const NormRows& r, int64_t row, int bytes)
+        : p(r.p ? r.p + row * r.stride + bytes : nullptr), stride(r.p ? r.stride : 0) {}
+    __device__ __forceinline__ void next() { p += stride; }
+};
 
 // The rows of block k of `blocks`, and the sequence of a token: consecutive.
 __host__ __device__ __forceinline__ int64_t first_row(int64_t tokens, int64_t blocks, int64_t k) {
@@ -298,28 +347,42 @@ __device__ __forceinline__ Part part_of(const RnParams& p, int64_t t) {
 // ---------------------------------------------------------------------------
 // kLayer: one of the norms is a layer norm.  Without, the mean square of the next row's y is formed
 // with a sum of this row.
-template <typename T, bool kVec, bool kLayer>
-__global__ void __launch_bounds__(kMostThreads) residual_norm_kernel(const RnParams p) {
+template <typename T, bool kVec, int kPairs, bool kLayer, int kThreads>
+__global__ void __launch_bounds__(kThreads) residual_norm_kernel(const RnParams p) {
     grid_dep_sync();
+    using V = Values<kPairs>;
+    using Row = RawRow<T, kVec, kPairs>;
     __shared__ float4 buffer[2][kMostThreads / 32];
     RowSum sums{buffer, 0, (int)blockDim.x / 32, 1.f / (float)p.width};
-    const Columns<kVec> c(p.width);
+    const Columns<kVec, kPairs> c(p.width);
     const int64_t end = first_row(p.tokens, gridDim.x, blockIdx.x + 1);
     int64_t t = first_row(p.tokens, gridDim.x, blockIdx.x);
     Part at{0, 0, 0};
-    RawRow<T, kVec> x, y;
-    const auto load = [&](int64_t row) {
-        x.load(row < end ? p.x.row(row) : nullptr, c);
-        y.load(row < end && p.y.p ? p.y.row(row) : nullptr, c);
+    const float* gate = nullptr;  // the sequence's
+    const int shift = c.first * (int)sizeof(T);
+    Walk in_x(p.x, t, shift), in_y(p.y, t, shift), out_r(p.r, t, shift), out_h(p.h, t, shift);
+    Row x, y;
+    x.clear();
+    y.clear();
+    const auto load = [&]() {  // the next row
+        if (c.n > 0) {
+            x.load(in_x.p, c);
+            if (p.y.p) y.load(in_y.p, c);
+        }
+        in_x.next();
+        in_y.next();
     };
-    load(t);
+    load();
     const bool ahead = !kLayer && p.post != GS_NORM_NONE && p.pre != GS_NORM_NONE;
     float square = 0.f;  // mean of y^2 where it is formed ahead
     if (ahead) square = sums.mean(dot(y.get(), y.get()));
     for (; t < end; ++t) {
-        Values v = x.get(), u = y.get();
-        load(t + 1);
-        if (t >= at.end) at = part_of(p, t);
+        V v = x.get(), u = y.get();
+        if (t + 1 < end) load();
+        if (t >= at.end) {
+            at = part_of(p, t);
+            if (p.gate) gate = p.gate + (int64_t)max(at.b, 0) * p.width;
+        }
         if (p.post != GS_NORM_NONE) {
             if (kLayer && p.post == GS_NORM_LAYER) centre(u, c, sums);
             if (!ahead) square = sums.mean(dot(u, u));
@@ -328,19 +391,19 @@ __global__ void __launch_bounds__(kMostThreads) residual_norm_kernel(const RnPar
             for (int k = 0; k < kPairs; ++k) u.v[k] = mul(u.v[k], f);
         }
         {
-            const Values g = c.weights(p.gate ? p.gate + (int64_t)max(at.b, 0) * p.width : nullptr, 1.f);
-            const Values a = c.weights(p.qw, 1.f), b = c.weights(p.qb, 0.f);
+            const V g = c.weights(gate, 1.f), a = c.weights(p.qw, 1.f), b = c.weights(p.qb, 0.f);
 #pragma unroll
             for (int k = 0; k < kPairs; ++k)
                 v.v[k] = fma2(both(p.alpha), v.v[k],
                               mul(mul(both(p.beta), g.v[k]), fma2(u.v[k], a.v[k], b.v[k])));
         }
-        if (p.r.p && at.b >= 0) RawRow<T, kVec>::store(p.r.row(t), v, c);
+        if (p.r.p && at.b >= 0) Row::store(out_r.p, v, c);
+        out_r.next();
         if (p.pre == GS_NORM_NONE) continue;
         c.trim(v);
         float s;
         if (ahead) {
-            const Values next = y.get();
+            const V next = y.get();
             const float4 m = sums.mean(dot(v, v), dot(next, next), 0.f, 0.f);
             s = m.x;
             square = m.y;
@@ -349,10 +412,11 @@ __global__ void __launch_bounds__(kMostThreads) residual_norm_kernel(const RnPar
             s = sums.mean(dot(v, v));
         }
         const float2 f = both(rsqrtf(s + p.eps));
-        const Values a = c.weights(p.pw, 1.f), b = c.weights(p.pb, 0.f);
+        const V a = c.weights(p.pw, 1.f), b = c.weights(p.pb, 0.f);
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) v.v[k] = fma2(mul(v.v[k], f), a.v[k], b.v[k]);
-        if (at.b >= 0) RawRow<T, kVec>::store(p.h.row(t), v, c);
+        if (at.b >= 0) Row::store(out_h.p, v, c);
+        out_h.next();
     }
 }
 
@@ -362,28 +426,43 @@ __global__ void __launch_bounds__(kMostThreads) residual_norm_kernel(const RnPar
 // The sums of dR un and of dR over rows of one sequence share the gate: kept without it, they give
 // the gate's gradient and, with it, those of post's weight and bias.  kBias: there are biases or
 // their gradients are wanted.  kLayer as above.
-template <typename T, bool kVec, bool kLayer, bool kBias, int kThreads>
+template <typename T, bool kVec, int kPairs, bool kLayer, bool kBias, int kThreads>
 __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnParams p) {
     grid_dep_sync();
+    using V = Values<kPairs>;
+    using Row = RawRow<T, kVec, kPairs>;
     __shared__ float4 buffer[2][kMostThreads / 32];
     RowSum sums{buffer, 0, (int)blockDim.x / 32, 1.f / (float)p.width};
-    const Columns<kVec> c(p.width);
+    const Columns<kVec, kPairs> c(p.width);
     const int64_t begin = first_row(p.tokens, gridDim.x, blockIdx.x);
     const int64_t end = first_row(p.tokens, gridDim.x, blockIdx.x + 1);
     int64_t t = begin;
     Part at{-1, 0, 0};
-    Values dpw{}, dpb{}, dqw{}, dqb{};  // over all rows
-    Values su{}, s1{};                  // of dR un and of dR over the sequence's rows
-    RawRow<T, kVec> x, y, dr, dh;
-    const auto load = [&](int64_t row) {
-        const bool some = row < end;
-        x.load(some ? p.x.row(row) : nullptr, c);
-        y.load(some && p.y.p ? p.y.row(row) : nullptr, c);
-        dr.load(some && p.dr.p ? p.dr.row(row) : nullptr, c);
-        dh.load(some && p.dh.p ? p.dh.row(row) : nullptr, c);
+    V dpw{}, dpb{}, dqw{}, dqb{};  // over all rows
+    V su{}, s1{};                  // of dR un and of dR over the sequence's rows
+    const float* gate = nullptr;  // the sequence's
+    const int shift = c.first * (int)sizeof(T);
+    Walk in_x(p.x, t, shift), in_y(p.y, t, shift), in_dr(p.dr, t, shift), in_dh(p.dh, t, shift),
+        out_x(p.dx, t, shift), out_y(p.dy, t, shift);
+    Row x, y, dr, dh;
+    x.clear();
+    y.clear();
+    dr.clear();
+    dh.clear();
+    const auto load = [&]() {  // the next row
+        if (c.n > 0) {
+            x.load(in_x.p, c);
+            if (p.y.p) y.load(in_y.p, c);
+            if (p.dr.p) dr.load(in_dr.p, c);
+            if (p.dh.p) dh.load(in_dh.p, c);
+        }
+        in_x.next();
+        in_y.next();
+        in_dr.next();
+        in_dh.next();
     };
     const auto gate_of = [&]() {  // beta gate
-        Values g = c.weights(p.gate ? p.gate + (int64_t)max(at.b, 0) * p.width : nullptr, 1.f);
+        V g = c.weights(gate, 1.f);
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) g.v[k] = mul(both(p.beta), g.v[k]);
         return g;
@@ -391,8 +470,8 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
     // the sequence's sums to those of all rows, and to its gate's gradient
     const auto leave = [&]() {
         if (at.b < 0) return;
-        const Values g = gate_of(), a = c.weights(p.qw, 1.f);
-        Values b{}, d;
+        const V g = gate_of(), a = c.weights(p.qw, 1.f);
+        V b{}, d;
         if (kBias) b = c.weights(p.qb, 0.f);
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) {
@@ -413,17 +492,18 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
         else
             c.store(p.part_gate + ((int64_t)blockIdx.x * 2 + (from_before ? 0 : 1)) * p.width, d);
     };
-    load(t);
+    load();
     const bool ahead = !kLayer && p.post != GS_NORM_NONE;
     float square = 0.f;  // mean of y^2 where it is formed ahead
     if (ahead) square = sums.mean(dot(y.get(), y.get()));
     for (; t < end; ++t) {
-        Values v = x.get(), u = y.get(), d = dr.get();
-        const Values g = dh.get();
-        load(t + 1);
+        V v = x.get(), u = y.get(), d = dr.get();
+        const V g = dh.get();
+        if (t + 1 < end) load();
         if (t >= at.end) {
             leave();
             at = part_of(p, t);
+            if (p.gate) gate = p.gate + (int64_t)max(at.b, 0) * p.width;
         }
         // a row that no sequence holds is gone through like the others, but for the results
         const bool held = at.b >= 0;
@@ -437,8 +517,8 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
         }
         if (p.pre != GS_NORM_NONE) {
             {
-                const Values bg = gate_of(), a = c.weights(p.qw, 1.f);
-                Values b{};
+                const V bg = gate_of(), a = c.weights(p.qw, 1.f);
+                V b{};
                 if (kBias) b = c.weights(p.qb, 0.f);
 #pragma unroll
                 for (int k = 0; k < kPairs; ++k)
@@ -448,7 +528,7 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
             }
             c.trim(v);
             if (kLayer && p.pre == GS_NORM_LAYER) centre(v, c, sums);
-            Values w = c.weights(p.pw, 1.f);
+            V w = c.weights(p.pw, 1.f);
 #pragma unroll
             for (int k = 0; k < kPairs; ++k) w.v[k] = mul(w.v[k], g.v[k]);
             const float4 s = sums.mean(dot(v, v), dot(w, v), kLayer ? total(w) : 0.f, 0.f);
@@ -467,7 +547,8 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
         }
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) v.v[k] = mul(both(p.alpha), d.v[k]);
-        if (held) RawRow<T, kVec>::store(p.dx.row(t), v, c);
+        if (held) Row::store(out_x.p, v, c);
+        out_x.next();
         if (!p.y.p) continue;
         if (held)
 #pragma unroll
@@ -476,18 +557,18 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
                 if (kBias) s1.v[k] = add(s1.v[k], d.v[k]);
             }
         {
-            const Values bg = gate_of();
+            const V bg = gate_of();
 #pragma unroll
             for (int k = 0; k < kPairs; ++k) d.v[k] = mul(d.v[k], bg.v[k]);
         }
         if (p.post != GS_NORM_NONE) {
-            const Values a = c.weights(p.qw, 1.f);
+            const V a = c.weights(p.qw, 1.f);
 #pragma unroll
             for (int k = 0; k < kPairs; ++k) d.v[k] = mul(d.v[k], a.v[k]);
             c.trim(d);
             float4 s;
             if (ahead) {
-                const Values next = y.get();
+                const V next = y.get();
                 s = sums.mean(dot(d, u), dot(next, next), 0.f, 0.f);
                 square = s.y;
             } else {
@@ -500,7 +581,8 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
                 d.v[k] = mul(both(fu), fma2(u.v[k], along, d.v[k]));
             }
         }
-        if (held) RawRow<T, kVec>::store(p.dy.row(t), d, c);
+        if (held) Row::store(out_y.p, d, c);
+        out_y.next();
     }
     leave();
     float* part = p.part + (int64_t)blockIdx.x * 4 * p.width;
@@ -577,10 +659,16 @@ __global__ void __launch_bounds__(kFinishThreads)
     }
 }
 
-int warps_of(int width) { return (width + 32 * kPer - 1) / (32 * kPer); }
+// How a row is shared out: threads of eight values, or of four.
+int pairs_of(int width, bool vec) { return !vec && width <= kFourUpTo ? 2 : 4; }
 
-int blocks_of(int64_t tokens, int width, int resident_warps) {
-    return (int)std::min<int64_t>(tokens, (int64_t)kSms * std::max(1, resident_warps / warps_of(width)));
+int warps_of(int width, bool vec) {
+    const int per_warp = 64 * pairs_of(width, vec);
+    return (width + per_warp - 1) / per_warp;
+}
+
+int64_t most_blocks(int width, bool vec, int resident_warps) {
+    return (int64_t)kSms * std::max(1, resident_warps / warps_of(width, vec));
 }
 
 NormRows rows_of(const gs_rows& r, int size) {
@@ -609,43 +697,60 @@ RnParams params_of(const ResidualNormArgs& a, const gs_rows& x, const gs_rows& y
     return p;
 }
 
-// whole 16-byte words: eight values a thread lie side by side (rows of the weights too)
+// whole 16-byte words: a thread's values lie side by side (of weights and gates too)
 bool whole_words(int width, std::initializer_list<NormRows> arrays) {
-    if (width % kPer) return false;
+    if (width % 8) return false;
     for (const NormRows& r : arrays)
         if (reinterpret_cast<uintptr_t>(r.p) % 16 || (r.p && r.stride % 16)) return false;
     return true;
 }
 
-template <typename T, bool kVec>
-cudaError_t launch_fwd(const RnParams& p, int blocks, cudaStream_t st) {
+template <typename T, bool kVec, int kPairs, int kThreads>
+cudaError_t launch_fwd_of(const RnParams& p, int blocks, cudaStream_t st) {
     const bool layer = p.pre == GS_NORM_LAYER || p.post == GS_NORM_LAYER;
-    return launch(layer ? residual_norm_kernel<T, kVec, true> : residual_norm_kernel<T, kVec, false>,
-                  dim3((unsigned)blocks), dim3((unsigned)warps_of(p.width) * 32), 0, st, p);
+    return launch(layer ? residual_norm_kernel<T, kVec, kPairs, true, kThreads>
+                        : residual_norm_kernel<T, kVec, kPairs, false, kThreads>,
+                  dim3((unsigned)blocks), dim3((unsigned)warps_of(p.width, kVec) * 32), 0, st, p);
+}
+
+template <typename T, bool kVec>
+cudaError_t launch_fwd(const RnParams& p, cudaStream_t st) {
+    const int blocks = (int)std::min(p.tokens, most_blocks(p.width, kVec, kFwdWarps));
+    if constexpr (!kVec)
+        if (pairs_of(p.width, kVec) == 2) return launch_fwd_of<T, kVec, 2, 512>(p, blocks, st);
+    return launch_fwd_of<T, kVec, 4, kMostThreads>(p, blocks, st);
+}
+
+template <typename T, bool kVec, int kPairs, int kThreads>
+cudaError_t launch_bwd_of(const RnParams& p, bool bias, int blocks, cudaStream_t st) {
+    const bool layer = p.pre == GS_NORM_LAYER || p.post == GS_NORM_LAYER;
+    void (*kernel)(const RnParams);
+    if (layer)
+        kernel = bias ? residual_norm_bwd_kernel<T, kVec, kPairs, true, true, kThreads>
+                      : residual_norm_bwd_kernel<T, kVec, kPairs, true, false, kThreads>;
+    else
+        kernel = bias ? residual_norm_bwd_kernel<T, kVec, kPairs, false, true, kThreads>
+                      : residual_norm_bwd_kernel<T, kVec, kPairs, false, false, kThreads>;
+    return launch(kernel, dim3((unsigned)blocks), dim3((unsigned)warps_of(p.width, kVec) * 32), 0, st,
+                  p);
 }
 
 // Up to 4,096 values a row its threads may have 128 registers each; beyond, 64 and spills.
 template <typename T, bool kVec>
 cudaError_t launch_bwd(const RnParams& p, bool bias, int blocks, cudaStream_t st) {
-    const unsigned threads = (unsigned)warps_of(p.width) * 32;
-    const bool layer = p.pre == GS_NORM_LAYER || p.post == GS_NORM_LAYER;
-    void (*kernel)(const RnParams);
-    if (threads > 512)
-        kernel = residual_norm_bwd_kernel<T, kVec, true, true, kMostThreads>;
-    else if (layer)
-        kernel = bias ? residual_norm_bwd_kernel<T, kVec, true, true, 512>
-                      : residual_norm_bwd_kernel<T, kVec, true, false, 512>;
-    else
-        kernel = bias ? residual_norm_bwd_kernel<T, kVec, false, true, 512>
-                      : residual_norm_bwd_kernel<T, kVec, false, false, 512>;
-    return launch(kernel, dim3((unsigned)blocks), dim3(threads), 0, st, p);
+    if constexpr (!kVec)
+        if (pairs_of(p.width, kVec) == 2) return launch_bwd_of<T, kVec, 2, 512>(p, bias, blocks, st);
+    if (warps_of(p.width, kVec) <= 16) return launch_bwd_of<T, kVec, 4, 512>(p, bias, blocks, st);
+    return launch(residual_norm_bwd_kernel<T, kVec, 4, true, true, kMostThreads>,
+                  dim3((unsigned)blocks), dim3((unsigned)warps_of(p.width, kVec) * 32), 0, st, p);
 }
 
 }  // namespace
 
 size_t residual_norm_workspace_bytes(int width) {
-    const size_t blocks = (size_t)kSms * std::max(1, kBwdWarps / warps_of(width));
-    return blocks * 6 * width * sizeof(float) + 16;
+    const int64_t blocks = std::max(most_blocks(width, true, kBwdWarps),  // whatever the strides
+                                    most_blocks(width, false, kBwdWarps));
+    return (size_t)blocks * 6 * width * sizeof(float) + 16;
 }
 
 cudaError_t launch_residual_norm(const ResidualNormArgs& a, const gs_rows& x, const gs_rows& y,
@@ -655,11 +760,9 @@ cudaError_t launch_residual_norm(const ResidualNormArgs& a, const gs_rows& x, co
     p.r = rows_of(r, size);
     p.h = rows_of(h, size);
     const bool vec = whole_words(a.width, {p.x, p.y, p.r, p.h});
-    const int blocks = blocks_of(a.tokens, a.width, kFwdWarps);
     if (a.bf16)
-        return vec ? launch_fwd<__nv_bfloat16, true>(p, blocks, st)
-                   : launch_fwd<__nv_bfloat16, false>(p, blocks, st);
-    return vec ? launch_fwd<float, true>(p, blocks, st) : launch_fwd<float, false>(p, blocks, st);
+        return vec ? launch_fwd<__nv_bfloat16, true>(p, st) : launch_fwd<__nv_bfloat16, false>(p, st);
+    return vec ? launch_fwd<float, true>(p, st) : launch_fwd<float, false>(p, st);
 }
 
 cudaError_t launch_residual_norm_bwd(const ResidualNormArgs& a, const gs_rows& x, const gs_rows& y,
@@ -673,10 +776,10 @@ cudaError_t launch_residual_norm_bwd(const ResidualNormArgs& a, const gs_rows& x
     p.dx = rows_of(dx, size);
     p.dy = rows_of(dy, size);
     p.dgate = g.gate;
-    const int blocks = blocks_of(a.tokens, a.width, kBwdWarps);
+    const bool vec = whole_words(a.width, {p.x, p.y, p.dr, p.dh, p.dx, p.dy});
+    const int blocks = (int)std::min(a.tokens, most_blocks(a.width, vec, kBwdWarps));
     p.part = static_cast<float*>(ws);
     p.part_gate = p.part + ((int64_t)blocks * 4 * a.width + 3) / 4 * 4;
-    const bool vec = whole_words(a.width, {p.x, p.y, p.dr, p.dh, p.dx, p.dy});
     const bool bias = p.pb || p.qb || g.pre_bias || g.post_bias;
     cudaError_t e = cudaSuccess;
     if (a.tokens > 0 && a.bf16)
