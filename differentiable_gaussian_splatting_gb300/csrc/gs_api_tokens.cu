@@ -192,6 +192,9 @@ gs_status attention_fwd(const gs_attention_shape* shape, const gs_window* window
                    nk = normal(k, s.tokens_k, s.heads_k, s.head_dim),
                    nv = normal(v, s.tokens_k, s.heads_k, s.head_dim),
                    no = normal(out, s.tokens_q, s.heads_q, s.head_dim);
+    if (window && few_queries(s))
+        return status_of(launch_attention_tokens(s, *window, nq, nk, nv, no, lse, cu_q, cu_k,
+                                                 (cudaStream_t)stream));
     return status_of(window ? launch_attention_window_fwd(s, *window, nq, nk, nv, no, lse, cu_q, cu_k,
                                                           workspace, (cudaStream_t)stream)
                             : launch_attention_fwd(s, nq, nk, nv, no, lse, cu_q, cu_k, workspace,

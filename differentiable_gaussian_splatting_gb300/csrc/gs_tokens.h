@@ -58,6 +58,11 @@ size_t attention_window_fwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, 
 size_t attention_window_bwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch,
                                             int heads_q, int heads_k, int head_dim,
                                             const gs_window& window);
+bool few_queries(const gs_attention_shape& s);
+cudaError_t launch_attention_tokens(const gs_attention_shape& s, const gs_window& window,
+                                    const gs_heads& q, const gs_heads& k, const gs_heads& v,
+                                    const gs_heads& out, float* lse, const int32_t* cu_q,
+                                    const int32_t* cu_k, cudaStream_t st);
 cudaError_t launch_attention_window_fwd(const gs_attention_shape& s, const gs_window& window,
                                         const gs_heads& q, const gs_heads& k, const gs_heads& v,
                                         const gs_heads& out, float* lse, const int32_t* cu_q,

@@ -160,6 +160,32 @@ def test_window_long_and_many(lens, hq, hk, D, window, causal):
             assert bool((a == b).all())
 
 
+@pytest.mark.parametrize("D", [8, 24, 32, 40, 64, 72, 96, 104, 128])
+@pytest.mark.parametrize("hq,hk", [(1, 1), (6, 2), (8, 1), (17, 1), (12, 4), (9, 9)])
+def test_window_of_single_tokens(D, hq, hk):
+    # one or two queries a sequence; keys none, few, and several steps of every warp
+    lens_q, lens_k = [1, 1, 0, 2, 1, 1, 2, 1], [700, 1, 50, 333, 0, 17, 1, 4100]
+    rng, q, k, v = _inputs(sum(lens_q), sum(lens_k), hq, hk, D, seed=D + hq)
+    ramp = np.concatenate([np.linspace(0.1, 1.0, max(n, 1))[:n] for n in lens_k])
+    k = bf16(k * ramp[:, None, None] * 1.9)  # maxima that keep rising
+    for window, causal in (((255, 0, 4), True), ((4096, 0, 0), True), ((0, 0, 128), False),
+                           ((130, 7, 16), False)):
+        _check(q, k, v, D ** -0.5, window, causal, lens_q, lens_k)
+    _check(q, k, v, -0.3 * D ** -0.5, (1000, 0, 4), True, lens_q, lens_k, poison=True)
+
+
+@pytest.mark.parametrize("batch", [1, 2, 31, 33, 1100])
+def test_window_of_single_tokens_in_many_sequences(batch):
+    # the search for a token's sequence, sequences without queries among them
+    rng = np.random.default_rng(batch)
+    lens_q, lens_k = list(rng.integers(0, 3, batch)), list(rng.integers(0, 40, batch))
+    lens_q[-1] = 1
+    while sum(lens_q) > 2 * batch:
+        lens_q[int(np.argmax(lens_q))] -= 1
+    _, q, k, v = _inputs(sum(lens_q), sum(lens_k), 4, 2, 64, seed=batch)
+    _check(q, k, v, 0.125, (9, 0, 2), True, lens_q, lens_k)
+
+
 def test_window_as_wide_as_all_equals_full_attention():
     import torch
 
