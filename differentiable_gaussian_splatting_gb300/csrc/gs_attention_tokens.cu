@@ -327,13 +327,12 @@ cudaError_t launch_attention_tokens(const gs_attention_shape& s, const gs_window
     p.o = view(out);
     p.lse = lse;
     const int64_t items = s.tokens_q * s.heads_k * p.parts;
-    // blocks enough for two an SM, as long as every warp has keys
+    // as many blocks as run at once, two an SM, as long as every warp has keys
     const int64_t keys =
         std::min<int64_t>(s.tokens_k, (int64_t)window.left + window.right + 1 + window.sinks);
-    p.splits = 1;
-    while (p.splits < kMostSplits && items * p.splits < 2 * kSms &&
-           p.splits * kTokenWarps * kStep < keys)
-        p.splits *= 2;
+    p.splits = (int)std::max<int64_t>(
+        1, std::min<int64_t>({kMostSplits, 2 * kSms / std::max<int64_t>(items, 1),
+                              (keys + kTokenWarps * kStep - 1) / (kTokenWarps * kStep)}));
     switch ((s.head_dim + 31) / 32) {
         case 1: return launch_words<1>(p, items, st);
         case 2: return launch_words<2>(p, items, st);
