@@ -94,6 +94,7 @@ struct BwdParams {
     int sink_rows;
     int64_t sink_blocks;
     float* parts_s;
+    unsigned int* next_dq;  // the next block of queries, counted from 0
 };
 
 // A sequence's first slot: there are sink_slots of them, and of sequences with more than `rows`
@@ -234,6 +235,7 @@ __global__ void __launch_bounds__(kDeltaThreads) attention_delta_kernel(const Bw
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (p.next_dq && blockIdx.x == 0 && threadIdx.x == 0) *p.next_dq = 0;
     if (t < p.batch.tq && lane == 0) {
         const float l = p.lse[h * p.batch.tq + t];
         p.nlse[h * p.batch.tq + t] = l == -INFINITY ? l : l * -1.4426950408889634f;
@@ -280,6 +282,59 @@ __device__ __forceinline__ void store_row(uint32_t at, __nv_bfloat16* out, float
                 *reinterpret_cast<uint4*>(out + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
+    }
+}
+
+// The same of a warp's 32 rows together, to rows first..end - 1 of them (with a window, whose blocks
+// are short: a row a lane, a store took 16 bytes of 32 rows, and a block's stores 2,000 clocks).  Four
+// lanes exchange their rows' 16-byte words, so that a store takes 64 bytes of eight rows.
+// `out`, `part`: of the warp's first row; rows of `part` lie kStride apart.
+template <int kDim, int kStride>
+__device__ __forceinline__ void store_rows(uint32_t at, __nv_bfloat16* out, int64_t ts, float* part,
+                                           int first, int end, int dim, float f, bool zero) {
+    const unsigned all = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
+    const int row0 = lane & ~3, col0 = (lane & 3) * 8;
+#pragma unroll
+    for (int c = 0; c < kDim; c += 32) {
+        uint32_t o[32];
+        if (!zero) {
+            tmem_ld32(o, at + c);
+            tmem_wait_ld();
+        }
+        if (part) {
+            if (lane >= first && lane < end)
+#pragma unroll
+                for (int k = 0; k < 32; k += 4)
+                    *reinterpret_cast<uint4*>(part + lane * kStride + c + k) =
+                        zero ? make_uint4(0, 0, 0, 0)
+                             : make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            continue;
+        }
+        uint32_t w[4][4];  // words of the lane's row, then the lane's words of four rows
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            w[k >> 2][k & 3] = zero ? 0u
+                                    : pack_bf16(__uint_as_float(o[2 * k]) * f,
+                                                __uint_as_float(o[2 * k + 1]) * f);
+#pragma unroll
+        for (int d = 2; d > 0; d >>= 1)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (!(k & d))
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const bool upper = lane & d;
+                        const uint32_t got =
+                            __shfl_xor_sync(all, upper ? w[k][e] : w[k + d][e], d);
+                        (upper ? w[k][e] : w[k + d][e]) = got;
+                    }
+        if (c + col0 < dim)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (row0 + k >= first && row0 + k < end)
+                    *reinterpret_cast<uint4*>(out + (row0 + k) * ts + c + col0) =
+                        make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
     }
 }
 
@@ -581,17 +636,27 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
         if (!any_dead(&dead)) {
             tmem_fence_after();
             const int key = work.row0 + r;
-            const bool valid = kWindow ? r >= work.key_first && r < work.key_end : key < work.sq.m;
             const bool split = work.part >= 0;
             const HeadView& g = half ? p.dk : p.dv;
-            __nv_bfloat16* out = valid && !split ? g.row(work.sq.k0 + key, work.khead) : nullptr;
-            float* part = nullptr;
-            if (valid && split)
-                part = kSinks ? p.parts_s + (work.part + r + (half ? 0 : p.window.sinks)) * DP
-                              : p.parts_k +
-                                    (work.part + r + (half ? 0 : part_rows(p.plan_k))) * DP;
-            store_row<DP>((half ? t_dk : t_dv) + lanes, out, part, p.dim, half ? p.scale : 1.f,
-                          items == 0);
+            if constexpr (kWindow) {
+                const int row = (warp & 3) * 32;  // the warp's first
+                float* parts = kSinks ? p.parts_s + (work.part + row + (half ? 0 : p.window.sinks)) * DP
+                                      : p.parts_k + (work.part + row +
+                                                     (half ? 0 : part_rows(p.plan_k))) * DP;
+                store_rows<DP, DP>((half ? t_dk : t_dv) + lanes,
+                                   g.row(work.sq.k0 + work.row0 + row, work.khead), g.ts,
+                                   split ? parts : nullptr, work.key_first - row, work.key_end - row,
+                                   p.dim, half ? p.scale : 1.f, items == 0);
+            } else {
+                const bool valid = key < work.sq.m;
+                __nv_bfloat16* out =
+                    valid && !split ? g.row(work.sq.k0 + key, work.khead) : nullptr;
+                float* part = valid && split ? p.parts_k + (work.part + r +
+                                                            (half ? 0 : part_rows(p.plan_k))) * DP
+                                             : nullptr;
+                store_row<DP>((half ? t_dk : t_dv) + lanes, out, part, p.dim, half ? p.scale : 1.f,
+                              items == 0);
+            }
         }
     }
     tmem_fence_before();
@@ -615,7 +680,7 @@ struct DqShape {
     static constexpr uint32_t kSmem = (2 + kSlotsK + kSlotsV) * kTileBytes + 1024;
 };
 
-template <int DP, bool kWindow>
+template <int DP>
 __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtensorMap& map_k,
                                          const CUtensorMap& map_v, const CUtensorMap& map_d,
                                          const BwdParams& p, int64_t id) {
@@ -632,7 +697,7 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
-        const bool ok = find_work<false, kWindow>(p, id, &work);
+        const bool ok = find_work<false, false>(p, id, &work);
         if (lane == 0) found = ok, dead = 0;
     }
     __syncthreads();
@@ -669,9 +734,8 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
 
     if (tiles > 0 && warp == kMathWarps + 1) {
         // ---- the producer ----
-        const int khead = work.khead;
-        const int left = work.sq.m - (kWindow ? 0 : work.first * kTileRows);
-        const int64_t k0 = work.sq.k0 + (kWindow ? 0 : (int64_t)work.first * kTileRows);
+        const int khead = work.khead, left = work.sq.m - work.first * kTileRows;
+        const int64_t k0 = work.sq.k0 + (int64_t)work.first * kTileRows;
         const bool tail = work.sq.k0 + work.sq.m < p.batch.tk;
         if (elect_one()) {
             const int64_t q = work.sq.q0 + work.row0;
@@ -686,11 +750,10 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
         for (int j = 0; j < tiles; ++j) {
             const int sk = j % Sh::kSlotsK, uk = j / Sh::kSlotsK;
             const int sv = j % Sh::kSlotsV, uv = j / Sh::kSlotsV;
-            const int tile = kWindow ? work.walk.tile(work.first + j) : j;
-            const int64_t token = k0 + (int64_t)tile * kTileRows;
+            const int64_t token = k0 + (int64_t)j * kTileRows;
             if (uk > 0) ok = mbar_wait(smem_u32(&empty_k[sk]), (uk - 1) & 1, &dead);
             if (!ok) break;
-            const int valid = left - tile * kTileRows;
+            const int valid = left - j * kTileRows;
             const bool mend = valid < kTileRows && tail;
             const uint32_t full = smem_u32(&full_k[sk]), dst = at_k + sk * Sh::kTileBytes;
             const uint32_t bar = mend ? smem_u32(&bar_raw) : full;
@@ -787,18 +850,7 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
             return seen_keys(work.row0 + row, work.sq.n, work.sq.m, p.batch.causal) -
                    work.first * kTileRows;
         };
-        const int limit = kWindow ? 0 : limit_of(r);
-        const int first_limit = kWindow ? 0 : limit_of((warp & 3) * 32);
-        // with a window: what the row sees, the end of the warp's first row's keys and the start of
-        // its last one's
-        Seen see{};
-        int first_hi = 0, last_lo = 0;
-        if constexpr (kWindow) {
-            const int row = work.row0 + (warp & 3) * 32;
-            see = seen_by(p.window, row + lane, work.sq.n, work.sq.m);
-            first_hi = seen_by(p.window, row, work.sq.n, work.sq.m).hi;
-            last_lo = seen_by(p.window, row + 31, work.sq.n, work.sq.m).lo;
-        }
+        const int limit = limit_of(r), first_limit = limit_of((warp & 3) * 32);
         float nl = -INFINITY, nd = 0.f;
         if (work.row0 + r < work.sq.n) {
             const int64_t at = (int64_t)work.head * p.batch.tq + work.sq.q0 + work.row0 + r;
@@ -836,16 +888,7 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
                 dp[c] = a.x;
                 dp[c + 1] = a.y;
             }
-            if constexpr (kWindow) {
-                const int key = work.walk.tile(work.first + j) * kTileRows;
-                if (key + kTileRows > first_hi || key < last_lo) {
-#pragma unroll
-                    for (int c = 0; c < 64; c += 32) {
-                        const int at = key + half * 64 + c;
-                        mask_by_bits(dp + c, seen_bits(see.lo - at, see.hi - at, see.sinks - at), 0.f);
-                    }
-                }
-            } else if ((j + 1) * kTileRows > first_limit) {
+            if ((j + 1) * kTileRows > first_limit) {
                 const int left = limit - j * kTileRows - half * 64;
 #pragma unroll
                 for (int c = 0; c < 64; ++c)
@@ -880,9 +923,18 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
     }
 }
 
-// The blocks of keys, with a window those of the sinks first, then those of queries.
+}  // namespace
+}  // namespace gs
+
+#include "gs_attention_window_dq.cuh"
+
+namespace gs {
+namespace {
+
+// The blocks of keys, then those of queries; with a window those of the sinks first, and for the
+// queries CTAs that go through their blocks.
 template <int DP, bool kWindow>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(kWindow ? kWindowBwdThreads : kBwdThreads, 1)
     attention_bwd_kernel(const __grid_constant__ CUtensorMap map_q,
                          const __grid_constant__ CUtensorMap map_k,
                          const __grid_constant__ CUtensorMap map_v,
@@ -899,8 +951,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     if (id < of_keys)
         dkv_block<DP, kWindow, false>(map_q, map_k, map_v, map_d, p, id);
+    else if constexpr (kWindow)
+        window_dq_blocks<DP>(map_q, map_k, map_v, map_d, p);
     else
-        dq_block<DP, kWindow>(map_q, map_k, map_v, map_d, p, id - of_keys);
+        dq_block<DP>(map_q, map_k, map_v, map_d, p, id - of_keys);
 }
 
 // The sum of a cut block's pieces, in their order, times the scale, in bfloat16.  DP / 4
@@ -1086,10 +1140,12 @@ cudaError_t launch_dim(const BwdMaps& m, BwdParams p, const gs_window* w, cudaSt
     constexpr uint32_t kSmem = std::max(DkvShape<DP>::kSmem, DqShape<DP>::kSmem);
     cudaError_t e = cudaFuncSetAttribute(
         attention_bwd_kernel<DP, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    const int64_t of_q = blocks_of(p.plan_q);
     if (e == cudaSuccess)
         e = launch(attention_bwd_kernel<DP, kWindow>,
-                   dim3((unsigned)(p.sink_blocks + blocks_of(p.plan_k) + blocks_of(p.plan_q))),
-                   dim3(kBwdThreads), kSmem, st, m.q, m.k, m.v, m.d, p);
+                   dim3((unsigned)(p.sink_blocks + blocks_of(p.plan_k) +
+                                   (kWindow ? std::min<int64_t>(of_q, kSms) : of_q))),
+                   dim3(kWindow ? kWindowBwdThreads : kBwdThreads), kSmem, st, m.q, m.k, m.v, m.d, p);
     if (e == cudaSuccess) e = launch_sum<DP, true, kWindow>(p, st);
     if (e == cudaSuccess) e = launch_sum<DP, false, kWindow>(p, st);
     if constexpr (kWindow)
@@ -1107,7 +1163,8 @@ HeadView view(const gs_heads& h) {
 
 }  // namespace
 
-// -lse and -delta of every query row, then the pieces of both kinds of blocks
+// -lse and -delta of every query row, then (with a window) the counter, then the pieces of both kinds
+// of blocks
 size_t attention_bwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads_q,
                                      int heads_k, int head_dim) {
     int64_t rows = 0;
@@ -1128,7 +1185,7 @@ size_t attention_window_bwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, 
     const int64_t rows =
         2 * part_rows(plan_dkv(tokens_q, tokens_k, batch, heads_q, heads_k, false, width)) +
         part_rows(plan_dq(tokens_q, tokens_k, batch, heads_q, false, width));
-    return ((size_t)tokens_q * heads_q * 2 * sizeof(float) + 255) / 256 * 256 +
+    return ((size_t)tokens_q * heads_q * 2 * sizeof(float) + 255) / 256 * 256 + 256 +
            (size_t)(rows * dp + sink_floats(w, tokens_q, heads_k, (int)dp)) * sizeof(float);
 }
 
@@ -1156,6 +1213,10 @@ cudaError_t launch_attention_bwd(const gs_attention_shape& s, const gs_heads& q,
     p.nlse = static_cast<float*>(ws);
     p.ndelta = p.nlse + s.tokens_q * s.heads_q;
     p.parts_k = p.nlse + (s.tokens_q * s.heads_q * 2 + 63) / 64 * 64;
+    if (window) {
+        p.next_dq = reinterpret_cast<unsigned int*>(p.parts_k);
+        p.parts_k += 64;
+    }
     cudaError_t e = gave_up_word(&p.gave_up);
     if (e != cudaSuccess) return e;
     BwdMaps m;
