@@ -501,6 +501,8 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                 const auto bar_of = [&](const Cursor& c) {
                     return c.t == 0 ? c.bar0 : Sh::kScores + c.bar1;
                 };
+                            // whether no step before took the key tile: it may still be on its way
+                const auto first_of_tile = [&](const Cursor& c) { return c.t == 0 || c.j >= c.end0; };
                 const auto move = [&](Cursor& c) {  // true: the key tile is left
                     if (++c.score == Sh::kScores) c.score = 0;
                     if (c.t == 0) {
@@ -525,7 +527,8 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                 int turn_q[2] = {0, 0};
                 const auto scores = [&]() {  // false: there are no more
                     if (!ahead.in && !enter(ahead)) return false;
-                    ok = ok && mbar_wait_one(smem_u32(&bar_full[ahead.slot]), ahead.phase, &dead);
+                    if (first_of_tile(ahead))
+                        ok = ok && mbar_wait_one(smem_u32(&bar_full[ahead.slot]), ahead.phase, &dead);
                     if (ahead.t == 0 ? !ahead.begun0 : !ahead.begun1) {
                         ok = ok && mbar_wait_one(smem_u32(&bar_q[ahead.t]), turn_q[ahead.t], &dead);
                         turn_q[ahead.t] ^= 1;
@@ -544,7 +547,9 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                 for (int k = 0; k < Sh::kScores && scores(); ++k) {
                 }
                 while (ok && (at.in || enter(at))) {
-                    ok = mbar_wait_one(smem_u32(&bar_full[at.slot + 1]), at.phase, &dead) &&
+                    if (first_of_tile(at))
+                        ok = mbar_wait_one(smem_u32(&bar_full[at.slot + 1]), at.phase, &dead);
+                    ok = ok &&
                          mbar_wait_one(smem_u32(&bar_p[bar_of(at)]), at.t == 0 ? at.turn0 : at.turn1,
                                        &dead);
                     if (!ok) break;
