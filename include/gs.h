@@ -689,8 +689,9 @@ gs_status gs_residual_norm_bwd(int64_t tokens, int32_t width, const gs_block_nor
  *   count      0..65536 arrays of at most 2^40 elements each, 2^42 in all
  *   grads      host array: device data (aligned to an element; at 16 bytes it goes faster, NULL
  *              where elements = 0), elements, and type
- *   outs       host array of the same elements and types; an out may be its gradient itself.  NULL:
- *              all are, and where norm <= max_norm nothing is written
+ *   outs       host array of the same elements and types; an out may be its gradient itself, but
+ *              overlaps nothing else (no array is given twice).  NULL: all are their gradients.
+ *              Where norm <= max_norm, such outs are not written
  *   max_norm   >= 0; infinity: the norm alone is wanted, outs as grads (NULL: nothing is written)
  *   norm       out, device float: the norm before clipping
  *   workspace  >= gs_clip_grad_norm_workspace_bytes(count); holds nothing between calls
