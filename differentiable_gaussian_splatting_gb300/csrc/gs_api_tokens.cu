@@ -324,6 +324,7 @@ gs_status gs_dropout_add_bwd(int64_t n, int32_t type, const void* dout, void* dx
 namespace {
 
 constexpr int32_t kMaxWidth = 8192;
+constexpr int64_t kMaxRowStride = int64_t(1) << 29;  // elements: bytes stay in 32 bits
 constexpr int32_t kMaxArrays = 65536;
 
 bool aligned(const void* p, int size) { return reinterpret_cast<uintptr_t>(p) % size == 0; }
@@ -332,7 +333,7 @@ bool aligned(const void* p, int size) { return reinterpret_cast<uintptr_t>(p) % 
 bool rows_ok(const gs_rows* r, int64_t tokens, int width, int size, bool optional) {
     if (!r || !r->data) return optional || tokens == 0;
     return aligned(r->data, size) &&
-           (tokens <= 1 || (r->row_stride >= width && r->row_stride <= kMaxStride));
+           (tokens <= 1 || (r->row_stride >= width && r->row_stride <= kMaxRowStride));
 }
 
 // with a missing array's pointer null, and the stride of a single row set to something valid

@@ -15,9 +15,9 @@
 //
 // Memory bounds it: four arrays forward, six backward.  A row is one block's, eight values a thread
 // held in registers from the first sum over the row to the last, so nothing is read twice; a row
-// of at most 256 values is one warp's and its sums need no barrier.  Weights and gates come
-// from L1 for every row: in registers they would take half of the warps' room.  A block has
-// consecutive rows, reads the next one while it works on the present one, and keeps sums of the
+// of at most 256 values is one warp's and its sums need no barrier.  Weights and gates stay in
+// registers, the gate multiplied into post's weight and bias: read from L1 for every row they kept
+// L1 busier than the arrays did.  A block has consecutive rows, reads the next one while it works on the present one, and keeps sums of the
 // column gradients in registers: of the weights and biases over all its rows, of the gate over
 // those of a sequence.  Other kernels add the blocks' sums up in the blocks' order: the same
 // inputs give the same bits.
@@ -45,7 +45,11 @@ constexpr int kMostGates = 256;     // sequences at once when the gates' gradien
 
 struct NormRows {
     char* p;
-    int64_t stride;  // bytes
+    uint32_t stride;  // bytes
+    // byte `shift` of a row: one multiplication instead of a pointer and a stride in registers
+    __device__ __forceinline__ char* at(uint32_t row, int shift) const {
+        return p + (uint64_t)row * stride + shift;
+    }
 };
 
 struct RnParams {
@@ -304,15 +308,6 @@ __device__ __forceinline__ void centre(Values<kPairs>& a, const Columns<kVec, kP
     c.trim(a);
 }
 
-// Rows one after the other, from column `first` on.
-struct Walk {
-    char* p;
-    int64_t stride;
-    __device__ __forceinline__ Walk(const NormRows& r, int64_t row, int bytes)
-        : p(r.p ? r.p + row * r.stride + bytes : nullptr), stride(r.p ? r.stride : 0) {}
-    __device__ __forceinline__ void next() { p += stride; }
-};
-
 // The rows of block k of `blocks`, and the sequence of a token: consecutive.
 __host__ __device__ __forceinline__ int64_t first_row(int64_t tokens, int64_t blocks, int64_t k) {
     return tokens * k / blocks;
@@ -342,12 +337,27 @@ __device__ __forceinline__ Part part_of(const RnParams& p, int64_t t) {
     return {lo, offset(p, lo), offset(p, lo + 1)};
 }
 
+// beta gate times post's weight and bias, of sequence b (the first one's where none holds the row)
+template <bool kVec, int kPairs>
+__device__ __forceinline__ void mix_of(const RnParams& p, const Columns<kVec, kPairs>& c, int b,
+                                       Values<kPairs>* factor, Values<kPairs>* rest) {
+    const Values<kPairs> g =
+        c.weights(p.gate ? p.gate + (int64_t)max(b, 0) * p.width : nullptr, 1.f);
+    const Values<kPairs> w = c.weights(p.qw, 1.f);
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) factor->v[k] = mul(mul(both(p.beta), g.v[k]), w.v[k]);
+    if (!rest) return;
+    const Values<kPairs> bias = c.weights(p.qb, 0.f);
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) rest->v[k] = mul(mul(both(p.beta), g.v[k]), bias.v[k]);
+}
+
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
 // kLayer: one of the norms is a layer norm.  Without, the mean square of the next row's y is formed
 // with a sum of this row.
-template <typename T, bool kVec, int kPairs, bool kLayer, int kThreads>
+template <typename T, bool kVec, int kPairs, bool kLayer, bool kBias, int kThreads>
 __global__ void __launch_bounds__(kThreads) residual_norm_kernel(const RnParams p) {
     grid_dep_sync();
     using V = Values<kPairs>;
@@ -358,30 +368,29 @@ __global__ void __launch_bounds__(kThreads) residual_norm_kernel(const RnParams 
     const int64_t end = first_row(p.tokens, gridDim.x, blockIdx.x + 1);
     int64_t t = first_row(p.tokens, gridDim.x, blockIdx.x);
     Part at{0, 0, 0};
-    const float* gate = nullptr;  // the sequence's
+    // pre's weight and bias; the factor and the rest of un in r, those of the row's sequence
+    const V pw = c.weights(p.pw, 1.f);
+    V pb{}, factor{}, rest{};
+    if (kBias) pb = c.weights(p.pb, 0.f);
     const int shift = c.first * (int)sizeof(T);
-    Walk in_x(p.x, t, shift), in_y(p.y, t, shift), out_r(p.r, t, shift), out_h(p.h, t, shift);
     Row x, y;
     x.clear();
     y.clear();
-    const auto load = [&]() {  // the next row
-        if (c.n > 0) {
-            x.load(in_x.p, c);
-            if (p.y.p) y.load(in_y.p, c);
-        }
-        in_x.next();
-        in_y.next();
+    const auto load = [&](uint32_t row) {
+        if (c.n == 0) return;
+        x.load(p.x.at(row, shift), c);
+        if (p.y.p) y.load(p.y.at(row, shift), c);
     };
-    load();
+    load((uint32_t)t);
     const bool ahead = !kLayer && p.post != GS_NORM_NONE && p.pre != GS_NORM_NONE;
     float square = 0.f;  // mean of y^2 where it is formed ahead
     if (ahead) square = sums.mean(dot(y.get(), y.get()));
     for (; t < end; ++t) {
         V v = x.get(), u = y.get();
-        if (t + 1 < end) load();
+        if (t + 1 < end) load((uint32_t)t + 1);
         if (t >= at.end) {
             at = part_of(p, t);
-            if (p.gate) gate = p.gate + (int64_t)max(at.b, 0) * p.width;
+            mix_of(p, c, at.b, &factor, kBias ? &rest : nullptr);
         }
         if (p.post != GS_NORM_NONE) {
             if (kLayer && p.post == GS_NORM_LAYER) centre(u, c, sums);
@@ -390,15 +399,11 @@ __global__ void __launch_bounds__(kThreads) residual_norm_kernel(const RnParams 
 #pragma unroll
             for (int k = 0; k < kPairs; ++k) u.v[k] = mul(u.v[k], f);
         }
-        {
-            const V g = c.weights(gate, 1.f), a = c.weights(p.qw, 1.f), b = c.weights(p.qb, 0.f);
 #pragma unroll
-            for (int k = 0; k < kPairs; ++k)
-                v.v[k] = fma2(both(p.alpha), v.v[k],
-                              mul(mul(both(p.beta), g.v[k]), fma2(u.v[k], a.v[k], b.v[k])));
-        }
-        if (p.r.p && at.b >= 0) Row::store(out_r.p, v, c);
-        out_r.next();
+        for (int k = 0; k < kPairs; ++k)
+            v.v[k] = fma2(both(p.alpha), v.v[k],
+                          kBias ? fma2(u.v[k], factor.v[k], rest.v[k]) : mul(u.v[k], factor.v[k]));
+        if (p.r.p && at.b >= 0) Row::store(p.r.at((uint32_t)t, shift), v, c);
         if (p.pre == GS_NORM_NONE) continue;
         c.trim(v);
         float s;
@@ -412,11 +417,10 @@ __global__ void __launch_bounds__(kThreads) residual_norm_kernel(const RnParams 
             s = sums.mean(dot(v, v));
         }
         const float2 f = both(rsqrtf(s + p.eps));
-        const V a = c.weights(p.pw, 1.f), b = c.weights(p.pb, 0.f);
 #pragma unroll
-        for (int k = 0; k < kPairs; ++k) v.v[k] = fma2(mul(v.v[k], f), a.v[k], b.v[k]);
-        if (at.b >= 0) Row::store(out_h.p, v, c);
-        out_h.next();
+        for (int k = 0; k < kPairs; ++k)
+            v.v[k] = kBias ? fma2(mul(v.v[k], f), pw.v[k], pb.v[k]) : mul(mul(v.v[k], f), pw.v[k]);
+        if (at.b >= 0) Row::store(p.h.at((uint32_t)t, shift), v, c);
     }
 }
 
@@ -440,41 +444,32 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
     Part at{-1, 0, 0};
     V dpw{}, dpb{}, dqw{}, dqb{};  // over all rows
     V su{}, s1{};                  // of dR un and of dR over the sequence's rows
-    const float* gate = nullptr;  // the sequence's
+    // pre's weight; the factor and the rest of un in r, those of the row's sequence
+    const V pw = c.weights(p.pw, 1.f);
+    V factor{}, rest{};
     const int shift = c.first * (int)sizeof(T);
-    Walk in_x(p.x, t, shift), in_y(p.y, t, shift), in_dr(p.dr, t, shift), in_dh(p.dh, t, shift),
-        out_x(p.dx, t, shift), out_y(p.dy, t, shift);
     Row x, y, dr, dh;
     x.clear();
     y.clear();
     dr.clear();
     dh.clear();
-    const auto load = [&]() {  // the next row
-        if (c.n > 0) {
-            x.load(in_x.p, c);
-            if (p.y.p) y.load(in_y.p, c);
-            if (p.dr.p) dr.load(in_dr.p, c);
-            if (p.dh.p) dh.load(in_dh.p, c);
-        }
-        in_x.next();
-        in_y.next();
-        in_dr.next();
-        in_dh.next();
-    };
-    const auto gate_of = [&]() {  // beta gate
-        V g = c.weights(gate, 1.f);
-#pragma unroll
-        for (int k = 0; k < kPairs; ++k) g.v[k] = mul(both(p.beta), g.v[k]);
-        return g;
+    const auto load = [&](uint32_t row) {
+        if (c.n == 0) return;
+        x.load(p.x.at(row, shift), c);
+        if (p.y.p) y.load(p.y.at(row, shift), c);
+        if (p.dr.p) dr.load(p.dr.at(row, shift), c);
+        if (p.dh.p) dh.load(p.dh.at(row, shift), c);
     };
     // the sequence's sums to those of all rows, and to its gate's gradient
     const auto leave = [&]() {
         if (at.b < 0) return;
-        const V g = gate_of(), a = c.weights(p.qw, 1.f);
+        V g = c.weights(p.gate ? p.gate + (int64_t)at.b * p.width : nullptr, 1.f);
+        const V a = c.weights(p.qw, 1.f);
         V b{}, d;
         if (kBias) b = c.weights(p.qb, 0.f);
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) {
+            g.v[k] = mul(both(p.beta), g.v[k]);
             dqw.v[k] = fma2(g.v[k], su.v[k], dqw.v[k]);
             d.v[k] = mul(a.v[k], su.v[k]);
             if (kBias) {
@@ -492,18 +487,18 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
         else
             c.store(p.part_gate + ((int64_t)blockIdx.x * 2 + (from_before ? 0 : 1)) * p.width, d);
     };
-    load();
+    load((uint32_t)t);
     const bool ahead = !kLayer && p.post != GS_NORM_NONE;
     float square = 0.f;  // mean of y^2 where it is formed ahead
     if (ahead) square = sums.mean(dot(y.get(), y.get()));
     for (; t < end; ++t) {
         V v = x.get(), u = y.get(), d = dr.get();
         const V g = dh.get();
-        if (t + 1 < end) load();
+        if (t + 1 < end) load((uint32_t)t + 1);
         if (t >= at.end) {
             leave();
             at = part_of(p, t);
-            if (p.gate) gate = p.gate + (int64_t)max(at.b, 0) * p.width;
+            mix_of(p, c, at.b, &factor, kBias ? &rest : nullptr);
         }
         // a row that no sequence holds is gone through like the others, but for the results
         const bool held = at.b >= 0;
@@ -516,21 +511,16 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
             for (int k = 0; k < kPairs; ++k) u.v[k] = mul(u.v[k], both(fu));  // un
         }
         if (p.pre != GS_NORM_NONE) {
-            {
-                const V bg = gate_of(), a = c.weights(p.qw, 1.f);
-                V b{};
-                if (kBias) b = c.weights(p.qb, 0.f);
 #pragma unroll
-                for (int k = 0; k < kPairs; ++k)
-                    v.v[k] = fma2(both(p.alpha), v.v[k],
-                                  mul(bg.v[k], kBias ? fma2(u.v[k], a.v[k], b.v[k])
-                                                     : mul(u.v[k], a.v[k])));
-            }
+            for (int k = 0; k < kPairs; ++k)
+                v.v[k] = fma2(both(p.alpha), v.v[k],
+                              kBias ? fma2(u.v[k], factor.v[k], rest.v[k])
+                                    : mul(u.v[k], factor.v[k]));
             c.trim(v);
             if (kLayer && p.pre == GS_NORM_LAYER) centre(v, c, sums);
-            V w = c.weights(p.pw, 1.f);
+            V w;
 #pragma unroll
-            for (int k = 0; k < kPairs; ++k) w.v[k] = mul(w.v[k], g.v[k]);
+            for (int k = 0; k < kPairs; ++k) w.v[k] = mul(pw.v[k], g.v[k]);
             const float4 s = sums.mean(dot(v, v), dot(w, v), kLayer ? total(w) : 0.f, 0.f);
             const float f = rsqrtf(s.x + p.eps);
             const float2 f2 = both(f), along = both(-s.y * f * f);
@@ -547,8 +537,7 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
         }
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) v.v[k] = mul(both(p.alpha), d.v[k]);
-        if (held) Row::store(out_x.p, v, c);
-        out_x.next();
+        if (held) Row::store(p.dx.at((uint32_t)t, shift), v, c);
         if (!p.y.p) continue;
         if (held)
 #pragma unroll
@@ -556,15 +545,9 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
                 su.v[k] = fma2(d.v[k], u.v[k], su.v[k]);
                 if (kBias) s1.v[k] = add(s1.v[k], d.v[k]);
             }
-        {
-            const V bg = gate_of();
 #pragma unroll
-            for (int k = 0; k < kPairs; ++k) d.v[k] = mul(d.v[k], bg.v[k]);
-        }
+        for (int k = 0; k < kPairs; ++k) d.v[k] = mul(d.v[k], factor.v[k]);
         if (p.post != GS_NORM_NONE) {
-            const V a = c.weights(p.qw, 1.f);
-#pragma unroll
-            for (int k = 0; k < kPairs; ++k) d.v[k] = mul(d.v[k], a.v[k]);
             c.trim(d);
             float4 s;
             if (ahead) {
@@ -581,8 +564,7 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
                 d.v[k] = mul(both(fu), fma2(u.v[k], along, d.v[k]));
             }
         }
-        if (held) Row::store(out_y.p, d, c);
-        out_y.next();
+        if (held) Row::store(p.dy.at((uint32_t)t, shift), d, c);
     }
     leave();
     float* part = p.part + (int64_t)blockIdx.x * 4 * p.width;
@@ -672,7 +654,7 @@ int64_t most_blocks(int width, bool vec, int resident_warps) {
 }
 
 NormRows rows_of(const gs_rows& r, int size) {
-    return {static_cast<char*>(r.data), r.row_stride * size};
+    return {static_cast<char*>(r.data), (uint32_t)(r.row_stride * size)};
 }
 
 RnParams params_of(const ResidualNormArgs& a, const gs_rows& x, const gs_rows& y) {
@@ -707,10 +689,16 @@ bool whole_words(int width, std::initializer_list<NormRows> arrays) {
 
 template <typename T, bool kVec, int kPairs, int kThreads>
 cudaError_t launch_fwd_of(const RnParams& p, int blocks, cudaStream_t st) {
-    const bool layer = p.pre == GS_NORM_LAYER || p.post == GS_NORM_LAYER;
-    return launch(layer ? residual_norm_kernel<T, kVec, kPairs, true, kThreads>
-                        : residual_norm_kernel<T, kVec, kPairs, false, kThreads>,
-                  dim3((unsigned)blocks), dim3((unsigned)warps_of(p.width, kVec) * 32), 0, st, p);
+    const bool layer = p.pre == GS_NORM_LAYER || p.post == GS_NORM_LAYER, bias = p.pb || p.qb;
+    void (*kernel)(const RnParams);
+    if (layer)
+        kernel = bias ? residual_norm_kernel<T, kVec, kPairs, true, true, kThreads>
+                      : residual_norm_kernel<T, kVec, kPairs, true, false, kThreads>;
+    else
+        kernel = bias ? residual_norm_kernel<T, kVec, kPairs, false, true, kThreads>
+                      : residual_norm_kernel<T, kVec, kPairs, false, false, kThreads>;
+    return launch(kernel, dim3((unsigned)blocks), dim3((unsigned)warps_of(p.width, kVec) * 32), 0, st,
+                  p);
 }
 
 template <typename T, bool kVec>

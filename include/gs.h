@@ -638,7 +638,7 @@ gs_status gs_dropout_add_bwd(int64_t n, int32_t type, const void* dout, void* dx
  *              which those of a norm that is not there must be
  *   workspace  >= gs_residual_norm_workspace_bytes(...); holds nothing between calls
  *
- * Rows may be those of a wider array (row_stride in elements, >= width); widths that are a multiple
+ * Rows may be those of a wider array (row_stride in elements, width..2^29); widths that are a multiple
  * of 8 in rows of whole 16-byte words go faster.  Outputs may be inputs (same data and stride),
  * but not overlap them otherwise, nor each other.  All sums are fp32.
  */

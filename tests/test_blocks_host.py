@@ -121,7 +121,7 @@ def test_residual_norm_arguments_are_checked_on_the_host(lib):
                dict(cu=P), dict(cu=MIS, w=params(gate=P)), dict(cu=P, w=params(gate=P), batch=1 << 21),
                dict(pre=0, w=params(pre_weight=P)), dict(pre=0), dict(post=0, w=params(post_bias=P)),
                dict(w=params(post_weight=MIS)), dict(w=params(gate=MIS)), dict(w=params(pre_bias=MIS)),
-               dict(x=none), dict(x=R(P + 1)), dict(x=R(s=63)), dict(y=none), dict(y=R(s=1 << 39)),
+               dict(x=none), dict(x=R(P + 1)), dict(x=R(s=63)), dict(y=none), dict(y=R(s=(1 << 29) + 1)),
                dict(y=none, post=0, w=params(gate=P)), dict(r=R(s=8)), dict(h=none), dict(h=R(P + 1)),
                dict(type=0, x=R(P + 2))):
         assert fwd(**kw) == 1, kw
