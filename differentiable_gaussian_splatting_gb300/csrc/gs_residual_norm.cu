@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
 }
 
 // The blocks' sums of a column: 32 threads take every 32nd block, and their sums are added in
-// order.  blockIdx.y: which of the four gradients, or behind them a sequence's gate (and every
+// pairs.  blockIdx.y: which of the four gradients, or behind them a sequence's gate (and every
 // gridDim.y - 4 th from it on): of those that several blocks met, and zeros for empty ones.
 constexpr int kFinishCols = 32, kFinishThreads = 1024, kFinishOf = kFinishThreads / kFinishCols;
 struct FourGradients {
@@ -587,14 +587,15 @@ __device__ __forceinline__ void sum_blocks(float (*s)[kFinishCols], const float*
     const int col = threadIdx.x % kFinishCols, row = threadIdx.x / kFinishCols;
     float a = 0.f;
     if (has)
-#pragma unroll 4
+#pragma unroll 8
         for (int b = row; b < count; b += kFinishOf) a += __ldg(part + (first + b) * step);
     s[row][col] = a;
-    __syncthreads();
-    if (row == 0 && has) {
-        for (int r = 1; r < kFinishOf; ++r) a += s[r][col];
-        *out = a;
+#pragma unroll
+    for (int o = kFinishOf / 2; o > 0; o >>= 1) {
+        __syncthreads();
+        if (row < o) s[row][col] += s[row + o][col];
     }
+    if (row == 0 && has) *out = s[0][col];
 }
 
 __global__ void __launch_bounds__(kFinishThreads)
