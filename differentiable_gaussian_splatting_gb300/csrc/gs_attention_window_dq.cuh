@@ -17,7 +17,11 @@ constexpr int kDqPlanner = kMathWarps + 2;
 constexpr int kWindowBwdThreads = kBwdThreads + 64;
 constexpr int kMathRegisters = 208, kOtherRegisters = 88;
 static_assert(2 * kMathRegisters + kOtherRegisters == 3 * 168, "the launch's registers");
-constexpr int kDqWorks = 4;    // descriptions in flight: more than scores may be blocks ahead
+// Descriptions in flight: the present block's and the next one's, whose scores are formed at its end.
+// The next block is taken kDqLate steps before that: earlier, a CTA keeps blocks to itself that others
+// could begin (2,000 tokens x 8 heads x 128, 1,024 keys: 66 us where it took four ahead, 54 where one
+// at the beginning of the one before it, 43 so).
+constexpr int kDqWorks = 2, kDqLate = 5;
 // who lets go of a description: the math warps, the producer and the thread of the products
 constexpr int kDqReaders = kMathWarps + 2;
 
@@ -50,7 +54,7 @@ __device__ __forceinline__ void window_dq_blocks(const CUtensorMap& map_q, const
     using Sh = DqShape<DP>;
     extern __shared__ char smem_raw[];
     __shared__ uint64_t bar_q, bar_d, bar_q_free, bar_d_free, bar_s[2], bar_dp, bar_read, bar_ds[2],
-        bar_dq[2], bar_raw, bar_all;
+        bar_dq[2], bar_raw, bar_all, bar_want;
     __shared__ uint64_t full_k[Sh::kSlotsK], empty_k[Sh::kSlotsK], full_v[Sh::kSlotsV],
         empty_v[Sh::kSlotsV], bar_work[kDqWorks], bar_work_free[kDqWorks];
     __shared__ uint32_t tmem_at;
@@ -66,7 +70,7 @@ __device__ __forceinline__ void window_dq_blocks(const CUtensorMap& map_q, const
     } else if (threadIdx.x == 0) {
         dead = 0;
         for (uint64_t* b : {&bar_q, &bar_d, &bar_q_free, &bar_d_free, &bar_s[0], &bar_s[1], &bar_dp,
-                            &bar_dq[0], &bar_dq[1], &bar_raw, &bar_all})
+                            &bar_dq[0], &bar_dq[1], &bar_raw, &bar_all, &bar_want})
             mbar_init(smem_u32(b), 1);
         for (uint64_t* b : {&bar_ds[0], &bar_ds[1], &bar_read}) mbar_init(smem_u32(b), kMathWarps);
         for (int i = 0; i < Sh::kSlotsK; ++i) {
@@ -183,7 +187,10 @@ __device__ __forceinline__ void window_dq_blocks(const CUtensorMap& map_q, const
             // ---- the planner ----
             const int64_t blocks = blocks_of(p.plan_q);
             int n = 0;  // descriptions so far
+            bool taken = false;  // whether block n has been asked for
             for (;;) {
+                if (n > 0 && !taken && !mbar_wait(smem_u32(&bar_want), (n - 1) & 1, &dead)) break;
+                taken = true;
                 unsigned int next = 0;
                 if (lane == 0) next = atomicAdd(p.next_dq, 1u);
                 const int64_t id = __shfl_sync(0xffffffffu, next, 0);
@@ -212,11 +219,12 @@ __device__ __forceinline__ void window_dq_blocks(const CUtensorMap& map_q, const
                         w.tiles = found.items;
                         w.part = found.part;
                         w.walk = found.walk;
-                        }
+                    }
                     mbar_arrive(smem_u32(&bar_work[slot]));
                 }
                 __syncwarp();
                 ++n;
+                taken = false;
                 if (end) break;
             }
         } else if (warp == kMathWarps + 1) {
@@ -353,6 +361,7 @@ __device__ __forceinline__ void window_dq_blocks(const CUtensorMap& map_q, const
                     }
                     int next = -1;
                     for (int j = 0; j < tiles && ok; ++j) {
+                        if (j == max(0, tiles - kDqLate)) mbar_arrive(smem_u32(&bar_want));
                         // the next dO V^T as soon as this one is read, while dS is formed from it
                         if (j + 1 < tiles) dprobs(false, j + 2 == tiles);
                         ok = ok && mbar_wait_one(smem_u32(&bar_ds[of_q & 1]), (of_q >> 1) & 1, &dead);

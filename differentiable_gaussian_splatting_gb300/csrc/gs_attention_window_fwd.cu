@@ -585,8 +585,10 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     }
 }
 
-// Blocks enough for the SMs, or few of them, with their keys spread over the SMs.  `window`: the
-// keys that a block may walk.
+// Blocks enough for the SMs, or few of them, with their keys spread over the SMs where that saves more
+// than the join costs, in units of one key tile's time.  (1,000 tokens x 8 heads x 64, 256 keys, 32
+// blocks of 7 tiles: 26 us spread, 12 not.)  `window`: the keys that a block may walk.
+constexpr int kJoin = 8;
 FwdPlan plan_window(int64_t tq, int64_t tk, int batch, int heads, int64_t window) {
     const int rows = 2 * kTileRows;
     const int64_t keys = std::min((tk + kTileRows - 1) / kTileRows, window / kTileRows + 1);
@@ -595,7 +597,8 @@ FwdPlan plan_window(int64_t tq, int64_t tk, int batch, int heads, int64_t window
     plan.pieces = 1;
     plan.most_keys = (int)keys;
     plan.slot_rows = (int)(tq < rows ? tq : rows);
-    plan.spread = plan.whole < kSms && batch <= 32 && keys > kLeastChunk;
+    const int64_t chunk = std::max<int64_t>(kLeastChunk, (plan.whole * keys + kSms - 1) / kSms);
+    plan.spread = plan.whole < kSms && batch <= 32 && keys - chunk >= kJoin;
     return plan;
 }
 
@@ -618,7 +621,7 @@ cudaError_t launch_dim(const CUtensorMap& mq, const CUtensorMap& mk, const CUten
                dim3(kWindowThreads), kSmem, st, mq, mk, mv, p, blocks);
     if (e != cudaSuccess || !p.plan.spread) return e;
     const int rows = kJoinThreads / (DP / 4);
-    const unsigned y = (unsigned)((p.plan.slot_rows + 4 * rows - 1) / (4 * rows));
+    const unsigned y = (unsigned)((p.plan.slot_rows + rows - 1) / rows);
     return launch(attention_join_kernel<DP, true>, dim3((unsigned)p.plan.whole, y),
                   dim3(kJoinThreads), 0, st, p);
 }
