@@ -587,8 +587,8 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
 
 // Blocks enough for the SMs, or few of them, with their keys spread over the SMs where that saves more
 // than the join costs, in units of one key tile's time.  (1,000 tokens x 8 heads x 64, 256 keys, 32
-// blocks of 7 tiles: 26 us spread, 12 not.)  `window`: the keys that a block may walk.
-constexpr int kJoin = 8;
+// blocks of 7 tiles: 26 us spread, 12 not; 2,000 x 8 x 128, 1,024 keys: 36 and 24.)  `window`: the keys that a block may walk.
+constexpr int kJoin = 11;
 FwdPlan plan_window(int64_t tq, int64_t tk, int batch, int heads, int64_t window) {
     const int rows = 2 * kTileRows;
     const int64_t keys = std::min((tk + kTileRows - 1) / kTileRows, window / kTileRows + 1);
