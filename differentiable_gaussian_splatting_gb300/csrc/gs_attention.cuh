@@ -269,6 +269,16 @@ __device__ __forceinline__ void zero_rows(char* tile, int first) {
 // Device address of the count of blocks in which a bounded wait of an attention kernel gave up.
 cudaError_t gave_up_word(unsigned int** word);
 
+// A launch of 384 threads that divides its registers anew among its groups of four warps must have
+// exactly those that the shares add up to: a share that the launch has not waits for ever.
+constexpr int kLaunchRegisters = 168;
+inline cudaError_t launch_registers_ok(const void* kernel) {
+    cudaFuncAttributes a{};
+    const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+    if (e != cudaSuccess) return e;
+    return a.numRegs == kLaunchRegisters ? cudaSuccess : cudaErrorInvalidConfiguration;
+}
+
 // the window as the kernels take it
 inline Window window_of(const gs_window& w, bool causal) {
     return {w.left, causal ? 0 : w.right, w.sinks, causal};

@@ -1137,6 +1137,11 @@ cudaError_t launch_dim(const BwdMaps& m, BwdParams p, const gs_window* w, cudaSt
         p.sink_rows = sink_rows_of(*w, v.tq);
         if (v.tq > 0) p.sink_blocks = tiles_at_most(v.tq, p.sink_rows, v.batch) * p.heads_k;
     }
+    if constexpr (kWindow) {
+        static const cudaError_t registers =
+            launch_registers_ok(reinterpret_cast<const void*>(attention_bwd_kernel<DP, true>));
+        if (registers != cudaSuccess) return registers;
+    }
     constexpr uint32_t kSmem = std::max(DkvShape<DP>::kSmem, DqShape<DP>::kSmem);
     cudaError_t e = cudaFuncSetAttribute(
         attention_bwd_kernel<DP, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);

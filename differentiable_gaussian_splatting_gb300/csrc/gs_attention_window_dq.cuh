@@ -13,10 +13,10 @@ namespace {
 
 constexpr int kDqPlanner = kMathWarps + 2;
 // With a window a warp more finds places and one makes the groups of four whole; registers of the
-// math warps' groups and of the last one: as many in all as at launch, 168 each.
+// math warps' groups and of the last one: as many in all as at launch.
 constexpr int kWindowBwdThreads = kBwdThreads + 64;
 constexpr int kMathRegisters = 208, kOtherRegisters = 88;
-static_assert(2 * kMathRegisters + kOtherRegisters == 3 * 168, "the launch's registers");
+static_assert(2 * kMathRegisters + kOtherRegisters == 3 * kLaunchRegisters, "the launch's");
 // Descriptions in flight: the present block's and the next one's, whose scores are formed at its end.
 // The next block is taken kDqLate steps before that: earlier, a CTA keeps blocks to itself that others
 // could begin (2,000 tokens x 8 heads x 128, 1,024 keys: 66 us where it took four ahead, 54 where one

@@ -29,9 +29,9 @@ namespace {
 constexpr int kProductWarp = kSoftmaxWarps, kProducerWarp = kProductWarp + 1,
               kPlannerWarp = kProducerWarp + 1;
 constexpr int kWindowThreads = (kPlannerWarp + 2) * 32;  // whole groups of four warps
-// Registers of the softmax warps' groups and of the last one: as many in all as at launch, 168 each.
+// Registers of the softmax warps' groups and of the last one: as many in all as at launch.
 constexpr int kSoftmaxRegisters = 208, kOtherRegisters = 88;
-static_assert(2 * kSoftmaxRegisters + kOtherRegisters == 3 * 168, "the launch's registers");
+static_assert(2 * kSoftmaxRegisters + kOtherRegisters == 3 * kLaunchRegisters, "the launch's");
 constexpr int kWorks = 6;      // descriptions in flight: more than scores may be blocks ahead
 constexpr int kStageBytes = 32 * 64;  // a warp's: 32 rows of 32 values on their way to memory
 constexpr int kSinkCols = 32;  // columns of the sinks' narrow tile
@@ -612,6 +612,9 @@ template <int DP>
 cudaError_t launch_dim(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                        const FwdParams& p, cudaStream_t st) {
     constexpr uint32_t kSmem = FwdShape<DP>::kSmem + kSoftmaxWarps * kStageBytes;
+    static const cudaError_t registers =
+        launch_registers_ok(reinterpret_cast<const void*>(attention_window_fwd_kernel<DP>));
+    if (registers != cudaSuccess) return registers;
     cudaError_t e = cudaFuncSetAttribute(attention_window_fwd_kernel<DP>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)kSmem);

@@ -2,6 +2,8 @@
 the host's checks refuse bad calls before anything is enqueued."""
 
 import ctypes as C
+import os
+import re
 
 import numpy as np
 import pytest
@@ -9,6 +11,7 @@ import pytest
 import block_ref as ref
 import token_ref
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 P, MIS = 0x100000, 0x100004  # addresses that are never read
 
 
@@ -139,3 +142,41 @@ def test_binding_refuses_bad_windows():
     with pytest.raises(TypeError):
         gs.gs_attention_window_fwd(x, x, x, x, lse, ws, 1.5, stream=0)
     gs.gs_attention_window_fwd(x, x, x, x, lse, ws, 2 ** 40, 0, 4, stream=0)  # no tokens: nothing to do
+
+
+def _source(name):
+    path = os.path.join(ROOT, "differentiable_gaussian_splatting_gb300", "csrc", name)
+    with open(path) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+@pytest.mark.parametrize("file,drain,rings,once", [
+    ("gs_attention_window_fwd.cu", "bar_drain", {"bar_full"}, {"bar_q[t]"}),
+    ("gs_attention_window_dq.cuh", "bar_all", {"full_k", "full_v"}, {"bar_q", "bar_d"})])
+def test_no_copy_or_product_outlives_a_cta(file, drain, rings, once):
+    # Whoever issued asynchronous work waits for it last of all, whether or not a wait has given up.
+    # (What such a CTA does cannot be run: here the sources are held to it.)
+    text = _source(file)
+    assert len(re.findall(rf"mma_commit\(smem_u32\(&{drain}\)\);\s*"
+                          rf"mbar_drain\(smem_u32\(&{drain}\), 0\);", text)) == 1
+    assert set(re.findall(r"drain_ring<Sh::\w+>\((\w+), \w+\)", text)) == rings
+    assert once <= set(re.findall(r"mbar_drain\(smem_u32\(&([\w\[\]]+)\)", text))
+    # a copy that is mended before it counts is waited for where that wait gives up
+    assert re.search(r"mbar_wait\(bar, parity, &dead\);\s*if \(!ok\) \{\s*mbar_drain\(bar, parity\);",
+                     text)
+    # every wait is one of the bounded ones
+    assert not re.search(r"while\s*\(\s*!?\s*mbar_try", text)
+
+
+def test_shares_of_registers_add_up():
+    # a share that the launch does not have would be waited for without end: the sources' shares are
+    # those of the launch, which the host checks against the kernel's own count
+    for file, first in (("gs_attention_window_fwd.cu", "kSoftmaxRegisters"),
+                        ("gs_attention_window_dq.cuh", "kMathRegisters")):
+        text = _source(file)
+        a, b = re.search(rf"{first} = (\d+), kOtherRegisters = (\d+);", text).groups()
+        assert 2 * int(a) + int(b) == 3 * 168 and int(a) % 8 == 0 and int(b) % 8 == 0
+        assert f"2 * {first} + kOtherRegisters == 3 * kLaunchRegisters" in text
+    assert "kLaunchRegisters = 168;" in _source("gs_attention.cuh")
+    assert "launch_registers_ok" in _source("gs_attention_window_fwd.cu")
+    assert "launch_registers_ok" in _source("gs_attention_bwd.cu")
