@@ -39,7 +39,7 @@ namespace {
 
 constexpr int kSms = 152;
 constexpr int kMostThreads = 1024;  // width <= 8,192
-constexpr int kFourUpTo = 2048;  // odd widths whose threads take four values instead of eight
+constexpr int kFourUpTo = 2048;  // widths up to which a thread may take four values: see pairs_of
 constexpr int kFwdWarps = 32, kBwdWarps = 16;  // resident on an SM
 constexpr int kMostGates = 256;     // sequences at once when the gates' gradients are added up
 
@@ -642,16 +642,19 @@ __global__ void __launch_bounds__(kFinishThreads)
     }
 }
 
-// How a row is shared out: threads of eight values, or of four.
-int pairs_of(int width, bool vec) { return !vec && width <= kFourUpTo ? 2 : 4; }
-
-int warps_of(int width, bool vec) {
-    const int per_warp = 64 * pairs_of(width, vec);
-    return (width + per_warp - 1) / per_warp;
+// How a row is shared out: threads of eight values, or of four where their addresses and column
+// sums would not fit the registers: odd widths in fp32 with biases or a layer norm.  (16,200 x 1,001
+// with both, backward: 135 us with four, 164 with eight; without either 78 and 66; 32,400 x 1,001
+// in bfloat16 377 and 195.)
+int pairs_of(const RnParams& p, bool vec, bool bf16, bool bias) {
+    const bool layer = p.pre == GS_NORM_LAYER || p.post == GS_NORM_LAYER;
+    return !vec && !bf16 && (bias || layer) && p.width <= kFourUpTo ? 2 : 4;
 }
 
-int64_t most_blocks(int width, bool vec, int resident_warps) {
-    return (int64_t)kSms * std::max(1, resident_warps / warps_of(width, vec));
+int warps_of(int width, int pairs) { return (width + 64 * pairs - 1) / (64 * pairs); }
+
+int64_t most_blocks(int width, int pairs, int resident_warps) {
+    return (int64_t)kSms * std::max(1, resident_warps / warps_of(width, pairs));
 }
 
 NormRows rows_of(const gs_rows& r, int size) {
@@ -689,8 +692,8 @@ bool whole_words(int width, std::initializer_list<NormRows> arrays) {
 }
 
 template <typename T, bool kVec, int kPairs, int kThreads>
-cudaError_t launch_fwd_of(const RnParams& p, int blocks, cudaStream_t st) {
-    const bool layer = p.pre == GS_NORM_LAYER || p.post == GS_NORM_LAYER, bias = p.pb || p.qb;
+cudaError_t launch_fwd_of(const RnParams& p, bool bias, cudaStream_t st) {
+    const bool layer = p.pre == GS_NORM_LAYER || p.post == GS_NORM_LAYER;
     void (*kernel)(const RnParams);
     if (layer)
         kernel = bias ? residual_norm_kernel<T, kVec, kPairs, true, true, kThreads>
@@ -698,16 +701,17 @@ cudaError_t launch_fwd_of(const RnParams& p, int blocks, cudaStream_t st) {
     else
         kernel = bias ? residual_norm_kernel<T, kVec, kPairs, false, true, kThreads>
                       : residual_norm_kernel<T, kVec, kPairs, false, false, kThreads>;
-    return launch(kernel, dim3((unsigned)blocks), dim3((unsigned)warps_of(p.width, kVec) * 32), 0, st,
-                  p);
+    return launch(kernel, dim3((unsigned)std::min(p.tokens, most_blocks(p.width, kPairs, kFwdWarps))),
+                  dim3((unsigned)warps_of(p.width, kPairs) * 32), 0, st, p);
 }
 
 template <typename T, bool kVec>
 cudaError_t launch_fwd(const RnParams& p, cudaStream_t st) {
-    const int blocks = (int)std::min(p.tokens, most_blocks(p.width, kVec, kFwdWarps));
-    if constexpr (!kVec)
-        if (pairs_of(p.width, kVec) == 2) return launch_fwd_of<T, kVec, 2, 512>(p, blocks, st);
-    return launch_fwd_of<T, kVec, 4, kMostThreads>(p, blocks, st);
+    const bool bias = p.pb || p.qb;
+    if constexpr (!kVec && sizeof(T) == 4)
+        if (pairs_of(p, kVec, false, bias) == 2)
+            return launch_fwd_of<T, kVec, 2, 512>(p, bias, st);
+    return launch_fwd_of<T, kVec, 4, kMostThreads>(p, bias, st);
 }
 
 template <typename T, bool kVec, int kPairs, int kThreads>
@@ -720,25 +724,25 @@ cudaError_t launch_bwd_of(const RnParams& p, bool bias, int blocks, cudaStream_t
     else
         kernel = bias ? residual_norm_bwd_kernel<T, kVec, kPairs, false, true, kThreads>
                       : residual_norm_bwd_kernel<T, kVec, kPairs, false, false, kThreads>;
-    return launch(kernel, dim3((unsigned)blocks), dim3((unsigned)warps_of(p.width, kVec) * 32), 0, st,
+    return launch(kernel, dim3((unsigned)blocks), dim3((unsigned)warps_of(p.width, kPairs) * 32), 0, st,
                   p);
 }
 
 // Up to 4,096 values a row its threads may have 128 registers each; beyond, 64 and spills.
 template <typename T, bool kVec>
 cudaError_t launch_bwd(const RnParams& p, bool bias, int blocks, cudaStream_t st) {
-    if constexpr (!kVec)
-        if (pairs_of(p.width, kVec) == 2) return launch_bwd_of<T, kVec, 2, 512>(p, bias, blocks, st);
-    if (warps_of(p.width, kVec) <= 16) return launch_bwd_of<T, kVec, 4, 512>(p, bias, blocks, st);
+    if constexpr (!kVec && sizeof(T) == 4)
+        if (pairs_of(p, kVec, false, bias) == 2)
+            return launch_bwd_of<T, kVec, 2, 512>(p, bias, blocks, st);
+    if (warps_of(p.width, 4) <= 16) return launch_bwd_of<T, kVec, 4, 512>(p, bias, blocks, st);
     return launch(residual_norm_bwd_kernel<T, kVec, 4, true, true, kMostThreads>,
-                  dim3((unsigned)blocks), dim3((unsigned)warps_of(p.width, kVec) * 32), 0, st, p);
+                  dim3((unsigned)blocks), dim3((unsigned)warps_of(p.width, 4) * 32), 0, st, p);
 }
 
 }  // namespace
 
 size_t residual_norm_workspace_bytes(int width) {
-    const int64_t blocks = std::max(most_blocks(width, true, kBwdWarps),  // whatever the strides
-                                    most_blocks(width, false, kBwdWarps));
+    const int64_t blocks = most_blocks(width, 4, kBwdWarps);  // with fewer values a thread: fewer
     return (size_t)blocks * 6 * width * sizeof(float) + 16;
 }
 
@@ -766,10 +770,11 @@ cudaError_t launch_residual_norm_bwd(const ResidualNormArgs& a, const gs_rows& x
     p.dy = rows_of(dy, size);
     p.dgate = g.gate;
     const bool vec = whole_words(a.width, {p.x, p.y, p.dr, p.dh, p.dx, p.dy});
-    const int blocks = (int)std::min(a.tokens, most_blocks(a.width, vec, kBwdWarps));
+    const bool bias = p.pb || p.qb || g.pre_bias || g.post_bias;
+    const int pairs = pairs_of(p, vec, a.bf16, bias);
+    const int blocks = (int)std::min(a.tokens, most_blocks(a.width, pairs, kBwdWarps));
     p.part = static_cast<float*>(ws);
     p.part_gate = p.part + ((int64_t)blocks * 4 * a.width + 3) / 4 * 4;
-    const bool bias = p.pb || p.qb || g.pre_bias || g.post_bias;
     cudaError_t e = cudaSuccess;
     if (a.tokens > 0 && a.bf16)
         e = vec ? launch_bwd<__nv_bfloat16, true>(p, bias, blocks, st)
