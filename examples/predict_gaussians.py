@@ -12,7 +12,12 @@ The token operators of the package do the hot parts of a block, forward and back
 
 The plain torch parts are the matrix products, the layer norms and the optimizer.
 
-    python examples/predict_gaussians.py [--steps 200] [--size 128]
+For large images, where all pairs of tiles are too many, --window lets a tile attend to the tiles
+near it and to the first few (gs_attention_window_fwd); --clip bounds the norm over all gradients of
+a step (gs_clip_grad_norm); --norms takes the layer norms from the package, those between a block's
+halves with the residual they follow (gs_residual_norm, without dropout).
+
+    python examples/predict_gaussians.py [--steps 200] [--size 128] [--window 64] [--clip 1.0] [--norms]
 """
 
 from __future__ import annotations
@@ -49,7 +54,7 @@ class HeadAttention(torch.autograd.Function):
     head_dim] of queries, keys and values; its gradient is written into one packed array."""
 
     @staticmethod
-    def forward(ctx, qkv, q_weight, k_weight, table, heads_k, cu):
+    def forward(ctx, qkv, q_weight, k_weight, table, heads_k, cu, window=None):
         T, heads, D = qkv.shape
         hq = heads - 2 * heads_k
         q, k, v = qkv[:, :hq], qkv[:, hq:hq + heads_k], qkv[:, hq + heads_k:]
@@ -58,10 +63,14 @@ class HeadAttention(torch.autograd.Function):
         gs.gs_qk_norm_rope(q, k, q_weight, k_weight, table, None, qn, kn)
         out, lse = torch.empty_like(qn), torch.empty((hq, T), device=qkv.device)
         batch = 1 if cu is None else cu.numel() - 1
-        ws = _workspace(gs.gs_attention_workspace_bytes(T, T, batch, hq, heads_k, D))
-        gs.gs_attention_fwd(qn, kn, v, out, lse, ws, cu_q=cu, cu_k=cu)
+        if window is None:
+            ws = _workspace(gs.gs_attention_workspace_bytes(T, T, batch, hq, heads_k, D))
+            gs.gs_attention_fwd(qn, kn, v, out, lse, ws, cu_q=cu, cu_k=cu)
+        else:  # (left, right, sinks)
+            ws = _workspace(gs.gs_attention_window_workspace_bytes(T, T, batch, hq, heads_k, D, *window))
+            gs.gs_attention_window_fwd(qn, kn, v, out, lse, ws, *window, cu_q=cu, cu_k=cu)
         ctx.save_for_backward(qkv, q_weight, k_weight, table, qn, kn, out, lse, cu)
-        ctx.heads = hq, heads_k
+        ctx.heads, ctx.window = (hq, heads_k), window
         return out
 
     @staticmethod
@@ -73,14 +82,41 @@ class HeadAttention(torch.autograd.Function):
         dqkv = torch.empty_like(qkv)
         dqn, dkn = torch.empty_like(qn), torch.empty_like(kn)
         batch = 1 if cu is None else cu.numel() - 1
-        ws = _workspace(gs.gs_attention_workspace_bytes(T, T, batch, hq, hk, D))
-        gs.gs_attention_bwd(qn, kn, v, out, lse, dout.contiguous(), dqn, dkn, dqkv[:, hq + hk:], ws,
-                            cu_q=cu, cu_k=cu)
+        grads = (qn, kn, v, out, lse, dout.contiguous(), dqn, dkn, dqkv[:, hq + hk:])
+        if ctx.window is None:
+            ws = _workspace(gs.gs_attention_workspace_bytes(T, T, batch, hq, hk, D))
+            gs.gs_attention_bwd(*grads, ws, cu_q=cu, cu_k=cu)
+        else:
+            ws = _workspace(gs.gs_attention_window_workspace_bytes(T, T, batch, hq, hk, D, *ctx.window))
+            gs.gs_attention_window_bwd(*grads, ws, *ctx.window, cu_q=cu, cu_k=cu)
         dqw, dkw = torch.empty_like(q_weight), torch.empty_like(k_weight)
         ws = _workspace(gs.gs_qk_norm_rope_workspace_bytes(T, hq, hk, D))
         gs.gs_qk_norm_rope_bwd(q, k, q_weight, k_weight, table, None, dqn, dkn, dqkv[:, :hq],
                                dqkv[:, hq:hq + hk], dqw, dkw, ws)
-        return dqkv, dqw, dkw, None, None, None
+        return dqkv, dqw, dkw, None, None, None, None
+
+
+class ResidualNorm(torch.autograd.Function):
+    """(x + y, its layer norm); y may be None: (x, its layer norm)"""
+
+    @staticmethod
+    def forward(ctx, x, y, weight, bias, eps):
+        r, h = (x if y is None else torch.empty_like(x)), torch.empty_like(x)
+        gs.gs_residual_norm(x, y, None if y is None else r, h, pre_weight=weight, pre_bias=bias,
+                            pre="layer", eps=eps)
+        ctx.save_for_backward(x, y, weight, bias)
+        ctx.eps = eps
+        return r, h
+
+    @staticmethod
+    def backward(ctx, dr, dh):
+        x, y, weight, bias = ctx.saved_tensors
+        dx, dw, db = torch.empty_like(x), torch.empty_like(weight), torch.empty_like(bias)
+        dy = None if y is None else torch.empty_like(y)
+        ws = _workspace(gs.gs_residual_norm_workspace_bytes(*x.shape))
+        gs.gs_residual_norm_bwd(x, y, dr.contiguous(), dh.contiguous(), dx, dy, ws, pre_weight=weight,
+                                pre_bias=bias, pre="layer", eps=ctx.eps, dpre_weight=dw, dpre_bias=db)
+        return dx, dy, dw, db, None
 
 
 class DropoutAdd(torch.autograd.Function):
@@ -137,9 +173,10 @@ def axial_table(rows: int, cols: int, rot: int) -> torch.Tensor:
 
 
 class Block(nn.Module):
-    def __init__(self, width: int, heads: int, heads_k: int, p: float):
+    def __init__(self, width: int, heads: int, heads_k: int, p: float, window=None):
         super().__init__()
         self.heads, self.heads_k, self.dim, self.p = heads, heads_k, width // heads, p
+        self.window = window
         self.norm1, self.norm2 = nn.LayerNorm(width), nn.LayerNorm(width)
         self.qkv = nn.Linear(width, (heads + 2 * heads_k) * self.dim, bias=False)
         self.proj = nn.Linear(width, width, bias=False)
@@ -155,23 +192,37 @@ class Block(nn.Module):
                                                      m.bias).bfloat16()
         T = x.shape[0]
         qkv = lin(self.qkv, norm(self.norm1, x)).view(T, -1, self.dim)
-        y = HeadAttention.apply(qkv, self.q_weight, self.k_weight, table, self.heads_k, cu)
+        y = HeadAttention.apply(qkv, self.q_weight, self.k_weight, table, self.heads_k, cu, self.window)
         p = self.p if self.training else 0.0
         x = DropoutAdd.apply(lin(self.proj, y.reshape(T, -1)), x, rng[0], p)
         y = lin(self.down, nn.functional.gelu(lin(self.up, norm(self.norm2, x))))
         return DropoutAdd.apply(y, x, rng[1], p)
+
+    def halves(self, x, y, table, cu):
+        """The block without dropout, its residuals and norms in one pass each: takes the stream x and
+        the branch y that the block before left to add (None: nothing), returns the same."""
+        lin = lambda m, v: nn.functional.linear(v, m.weight.bfloat16(),
+                                                None if m.bias is None else m.bias.bfloat16())
+        T = x.shape[0]
+        x, h = ResidualNorm.apply(x, y, self.norm1.weight, self.norm1.bias, self.norm1.eps)
+        qkv = lin(self.qkv, h).view(T, -1, self.dim)
+        y = HeadAttention.apply(qkv, self.q_weight, self.k_weight, table, self.heads_k, cu, self.window)
+        x, h = ResidualNorm.apply(x, lin(self.proj, y.reshape(T, -1)), self.norm2.weight,
+                                  self.norm2.bias, self.norm2.eps)
+        return x, lin(self.down, nn.functional.gelu(lin(self.up, h)))
 
 
 class TilePredictor(nn.Module):
     """Gaussians for every 16 x 16 tile of an image (whose sides are multiples of 16)."""
 
     def __init__(self, rows: int, cols: int, width=256, heads=4, heads_k=2, blocks=3,
-                 per_tile=8, p=0.05, seed=0):
+                 per_tile=8, p=0.05, seed=0, window=None, norms=False):
         super().__init__()
         torch.manual_seed(seed)
-        self.rows, self.cols, self.per_tile = rows, cols, per_tile
+        self.rows, self.cols, self.per_tile, self.norms = rows, cols, per_tile, norms
         self.embed = nn.Linear(3 * TILE * TILE, width)
-        self.blocks = nn.ModuleList([Block(width, heads, heads_k, p) for _ in range(blocks)])
+        self.blocks = nn.ModuleList([Block(width, heads, heads_k, p, window)
+                                     for _ in range(blocks)])
         self.norm = nn.LayerNorm(width)
         self.head = nn.Linear(width, per_tile * RAW)
         nn.init.normal_(self.head.weight, std=0.02)
@@ -197,12 +248,18 @@ class TilePredictor(nn.Module):
     def forward(self, image, cam):
         """(means, scales, quats, opacities, sh) of all Gaussians, in front of the camera"""
         x = self.tokens(image)
-        for i, block in enumerate(self.blocks):
-            x = block(x, self.table, self.rng[2 * i:2 * i + 2], None)
-        if self.training:
-            self.rng[:, 1] += 2 * len(self.blocks)  # the next step's masks
-        x = nn.functional.layer_norm(x.float(), self.norm.normalized_shape, self.norm.weight,
-                                     self.norm.bias)
+        if self.norms:
+            y = None
+            for block in self.blocks:
+                x, y = block.halves(x, y, self.table, None)
+            x = ResidualNorm.apply(x, y, self.norm.weight, self.norm.bias, self.norm.eps)[1].float()
+        else:
+            for i, block in enumerate(self.blocks):
+                x = block(x, self.table, self.rng[2 * i:2 * i + 2], None)
+            if self.training:
+                self.rng[:, 1] += 2 * len(self.blocks)  # the next step's masks
+            x = nn.functional.layer_norm(x.float(), self.norm.normalized_shape, self.norm.weight,
+                                         self.norm.bias)
         raw = self.head(x).view(self.rows, self.cols, self.per_tile, RAW)
         z = 4.0 + torch.tanh(raw[..., 2])
         at = torch.arange(max(self.rows, self.cols), device="cuda", dtype=torch.float32)
@@ -223,20 +280,28 @@ def target_image(size: int, seed: int = 0) -> torch.Tensor:
     return torch.from_numpy(y).cuda()
 
 
-def train(steps=200, size=128, lr=3e-4, p=0.05, seed=0, log=None):
-    """Fits the predictor to one synthetic image; returns the losses."""
+def train(steps=200, size=128, lr=3e-4, p=0.05, seed=0, log=None, window=None, clip=None, norms=False):
+    """Fits the predictor to one synthetic image; returns the losses.  window: tiles that a tile sees
+    before and behind it, beside the first four (None: all); clip: the largest norm over all gradients
+    (None: whatever it is); norms: layer norms of the package, with the residuals, without dropout."""
     tiles = size // TILE
     target = target_image(size, seed)
     cam = ss.pinhole(np.eye(4), 2.0 * size, size, size)
-    model = TilePredictor(tiles, tiles, p=p, seed=seed).train()
+    model = TilePredictor(tiles, tiles, p=p, seed=seed, norms=norms,
+                          window=None if window is None else (window, window, 4)).train()
     raster = gs.Rasterizer(cam, 0, tiles * tiles * model.per_tile)
     ws = _workspace(gs.gs_loss_workspace_bytes(size, size))
     opt = torch.optim.Adam(model.parameters(), lr=lr)
+    norm = torch.empty(1, device="cuda")
     losses = []
     for step in range(steps):
         opt.zero_grad(set_to_none=True)
         loss = RenderLoss.apply(*model(target, cam), raster, target, ws)
         loss.backward()
+        if clip is not None:
+            grads = [q.grad for q in model.parameters() if q.grad is not None]
+            gs.gs_clip_grad_norm(grads, clip, norm,
+                                 _workspace(gs.gs_clip_grad_norm_workspace_bytes(len(grads))))
         opt.step()
         losses.append(loss.detach())
         if log and (step % 20 == 0 or step == steps - 1):
@@ -249,8 +314,12 @@ def main() -> None:
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--steps", type=int, default=200)
     ap.add_argument("--size", type=int, default=128, help="side of the image, a multiple of 16")
+    ap.add_argument("--window", type=int, help="tiles that a tile sees on either side (all)")
+    ap.add_argument("--clip", type=float, help="largest norm over all gradients (any)")
+    ap.add_argument("--norms", action="store_true", help="the package's layer norms, no dropout")
     args = ap.parse_args()
-    train(args.steps, args.size // TILE * TILE, log=print)
+    train(args.steps, args.size // TILE * TILE, log=print, window=args.window, clip=args.clip,
+          norms=args.norms)
 
 
 if __name__ == "__main__":

@@ -198,3 +198,46 @@ def test_steps_on_two_streams_at_once():
         for g, w in zip(got, want):
             for n, t in g.items():
                 assert torch.equal(t, w[n]), n
+
+
+def _example():
+    import importlib.util
+    import os
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    spec = importlib.util.spec_from_file_location(
+        "predict_gaussians", os.path.join(root, "examples", "predict_gaussians.py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+@pytest.mark.parametrize("options", [dict(window=5), dict(clip=0.05), dict(norms=True),
+                                     dict(window=9, clip=0.05, norms=True)])
+def test_example_runs_with(options):
+    losses = _example().train(steps=3, size=96, seed=1, **options)
+    assert len(losses) == 3 and np.isfinite(losses).all()
+
+
+def test_example_gradients_of_residual_norm():
+    import torch
+
+    ex = _example()
+    torch.manual_seed(5)
+    x, y = (torch.randn(77, 96, device="cuda").bfloat16() for _ in range(2))
+    w, b = 1 + 0.1 * torch.randn(96, device="cuda"), 0.1 * torch.randn(96, device="cuda")
+    dr, dh = (torch.randn(77, 96, device="cuda").bfloat16() for _ in range(2))
+    for second in (y, None):
+        ours = [t if t is None else t.clone().requires_grad_() for t in (x, second, w, b)]
+        out = ex.ResidualNorm.apply(*ours, 1e-5)
+        torch.autograd.backward(list(out), [dr, dh])
+        plain = [t if t is None else t.clone().float().requires_grad_() for t in (x, second, w, b)]
+        r = plain[0] if second is None else plain[0] + plain[1]
+        h = torch.nn.functional.layer_norm(r, (96,), plain[2], plain[3], 1e-5)
+        torch.autograd.backward([r, h], [dr.float(), dh.float()])
+        # outputs and gradients are rounded to bfloat16 once: at most 2^-8, by norms (and without y
+        # the stream's gradient is joined by autograd: twice)
+        for a, c in ((out[0], r), (out[1], h),
+                     *((p.grad, q.grad) for p, q in zip(ours, plain) if p is not None)):
+            a, c = a.detach().float(), c.detach()
+            assert ((a - c).norm() / c.norm()).item() < 2 * 2.0 ** -8
