@@ -321,45 +321,55 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bar_work_free[at]));
-#pragma unroll
-            for (int c = 0; c < DP; c += 32) {
-                uint32_t o[32];
+            const float2 f2 = make_float2(f, f);
+            // 32 columns of the row, normalised
+            const auto columns = [&](float2 (&o)[16], int c) {
                 if (tiles_t > 0) {
-                    tmem_ld32(o, o_at + c);
+                    tmem_ld32(reinterpret_cast<uint32_t*>(o), o_at + c);
                     tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] = __fmul2_rn(o[k], f2);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] = make_float2(0.f, 0.f);
                 }
+            };
+            if (!split) {
+                // Through shared memory, so that a store takes 64 bytes of 8 rows instead of 16 of 32.
+                // A row's 16-byte words change places by its number: no two lanes meet in a bank.
+                const int first = lane >> 2, turn = lane >> 1 & 3;
+                char* put = stage + lane * 64;
+                const char* get = stage + first * 64 + ((lane & 3) ^ (first >> 1 & 3)) * 16;
+                __nv_bfloat16* to = out + first * p.o.ts + (lane & 3) * 8;
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    o[k] = some ? __float_as_uint(__uint_as_float(o[k]) * f) : 0u;
-                if (!split) {
-                    // Through shared memory, so that a store takes 64 bytes of 8 rows instead of 16 of 32.
-                    // 16-byte words of a row change places by its number: no two lanes meet in a bank.
+                for (int c = 0; c < DP; c += 32) {
+                    float2 o[16];
+                    columns(o, c);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t words[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            words[e] = pack_bf16(__uint_as_float(o[8 * k + 2 * e]),
-                                                 __uint_as_float(o[8 * k + 2 * e + 1]));
-                        *reinterpret_cast<uint4*>(stage + lane * 64 + (k ^ (lane >> 1 & 3)) * 16) =
-                            make_uint4(words[0], words[1], words[2], words[3]);
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        *reinterpret_cast<uint4*>(put + (k ^ turn) * 16) = make_uint4(
+                            pack_bf16(o[4 * k].x, o[4 * k].y), pack_bf16(o[4 * k + 1].x, o[4 * k + 1].y),
+                            pack_bf16(o[4 * k + 2].x, o[4 * k + 2].y),
+                            pack_bf16(o[4 * k + 3].x, o[4 * k + 3].y));
                     __syncwarp();
-                    const int col = c + (lane & 3) * 8;
+                    if (c + (lane & 3) * 8 < p.dim)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int at_row = k * 8 + (lane >> 2);
-                        const uint4 word = *reinterpret_cast<const uint4*>(
-                            stage + at_row * 64 + ((lane & 3) ^ (at_row >> 1 & 3)) * 16);
-                        if (at_row < rows && col < p.dim)
-                            *reinterpret_cast<uint4*>(out + at_row * p.o.ts + col) = word;
-                    }
+                        for (int k = 0; k < 4; ++k)  // eight rows on, a row's words lie as here
+                            if (k * 8 + first < rows)
+                                *reinterpret_cast<uint4*>(to + k * 8 * p.o.ts + c) =
+                                    *reinterpret_cast<const uint4*>(get + k * 8 * 64);
                     __syncwarp();
-                } else if (out32) {
+                }
+            } else {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4)
-                        *reinterpret_cast<uint4*>(out32 + c + k) =
-                            make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                for (int c = 0; c < DP; c += 32) {
+                    float2 o[16];
+                    columns(o, c);
+                    if (out32)
+#pragma unroll
+                        for (int k = 0; k < 16; k += 2)
+                            *reinterpret_cast<float4*>(out32 + c + 2 * k) =
+                                make_float4(o[k].x, o[k].y, o[k + 1].x, o[k + 1].y);
                 }
             }
             tmem_fence_before();  // the output may be written over once the next P is there
