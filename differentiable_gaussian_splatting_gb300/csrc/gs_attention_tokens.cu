@@ -198,7 +198,8 @@ __global__ void __launch_bounds__(kTokenThreads, 2) attention_tokens_kernel(cons
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            s[e] = top[e & 1] == -INFINITY ? 0.f : ex2_approx(s[e] - top[e & 1]);
+            // (by the score, not by the maximum: a row of NaN has none)
+            s[e] = s[e] == -INFINITY ? 0.f : ex2_approx(s[e] - top[e & 1]);
             sum[e & 1] += s[e];
         }
         const uint32_t p0 = transposed(pack_bf16(s[0], s[1])), p1 = transposed(pack_bf16(s[2], s[3]));

@@ -292,3 +292,20 @@ def test_window_strided_heads_and_another_stream():
     torch.cuda.synchronize()
     for a, b in ((out, want[0]), (lse, want[1]), *zip(part(g), want[2])):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("lens_q,lens_k", [([1, 2, 1], [300, 40, 1500]), ([300], [900])])
+def test_queries_that_are_not_finite_say_so(lens_q, lens_k):
+    # NaN for the rows of such a query's head, as their softmax is; no other row's
+    import torch
+
+    rng, q, k, v = _inputs(sum(lens_q), sum(lens_k), 4, 2, 64, seed=9)
+    clean = _run(q, k, v, 0.125, (200, 0, 4), True, lens_q, lens_k)
+    bad = q.copy()
+    bad[1, 2, 5], bad[0, 0, 0] = np.nan, np.nan
+    out, lse = _run(bad, k, v, 0.125, (200, 0, 4), True, lens_q, lens_k)
+    hit = torch.zeros(out.shape[:2], dtype=torch.bool, device="cuda")
+    hit[1, 2] = hit[0, 0] = True
+    assert out[hit].isnan().all() and lse.t()[hit].isnan().all()
+    assert torch.equal(out[~hit], clean[0][~hit])
+    assert torch.equal(lse.t()[~hit], clean[1].t()[~hit])
