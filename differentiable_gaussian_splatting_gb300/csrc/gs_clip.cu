@@ -278,14 +278,15 @@ __global__ void __launch_bounds__(kClipThreads, 4)
     Chunk c{};
     ChunkWords x;
     bool whole = false;
-    const auto load = [&]() {
+    const auto load = [&](bool same) {  // same: chunks that stay in their place are not read
         if (id < begin) return;
         while (t.chunk0[array] > id) --array;
         c = chunk_of(t, array, id);
         whole = whole_chunk(c);
-        if (whole) x.load(c);
+        if (whole && !(same && c.in == c.out)) x.load(c);
     };
-    load();
+    load(false);
+    // (the first chunk is on its way before the factor is known)
     double sum = 0.0;
     for (int i = threadIdx.x; i < parts; i += kClipThreads) sum += __ldg(part + i);
     sum = block_sum(sum);
@@ -300,13 +301,16 @@ __global__ void __launch_bounds__(kClipThreads, 4)
         } else {
             const double norm = sqrt(sum);
             if (norm_out && blockIdx.x == 0) *norm_out = (float)norm;
-            // 0 where the norm is not finite
-            total = !(norm < INFINITY) ? 0.0 : norm > max_norm ? max_norm / norm : 1.0;
+            // 0 where the norm is not finite, unless all is wanted as it is
+            total = max_norm == INFINITY  ? 1.0
+                    : !(norm < INFINITY)  ? 0.0
+                    : norm > max_norm     ? max_norm / norm
+                                          : 1.0;
         }
     }
     __syncthreads();
     const double d = total;
-    for (; id >= begin; --id, load()) {
+    for (; id >= begin; --id, load(d == 1.0)) {
         if (c.in == c.out && d == 1.0) continue;
         if (d == 0.0 || d >= 0x1p-126)
             scale_chunk<false>(c, x, whole, d);
@@ -350,6 +354,8 @@ int fill(Table<kArrays>* t, int first, int count, const gs_array* in, const gs_a
 template <int kArrays>
 cudaError_t launch_tables(int count, const gs_array* in, const gs_array* out, double max_norm,
                           float* norm, double* part, cudaStream_t st) {
+    bool alone = max_norm == INFINITY;  // the norm alone is wanted
+    for (int i = 0; i < count && alone; ++i) alone = in[i].data == out[i].data;
     Table<kArrays> t;
     int starts[kMaxTables], tables = 0, parts = 0, next = 0;
     do {
@@ -361,6 +367,11 @@ cudaError_t launch_tables(int count, const gs_array* in, const gs_array* out, do
         if (e != cudaSuccess) return e;
         parts += (int)blocks;
     } while (next < count);
+    if (alone) {
+        fill(&t, 0, 0, in, out);
+        return launch(clip_kernel<kArrays>, dim3(1), dim3(kClipThreads), 0, st, t, (const double*)part,
+                      parts, max_norm, norm);
+    }
     // from the last table on, which is still filled: what was read last is still in L2
     for (int i = tables - 1; i >= 0; --i) {
         if (i < tables - 1) fill(&t, starts[i], count, in, out);

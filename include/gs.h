@@ -692,7 +692,8 @@ gs_status gs_residual_norm_bwd(int64_t tokens, int32_t width, const gs_block_nor
  *   outs       host array of the same elements and types; an out may be its gradient itself, but
  *              overlaps nothing else (no array is given twice).  NULL: all are their gradients.
  *              Where norm <= max_norm, such outs are not written
- *   max_norm   >= 0; infinity: the norm alone is wanted, outs as grads (NULL: nothing is written)
+ *   max_norm   >= 0; infinity: the norm alone is wanted, outs are as their gradients whatever these
+ *              hold (NULL: nothing is written)
  *   norm       out, device float: the norm before clipping
  *   workspace  >= gs_clip_grad_norm_workspace_bytes(count); holds nothing between calls
  */

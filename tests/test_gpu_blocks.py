@@ -312,3 +312,36 @@ def test_norm_alone_and_untouched_gradients():
     assert torch.equal(a, norm)  # the same bits again
     gs.gs_clip_grad_norm(g, float("inf"), norm, ws)
     assert abs(norm.item() - want / 2) <= 32 * U * want
+
+
+def test_norm_alone_leaves_what_is_not_finite():
+    import torch
+
+    gs = _gs()
+    g = [torch.randn(n, device="cuda") for n in (40000, 3)]
+    g[0][7], g[1][2] = float("nan"), float("inf")
+    kept, norm = [x.clone() for x in g], torch.zeros(1, device="cuda")
+    ws = torch.empty(gs.gs_clip_grad_norm_workspace_bytes(2), dtype=torch.uint8, device="cuda")
+    outs = [torch.zeros_like(x) for x in g]
+    for o in (None, outs):
+        gs.gs_clip_grad_norm(g, float("inf"), norm, ws, outs=o)
+        assert norm.isnan().item()
+        for a in (g, outs if o else g):
+            assert all(torch.equal(x.nan_to_num(5.0), y.nan_to_num(5.0)) for x, y in zip(a, kept))
+
+
+def test_clip_grad_norm_within_its_bound_beside_outs_of_their_own():
+    # some gradients in place, some not: those in place are neither read again nor written
+    import torch
+
+    gs = _gs()
+    sizes = (3, 100000, 16384, 5, 70000)
+    g = [torch.randn(n, device="cuda") for n in sizes]
+    kept = [x.clone() for x in g]
+    outs = [x if i % 2 else torch.zeros_like(x) for i, x in enumerate(g)]
+    norm = torch.zeros(1, device="cuda")
+    ws = torch.empty(gs.gs_clip_grad_norm_workspace_bytes(len(g)), dtype=torch.uint8, device="cuda")
+    gs.gs_clip_grad_norm(g, 1e6, norm, ws, outs=outs)
+    want = float(torch.cat(g).double().norm())
+    assert abs(norm.item() - want) <= 12 * U * want
+    assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(kept, g, outs))
