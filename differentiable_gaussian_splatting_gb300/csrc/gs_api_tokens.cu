@@ -2,8 +2,11 @@
 // include/gs.h): argument checks on the host, before anything is enqueued.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <memory>
+#include <new>
 
 #include "gs_internal.h"
 #include "gs_tokens.h"
@@ -364,6 +367,35 @@ bool block_norm_ok(int64_t tokens, int32_t width, const gs_block_norm* n, const 
     return true;
 }
 
+// Whether no out of the arrays meets another, nor a gradient that is not its own.
+bool outs_apart(int32_t count, const gs_array* grads, const gs_array* outs, gs_status* st) {
+    struct Span {
+        uintptr_t begin, end;
+    };
+    const auto span = [](const gs_array& a) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(a.data);
+        return Span{at, at + (uintptr_t)a.elements * (a.type == GS_TYPE_BF16 ? 2 : 4)};
+    };
+    const std::unique_ptr<Span[]> spans(new (std::nothrow) Span[(size_t)count + 1]);
+    *st = spans ? GS_ERR_INVALID_ARG : GS_ERR_WORKSPACE;
+    if (!spans) return false;
+    int n = 0;
+    for (int32_t i = 0; i < count; ++i)
+        if (outs[i].elements > 0) spans[n++] = span(outs[i]);
+    const auto before = [](const Span& a, const Span& b) { return a.begin < b.begin; };
+    if (!std::is_sorted(&spans[0], &spans[n], before)) std::sort(&spans[0], &spans[n], before);
+    for (int i = 1; i < n; ++i)
+        if (spans[i].begin < spans[i - 1].end) return false;
+    for (int32_t i = 0; i < count; ++i) {
+        if (grads[i].data == outs[i].data || grads[i].elements == 0) continue;
+        const Span g = span(grads[i]);  // the first out that ends behind its start
+        const Span* o = std::upper_bound(&spans[0], &spans[n], g,
+                                         [](const Span& a, const Span& b) { return a.begin < b.end; });
+        if (o != &spans[n] && o->begin < g.end) return false;
+    }
+    return true;
+}
+
 ResidualNormArgs norm_args(int64_t tokens, int32_t width, const gs_block_norm& n,
                            const gs_norm_params& w, const int32_t* cu) {
     return {tokens,  width,  n.batch, n.type == GS_TYPE_BF16, n.pre, n.post,
@@ -450,6 +482,8 @@ gs_status gs_clip_grad_norm(int32_t count, const gs_array* grads, const gs_array
         all += g.elements;
     }
     if (all > (int64_t(1) << 42)) return GS_ERR_INVALID_ARG;
+    gs_status st;
+    if (!outs_apart(count, grads, outs, &st)) return st;
     if (workspace_bytes < clip_workspace_bytes(count)) return GS_ERR_WORKSPACE;
     return status_of(launch_clip(count, grads, outs, (double)max_norm, norm, workspace,
                                  (cudaStream_t)stream));

@@ -690,7 +690,8 @@ gs_status gs_residual_norm_bwd(int64_t tokens, int32_t width, const gs_block_nor
  *   grads      host array: device data (aligned to an element; at 16 bytes it goes faster, NULL
  *              where elements = 0), elements, and type
  *   outs       host array of the same elements and types; an out may be its gradient itself, but
- *              overlaps nothing else (no array is given twice).  NULL: all are their gradients.
+ *              overlaps nothing else (an array given twice in place, too): refused otherwise.
+ *              NULL: all are their gradients.
  *              Where norm <= max_norm, such outs are not written
  *   max_norm   >= 0; infinity: the norm alone is wanted, outs are as their gradients whatever these
  *              hold (NULL: nothing is written)

@@ -214,3 +214,28 @@ def test_binding_refuses_other_shapes(lib, fake):
         gs.gs_clip_grad_norm([x], 1.0, norm, ws, stream=0)
     with pytest.raises(ValueError, match="norm"):
         gs.gs_clip_grad_norm([x], 1.0, None, ws, stream=0)
+
+
+def test_clip_outputs_that_meet_are_refused(lib):
+    import differentiable_gaussian_splatting_gb300 as gs
+
+    def call(grads, outs=None):
+        n = len(grads)
+        g = (gs.Array * n)(*[gs.Array(*x) for x in grads])
+        o = (gs.Array * n)(*[gs.Array(*x) for x in outs]) if outs else None
+        # no workspace is that small: what the arrays pass, this refuses
+        return lib.gs_clip_grad_norm(n, g, o, 1.0, P, P, 8, None)
+
+    a, b, c = (P, 100, 0), (P + 400, 50, 1), (P + 8192, 7, 0)
+    apart = [(P + (1 << 20), 100, 0), (P + (2 << 20), 50, 1), (P + (3 << 20), 7, 0)]
+    assert call([a, b, c]) == 5 and call([c, a, b]) == 5
+    assert call([a, b, c], apart) == 5
+    assert call([a, (None, 0, 0), (P, 0, 0)]) == 5       # nothing in an empty array
+    assert call([a, a], [apart[0], (P + (4 << 20), 100, 0)]) == 5  # only read twice
+    assert call([a, a], [a, apart[0]]) == 1              # read while it is written
+    assert call([a, b, a]) == 1                          # in place twice
+    assert call([a, (P + 396, 50, 1)]) == 1              # by its last element
+    assert call([(P + 396, 50, 1), a]) == 1
+    assert call([a, b, c], [apart[0], apart[1], (P + (1 << 20) + 396, 7, 0)]) == 1
+    assert call([a, b, c], [apart[0], apart[1], (P + 4, 7, 0)]) == 1   # over a's gradient
+    assert call([a, b, c], [(P + 4, 100, 0), apart[1], apart[2]]) == 1  # over its own, moved
