@@ -279,6 +279,18 @@ inline cudaError_t launch_registers_ok(const void* kernel) {
     return a.numRegs == kLaunchRegisters ? cudaSuccess : cudaErrorInvalidConfiguration;
 }
 
+// A wait that may take as long as blocks do, for the blocks' planner and whoever waits for it: as
+// mbar_wait, with the limit of many tiles' waits.  (A tile that does not come ends it too: its own
+// wait gives up and sets `dead`.)
+constexpr int kBlockWaits = 64;
+__device__ __forceinline__ bool mbar_wait_block(uint32_t bar, uint32_t parity, volatile int* dead) {
+    bool there = mbar_try(bar, parity);
+    const long long t0 = clock64();
+    while (!there && !*dead && clock64() - t0 < kBlockWaits * kWaitClocks) there = mbar_try(bar, parity);
+    if (!there) *dead = 1;
+    return __all_sync(0xffffffffu, there);
+}
+
 // the window as the kernels take it
 inline Window window_of(const gs_window& w, bool causal) {
     return {w.left, causal ? 0 : w.right, w.sinks, causal};

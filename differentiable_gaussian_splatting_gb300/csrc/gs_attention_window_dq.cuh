@@ -189,7 +189,7 @@ __device__ __forceinline__ void window_dq_blocks(const CUtensorMap& map_q, const
             int n = 0;  // descriptions so far
             bool taken = false;  // whether block n has been asked for
             for (;;) {
-                if (n > 0 && !taken && !mbar_wait(smem_u32(&bar_want), (n - 1) & 1, &dead)) break;
+                if (n > 0 && !taken && !mbar_wait_block(smem_u32(&bar_want), (n - 1) & 1, &dead)) break;
                 taken = true;
                 unsigned int next = 0;
                 if (lane == 0) next = atomicAdd(p.next_dq, 1u);
@@ -206,7 +206,8 @@ __device__ __forceinline__ void window_dq_blocks(const CUtensorMap& map_q, const
                     }
                 }
                 const int slot = n % kDqWorks, use = n / kDqWorks;
-                if (use > 0 && !mbar_wait(smem_u32(&bar_work_free[slot]), (use - 1) & 1, &dead)) break;
+                if (use > 0 && !mbar_wait_block(smem_u32(&bar_work_free[slot]), (use - 1) & 1, &dead))
+                    break;
                 if (lane == 0) {
                     DqWork& w = works[slot];
                     w.last = end;
@@ -234,7 +235,7 @@ __device__ __forceinline__ void window_dq_blocks(const CUtensorMap& map_q, const
             bool ok = true;
             for (; ok; ++blocks) {
                 const int at = blocks % kDqWorks;
-                if (!mbar_wait(smem_u32(&bar_work[at]), (blocks / kDqWorks) & 1, &dead)) break;
+                if (!mbar_wait_block(smem_u32(&bar_work[at]), (blocks / kDqWorks) & 1, &dead)) break;
                 if (works[at].last) break;
                 const DqWork w = works[at];
                 __syncwarp();

@@ -390,7 +390,8 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                     }
                 }
                 const int slot = n % kWorks, use = n / kWorks;
-                if (use > 0 && !mbar_wait(smem_u32(&bar_work_free[slot]), (use - 1) & 1, &dead)) break;
+                if (use > 0 && !mbar_wait_block(smem_u32(&bar_work_free[slot]), (use - 1) & 1, &dead))
+                    break;
                 w.last = end;
                 if (lane == 0) {
                     works[slot] = w;
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                 const int head = w.head, khead = w.khead, m = w.sq.m, step0 = w.step0;
                 const Walk walk = w.walk;
                 const bool tail = k0 + m < p.batch.tk;
-    #pragma unroll
+#pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (!ok || tiles_of(w, t) == 0) continue;
                     // once the last block's scores of this query tile are formed
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                 const auto bar_of = [&](const Cursor& c) {
                     return c.t == 0 ? c.bar0 : Sh::kScores + c.bar1;
                 };
-                            // whether no step before took the key tile: it may still be on its way
+                // whether no step before took the key tile: it may still be on its way
                 const auto first_of_tile = [&](const Cursor& c) { return c.t == 0 || c.j >= c.end0; };
                 const auto move = [&](Cursor& c) {  // true: the key tile is left
                     if (++c.score == Sh::kScores) c.score = 0;
@@ -567,7 +568,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                     const Cursor s = at;
                     const bool add = s.t == 0 ? s.begun0 : s.begun1;
                     if (s.j < s.narrow) {
-    #pragma unroll
+#pragma unroll
                         for (int k = 0; k < kSinkCols / 16; ++k)
                             mma_ts(tmem_o(s.t), tmem_s(s.score) + k * 8,
                                    op_v + s.slot * kTileStep + k * 128, word_o, add || k > 0);
