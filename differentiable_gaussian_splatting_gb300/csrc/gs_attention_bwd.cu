@@ -88,13 +88,15 @@ struct BwdParams {
     float *parts_k, *parts_q;   // [pieces][rest][slot_rows][DP]: dK, then dV; dQ
     // With a window (batch.causal is not set then).  Every query may see the sinks: their blocks
     // take `sink_rows` queries each, `sink_blocks` in all, before the other blocks of keys, which
-    // leave the sinks out.  Sequences of more queries keep the pieces' sums in
-    // parts_s [slots][heads_k][dK, dV][sinks][DP].
+    // leave the sinks out.  Of sequences with more queries the pieces' sums are kept in
+    // parts_s [slots][heads_k][dK, dV][sinks][DP] and joined by the block that is done last,
+    // which it learns from sinks_done [slots][heads_k].
     Window window;
     int sink_rows;
     int64_t sink_blocks;
     float* parts_s;
-    unsigned int* next_dq;  // the next block of queries, counted from 0
+    unsigned int *next_dq, *sinks_done;  // the next block of queries, counted from 0
+    int64_t counters;                    // next_dq and sinks_done, side by side
 };
 
 // A sequence's first slot: there are sink_slots of them, and of sequences with more than `rows`
@@ -122,11 +124,11 @@ __device__ __forceinline__ int queries_of(const Window& w, const Sequence& sq, i
     return (q1 + kTileRows - 1) / kTileRows - *tile;
 }
 
-// keys of the block at row0 that are no sinks: first..end - 1
+// keys of the block at row0 that are no sinks (all, where there are no queries): first..end - 1
 __device__ __forceinline__ void window_keys(const Window& w, const Sequence& sq, int row0, int* first,
                                             int* end) {
     *end = min(sq.m, row0 + kTileRows);
-    *first = min(max(row0, w.sinks), *end);
+    *first = sq.n > 0 ? min(max(row0, w.sinks), *end) : min(row0, *end);
 }
 
 // key tiles that a block of queries sees
@@ -235,7 +237,9 @@ __global__ void __launch_bounds__(kDeltaThreads) attention_delta_kernel(const Bw
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (p.next_dq && blockIdx.x == 0 && threadIdx.x == 0) *p.next_dq = 0;
+    // (there are more threads than counters)
+    const int64_t counter = (int64_t)blockIdx.x * kDeltaThreads + threadIdx.x;
+    if (counter < p.counters) p.next_dq[counter] = 0;
     if (t < p.batch.tq && lane == 0) {
         const float l = p.lse[h * p.batch.tq + t];
         p.nlse[h * p.batch.tq + t] = l == -INFINITY ? l : l * -1.4426950408889634f;
@@ -352,6 +356,40 @@ struct DkvShape {
     static constexpr uint32_t kRows = (2 + 2 * kSlots) * kTileBytes;  // behind the tiles
     static constexpr uint32_t kSmem = kRows + kSlots * 2 * kTileRows * sizeof(float) + 1024;
 };
+
+// dK and dV of the sinks of a sequence that several blocks took, in the blocks' order, by the one that
+// is done last.  DP / 4 lanes a row.  (A kernel behind this one: 4 us.)
+template <int DP>
+__device__ __forceinline__ void join_sinks(const BwdParams& p, const BwdWork& w) {
+    __shared__ int last;
+    const Sequence sq = w.sq;
+    const int64_t slot = sink_slot(sq.q0, p.sink_rows);
+    const int pieces = (sq.n + p.sink_rows - 1) / p.sink_rows, sinks = p.window.sinks;
+    if (threadIdx.x == 0) {
+        __threadfence();
+        last = atomicAdd(p.sinks_done + slot * p.heads_k + w.khead, 1u) == (unsigned)pieces - 1;
+        __threadfence();
+    }
+    __syncthreads();
+    if (!last) return;
+    constexpr int kLanes = DP / 4;
+    const int lane = threadIdx.x % kLanes;
+    for (int r = threadIdx.x / kLanes; r < 2 * w.key_end; r += (int)blockDim.x / kLanes) {
+        const bool of_v = r >= w.key_end;
+        const int key = of_v ? r - w.key_end : r;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int z = 0; z < pieces; ++z) {
+            const int64_t row = ((slot + z) * p.heads_k + w.khead) * 2 * sinks + (of_v ? sinks : 0) + key;
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.parts_s) + row * kLanes + lane);
+            o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+        }
+        const float f = of_v ? 1.f : p.scale;
+        if (lane * 4 < p.dim)
+            *reinterpret_cast<uint2*>((of_v ? p.dv : p.dk).row(sq.k0 + key, w.khead) + lane * 4) =
+                make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
+    }
+}
 
 // kSinks: a block of the sinks (with a window)
 template <int DP, bool kWindow, bool kSinks>
@@ -662,6 +700,8 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
     tmem_fence_before();
     __syncthreads();
     if (dead && threadIdx.x == 0) atomicAdd(p.gave_up, 1u);
+    if constexpr (kSinks)
+        if (work.part >= 0 && !dead) join_sinks<DP>(p, work);
     if (warp == kMathWarps) {
         __syncwarp();
         tmem_fence_after();
@@ -1016,36 +1056,6 @@ __global__ void __launch_bounds__(kSumThreads) attention_sum_kernel(const BwdPar
     }
 }
 
-// dK and dV of the sinks of sequences that several blocks took, in their order; zeros where there
-// are no queries.  DP / 4 lanes a row; blockIdx.y = key head.
-template <int DP>
-__global__ void __launch_bounds__(kSumThreads) attention_sink_kernel(const BwdParams p) {
-    grid_dep_sync();
-    constexpr int kLanes = DP / 4, kRows = kSumThreads / kLanes;
-    const int lane = threadIdx.x % kLanes, head = blockIdx.y, sinks = p.window.sinks;
-    for (int b = blockIdx.x; b < p.batch.batch; b += gridDim.x) {
-        const Sequence sq = sequence(p.batch, b);
-        const int pieces = (sq.n + p.sink_rows - 1) / p.sink_rows, rows = min(sinks, sq.m);
-        if (pieces == 1) continue;  // its block has written them
-        const int64_t slot = sink_slot(sq.q0, p.sink_rows);
-        for (int r = threadIdx.x / kLanes; r < 2 * rows; r += kRows) {
-            const bool of_v = r >= rows;
-            const int key = of_v ? r - rows : r;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int z = 0; z < pieces; ++z) {
-                const int64_t row = ((slot + z) * p.heads_k + head) * 2 * sinks + (of_v ? sinks : 0) + key;
-                const float4 v = reinterpret_cast<const float4*>(p.parts_s)[row * kLanes + lane];
-                o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
-            }
-            const float f = of_v ? 1.f : p.scale;
-            if (lane * 4 < p.dim)
-                *reinterpret_cast<uint2*>((of_v ? p.dv : p.dk).row(sq.k0 + key, head) + lane * 4) =
-                    make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
-        }
-    }
-}
-
 // Cuts the last wave, or all blocks where they are fewer than the SMs, where a model of the
 // waves says that it pays, in units of one tile's time: a block costs its tiles and kStart,
 // the sum kSum; less than kGain of the whole is not worth it.  `items`: tiles that the longest
@@ -1105,6 +1115,10 @@ int sink_rows_of(const gs_window& w, int64_t tq) {
     const int64_t tiles = (w.left + (int64_t)w.right) / kTileRows + 2;
     return (int)std::max<int64_t>(1, std::min(tiles, tiles_of(tq))) * kTileRows;
 }
+// the counter of the blocks of queries, and those of the sinks' blocks that are done
+int64_t counters_of(const gs_window& w, int64_t tq, int heads_k) {
+    return 1 + (w.sinks > 0 ? sink_slots(tq, sink_rows_of(w, tq)) * heads_k : 0);
+}
 int64_t sink_floats(const gs_window& w, int64_t tq, int heads_k, int dp) {
     return sink_slots(tq, sink_rows_of(w, tq)) * heads_k * 2 * w.sinks * dp;
 }
@@ -1153,12 +1167,6 @@ cudaError_t launch_dim(const BwdMaps& m, BwdParams p, const gs_window* w, cudaSt
                    dim3(kWindow ? kWindowBwdThreads : kBwdThreads), kSmem, st, m.q, m.k, m.v, m.d, p);
     if (e == cudaSuccess) e = launch_sum<DP, true, kWindow>(p, st);
     if (e == cudaSuccess) e = launch_sum<DP, false, kWindow>(p, st);
-    if constexpr (kWindow)
-        // one sequence that one block takes: nothing is left to do
-        if (e == cudaSuccess && sinks && (v.batch > 1 || v.tq == 0 || v.tq > p.sink_rows))
-            e = launch(attention_sink_kernel<DP>,
-                       dim3((unsigned)std::min(v.batch, 8 * kSms), (unsigned)p.heads_k),
-                       dim3(kSumThreads), 0, st, p);
     return e;
 }
 
@@ -1168,7 +1176,7 @@ HeadView view(const gs_heads& h) {
 
 }  // namespace
 
-// -lse and -delta of every query row, then (with a window) the counter, then the pieces of both kinds
+// -lse and -delta of every query row, then (with a window) the counters, then the pieces of both kinds
 // of blocks
 size_t attention_bwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, int batch, int heads_q,
                                      int heads_k, int head_dim) {
@@ -1190,7 +1198,8 @@ size_t attention_window_bwd_workspace_bytes(int64_t tokens_q, int64_t tokens_k, 
     const int64_t rows =
         2 * part_rows(plan_dkv(tokens_q, tokens_k, batch, heads_q, heads_k, false, width)) +
         part_rows(plan_dq(tokens_q, tokens_k, batch, heads_q, false, width));
-    return ((size_t)tokens_q * heads_q * 2 * sizeof(float) + 255) / 256 * 256 + 256 +
+    return ((size_t)tokens_q * heads_q * 2 * sizeof(float) + 255) / 256 * 256 +
+           ((size_t)counters_of(w, tokens_q, heads_k) * sizeof(int) + 255) / 256 * 256 +
            (size_t)(rows * dp + sink_floats(w, tokens_q, heads_k, (int)dp)) * sizeof(float);
 }
 
@@ -1220,7 +1229,9 @@ cudaError_t launch_attention_bwd(const gs_attention_shape& s, const gs_heads& q,
     p.parts_k = p.nlse + (s.tokens_q * s.heads_q * 2 + 63) / 64 * 64;
     if (window) {
         p.next_dq = reinterpret_cast<unsigned int*>(p.parts_k);
-        p.parts_k += 64;
+        p.sinks_done = p.next_dq + 1;
+        p.counters = counters_of(*window, s.tokens_q, s.heads_k);
+        p.parts_k += (p.counters + 63) / 64 * 64;
     }
     cudaError_t e = gave_up_word(&p.gave_up);
     if (e != cudaSuccess) return e;
