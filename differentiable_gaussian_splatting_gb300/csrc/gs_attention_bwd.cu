@@ -95,8 +95,9 @@ struct BwdParams {
     int sink_rows;
     int64_t sink_blocks;
     float* parts_s;
-    unsigned int *next_dq, *sinks_done;  // the next block of queries, counted from 0
-    int64_t counters;                    // next_dq and sinks_done, side by side
+    unsigned int *next_dq, *next_dkv;  // the next blocks of queries and of keys, counted from 0
+    unsigned int* sinks_done;
+    int64_t counters;  // all of these, side by side
 };
 
 // A sequence's first slot: there are sink_slots of them, and of sequences with more than `rows`
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(kDeltaThreads) attention_delta_kernel(const Bw
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    // (there are more threads than counters)
+    // (there are more threads than counters; where there are no queries the first two count)
     const int64_t counter = (int64_t)blockIdx.x * kDeltaThreads + threadIdx.x;
     if (counter < p.counters) p.next_dq[counter] = 0;
     if (t < p.batch.tq && lane == 0) {
@@ -357,42 +358,7 @@ struct DkvShape {
     static constexpr uint32_t kSmem = kRows + kSlots * 2 * kTileRows * sizeof(float) + 1024;
 };
 
-// dK and dV of the sinks of a sequence that several blocks took, in the blocks' order, by the one that
-// is done last.  DP / 4 lanes a row.  (A kernel behind this one: 4 us.)
 template <int DP>
-__device__ __forceinline__ void join_sinks(const BwdParams& p, const BwdWork& w) {
-    __shared__ int last;
-    const Sequence sq = w.sq;
-    const int64_t slot = sink_slot(sq.q0, p.sink_rows);
-    const int pieces = (sq.n + p.sink_rows - 1) / p.sink_rows, sinks = p.window.sinks;
-    if (threadIdx.x == 0) {
-        __threadfence();
-        last = atomicAdd(p.sinks_done + slot * p.heads_k + w.khead, 1u) == (unsigned)pieces - 1;
-        __threadfence();
-    }
-    __syncthreads();
-    if (!last) return;
-    constexpr int kLanes = DP / 4;
-    const int lane = threadIdx.x % kLanes;
-    for (int r = threadIdx.x / kLanes; r < 2 * w.key_end; r += (int)blockDim.x / kLanes) {
-        const bool of_v = r >= w.key_end;
-        const int key = of_v ? r - w.key_end : r;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int z = 0; z < pieces; ++z) {
-            const int64_t row = ((slot + z) * p.heads_k + w.khead) * 2 * sinks + (of_v ? sinks : 0) + key;
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.parts_s) + row * kLanes + lane);
-            o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
-        }
-        const float f = of_v ? 1.f : p.scale;
-        if (lane * 4 < p.dim)
-            *reinterpret_cast<uint2*>((of_v ? p.dv : p.dk).row(sq.k0 + key, w.khead) + lane * 4) =
-                make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
-    }
-}
-
-// kSinks: a block of the sinks (with a window)
-template <int DP, bool kWindow, bool kSinks>
 __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtensorMap& map_k,
                                           const CUtensorMap& map_v, const CUtensorMap& map_d,
                                           const BwdParams& p, int64_t id) {
@@ -409,11 +375,7 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
-        bool ok;
-        if constexpr (kSinks)
-            ok = find_sink_work(p, id, &work);
-        else
-            ok = find_work<true, kWindow>(p, id, &work);
+        const bool ok = find_work<true, false>(p, id, &work);
         if (lane == 0) found = ok, dead = 0;
     }
     __syncthreads();
@@ -453,9 +415,8 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
     if (items > 0 && warp == kMathWarps + 1) {
         // ---- the producer ----
         const Sequence sq = work.sq;
-        int q_first = work.q_first;
-        const int per_head =
-            kWindow ? work.per_head : queries_of(sq, work.row0, p.batch.causal, &q_first);
+        int q_first;
+        const int per_head = queries_of(sq, work.row0, p.batch.causal, &q_first);
         if (elect_one()) {
             const int64_t key = sq.k0 + work.row0;
             mbar_expect(smem_u32(&bar_k), Sh::kTileBytes);
@@ -582,28 +543,18 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
         const uint32_t s_at = t_s + lanes + half * 64;
         const float sl = p.log2_scale;
         const int n = work.sq.n;
-        int q_first = work.q_first;
-        const int q_end =
-            (kWindow ? work.per_head : queries_of(work.sq, work.row0, p.batch.causal, &q_first)) +
-            q_first;
+        int q_first;
+        const int q_end = queries_of(work.sq, work.row0, p.batch.causal, &q_first) + q_first;
         // the first query that sees this thread's key; the last of the tile's keys' first
         const int ahead = work.row0 + n - work.sq.m;
-        int sees = p.batch.causal ? max(0, ahead + r) : 0;
-        int all_see = p.batch.causal ? max(0, ahead + kTileRows - 1) : 0;
-        // the query behind the last that sees it; the first of the tile's keys'
-        int sees_end = n, all_end = n;
-        if constexpr (kWindow) {
-            int unused;
-            seers_of(p.window, work.row0 + r, n, work.sq.m, &sees, &sees_end);
-            seers_of(p.window, work.row0 + work.key_first, n, work.sq.m, &unused, &all_end);
-            seers_of(p.window, work.row0 + work.key_end - 1, n, work.sq.m, &all_see, &unused);
-        }
+        const int sees = p.batch.causal ? max(0, ahead + r) : 0;
+        const int all_see = p.batch.causal ? max(0, ahead + kTileRows - 1) : 0;
         int tile = q_first + (items > 0 ? work.first % (q_end - q_first) : 0);
         for (int i = 0; i < items; ++i) {
             const int slot = i % Sh::kSlots, i0 = tile * kTileRows;
             if (++tile == q_end) tile = q_first;
-            const bool masked = i0 < all_see || i0 + kTileRows > all_end;
-            const int lo = sees - i0 - half * 64, hi = sees_end - i0 - half * 64;
+            const bool masked = i0 < all_see || i0 + kTileRows > n;
+            const int lo = sees - i0 - half * 64, hi = n - i0 - half * 64;
             mbar_pass(smem_u32(&full_q[slot]), (i / Sh::kSlots) & 1, &dead);
             mbar_pass(smem_u32(&bar_s), i & 1, &dead);
             tmem_fence_after();
@@ -625,10 +576,7 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
                 pr[c + 2] = ex2_approx(b.x);
                 pr[c + 3] = ex2_approx(b.y);
             }
-            if (kWindow && masked) {
-                mask_by_bits(pr, seen_bits(lo, hi, 0), 0.f);
-                mask_by_bits(pr + 32, seen_bits(lo - 32, hi - 32, 0), 0.f);
-            } else if (masked) {
+            if (masked) {
 #pragma unroll
                 for (int c = 0; c < 64; ++c)
                     if (c < lo || c >= hi) pr[c] = 0.f;
@@ -656,10 +604,7 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
                     __fadd2_rn(make_float2(dp[c + 2], dp[c + 3]), make_float2(v.z, v.w)));
                 dp[c] = a.x, dp[c + 1] = a.y, dp[c + 2] = b.x, dp[c + 3] = b.y;
             }
-            if (kWindow && masked) {
-                mask_by_bits(dp, seen_bits(lo, hi, 0), 0.f);
-                mask_by_bits(dp + 32, seen_bits(lo - 32, hi - 32, 0), 0.f);
-            } else if (masked) {
+            if (masked) {
 #pragma unroll
                 for (int c = 0; c < 64; ++c)
                     if (c < lo || c >= hi) dp[c] = 0.f;
@@ -674,34 +619,19 @@ __device__ __forceinline__ void dkv_block(const CUtensorMap& map_q, const CUtens
         if (!any_dead(&dead)) {
             tmem_fence_after();
             const int key = work.row0 + r;
-            const bool split = work.part >= 0;
+            const bool valid = key < work.sq.m, split = work.part >= 0;
             const HeadView& g = half ? p.dk : p.dv;
-            if constexpr (kWindow) {
-                const int row = (warp & 3) * 32;  // the warp's first
-                float* parts = kSinks ? p.parts_s + (work.part + row + (half ? 0 : p.window.sinks)) * DP
-                                      : p.parts_k + (work.part + row +
-                                                     (half ? 0 : part_rows(p.plan_k))) * DP;
-                store_rows<DP, DP>((half ? t_dk : t_dv) + lanes,
-                                   g.row(work.sq.k0 + work.row0 + row, work.khead), g.ts,
-                                   split ? parts : nullptr, work.key_first - row, work.key_end - row,
-                                   p.dim, half ? p.scale : 1.f, items == 0);
-            } else {
-                const bool valid = key < work.sq.m;
-                __nv_bfloat16* out =
-                    valid && !split ? g.row(work.sq.k0 + key, work.khead) : nullptr;
-                float* part = valid && split ? p.parts_k + (work.part + r +
-                                                            (half ? 0 : part_rows(p.plan_k))) * DP
-                                             : nullptr;
-                store_row<DP>((half ? t_dk : t_dv) + lanes, out, part, p.dim, half ? p.scale : 1.f,
-                              items == 0);
-            }
+            __nv_bfloat16* out = valid && !split ? g.row(work.sq.k0 + key, work.khead) : nullptr;
+            float* part = valid && split
+                              ? p.parts_k + (work.part + r + (half ? 0 : part_rows(p.plan_k))) * DP
+                              : nullptr;
+            store_row<DP>((half ? t_dk : t_dv) + lanes, out, part, p.dim, half ? p.scale : 1.f,
+                          items == 0);
         }
     }
     tmem_fence_before();
     __syncthreads();
     if (dead && threadIdx.x == 0) atomicAdd(p.gave_up, 1u);
-    if constexpr (kSinks)
-        if (work.part >= 0 && !dead) join_sinks<DP>(p, work);
     if (warp == kMathWarps) {
         __syncwarp();
         tmem_fence_after();
@@ -966,13 +896,13 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& map_q, const CUtenso
 }  // namespace
 }  // namespace gs
 
+#include "gs_attention_window_dkv.cuh"
 #include "gs_attention_window_dq.cuh"
 
 namespace gs {
 namespace {
 
-// The blocks of keys, then those of queries; with a window those of the sinks first, and for the
-// queries CTAs that go through their blocks.
+// The blocks of keys, then those of queries; with a window CTAs that go through their blocks.
 template <int DP, bool kWindow>
 __global__ void __launch_bounds__(kWindow ? kWindowBwdThreads : kBwdThreads, 1)
     attention_bwd_kernel(const __grid_constant__ CUtensorMap map_q,
@@ -980,21 +910,15 @@ __global__ void __launch_bounds__(kWindow ? kWindowBwdThreads : kBwdThreads, 1)
                          const __grid_constant__ CUtensorMap map_v,
                          const __grid_constant__ CUtensorMap map_d, const BwdParams p) {
     grid_dep_sync();
-    const int64_t of_keys = blocks_of(p.plan_k);
-    int64_t id = blockIdx.x;
     if constexpr (kWindow) {
-        if (id < p.sink_blocks) {
-            dkv_block<DP, true, true>(map_q, map_k, map_v, map_d, p, id);
-            return;
-        }
-        id -= p.sink_blocks;
+        window_bwd_blocks<DP>(map_q, map_k, map_v, map_d, p);
+    } else {
+        const int64_t of_keys = blocks_of(p.plan_k);
+        if (blockIdx.x < of_keys)
+            dkv_block<DP>(map_q, map_k, map_v, map_d, p, blockIdx.x);
+        else
+            dq_block<DP>(map_q, map_k, map_v, map_d, p, blockIdx.x - of_keys);
     }
-    if (id < of_keys)
-        dkv_block<DP, kWindow, false>(map_q, map_k, map_v, map_d, p, id);
-    else if constexpr (kWindow)
-        window_dq_blocks<DP>(map_q, map_k, map_v, map_d, p);
-    else
-        dq_block<DP>(map_q, map_k, map_v, map_d, p, id - of_keys);
 }
 
 // The sum of a cut block's pieces, in their order, times the scale, in bfloat16.  DP / 4
@@ -1115,9 +1039,9 @@ int sink_rows_of(const gs_window& w, int64_t tq) {
     const int64_t tiles = (w.left + (int64_t)w.right) / kTileRows + 2;
     return (int)std::max<int64_t>(1, std::min(tiles, tiles_of(tq))) * kTileRows;
 }
-// the counter of the blocks of queries, and those of the sinks' blocks that are done
+// the counters of the blocks of either kind, and those of the sinks' blocks that are done
 int64_t counters_of(const gs_window& w, int64_t tq, int heads_k) {
-    return 1 + (w.sinks > 0 ? sink_slots(tq, sink_rows_of(w, tq)) * heads_k : 0);
+    return 2 + (w.sinks > 0 ? sink_slots(tq, sink_rows_of(w, tq)) * heads_k : 0);
 }
 int64_t sink_floats(const gs_window& w, int64_t tq, int heads_k, int dp) {
     return sink_slots(tq, sink_rows_of(w, tq)) * heads_k * 2 * w.sinks * dp;
@@ -1159,11 +1083,10 @@ cudaError_t launch_dim(const BwdMaps& m, BwdParams p, const gs_window* w, cudaSt
     constexpr uint32_t kSmem = std::max(DkvShape<DP>::kSmem, DqShape<DP>::kSmem);
     cudaError_t e = cudaFuncSetAttribute(
         attention_bwd_kernel<DP, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-    const int64_t of_q = blocks_of(p.plan_q);
+    const int64_t blocks = p.sink_blocks + blocks_of(p.plan_k) + blocks_of(p.plan_q);
     if (e == cudaSuccess)
         e = launch(attention_bwd_kernel<DP, kWindow>,
-                   dim3((unsigned)(p.sink_blocks + blocks_of(p.plan_k) +
-                                   (kWindow ? std::min<int64_t>(of_q, kSms) : of_q))),
+                   dim3((unsigned)(kWindow ? std::min<int64_t>(blocks, kSms) : blocks)),
                    dim3(kWindow ? kWindowBwdThreads : kBwdThreads), kSmem, st, m.q, m.k, m.v, m.d, p);
     if (e == cudaSuccess) e = launch_sum<DP, true, kWindow>(p, st);
     if (e == cudaSuccess) e = launch_sum<DP, false, kWindow>(p, st);
@@ -1229,7 +1152,8 @@ cudaError_t launch_attention_bwd(const gs_attention_shape& s, const gs_heads& q,
     p.parts_k = p.nlse + (s.tokens_q * s.heads_q * 2 + 63) / 64 * 64;
     if (window) {
         p.next_dq = reinterpret_cast<unsigned int*>(p.parts_k);
-        p.sinks_done = p.next_dq + 1;
+        p.next_dkv = p.next_dq + 1;
+        p.sinks_done = p.next_dkv + 1;
         p.counters = counters_of(*window, s.tokens_q, s.heads_k);
         p.parts_k += (p.counters + 63) / 64 * 64;
     }
@@ -1249,8 +1173,8 @@ cudaError_t launch_attention_bwd(const gs_attention_shape& s, const gs_heads& q,
     if (s.tokens_q == 0) m.q = m.d = m.k;  // nothing is loaded by them
     if (s.tokens_k == 0) m.k = m.v = m.q;
     if (e != cudaSuccess) return e;
-    if (p.batch.tq > 0) {
-        const int64_t threads = p.batch.tq * s.heads_q * 16;
+    if (p.batch.tq > 0 || window) {
+        const int64_t threads = std::max<int64_t>(p.batch.tq * s.heads_q * 16, 1);
         e = launch(attention_delta_kernel,
                    dim3((unsigned)((threads + kDeltaThreads - 1) / kDeltaThreads)),
                    dim3(kDeltaThreads), 0, st, p);

@@ -47,10 +47,11 @@ __device__ __forceinline__ void write_no_dq(const BwdParams& p, const BwdWork& w
     }
 }
 
+// A CTA: its blocks of keys (gs_attention_window_dkv.cuh), then its blocks of queries.
 template <int DP>
-__device__ __forceinline__ void window_dq_blocks(const CUtensorMap& map_q, const CUtensorMap& map_k,
-                                                 const CUtensorMap& map_v, const CUtensorMap& map_d,
-                                                 const BwdParams& p) {
+__device__ __forceinline__ void window_bwd_blocks(const CUtensorMap& map_q, const CUtensorMap& map_k,
+                                                  const CUtensorMap& map_v, const CUtensorMap& map_d,
+                                                  const BwdParams& p) {
     using Sh = DqShape<DP>;
     extern __shared__ char smem_raw[];
     __shared__ uint64_t bar_q, bar_d, bar_q_free, bar_d_free, bar_s[2], bar_dp, bar_read, bar_ds[2],
@@ -60,6 +61,7 @@ __device__ __forceinline__ void window_dq_blocks(const CUtensorMap& map_q, const
     __shared__ uint32_t tmem_at;
     __shared__ volatile int dead;
     __shared__ DqWork works[kDqWorks];
+    __shared__ DkvState<DP> dkv;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -85,6 +87,7 @@ __device__ __forceinline__ void window_dq_blocks(const CUtensorMap& map_q, const
             mbar_init(smem_u32(&bar_work[i]), 1);
             mbar_init(smem_u32(&bar_work_free[i]), kDqReaders);
         }
+        dkv.init();
         fence_barrier_init();
     }
     tmem_fence_before();
@@ -92,9 +95,20 @@ __device__ __forceinline__ void window_dq_blocks(const CUtensorMap& map_q, const
     tmem_fence_after();
     // all 512 columns are the CTA's: their addresses start at 0
     constexpr uint32_t tmem = 0, t_dp = 256, t_dq = 384;
+    // Between the two kinds of blocks: all warps are through with the first, whose shared and tensor
+    // memory the second one takes.  False: a wait has given up.
+    const auto next_kind = [&]() {
+        tmem_fence_before();
+        fence_async_shared();
+        __syncthreads();
+        tmem_fence_after();
+        return !any_dead(&dead);
+    };
 
     if (warp < kMathWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMathRegisters));
+        dkv_math<DP>(p, smem_raw, smem, dkv, &dead);
+        bool go = next_kind();
         // ---- dS: one query a thread, half of the tile's keys ----
         const int half = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
@@ -102,7 +116,7 @@ __device__ __forceinline__ void window_dq_blocks(const CUtensorMap& map_q, const
         const float sl = p.log2_scale;
         const float2 sl2 = make_float2(sl, sl);
         int x = 0;  // steps of all blocks
-        for (int n = 0;; ++n) {
+        for (int n = 0; go; ++n) {
             const int slot = n % kDqWorks;
             if (!mbar_wait(smem_u32(&bar_work[slot]), (n / kDqWorks) & 1, &dead)) break;
             const DqWork& w = works[slot];
@@ -185,10 +199,12 @@ __device__ __forceinline__ void window_dq_blocks(const CUtensorMap& map_q, const
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters));
         if (warp == kDqPlanner) {
             // ---- the planner ----
+            dkv_plan<DP>(p, dkv, &dead);
+            const bool go = next_kind();
             const int64_t blocks = blocks_of(p.plan_q);
             int n = 0;  // descriptions so far
             bool taken = false;  // whether block n has been asked for
-            for (;;) {
+            while (go) {
                 if (n > 0 && !taken && !mbar_wait_block(smem_u32(&bar_want), (n - 1) & 1, &dead)) break;
                 taken = true;
                 unsigned int next = 0;
@@ -230,9 +246,10 @@ __device__ __forceinline__ void window_dq_blocks(const CUtensorMap& map_q, const
             }
         } else if (warp == kMathWarps + 1) {
             // ---- the producer: Q, the first K, dO, then V and K in turn ----
+            dkv_bring<DP>(map_q, map_k, map_v, map_d, p, smem_raw, smem, dkv, &dead);
             int blocks = 0, tiles_k = 0, tiles_v = 0, mends = 0;  // brought so far
             int loads_q = 0, loads_d = 0;
-            bool ok = true;
+            bool ok = next_kind();
             for (; ok; ++blocks) {
                 const int at = blocks % kDqWorks;
                 if (!mbar_wait_block(smem_u32(&bar_work[at]), (blocks / kDqWorks) & 1, &dead)) break;
@@ -308,7 +325,9 @@ __device__ __forceinline__ void window_dq_blocks(const CUtensorMap& map_q, const
             drain_ring<Sh::kSlotsV>(full_v, tiles_v);
         } else if (warp == kMathWarps) {
             // ---- the products ----
-            if (elect_one()) {
+            if (elect_one()) dkv_multiply<DP>(p, smem_raw, smem, dkv, &dead);
+            __syncwarp();
+            if (next_kind() && elect_one()) {
                 constexpr uint32_t word_o = mma_word(128, DP, false, true);
                 constexpr uint32_t word_dp = mma_word(128, 128, false, false);
                 const uint32_t word_s = word_dp | (p.negative ? kNegateA : 0u);
@@ -391,6 +410,8 @@ __device__ __forceinline__ void window_dq_blocks(const CUtensorMap& map_q, const
                 mma_commit(smem_u32(&bar_all));
                 mbar_drain(smem_u32(&bar_all), 0);
             }
+        } else {
+            next_kind();
         }
     }
     tmem_fence_before();

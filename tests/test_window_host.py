@@ -152,7 +152,8 @@ def _source(name):
 
 @pytest.mark.parametrize("file,drain,rings,once", [
     ("gs_attention_window_fwd.cu", "bar_drain", {"bar_full"}, {"bar_q[t]"}),
-    ("gs_attention_window_dq.cuh", "bar_all", {"full_k", "full_v"}, {"bar_q", "bar_d"})])
+    ("gs_attention_window_dq.cuh", "bar_all", {"full_k", "full_v"}, {"bar_q", "bar_d"}),
+    ("gs_attention_window_dkv.cuh", "sh.bar_all", {"full_q", "full_d"}, {"sh.bar_k", "sh.bar_v"})])
 def test_no_copy_or_product_outlives_a_cta(file, drain, rings, once):
     # Whoever issued asynchronous work waits for it last of all, whether or not a wait has given up.
     # (What such a CTA does cannot be run: here the sources are held to it.)
@@ -160,9 +161,9 @@ def test_no_copy_or_product_outlives_a_cta(file, drain, rings, once):
     assert len(re.findall(rf"mma_commit\(smem_u32\(&{drain}\)\);\s*"
                           rf"mbar_drain\(smem_u32\(&{drain}\), 0\);", text)) == 1
     assert set(re.findall(r"drain_ring<Sh::\w+>\((\w+), \w+\)", text)) == rings
-    assert once <= set(re.findall(r"mbar_drain\(smem_u32\(&([\w\[\]]+)\)", text))
+    assert once <= set(re.findall(r"mbar_drain\(smem_u32\(&([\w.\[\]]+)\)", text))
     # a copy that is mended before it counts is waited for where that wait gives up
-    assert re.search(r"mbar_wait\(bar, parity, &dead\);\s*if \(!ok\) \{\s*mbar_drain\(bar, parity\);",
+    assert re.search(r"mbar_wait\(bar, parity, &?dead\);\s*if \(!ok\) \{\s*mbar_drain\(bar, parity\);",
                      text)
     # every wait is one of the bounded ones
     assert not re.search(r"while\s*\(\s*!?\s*mbar_try", text)
