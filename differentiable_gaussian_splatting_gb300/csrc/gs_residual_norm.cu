@@ -578,6 +578,7 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
 // pairs.  blockIdx.y: which of the four gradients, or behind them a sequence's gate (and every
 // gridDim.y - 4 th from it on): of those that several blocks met, and zeros for empty ones.
 constexpr int kFinishCols = 32, kFinishThreads = 1024, kFinishOf = kFinishThreads / kFinishCols;
+constexpr int kFinishLoads = 10;  // of a thread at once: two rounds for 608 blocks
 struct FourGradients {
     float* g[4];
 };
@@ -587,8 +588,16 @@ __device__ __forceinline__ void sum_blocks(float (*s)[kFinishCols], const float*
     const int col = threadIdx.x % kFinishCols, row = threadIdx.x / kFinishCols;
     float a = 0.f;
     if (has)
-#pragma unroll 8
-        for (int b = row; b < count; b += kFinishOf) a += __ldg(part + (first + b) * step);
+        for (int b0 = row; b0 < count; b0 += kFinishLoads * kFinishOf) {
+            float v[kFinishLoads];
+#pragma unroll
+            for (int k = 0; k < kFinishLoads; ++k) {
+                const int b = b0 + k * kFinishOf;
+                v[k] = b < count ? __ldg(part + (first + b) * step) : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < kFinishLoads; ++k) a += v[k];
+        }
     s[row][col] = a;
 #pragma unroll
     for (int o = kFinishOf / 2; o > 0; o >>= 1) {
