@@ -298,11 +298,9 @@ struct RowSum {
     }
 };
 
-// the values less their mean (layer norms), zero where there is none
+// the values less their mean m (layer norms), zero where there is none
 template <bool kVec, int kPairs>
-__device__ __forceinline__ void centre(Values<kPairs>& a, const Columns<kVec, kPairs>& c,
-                                       RowSum& sums) {
-    const float m = sums.mean(total(a));
+__device__ __forceinline__ void centre(Values<kPairs>& a, const Columns<kVec, kPairs>& c, float m) {
 #pragma unroll
     for (int k = 0; k < kPairs; ++k) a.v[k] = add(a.v[k], both(-m));
     c.trim(a);
@@ -355,8 +353,8 @@ __device__ __forceinline__ void mix_of(const RnParams& p, const Columns<kVec, kP
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-// kLayer: one of the norms is a layer norm.  Without, the mean square of the next row's y is formed
-// with a sum of this row.
+// kLayer: one of the norms is a layer norm.  The statistics of the next row's y are formed with sums of
+// this row, where there are such (ahead).
 template <typename T, bool kVec, int kPairs, bool kLayer, bool kBias, int kThreads>
 __global__ void __launch_bounds__(kThreads) residual_norm_kernel(const RnParams p) {
     grid_dep_sync();
@@ -382,9 +380,17 @@ __global__ void __launch_bounds__(kThreads) residual_norm_kernel(const RnParams 
         if (p.y.p) y.load(p.y.at(row, shift), c);
     };
     load((uint32_t)t);
-    const bool ahead = !kLayer && p.post != GS_NORM_NONE && p.pre != GS_NORM_NONE;
-    float square = 0.f;  // mean of y^2 where it is formed ahead
-    if (ahead) square = sums.mean(dot(y.get(), y.get()));
+    const bool centred = kLayer && p.post == GS_NORM_LAYER, centred_r = kLayer && p.pre == GS_NORM_LAYER;
+    const bool ahead = p.post != GS_NORM_NONE && p.pre != GS_NORM_NONE && (!centred || centred_r);
+    float mean_y = 0.f, square = 0.f;  // of y and, less its mean (layer norms), of y^2
+    const auto statistics = [&](V u) {
+        if (centred) {
+            mean_y = sums.mean(total(u));
+            centre(u, c, mean_y);
+        }
+        square = sums.mean(dot(u, u));
+    };
+    if (ahead) statistics(y.get());
     for (; t < end; ++t) {
         V v = x.get(), u = y.get();
         if (t + 1 < end) load((uint32_t)t + 1);
@@ -393,8 +399,8 @@ __global__ void __launch_bounds__(kThreads) residual_norm_kernel(const RnParams 
             mix_of(p, c, at.b, &factor, kBias ? &rest : nullptr);
         }
         if (p.post != GS_NORM_NONE) {
-            if (kLayer && p.post == GS_NORM_LAYER) centre(u, c, sums);
-            if (!ahead) square = sums.mean(dot(u, u));
+            if (!ahead) statistics(u);
+            if (centred) centre(u, c, mean_y);
             const float2 f = both(rsqrtf(square + p.eps));
 #pragma unroll
             for (int k = 0; k < kPairs; ++k) u.v[k] = mul(u.v[k], f);
@@ -408,12 +414,17 @@ __global__ void __launch_bounds__(kThreads) residual_norm_kernel(const RnParams 
         c.trim(v);
         float s;
         if (ahead) {
-            const V next = y.get();
+            V next = y.get();
+            if (centred_r) {
+                const float4 m = sums.mean(total(v), centred ? total(next) : 0.f, 0.f, 0.f);
+                centre(v, c, m.x);
+                if (centred) centre(next, c, mean_y = m.y);
+            }
             const float4 m = sums.mean(dot(v, v), dot(next, next), 0.f, 0.f);
             s = m.x;
             square = m.y;
         } else {
-            if (kLayer && p.pre == GS_NORM_LAYER) centre(v, c, sums);
+            if (centred_r) centre(v, c, sums.mean(total(v)));
             s = sums.mean(dot(v, v));
         }
         const float2 f = both(rsqrtf(s + p.eps));
@@ -488,9 +499,17 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
             c.store(p.part_gate + ((int64_t)blockIdx.x * 2 + (from_before ? 0 : 1)) * p.width, d);
     };
     load((uint32_t)t);
-    const bool ahead = !kLayer && p.post != GS_NORM_NONE;
-    float square = 0.f;  // mean of y^2 where it is formed ahead
-    if (ahead) square = sums.mean(dot(y.get(), y.get()));
+    const bool centred = kLayer && p.post == GS_NORM_LAYER;
+    const bool ahead = p.post != GS_NORM_NONE && (!centred || p.pre != GS_NORM_NONE);
+    float mean_y = 0.f, square = 0.f;  // of y and, less its mean (layer norms), of y^2
+    const auto statistics = [&](V u) {
+        if (centred) {
+            mean_y = sums.mean(total(u));
+            centre(u, c, mean_y);
+        }
+        square = sums.mean(dot(u, u));
+    };
+    if (ahead) statistics(y.get());
     for (; t < end; ++t) {
         V v = x.get(), u = y.get(), d = dr.get();
         const V g = dh.get();
@@ -504,8 +523,8 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
         const bool held = at.b >= 0;
         float fu = 1.f;
         if (p.post != GS_NORM_NONE) {
-            if (kLayer && p.post == GS_NORM_LAYER) centre(u, c, sums);
-            if (!ahead) square = sums.mean(dot(u, u));
+            if (!ahead) statistics(u);
+            if (centred) centre(u, c, mean_y);
             fu = rsqrtf(square + p.eps);
 #pragma unroll
             for (int k = 0; k < kPairs; ++k) u.v[k] = mul(u.v[k], both(fu));  // un
@@ -517,11 +536,13 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
                               kBias ? fma2(u.v[k], factor.v[k], rest.v[k])
                                     : mul(u.v[k], factor.v[k]));
             c.trim(v);
-            if (kLayer && p.pre == GS_NORM_LAYER) centre(v, c, sums);
+            if (kLayer && p.pre == GS_NORM_LAYER) centre(v, c, sums.mean(total(v)));
             V w;
 #pragma unroll
             for (int k = 0; k < kPairs; ++k) w.v[k] = mul(pw.v[k], g.v[k]);
-            const float4 s = sums.mean(dot(v, v), dot(w, v), kLayer ? total(w) : 0.f, 0.f);
+            const float4 s = sums.mean(dot(v, v), dot(w, v), kLayer ? total(w) : 0.f,
+                                       centred ? total(y.get()) : 0.f);
+            if (centred) mean_y = s.w;  // the next row's
             const float f = rsqrtf(s.x + p.eps);
             const float2 f2 = both(f), along = both(-s.y * f * f);
             const float2 mean = both(kLayer && p.pre == GS_NORM_LAYER ? -s.z : 0.f);
@@ -551,13 +572,14 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
             c.trim(d);
             float4 s;
             if (ahead) {
-                const V next = y.get();
-                s = sums.mean(dot(d, u), dot(next, next), 0.f, 0.f);
+                V next = y.get();
+                if (centred) centre(next, c, mean_y);
+                s = sums.mean(dot(d, u), dot(next, next), kLayer ? total(d) : 0.f, 0.f);
                 square = s.y;
             } else {
-                s = sums.mean(dot(d, u), total(d), 0.f, 0.f);
+                s = sums.mean(dot(d, u), 0.f, total(d), 0.f);
             }
-            const float2 along = both(-s.x), mean = both(p.post == GS_NORM_LAYER ? -s.y : 0.f);
+            const float2 along = both(-s.x), mean = both(centred ? -s.z : 0.f);
 #pragma unroll
             for (int k = 0; k < kPairs; ++k) {
                 if (kLayer) d.v[k] = add(d.v[k], mean);
