@@ -10,7 +10,9 @@
 namespace gs {
 namespace {
 
-// Descriptions in flight, and how late the next one is taken: see kDqWorks.
+// Descriptions in flight, and how many steps before a block's end the next one is taken: see kDqWorks.
+// (2,500 + 1,104 tokens x 8 heads x 64, 513 keys: 41.9 us with 2, 41.0 with 4, 41.3 with 8; a CTA a block
+// 44.9.)
 constexpr int kDkvWorks = 2, kDkvLate = 4;
 // who lets go of a description: the math warps, the producer and the thread of the products
 constexpr int kDkvReaders = kMathWarps + 2;

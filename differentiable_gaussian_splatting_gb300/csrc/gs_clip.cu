@@ -10,7 +10,9 @@
 // the constant cache after the other).
 //
 // Memory bounds it: the arrays are read, then read and written.  The second kernel walks a block's
-// chunks backwards, so that it meets first what the first one left in L2.
+// chunks backwards, so that it meets first what the first one left in L2.  88.5M fp32 values: 175 us,
+// 6.1 TB/s of three times their bytes; 139M bfloat16 ones 145 us; 2.4M fp32 ones (L2 holds them) 11.0 us,
+// the latency of two kernels.
 //
 // Sums.  A thread's squares of one chunk (at most 64) go into fp32, the chunks' sums into pairs of
 // fp32 (a sum and what its roundings left), the blocks' into fp64, whose units take a third of the
@@ -33,8 +35,8 @@ namespace gs {
 namespace {
 
 constexpr int kClipThreads = 256;
-// Four blocks an SM and chunks of 32 KB (six and 16 KB: 12.8 us instead of 11.8 on 2.4M fp32 values,
-// 180 instead of 176 on 88.5M).
+// Four blocks an SM and chunks of 32 KB (six and 16 KB: 12.6 us instead of 11.0 on 2.4M fp32 values,
+// 181 instead of 175 on 88.5M).
 constexpr int kVecs = 8;  // 16-byte words a thread takes of a chunk
 constexpr int kChunkBytes = kClipThreads * kVecs * 16;
 constexpr int kBlocks = 152 * 4;  // resident at once

@@ -309,3 +309,11 @@ def test_queries_that_are_not_finite_say_so(lens_q, lens_k):
     assert out[hit].isnan().all() and lse.t()[hit].isnan().all()
     assert torch.equal(out[~hit], clean[0][~hit])
     assert torch.equal(lse.t()[~hit], clean[1].t()[~hit])
+
+
+@pytest.mark.parametrize("hq,hk,D", [(8, 2, 128), (4, 2, 64), (10, 1, 40), (2, 2, 64)])
+@pytest.mark.parametrize("window,causal", [((90, 0, 4), True), ((40, 3, 100), False), ((0, 0, 0), True)])
+def test_some_queries_of_every_sequence(hq, hk, D, window, causal):
+    # by the kernel of few queries or by tiles, as the heads on a key head decide
+    rng, q, k, v = _inputs(15, 1161, hq, hk, D, seed=12)
+    _check(q, k, v, D ** -0.5, window, causal, [3, 5, 1, 4, 2], [300, 4, 0, 857, 0])
