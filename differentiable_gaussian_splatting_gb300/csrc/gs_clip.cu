@@ -10,8 +10,8 @@
 // the constant cache after the other).
 //
 // Memory bounds it: the arrays are read, then read and written.  The second kernel walks a block's
-// chunks backwards, so that it meets first what the first one left in L2.  88.5M fp32 values: 175 us,
-// 6.1 TB/s of three times their bytes; 139M bfloat16 ones 145 us; 2.4M fp32 ones (L2 holds them) 11.0 us,
+// chunks backwards, so that it meets first what the first one left in L2.  88.5M fp32 values: 169 us,
+// 6.3 TB/s of three times their bytes; 139M bfloat16 ones 143 us; 2.4M fp32 ones (L2 holds them) 11.0 us,
 // the latency of two kernels.
 //
 // Sums.  A thread's squares of one chunk (at most 64) go into fp32, the chunks' sums into pairs of
@@ -36,10 +36,13 @@ namespace {
 
 constexpr int kClipThreads = 256;
 // Four blocks an SM and chunks of 32 KB (six and 16 KB: 12.6 us instead of 11.0 on 2.4M fp32 values,
-// 181 instead of 175 on 88.5M).
+// 181 instead of 175 on 88.5M, all read alike).
 constexpr int kVecs = 8;  // 16-byte words a thread takes of a chunk
 constexpr int kChunkBytes = kClipThreads * kVecs * 16;
 constexpr int kBlocks = 152 * 4;  // resident at once
+// What is to stay in L2 from the first kernel to the second.  (Half of L2; 88.5M fp32 values: 175 us
+// where all is read alike, 171 with 40 MB, 169 with 64 and 96.)
+constexpr int64_t kKeptBytes = 64 << 20;
 constexpr int kFewArrays = 96, kManyArrays = 1024;  // of a table: 5 KB and 31 KB of parameters
 constexpr int kMaxTables = 64;
 
@@ -157,6 +160,9 @@ __global__ void __launch_bounds__(kClipThreads, 4)
     grid_dep_sync();
     const int chunks = t.chunk0[t.count];
     const int end = first_chunk(chunks, gridDim.x, blockIdx.x + 1);
+    // the last chunks, which the second kernel takes first; the others are the first to leave L2
+    const int kept =
+        end - max(1, (int)(kKeptBytes / ((int64_t)gridDim.x * kChunkBytes)));
     int array = t.first[blockIdx.x];
     Sum sum;
     for (int id = first_chunk(chunks, gridDim.x, blockIdx.x); id < end; ++id) {
@@ -166,8 +172,11 @@ __global__ void __launch_bounds__(kClipThreads, 4)
         if (whole) {
             uint4 w[kVecs];
 #pragma unroll
-            for (int k = 0; k < kVecs; ++k)
-                w[k] = __ldg(reinterpret_cast<const uint4*>(c.in) + k * kClipThreads + threadIdx.x);
+            for (int k = 0; k < kVecs; ++k) {
+                const uint4* from =
+                    reinterpret_cast<const uint4*>(c.in) + k * kClipThreads + threadIdx.x;
+                w[k] = id >= kept ? __ldg(from) : __ldcs(from);
+            }
             if (c.bf16) {
                 float v[8 * kVecs];
 #pragma unroll
