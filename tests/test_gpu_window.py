@@ -317,3 +317,29 @@ def test_some_queries_of_every_sequence(hq, hk, D, window, causal):
     # by the kernel of few queries or by tiles, as the heads on a key head decide
     rng, q, k, v = _inputs(15, 1161, hq, hk, D, seed=12)
     _check(q, k, v, D ** -0.5, window, causal, [3, 5, 1, 4, 2], [300, 4, 0, 857, 0])
+
+
+@pytest.mark.parametrize("lens_q,lens_k", [([1, 0, 2], [200, 10, 90]), ([270, 0, 33], [300, 9, 33]),
+                                           ([0, 0, 0], [50, 0, 2]), ([5, 0, 300], [0, 0, 0])])
+@pytest.mark.parametrize("more", [4, 300])
+def test_rows_behind_the_last_sequence_stay(lens_q, lens_k, more):
+    import torch
+
+    import differentiable_gaussian_splatting_gb300 as gs
+
+    nq, nk, window = sum(lens_q), sum(lens_k), (60, 5, 4)
+    Tq, Tk = nq + more, nk + 140
+    rng, q, k, v = _inputs(Tq, Tk, 2, 1, 64, seed=3)
+    t = [_dev(x) for x in (q, k, v)]
+    cu = [torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32, device="cuda")
+          for n in (lens_q, lens_k)]
+    ws = torch.full((gs.gs_attention_window_workspace_bytes(Tq, Tk, 3, 2, 1, 64, *window),), 255,
+                    dtype=torch.uint8, device="cuda")
+    out, lse = torch.full_like(t[0], 7.0), torch.full((2, Tq), 7.0, device="cuda")
+    g = [torch.full_like(x, 7.0) for x in t]
+    kw = dict(cu_q=cu[0], cu_k=cu[1])
+    gs.gs_attention_window_fwd(*t, out, lse, ws, *window, **kw)
+    gs.gs_attention_window_bwd(*t, out, lse, t[0], *g, ws, *window, **kw)
+    for x, n in ((out, nq), (lse.t(), nq), (g[0], nq), (g[1], nk), (g[2], nk)):
+        assert (x[n:] == 7.0).all() and not x[:n].float().isnan().any()
+        assert not (x[:n] == 7.0).all(1).any()
