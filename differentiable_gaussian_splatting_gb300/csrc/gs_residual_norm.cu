@@ -17,15 +17,15 @@
 // held in registers from the first sum over the row to the last, so nothing is read twice; a row
 // of at most 256 values is one warp's and its sums need no barrier.  Weights and gates stay in
 // registers, the gate multiplied into post's weight and bias: read from L1 for every row they kept
-// L1 busier than the arrays did.  A block has consecutive rows, reads the next one while it works on
-// the present one, and keeps sums of the column gradients in registers: of the weights and biases over
+// L1 busier than the arrays did.  A block has consecutive rows, reads the next ones while it works
+// on the present one, and keeps sums of the column gradients in registers: of the weights and biases over
 // all its rows, of the gate over those of a sequence.  Another kernel adds the blocks' sums up in the
 // blocks' order: the same inputs give the same bits.
 //
-// Measured, 32,400 x 1,024 in bfloat16 with RMS norms on both sides and a gate: forward 49.6 us, 5.35
-// TB/s, 0.79 of the copy rate; backward 88.4 us, 4.5 TB/s, with two or three sums over a row and 16 warps
+// Measured, 32,400 x 1,024 in bfloat16 with RMS norms on both sides and a gate: forward 49.2 us, 5.4
+// TB/s, 0.79 of the copy rate; backward 79.6 us, 5.0 TB/s, with two or three sums over a row and 16 warps
 // an SM (128 registers) on the way, and 8 us of the blocks' sums.  64 x 256: 4.2 us, the latency of a
-// row.  Odd widths go value by value: 4,346 x 515 in fp32 with layer norms and biases, backward, 31 us.
+// row.  Odd widths go value by value: 4,346 x 515 in fp32 with layer norms and biases, backward, 30.5 us.
 //
 // All sums and statistics are fp32, the variance from the differences to the mean.
 #include <cuda_bf16.h>
@@ -179,6 +179,7 @@ struct RawRow<float, kVec, kPairs> {
     using C = Columns<kVec, kPairs>;
     using V = Values<kPairs>;
     V r;
+    static constexpr int kWords = kPairs / 2;  // of 16 bytes
     __device__ __forceinline__ void clear() { r = V{}; }
     __device__ __forceinline__ void load(const char* at, const C& c) {
         float* v = &r.v[0].x;
@@ -204,6 +205,14 @@ struct RawRow<__nv_bfloat16, kVec, kPairs> {
     using C = Columns<kVec, kPairs>;
     using V = Values<kPairs>;
     uint32_t w[kPairs];
+    static constexpr int kWords = kPairs / 4;  // of 16 bytes
+    __device__ __forceinline__ void take(const uint4* from, int step) {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+            const uint4 a = from[k * step];
+            w[4 * k] = a.x, w[4 * k + 1] = a.y, w[4 * k + 2] = a.z, w[4 * k + 3] = a.w;
+        }
+    }
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) w[k] = 0;
@@ -340,6 +349,35 @@ __device__ __forceinline__ Part part_of(const RnParams& p, int64_t t) {
     return {lo, offset(p, lo), offset(p, lo + 1)};
 }
 
+// Rows on their way to a thread: its words of the next kAhead rows of kArrays arrays, in shared memory.
+// Each thread copies and takes its own words, so nothing but its own copies is waited for.  One row
+// ahead in registers, as elsewhere, does not cover memory's latency where few blocks of large rows
+// are on an SM: backward (16 warps), 32,400 x 1,024 in bfloat16 took 88.4 us that way and takes 79.8
+// with 3 rows, 81.2 with 2, 80.3 with 4; forward, 8,100 x 4,096 58 and 49, but 64 x 256 4.1 and 4.5:
+// there rows of up to 1,024 values have no ring.  In fp32, twice the words: 16,200 x 1,024, backward, 71 us
+// without and 85 with it.
+constexpr int kAhead = 3;
+constexpr int kShortRow = 128;  // threads
+template <typename T, bool kVec, int kThreads>
+constexpr bool kUsesRing = kVec && sizeof(T) == 2 && kThreads > kShortRow;
+template <typename Row, int kArrays>
+struct RowRing {
+    static constexpr int kRowWords = kArrays * Row::kWords;
+    uint4* at;  // the thread's first word
+    int step;   // words of the block's threads
+    int stage;  // of the row that is next to be taken
+    static size_t bytes(int threads) { return (size_t)kAhead * kRowWords * threads * 16; }
+    __device__ __forceinline__ uint4* words(int s, int array) const {
+        return at + (s * kRowWords + array * Row::kWords) * step;
+    }
+    __device__ __forceinline__ void bring(int s, int array, const char* from) const {
+#pragma unroll
+        for (int k = 0; k < Row::kWords; ++k) cp_async16(words(s, array) + k * step, from + k * 16);
+    }
+    __device__ __forceinline__ void take(Row& r, int array) const { r.take(words(stage, array), step); }
+    __device__ __forceinline__ void next() { stage = stage == kAhead - 1 ? 0 : stage + 1; }
+};
+
 // beta gate times post's weight and bias, of sequence b (the first one's where none holds the row)
 template <bool kVec, int kPairs>
 __device__ __forceinline__ void mix_of(const RnParams& p, const Columns<kVec, kPairs>& c, int b,
@@ -361,7 +399,7 @@ __device__ __forceinline__ void mix_of(const RnParams& p, const Columns<kVec, kP
 // kLayer: one of the norms is a layer norm.  The statistics of the next row's y are formed with sums of
 // this row, where there are such (ahead).
 template <typename T, bool kVec, int kPairs, bool kLayer, bool kBias, int kThreads>
-__global__ void __launch_bounds__(kThreads) residual_norm_kernel(const RnParams p) {
+__global__ void __launch_bounds__(kThreads, kFwdWarps * 32 / kThreads) residual_norm_kernel(const RnParams p) {
     grid_dep_sync();
     using V = Values<kPairs>;
     using Row = RawRow<T, kVec, kPairs>;
@@ -384,7 +422,27 @@ __global__ void __launch_bounds__(kThreads) residual_norm_kernel(const RnParams 
         x.load(p.x.at(row, shift), c);
         if (p.y.p) y.load(p.y.at(row, shift), c);
     };
-    load((uint32_t)t);
+    constexpr bool kRing = kUsesRing<T, kVec, kThreads>;
+    extern __shared__ uint4 ring_words[];
+    RowRing<Row, 2> ring{ring_words + threadIdx.x, (int)blockDim.x, 0};
+    const auto bring = [&](int stage, int64_t row) {
+        if (kRing && c.n > 0 && row < end) {
+            ring.bring(stage, 0, p.x.at((uint32_t)row, shift));
+            if (p.y.p) ring.bring(stage, 1, p.y.at((uint32_t)row, shift));
+        }
+        cp_async_commit();
+    };
+    const auto take_y = [&]() {  // once its row is there: all but the two last ones that were brought
+        cp_async_wait<kAhead - 1>();
+        if constexpr (kRing)
+            if (c.n > 0 && p.y.p) ring.take(y, 1);
+    };
+    if constexpr (kRing) {
+        for (int s = 0; s < kAhead; ++s) bring(s, t + s);
+        take_y();
+    } else {
+        load((uint32_t)t);
+    }
     const bool centred = kLayer && p.post == GS_NORM_LAYER, centred_r = kLayer && p.pre == GS_NORM_LAYER;
     const bool ahead = p.post != GS_NORM_NONE && p.pre != GS_NORM_NONE && (!centred || centred_r);
     float mean_y = 0.f, square = 0.f;  // of y and, less its mean (layer norms), of y^2
@@ -397,8 +455,17 @@ __global__ void __launch_bounds__(kThreads) residual_norm_kernel(const RnParams 
     };
     if (ahead) statistics(y.get());
     for (; t < end; ++t) {
+        if constexpr (kRing)
+            if (c.n > 0) ring.take(x, 0);
         V v = x.get(), u = y.get();
-        if (t + 1 < end) load((uint32_t)t + 1);
+        if constexpr (kRing) {
+            const int stage = ring.stage;
+            ring.next();
+            bring(stage, t + kAhead);
+            take_y();
+        } else if (t + 1 < end) {
+            load((uint32_t)t + 1);
+        }
         if (t >= at.end) {
             at = part_of(p, t);
             mix_of(p, c, at.b, &factor, kBias ? &rest : nullptr);
@@ -447,7 +514,7 @@ __global__ void __launch_bounds__(kThreads) residual_norm_kernel(const RnParams 
 // the gate's gradient and, with it, those of post's weight and bias.  kBias: there are biases or
 // their gradients are wanted.  kLayer as above.
 template <typename T, bool kVec, int kPairs, bool kLayer, bool kBias, int kThreads>
-__global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnParams p) {
+__global__ void __launch_bounds__(kThreads, 1) residual_norm_bwd_kernel(const RnParams p) {
     grid_dep_sync();
     using V = Values<kPairs>;
     using Row = RawRow<T, kVec, kPairs>;
@@ -476,6 +543,24 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
         if (p.dr.p) dr.load(p.dr.at(row, shift), c);
         if (p.dh.p) dh.load(p.dh.at(row, shift), c);
     };
+    constexpr bool kRing = kUsesRing<T, kVec, kThreads>;
+    extern __shared__ uint4 ring_words[];
+    RowRing<Row, 4> ring{ring_words + threadIdx.x, (int)blockDim.x, 0};
+    const auto bring = [&](int stage, int64_t row) {
+        if (c.n > 0 && row < end) {
+            const uint32_t at = (uint32_t)row;
+            ring.bring(stage, 0, p.x.at(at, shift));
+            if (p.y.p) ring.bring(stage, 1, p.y.at(at, shift));
+            if (p.dr.p) ring.bring(stage, 2, p.dr.at(at, shift));
+            if (p.dh.p) ring.bring(stage, 3, p.dh.at(at, shift));
+        }
+        cp_async_commit();
+    };
+    const auto take_y = [&]() {  // once its row is there: all but the two last ones that were brought
+        cp_async_wait<kAhead - 1>();
+        if constexpr (kRing)
+            if (c.n > 0 && p.y.p) ring.take(y, 1);
+    };
     // the sequence's sums to those of all rows, and to its gate's gradient
     const auto leave = [&]() {
         if (at.b < 0) return;
@@ -503,7 +588,12 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
         else
             c.store(p.part_gate + ((int64_t)blockIdx.x * 2 + (from_before ? 0 : 1)) * p.width, d);
     };
-    load((uint32_t)t);
+    if constexpr (kRing) {
+        for (int s = 0; s < kAhead; ++s) bring(s, t + s);
+        take_y();
+    } else {
+        load((uint32_t)t);
+    }
     const bool centred = kLayer && p.post == GS_NORM_LAYER;
     const bool ahead = p.post != GS_NORM_NONE && (!centred || p.pre != GS_NORM_NONE);
     float mean_y = 0.f, square = 0.f;  // of y and, less its mean (layer norms), of y^2
@@ -516,9 +606,23 @@ __global__ void __launch_bounds__(kThreads) residual_norm_bwd_kernel(const RnPar
     };
     if (ahead) statistics(y.get());
     for (; t < end; ++t) {
+        if constexpr (kRing) {
+            if (c.n > 0) {
+                ring.take(x, 0);
+                if (p.dr.p) ring.take(dr, 2);
+                if (p.dh.p) ring.take(dh, 3);
+            }
+        }
         V v = x.get(), u = y.get(), d = dr.get();
         const V g = dh.get();
-        if (t + 1 < end) load((uint32_t)t + 1);
+        if constexpr (kRing) {
+            const int stage = ring.stage;
+            ring.next();
+            bring(stage, t + kAhead);
+            take_y();
+        } else if (t + 1 < end) {
+            load((uint32_t)t + 1);
+        }
         if (t >= at.end) {
             leave();
             at = part_of(p, t);
@@ -680,8 +784,8 @@ __global__ void __launch_bounds__(kFinishThreads)
 
 // How a row is shared out: threads of eight values, or of four where their addresses and column
 // sums would not fit the registers: odd widths in fp32 with biases or a layer norm.  (With both,
-// backward and forward, with four values: 16,200 x 515 79 and 40 us, 16,200 x 1,001 125 and 61, 8,103 x
-// 2,047 152 and 72; with eight 120 and 41, 180 and 60, 200 and 65.  Without either, 16,200 x 1,001: 78
+// backward and forward, with four values: 16,200 x 515 77 and 40 us, 16,200 x 1,001 124 and 61, 8,103 x
+// 2,047 151 and 73; with eight 120 and 41, 180 and 60, 200 and 65.  Without either, 16,200 x 1,001: 78
 // with four and 66 with eight; 32,400 x 1,001 in bfloat16 377 and 195.  96 registers, for five rows
 // instead of four at 515 values: 34 us instead of 31 on 4,346.)
 int pairs_of(const RnParams& p, bool vec, bool bf16, bool bias) {
@@ -729,6 +833,21 @@ bool whole_words(int width, std::initializer_list<NormRows> arrays) {
     return true;
 }
 
+// with the shared memory of a ring for kArrays arrays
+template <typename T, bool kVec, int kPairs, int kThreads, int kArrays>
+cudaError_t launch_rows(void (*kernel)(const RnParams), const RnParams& p, unsigned blocks,
+                        cudaStream_t st) {
+    const unsigned threads = (unsigned)warps_of(p.width, kPairs) * 32;
+    size_t ring = 0;
+    if constexpr (kUsesRing<T, kVec, kThreads>) {
+        ring = RowRing<RawRow<T, kVec, kPairs>, kArrays>::bytes(threads);
+        const cudaError_t e = cudaFuncSetAttribute(
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring);
+        if (e != cudaSuccess) return e;
+    }
+    return launch(kernel, dim3(blocks), dim3(threads), ring, st, p);
+}
+
 template <typename T, bool kVec, int kPairs, int kThreads>
 cudaError_t launch_fwd_of(const RnParams& p, bool bias, cudaStream_t st) {
     const bool layer = p.pre == GS_NORM_LAYER || p.post == GS_NORM_LAYER;
@@ -739,8 +858,8 @@ cudaError_t launch_fwd_of(const RnParams& p, bool bias, cudaStream_t st) {
     else
         kernel = bias ? residual_norm_kernel<T, kVec, kPairs, false, true, kThreads>
                       : residual_norm_kernel<T, kVec, kPairs, false, false, kThreads>;
-    return launch(kernel, dim3((unsigned)std::min(p.tokens, most_blocks(p.width, kPairs, kFwdWarps))),
-                  dim3((unsigned)warps_of(p.width, kPairs) * 32), 0, st, p);
+    return launch_rows<T, kVec, kPairs, kThreads, 2>(
+        kernel, p, (unsigned)std::min(p.tokens, most_blocks(p.width, kPairs, kFwdWarps)), st);
 }
 
 template <typename T, bool kVec>
@@ -749,6 +868,9 @@ cudaError_t launch_fwd(const RnParams& p, cudaStream_t st) {
     if constexpr (!kVec && sizeof(T) == 4)
         if (pairs_of(p, kVec, false, bias) == 2)
             return launch_fwd_of<T, kVec, 2, 512>(p, bias, st);
+    if constexpr (kVec && sizeof(T) == 2)
+        if (warps_of(p.width, 4) * 32 <= kShortRow)
+            return launch_fwd_of<T, kVec, 4, kShortRow>(p, bias, st);
     return launch_fwd_of<T, kVec, 4, kMostThreads>(p, bias, st);
 }
 
@@ -762,19 +884,20 @@ cudaError_t launch_bwd_of(const RnParams& p, bool bias, int blocks, cudaStream_t
     else
         kernel = bias ? residual_norm_bwd_kernel<T, kVec, kPairs, false, true, kThreads>
                       : residual_norm_bwd_kernel<T, kVec, kPairs, false, false, kThreads>;
-    return launch(kernel, dim3((unsigned)blocks), dim3((unsigned)warps_of(p.width, kPairs) * 32), 0, st,
-                  p);
+    return launch_rows<T, kVec, kPairs, kThreads, 4>(kernel, p, (unsigned)blocks, st);
 }
 
-// Up to 4,096 values a row its threads may have 128 registers each; beyond, 64 and spills.
+// Up to 4,096 values a row its threads may have 128 registers each; beyond, 64 and spills.  (Without
+// a number of blocks in its bounds the compiler gave these 32: 577 us instead of 268 on 2,025 x 8,192 in
+// fp32.)
 template <typename T, bool kVec>
 cudaError_t launch_bwd(const RnParams& p, bool bias, int blocks, cudaStream_t st) {
     if constexpr (!kVec && sizeof(T) == 4)
         if (pairs_of(p, kVec, false, bias) == 2)
             return launch_bwd_of<T, kVec, 2, 512>(p, bias, blocks, st);
     if (warps_of(p.width, 4) <= 16) return launch_bwd_of<T, kVec, 4, 512>(p, bias, blocks, st);
-    return launch(residual_norm_bwd_kernel<T, kVec, 4, true, true, kMostThreads>,
-                  dim3((unsigned)blocks), dim3((unsigned)warps_of(p.width, 4) * 32), 0, st, p);
+    return launch_rows<T, kVec, 4, kMostThreads, 4>(
+        residual_norm_bwd_kernel<T, kVec, 4, true, true, kMostThreads>, p, (unsigned)blocks, st);
 }
 
 }  // namespace
