@@ -74,6 +74,11 @@ CASES = [  # lens (of the gate's sequences, or one number of tokens), width, dty
     ([2600, 3, 900], 40, "f32", "layer", "layer", True, True, 44),
     ([1] * 500, 96, "f32", "rms", "none", True, False, None),  # a gate a token
     ([700, 1500], 1000, "f32", "rms", "rms", True, False, None),
+    # several rows of a block behind each other, on their way ahead of it
+    (1700, 2048, "bf16", "rms", "rms", True, False, None),
+    ([900, 0, 1100], 2048, "bf16", "layer", "layer", True, True, 2056),
+    (1300, 4096, "bf16", "none", "rms", False, False, None),
+    (1300, 4096, "bf16", "layer", "none", True, False, None),
 ]
 
 
@@ -345,3 +350,31 @@ def test_clip_grad_norm_within_its_bound_beside_outs_of_their_own():
     want = float(torch.cat(g).double().norm())
     assert abs(norm.item() - want) <= 12 * U * want
     assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(kept, g, outs))
+
+
+@pytest.mark.parametrize("pre,post,with_y,with_dr", [("rms", "rms", True, True), ("layer", "layer", True, False),
+                                                     ("rms", "none", False, True), ("none", "rms", True, True)])
+@pytest.mark.parametrize("tokens,width", [(2100, 2048), (6, 4096), (900, 8192), (3000, 256)])
+def test_residual_norm_in_place_of_rows_that_are_read_ahead(pre, post, with_y, with_dr, tokens, width):
+    import torch
+
+    gs = _gs()
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(width)
+    n = lambda on=True: (torch.randn((tokens, width), generator=gen, device="cuda").bfloat16()
+                         if on else None)
+    x, y, dr, dh = n(), n(with_y), n(with_dr or pre == "none"), n(pre != "none")
+    kw = dict(pre=pre, post=post, alpha=0.75, beta=1.5)
+    r, h = torch.empty_like(x), torch.empty_like(x) if pre != "none" else None
+    gs.gs_residual_norm(x, y, r, h, **kw)
+    a, b = x.clone(), None if y is None else y.clone()
+    out = b if b is not None and h is not None else None
+    gs.gs_residual_norm(a, b, a, out if out is not None else (h if h is None else torch.empty_like(x)), **kw)
+    assert torch.equal(a, r) and (out is None or torch.equal(out, h))
+    ws = torch.empty(gs.gs_residual_norm_workspace_bytes(tokens, width), dtype=torch.uint8, device="cuda")
+    dx, dy = torch.empty_like(x), None if y is None else torch.empty_like(x)
+    gs.gs_residual_norm_bwd(x, y, dr, dh, dx, dy, ws, **kw)
+    to_x = dr if dr is not None else dh
+    to_y = None if y is None else y
+    gs.gs_residual_norm_bwd(x, y, dr, dh, to_x, to_y, ws, **kw)
+    assert torch.equal(to_x, dx) and (dy is None or torch.equal(to_y, dy))
