@@ -31,7 +31,7 @@ template <int DP>
 struct DkvState {
     using Sh = DkvShape<DP>;
     uint64_t bar_k, bar_v, bar_k_free, bar_v_free, bar_s, bar_dp[Sh::kDp], bar_p, bar_ds[Sh::kDp],
-        bar_done, bar_out_free, bar_raw, bar_all, bar_want;
+        bar_done, bar_out_free, bar_raw, bar_all, bar_want, bar_kept, bar_join;
     uint64_t full_q[Sh::kSlots], empty_q[Sh::kSlots], full_d[Sh::kSlots], empty_d[Sh::kSlots],
         bar_work[kDkvWorks], bar_work_free[kDkvWorks];
     DkvWork works[kDkvWorks];
@@ -40,10 +40,9 @@ struct DkvState {
 
     __device__ __forceinline__ void init() {
         for (uint64_t* b : {&bar_k, &bar_v, &bar_k_free, &bar_v_free, &bar_s, &bar_done, &bar_raw,
-                            &bar_all, &bar_want})
+                            &bar_all, &bar_want, &bar_join})
             mbar_init(smem_u32(b), 1);
-        mbar_init(smem_u32(&bar_p), kMathWarps);
-        mbar_init(smem_u32(&bar_out_free), kMathWarps);
+        for (uint64_t* b : {&bar_p, &bar_out_free, &bar_kept}) mbar_init(smem_u32(b), kMathWarps);
         for (int i = 0; i < Sh::kDp; ++i) {
             mbar_init(smem_u32(&bar_dp[i]), 1);
             mbar_init(smem_u32(&bar_ds[i]), kMathWarps);
@@ -101,25 +100,32 @@ __device__ __forceinline__ void write_no_dkv(const BwdParams& p, const BwdWork& 
     }
 }
 
-__device__ __forceinline__ void math_sync() {  // of the math warps
-    asm volatile("bar.sync 1, %0;" ::"n"(kMathWarps * 32) : "memory");
-}
-
 // dK and dV of the sinks of a sequence that several blocks took, in the blocks' order, by the math
 // warps of the one that is done last.  DP / 4 lanes a row.  (By a kernel behind this one: 4 us more.)
+// The warps meet at barriers whose waits are bounded, as all here: some of them may have left where a
+// wait gave up, and at a barrier of the hardware the others would stay for ever.  `joins`: such blocks
+// of this CTA before this one.  False: a wait has given up.
 template <int DP>
-__device__ __forceinline__ void join_sinks(const BwdParams& p, const DkvWork& w, int* join) {
+__device__ __forceinline__ bool join_sinks(const BwdParams& p, const DkvWork& w, DkvState<DP>& sh,
+                                           int joins, volatile int* dead) {
     const Sequence sq = w.sq;
     const int64_t slot = sink_slot(sq.q0, p.sink_rows);
     const int pieces = (sq.n + p.sink_rows - 1) / p.sink_rows, sinks = p.window.sinks;
-    math_sync();
-    if (threadIdx.x == 0) {
-        __threadfence();
-        *join = atomicAdd(p.sinks_done + slot * p.heads_k + w.khead, 1u) == (unsigned)pieces - 1;
-        __threadfence();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sh.bar_kept));  // the warp's rows are kept
+    if (threadIdx.x < 32) {
+        if (!mbar_wait(smem_u32(&sh.bar_kept), joins & 1, dead)) return false;
+        if (threadIdx.x == 0) {
+            __threadfence();
+            sh.join =
+                atomicAdd(p.sinks_done + slot * p.heads_k + w.khead, 1u) == (unsigned)pieces - 1;
+            __threadfence();
+            mbar_arrive(smem_u32(&sh.bar_join));
+        }
+        __syncwarp();
     }
-    math_sync();
-    if (!*join) return;
+    if (!mbar_wait(smem_u32(&sh.bar_join), joins & 1, dead)) return false;
+    if (!sh.join) return true;
     constexpr int kLanes = DP / 4;
     const int lane = threadIdx.x % kLanes;
     for (int r = threadIdx.x / kLanes; r < 2 * w.key_end; r += kMathWarps * 32 / kLanes) {
@@ -137,6 +143,7 @@ __device__ __forceinline__ void join_sinks(const BwdParams& p, const DkvWork& w,
             *reinterpret_cast<uint2*>((of_v ? p.dv : p.dk).row(sq.k0 + key, w.khead) + lane * 4) =
                 make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
     }
+    return true;
 }
 
 // ---- the planner: one whole warp ----
@@ -384,7 +391,8 @@ __device__ __forceinline__ void dkv_math(const BwdParams& p, char* raw, uint32_t
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t s_at = At::s + lanes + half * 64;
     const float2 sl2 = make_float2(p.log2_scale, p.log2_scale);
-    int x = 0;  // steps of all blocks
+    int x = 0;      // steps of all blocks
+    int joins = 0;  // blocks so far whose sinks' sums are kept
     for (int n = 0;; ++n) {
         const int slot_w = n % kDkvWorks;
         if (!mbar_wait(smem_u32(&sh.bar_work[slot_w]), (n / kDkvWorks) & 1, dead)) break;
@@ -473,7 +481,7 @@ __device__ __forceinline__ void dkv_math(const BwdParams& p, char* raw, uint32_t
         tmem_fence_before();  // they may be written over
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.bar_out_free));
-        if (w.sinks && split) join_sinks<DP>(p, w, &sh.join);
+        if (w.sinks && split && !join_sinks<DP>(p, w, sh, joins++, dead)) break;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.bar_work_free[slot_w]));
     }
