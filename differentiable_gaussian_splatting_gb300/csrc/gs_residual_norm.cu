@@ -833,17 +833,21 @@ bool whole_words(int width, std::initializer_list<NormRows> arrays) {
     return true;
 }
 
-// with the shared memory of a ring for kArrays arrays
+// With the shared memory of a ring for kArrays arrays.  The kernel's limit on it is that of the widest
+// row, whatever this call's width: it belongs to the kernel, and another thread's call may set it
+// between this one's setting and launch.
 template <typename T, bool kVec, int kPairs, int kThreads, int kArrays>
 cudaError_t launch_rows(void (*kernel)(const RnParams), const RnParams& p, unsigned blocks,
                         cudaStream_t st) {
     const unsigned threads = (unsigned)warps_of(p.width, kPairs) * 32;
     size_t ring = 0;
     if constexpr (kUsesRing<T, kVec, kThreads>) {
-        ring = RowRing<RawRow<T, kVec, kPairs>, kArrays>::bytes(threads);
-        const cudaError_t e = cudaFuncSetAttribute(
-            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring);
+        using Ring = RowRing<RawRow<T, kVec, kPairs>, kArrays>;
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)Ring::bytes(kThreads));
         if (e != cudaSuccess) return e;
+        ring = Ring::bytes(threads);
     }
     return launch(kernel, dim3(blocks), dim3(threads), ring, st, p);
 }
