@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "gs_device.cuh"
@@ -271,13 +272,17 @@ __device__ __forceinline__ void zero_rows(char* tile, int first) {
 cudaError_t gave_up_word(unsigned int** word);
 
 // A launch of 384 threads that divides its registers anew among its groups of four warps must have
-// exactly those that the shares add up to: a share that the launch has not waits for ever.
+// those that the shares add up to: a share that the launch has not is waited for without end.
+// `known`: whether an earlier call found them there; anything else is looked at again.
 constexpr int kLaunchRegisters = 168;
-inline cudaError_t launch_registers_ok(const void* kernel) {
+inline cudaError_t launch_registers_ok(const void* kernel, std::atomic<bool>* known) {
+    if (known->load(std::memory_order_relaxed)) return cudaSuccess;
     cudaFuncAttributes a{};
     const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
     if (e != cudaSuccess) return e;
-    return a.numRegs == kLaunchRegisters ? cudaSuccess : cudaErrorInvalidConfiguration;
+    if (a.numRegs < kLaunchRegisters) return cudaErrorInvalidConfiguration;
+    known->store(true, std::memory_order_relaxed);
+    return cudaSuccess;
 }
 
 // A wait that may take as long as blocks do, for the blocks' planner and whoever waits for it: as

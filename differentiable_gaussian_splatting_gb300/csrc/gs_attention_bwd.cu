@@ -1084,8 +1084,9 @@ cudaError_t launch_dim(const BwdMaps& m, BwdParams p, const gs_window* w, cudaSt
         if (v.tq > 0) p.sink_blocks = tiles_at_most(v.tq, p.sink_rows, v.batch) * p.heads_k;
     }
     if constexpr (kWindow) {
-        static const cudaError_t registers =
-            launch_registers_ok(reinterpret_cast<const void*>(attention_bwd_kernel<DP, true>));
+        static std::atomic<bool> known{false};
+        const cudaError_t registers = launch_registers_ok(
+            reinterpret_cast<const void*>(attention_bwd_kernel<DP, true>), &known);
         if (registers != cudaSuccess) return registers;
     }
     constexpr uint32_t kSmem = std::max(DkvShape<DP>::kSmem, DqShape<DP>::kSmem);

@@ -632,12 +632,12 @@ template <int DP>
 cudaError_t launch_dim(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                        const FwdParams& p, cudaStream_t st) {
     constexpr uint32_t kSmem = FwdShape<DP>::kSmem + kSoftmaxWarps * kStageBytes;
-    static const cudaError_t registers =
-        launch_registers_ok(reinterpret_cast<const void*>(attention_window_fwd_kernel<DP>));
-    if (registers != cudaSuccess) return registers;
-    cudaError_t e = cudaFuncSetAttribute(attention_window_fwd_kernel<DP>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kSmem);
+    static std::atomic<bool> known{false};
+    cudaError_t e = launch_registers_ok(
+        reinterpret_cast<const void*>(attention_window_fwd_kernel<DP>), &known);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(attention_window_fwd_kernel<DP>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
     const int64_t blocks = p.plan.spread ? kSms : p.plan.whole;
     e = launch(attention_window_fwd_kernel<DP>, dim3((unsigned)std::min<int64_t>(blocks, kSms)),
