@@ -274,14 +274,11 @@ struct RowSum {
         if (writes) (&to[threadIdx.x >> 5].x)[at] = v;
         __syncthreads();
         float4 s = to[0];
-        const auto plus = [&](int w) {
+        // (Sums of up to four warps written out: 49.5 and 78.7 instead of 50.6 and 79.5 us at 32,400 x
+        // 1,024, but 75.7 instead of 74.3 at 64,800 x 512 and 57.4 instead of 55.6 at 8,100 x 2,048 fp32.)
+        for (int w = 1; w < warps; ++w) {
             const float4 o = to[w];
             s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
-        };
-        if (warps == 4) {
-            plus(1), plus(2), plus(3);
-        } else {
-            for (int w = 1; w < warps; ++w) plus(w);
         }
         return s;
     }
