@@ -114,6 +114,10 @@ struct Words {
                 w[i] = __ldg(reinterpret_cast<const uint4*>(row) + c + 4 * i);
         }
     }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = make_uint4(0, 0, 0, 0);
+    }
     __device__ __forceinline__ uint32_t at(int i, int j) const {
         return j == 0 ? w[i].x : j == 1 ? w[i].y : j == 2 ? w[i].z : w[i].w;
     }
@@ -205,6 +209,12 @@ __global__ void __launch_bounds__(kTokenThreads, 2) attention_tokens_kernel(cons
             // (by the score, not by the maximum: a row of NaN has none)
             s[e] = s[e] == -INFINITY ? 0.f : ex2_approx(s[e] - top[e & 1]);
             sum[e & 1] += s[e];
+        }
+        // values behind the last key are the last one's, with probability 0: zeros instead, which that
+        // leaves out whatever they are.  (Loaded as zeros: up to 7 % more for every step's choice.)
+        if (at + kStep > keys) {
+            if (at + r >= keys) v0.clear();
+            if (at + r + 8 >= keys) v1.clear();
         }
         const uint32_t p0 = transposed(pack_bf16(s[0], s[1])), p1 = transposed(pack_bf16(s[2], s[3]));
 #pragma unroll
