@@ -14,8 +14,8 @@ device is present, the calls raise.
 Next to the path stand the token operators of a network that predicts Gaussians
 and is trained through it: ``gs_qk_norm_rope``, ``gs_attention_fwd``,
 ``gs_dropout_add``, ``gs_residual_norm`` and their gradients, and
-``gs_clip_grad_norm``.  They take torch tensors, which a small compiled module
-checks and passes on (``csrc/token_binding.cpp``).
+``gs_clip_grad_norm``.  They take torch tensors of the current device, which a
+small compiled module checks and passes on (``csrc/token_binding.cpp``).
 
 ``Rasterizer`` is a convenience that allocates the outputs and workspaces of
 one view and runs the five calls in order.

@@ -5,6 +5,7 @@
 // (6 for attention's gradient with its two launches) instead of 6 to 23.  Errors are those of
 // the Python code: TypeError and ValueError for tensors; the status of the call is returned.
 #include <Python.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -46,10 +47,21 @@ std::string text(const A&... a) {
     return s.str();
 }
 
+// The device that this thread's call launches on (-1: there is none).  A kernel there that was given
+// another device's memory would fault.
+thread_local c10::DeviceIndex current_device = -1;
+
+void look_up_device() {
+    if (c10::cuda::GetDevice(&current_device) != cudaSuccess) current_device = -1;
+}
+
 const Tensor& tensor(PyObject* o, const char* name) {
     if (!THPVariable_Check(o)) throw TypeError(text(name, ": expected a torch tensor"));
     const Tensor& t = THPVariable_Unpack(o);
     if (!t.is_cuda()) throw ValueError(text(name, ": must be a CUDA tensor"));
+    if (current_device >= 0 && t.device().index() != current_device)
+        throw ValueError(text(name, ": is on ", t.device(), ", the current device is cuda:",
+                              (int)current_device));
     return t;
 }
 
@@ -465,6 +477,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
         return nullptr;
     }
     try {
+        look_up_device();
         return PyLong_FromLong((long)kCall(args));
     } catch (const TypeError& e) {
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_TypeError, e.what());
