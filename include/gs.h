@@ -683,8 +683,9 @@ gs_status gs_residual_norm_bwd(int64_t tokens, int32_t width, const gs_block_nor
  * gs_clip_grad_norm -- the norm over all values of a step's gradients, and the gradients scaled to
  * a norm of at most max_norm:
  *   norm = (sum over all arrays of g^2)^(1/2),  out = g min(1, max_norm / norm)
- * Where norm is not finite (a gradient is infinite or NaN; finite ones do not overflow: squares
- * are summed in fp64 where they would) the factor is 0 and every out value 0.
+ * Where a gradient is infinite or NaN so is norm, the factor is 0 and every out value 0.  Finite
+ * gradients do not overflow (squares are summed in fp64 where they would): beyond fp32's range norm
+ * is stored as infinity, and the outs are scaled by its fp64 value all the same.
  *
  *   count      0..65536 arrays of at most 2^40 elements each, 2^42 in all
  *   grads      host array: device data (aligned to an element; at 16 bytes it goes faster, NULL
