@@ -21,6 +21,10 @@ constexpr int32_t kMaxHeads = 1024;
 constexpr int32_t kMaxBatch = 1 << 20;
 constexpr int32_t kMaxNormDim = 256, kMaxAttentionDim = 128;
 constexpr int32_t kMaxSinks = 128;  // of one key tile
+// Sequences times query heads of a call by tiles with a window.  Every sequence has places for its tiles,
+// used or not, and a CTA's planner takes 0.8 us (forward) or 1.3 us (gradient, whose two kinds of blocks
+// of keys follow each other) to find one empty: 0.6 s at most, while waits give up after two.
+constexpr int64_t kMaxWindowPlaces = int64_t(1) << 25;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -190,12 +194,14 @@ gs_status attention_fwd(const gs_attention_shape* shape, const gs_window* window
         !heads_ok(v, s.tokens_k, s.heads_k, s.head_dim, 2) ||
         !heads_ok(out, s.tokens_q, s.heads_q, s.head_dim, 2))
         return GS_ERR_INVALID_ARG;
+    const bool few = window && few_queries(s);
+    if (window && !few && (int64_t)s.batch * s.heads_q > kMaxWindowPlaces) return GS_ERR_INVALID_ARG;
     if (workspace_bytes < needed) return GS_ERR_WORKSPACE;
     const gs_heads nq = normal(q, s.tokens_q, s.heads_q, s.head_dim),
                    nk = normal(k, s.tokens_k, s.heads_k, s.head_dim),
                    nv = normal(v, s.tokens_k, s.heads_k, s.head_dim),
                    no = normal(out, s.tokens_q, s.heads_q, s.head_dim);
-    if (window && few_queries(s))
+    if (few)
         return status_of(launch_attention_tokens(s, *window, nq, nk, nv, no, lse, cu_q, cu_k,
                                                  (cudaStream_t)stream));
     return status_of(window ? launch_attention_window_fwd(s, *window, nq, nk, nv, no, lse, cu_q, cu_k,
@@ -221,6 +227,7 @@ gs_status attention_bwd(const gs_attention_shape* shape, const gs_window* window
         if (!heads_ok(h, s.tokens_q, s.heads_q, s.head_dim, 2)) return GS_ERR_INVALID_ARG;
     for (const gs_heads* h : of_k)
         if (!heads_ok(h, s.tokens_k, s.heads_k, s.head_dim, 2)) return GS_ERR_INVALID_ARG;
+    if (window && (int64_t)s.batch * s.heads_q > kMaxWindowPlaces) return GS_ERR_INVALID_ARG;
     if (workspace_bytes < needed) return GS_ERR_WORKSPACE;
     const auto nq = [&](const gs_heads* h) {
         return normal(h, s.tokens_q, s.heads_q, s.head_dim);

@@ -559,6 +559,8 @@ gs_status gs_attention_bwd(const gs_attention_shape* shape, const gs_heads* q, c
  *
  *   left, right  >= 0; as large as the sequences: all keys on that side
  *   sinks        0..128
+ *   shape        batch times heads_q at most 2^25; in forward calls of at most one query a sequence,
+ *                on average, 2^27
  *   workspace    >= gs_attention_window_workspace_bytes(shape, window)
  */
 typedef struct {
