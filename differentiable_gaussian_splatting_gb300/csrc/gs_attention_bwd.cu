@@ -35,10 +35,10 @@
 // With a window (gs_attention_window_dkv.cuh, gs_attention_window_dq.cuh) a block meets few tiles, so
 // CTAs go through blocks of either kind without a gap.  The first `sinks` keys, which any query may
 // see, have blocks of their own.  8,160 tokens, 16 heads on 4 x 128, 1,024 keys: 197 us with the row
-// sums, 223 with 4 sinks (a tile more for every block of queries, and for the sinks tiles of 128 keys of
+// sums, 222 with 4 sinks (a tile more for every block of queries, and for the sinks tiles of 128 keys of
 // which 4 are some), 720 TFLOP/s of the gradient's five products, 1,010 of the seven; the steps alone
 // would take 177 at the pace of the full gradient.  2,500 + 64 + 1 + 1,039 tokens, 8 heads x 64, 513
-// keys and 16 sinks: 41 us.
+// keys and 16 sinks: 42 us.
 //
 // Rows of a tile that lie beyond the sequence and are contracted over are zeroed in shared
 // memory, and P and dS are set to zero there by selection, so that what lies behind a

@@ -14,7 +14,7 @@
 // their own running maximum and sum; the blocks join them in shared memory, the cluster its blocks'
 // over distributed shared memory: one launch, no workspace.
 //
-// Measured: 32 tokens, 16 heads on 4 x 128, 2,048 keys and 4 sinks each, 130 MB: 31.5 us, 4.1 TB/s;
+// Measured: 32 tokens, 16 heads on 4 x 128, 2,048 keys and 4 sinks each, 130 MB: 31.3 us, 4.2 TB/s;
 // 64 tokens 53 us, 5.0 TB/s, with 8 warps' loads of 16 keys ahead on two blocks an SM.  What is left is
 // the start (the sequence's place, then the first keys: two latencies) and the join of the blocks.
 //
@@ -321,6 +321,11 @@ cudaError_t launch_words(const TokenParams& p, int64_t items, cudaStream_t st) {
 // to 8,192 of them seen, 16 heads on 4 x 128, 1, 2, 4, 8 queries of each of 32 sequences: 31, 43, 75,
 // 139 us here, 118 to 126 by tiles; 8 x 64 on as many, 513 keys, 128 sequences, 1, 2, 3: 37, 58, 83 and
 // 64 by tiles.)
+// The host knows no lengths, so a batch of mixed ones goes by its average.  Single queries beside a prompt
+// are still better off here while windows are short, and up to three times worse where most queries are
+// one sequence's: 31 tokens on 8,000 keys and 129 queries on 32,400, as many heads, 1,024, 2,048, 32,400 of
+// the keys seen: 52, 90, 990 us here, 77, 129, 695 by tiles; 160 queries on 32,400 keys among 31 empty
+// sequences: 50, 88, 1,275 and 25, 38, 400.
 bool few_queries(const gs_attention_shape& s) {
     const int64_t few = 1 + std::min(s.heads_q / s.heads_k, 4);
     return s.tokens_q <= few * s.batch && s.tokens_q * s.heads_q <= (int64_t(1) << 27);

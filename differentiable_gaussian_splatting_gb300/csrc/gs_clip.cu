@@ -11,8 +11,8 @@
 //
 // Memory bounds it: the arrays are read, then read and written.  The second kernel walks a block's
 // chunks backwards, so that it meets first what the first one left in L2.  88.5M fp32 values: 169 us,
-// 6.3 TB/s of three times their bytes; 139M bfloat16 ones 143 us; 2.4M fp32 ones (L2 holds them) 11.0 us,
-// the latency of two kernels.
+// 6.3 TB/s of three times their bytes; 139M bfloat16 ones 143 us; 2.4M fp32 ones (L2 holds them) 11.1 us,
+// the latency of two kernels and of the arrays' ends, which go element by element.
 //
 // Sums.  A thread's squares of one chunk (at most 64) go into fp32, the chunks' sums into pairs of
 // fp32 (a sum and what its roundings left), the blocks' into fp64, whose units take a third of the

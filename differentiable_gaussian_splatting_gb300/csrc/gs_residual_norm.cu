@@ -22,8 +22,8 @@
 // all its rows, of the gate over those of a sequence.  Another kernel adds the blocks' sums up in the
 // blocks' order: the same inputs give the same bits.
 //
-// Measured, 32,400 x 1,024 in bfloat16 with RMS norms on both sides and a gate: forward 49.2 us, 5.4
-// TB/s, 0.79 of the copy rate; backward 79.6 us, 5.0 TB/s, with two or three sums over a row and 16 warps
+// Measured, 32,400 x 1,024 in bfloat16 with RMS norms on both sides and a gate: forward 50.4 us, 5.3
+// TB/s, 0.78 of the copy rate; backward 81.6 us, 4.9 TB/s, with two or three sums over a row and 16 warps
 // an SM (128 registers) on the way, and 8 us of the blocks' sums.  64 x 256: 4.2 us, the latency of a
 // row.  Odd widths go value by value: 4,346 x 515 in fp32 with layer norms and biases, backward, 30.5 us.
 //
@@ -349,8 +349,8 @@ __device__ __forceinline__ Part part_of(const RnParams& p, int64_t t) {
 // Rows on their way to a thread: its words of the next kAhead rows of kArrays arrays, in shared memory.
 // Each thread copies and takes its own words, so nothing but its own copies is waited for.  One row
 // ahead in registers, as elsewhere, does not cover memory's latency where few blocks of large rows
-// are on an SM: backward (16 warps), 32,400 x 1,024 in bfloat16 took 88.4 us that way and takes 79.8
-// with 3 rows, 81.2 with 2, 80.3 with 4; forward, 8,100 x 4,096 58 and 49, but 64 x 256 4.1 and 4.5:
+// are on an SM: backward (16 warps), 32,400 x 1,024 in bfloat16 took 88.4 us that way and takes 79.5
+// with 3 rows, 81.5 with 2, 80.3 with 4; forward, 8,100 x 4,096 58 and 49, but 64 x 256 4.1 and 4.5:
 // there rows of up to 1,024 values have no ring.  In fp32, twice the words: 16,200 x 1,024, backward, 71 us
 // without and 85 with it.
 constexpr int kAhead = 3;
@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(kFinishThreads)
 // sums would not fit the registers: odd widths in fp32 with biases or a layer norm.  (With both,
 // backward and forward, with four values: 16,200 x 515 77 and 40 us, 16,200 x 1,001 124 and 61, 8,103 x
 // 2,047 151 and 73; with eight 120 and 41, 180 and 60, 200 and 65.  Without either, 16,200 x 1,001: 78
-// with four and 66 with eight; 32,400 x 1,001 in bfloat16 377 and 195.  96 registers, for five rows
+// with four and 66 with eight; 32,400 x 1,001 in bfloat16 377 and 199.  96 registers, for five rows
 // instead of four at 515 values: 34 us instead of 31 on 4,346.)
 int pairs_of(const RnParams& p, bool vec, bool bf16, bool bias) {
     const bool layer = p.pre == GS_NORM_LAYER || p.post == GS_NORM_LAYER;
