@@ -555,7 +555,8 @@ gs_status gs_attention_bwd(const gs_attention_shape* shape, const gs_heads* q, c
  * key c = i + m - n of m (the last query at the last key) and sees key j iff
  *   c - left <= j <= c + right  or  j < sinks,  and with causal: j <= c.
  * Work and time go with the pairs seen, not with n m.  Everything else is as there; what the window
- * hides must be finite as what the mask hides.
+ * hides must be finite as what the mask hides.  A forward call of up to five queries a sequence, on
+ * average, takes every query by itself: a prompt among many empty sequences is faster without them.
  *
  *   left, right  >= 0; as large as the sequences: all keys on that side
  *   sinks        0..128
