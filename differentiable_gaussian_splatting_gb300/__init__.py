@@ -747,7 +747,8 @@ def gs_clip_grad_norm_workspace_bytes(count) -> int:
 def gs_clip_grad_norm(grads, max_norm, norm, workspace, outs=None, stream=None):
     """The norm over all of grads, a list of contiguous float32 or bfloat16 tensors, into norm
     (float32 [1]), and the gradients scaled to at most max_norm into outs, tensors of the same
-    sizes and types (None: in place); see gs.h."""
+    sizes and types (None: in place); see gs.h.  A finite max_norm beyond float32 counts as its
+    largest number."""
     st = (_calls or _token_calls()).clip_grad_norm(grads, max_norm, norm, workspace, outs, stream)
     if st:
         _check("gs_clip_grad_norm", st)

@@ -10,6 +10,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <exception>
@@ -142,11 +143,9 @@ float number(PyObject* o) {
 }
 
 // A number for which infinity has a meaning of its own: a finite one beyond fp32 does not become it.
-float finite_or_infinite(PyObject* o, const char* name) {
+float finite_or_infinite(PyObject* o) {
     const float f = number(o);
-    if (std::isinf(f) && !std::isinf(PyFloat_AsDouble(o)))
-        throw ValueError(text(name, ": ", PyFloat_AsDouble(o), " is beyond float32"));
-    return f;
+    return std::isinf(f) && !std::isinf(PyFloat_AsDouble(o)) ? std::copysign(FLT_MAX, f) : f;
 }
 
 // what an object is as a condition; one that has no truth value raises
@@ -472,9 +471,8 @@ gs_status clip_grad_norm(PyObject* const* a) {
     const Bytes ws = workspace(a[3]);
     std::vector<gs_array> o;
     if (a[4] != Py_None) o = arrays(a[4], "outs", &g);
-    const float max_norm = finite_or_infinite(a[1], "max_norm");
     return unlocked(gs_clip_grad_norm, small((int64_t)g.size(), "grads"), g.data(),
-                    a[4] != Py_None ? o.data() : nullptr, max_norm, norm, ws.p, ws.n,
+                    a[4] != Py_None ? o.data() : nullptr, finite_or_infinite(a[1]), norm, ws.p, ws.n,
                     stream_of(a[5]));
 }
 
